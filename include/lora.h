@@ -77,6 +77,9 @@ typedef enum {
 #define LORA_DEV_SLOT_OUT_OF_RANGE 0x1 /* a row named an id >= n_slots or < -1; row skipped */
 #define LORA_DEV_BAD_SEGMENT 0x2       /* a segment/perm entry fell outside its rows, or a
                                           group outgrew meta->max_gseg_len; rows skipped */
+#define LORA_DEV_BAD_PAGE 0x8          /* a block table named a page outside [0, n_pages): nothing is
+                                          read from or written to it (see lora_kv4_*) */
+#define LORA_DEV_BAD_POSITION 0x10     /* a rotary position outside [0, max_pos); row skipped */
 #define LORA_DEV_TIMEOUT 0x4           /* an asynchronous copy did not land within 0.2 s (never
                                           expected): the kernel that waited stops; rows of y it
                                           had not finished keep their previous values (a shrink
@@ -365,6 +368,186 @@ lora_status_t lora_merge(lora_bf16_t* W, int ld_w, int out, int h_in, const lora
 lora_status_t lora_merge_batch(int n, lora_bf16_t* const* W, const int* ld_w, const int* out, const int* h_in,
                                const lora_bf16_t* const* A, const lora_bf16_t* const* B, int r_slot, int sign,
                                lora_stream_t stream);
+
+/* ------------------------------------------------------------------ *
+ *  Around the projections of an attention block: the norm before them,
+ *  and the rotary embedding, 4-bit cache and attention between the q/k/v
+ *  and the output projection.  The source pages have no counterpart to
+ *  these entry points; a serving layer needs them next to the projections.
+ *
+ *  Ordering: their kernels use programmatic dependent launch only to hide
+ *  their own start; they read and write memory as in plain stream order.
+ * ------------------------------------------------------------------ */
+
+/*
+ * Root-mean-square norm with the residual's addition, and an output in 8
+ * bits with scales.  For every row t, over `width` columns c:
+ *   h[c] = bf16_rne( x[t][c] + residual[t][c] )        (residual NULL: x[t][c])
+ *   n[c] = h[c] / sqrt( sum_c h[c]^2 / width + eps ) * weight[c]   (fp32)
+ *   y[t][c]   = bf16_rne( n[c] )
+ *   scales[t][g] = max_{c in group g} |n[c]| / 448,  y8[t][c] = e4m3_rne( n[c] / scales[t][g] )
+ * h goes back to memory (residual_out), so the norm is that of the value
+ * that later layers read.  y is the input of the LoRA projections, y8 with
+ * its scales that of an 8-bit base product; both come from one pass.
+ * x, residual     [dev] bf16 [n_rows][ld_x], [n_rows][ld_res]
+ * residual_out    [dev] bf16 [n_rows][ld_res_out]; may be residual or x
+ *                 itself; NULL only when residual is NULL
+ * weight          [dev] bf16 [width]
+ * y               [dev] bf16 [n_rows][ld_y], may be x itself, or NULL
+ * y8              [dev] e4m3 [n_rows][ld_y8], 8-byte aligned, or NULL
+ * scales          [dev] fp32 [n_rows][ld_scales], 4-byte aligned (with y8)
+ * group           columns per scale: 128 (the last group may be shorter),
+ *                 or 0 for one scale per row
+ * A group of zeros has scale 0 and codes 0.  A NaN in a row makes the whole
+ * row NaN.  Apart from the aliases named above, outputs overlap no input.
+ * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL x or
+ * weight, neither y nor y8, y8 without scales, residual without
+ * residual_out or the reverse, n_rows < 0, width <= 0, eps negative or not finite),
+ * LORA_ERR_SHAPE (a leading dimension below width, ld_scales below the
+ * groups of a row, width > 65536, group neither 0 nor 128),
+ * LORA_ERR_ALIGNMENT, LORA_ERR_CUDA.
+ */
+lora_status_t lora_rms_norm(lora_bf16_t* y, int ld_y, uint8_t* y8, int ld_y8, float* scales, int ld_scales,
+                            int group, lora_bf16_t* residual_out, int ld_res_out, const lora_bf16_t* x, int ld_x,
+                            const lora_bf16_t* residual, int ld_res, const lora_bf16_t* weight, int n_rows,
+                            int width, float eps, lora_stream_t stream);
+
+/*
+ * A paged cache of keys and values in 4 bits.  A page holds page_size
+ * consecutive positions of one sequence for every kv head; page p starts
+ * at pages + p * page_stride, and its kv head h at h * block bytes,
+ *   block bytes = page_size * (D + 8 * D/64)            (D = head_dim)
+ * (lora_kv4_block_bytes), laid out as
+ *   K codes   uint32 [page_size][4][D/32]    word (t, w): dims 32w + 8t + n, nibble n
+ *   V codes   uint32 [page_size/2][D/4]      word i: dims 4i + j, nibble j of the even
+ *                                            position, nibble 4 + j of the odd one
+ *   K params  fp16 [page_size][D/64][2]      (step, low) of the group's 64 dims
+ *   V params  fp16 [page_size/2][D/64][4]    (step even, step odd, low even, low odd)
+ * A cached value is code * step + low, with code 0..15.  An append stores,
+ * for each group of 64 dims of a head,
+ *   low = fp16_rne(min),  step = fp16_rne((max - min) / 15),
+ *   code = min(15, max(0, rint((value - low) / step)))     (0 where step is 0)
+ * of values saturated at +-60000; a NaN makes its group NaN.
+ * The layout is the order in which the attention kernel's matrix fragments
+ * take the codes: the four lanes of a K row each read 16 adjacent bytes,
+ * and a V word's two halves are the two positions of one matrix operand.
+ */
+typedef struct {
+    uint8_t* pages;      /* [dev] 16-byte aligned */
+    int64_t page_stride; /* bytes, a multiple of 16, at least n_kv * block bytes */
+    int n_pages;
+    int page_size;       /* 16, 32, 64, 128 or 256 */
+    int n_kv;            /* kv heads */
+    int head_dim;        /* 64 or 128 */
+} lora_kv4_cache_t;
+
+/*
+ * The rows of a batch and where they stand in the cache.  Sequence s owns
+ * the rows [q_starts[s], q_starts[s+1]) and has ctx_lens[s] positions, its
+ * rows being the last ones: with n rows, row q_starts[s] + i stands at
+ * position p = ctx_lens[s] - n + i, in page block_table[s][p / page_size].
+ * A sequence may have no rows.  A row whose position is negative (n >
+ * ctx_lens[s]) has no place in the cache: nothing is stored for it and it
+ * attends to nothing.
+ * Device-detected faults: a sequence whose table entries are inconsistent
+ * (q_starts decreasing or past n_rows, more rows than max_q_len, ctx_lens
+ * negative or above max_ctx_len) is skipped and sets LORA_DEV_BAD_SEGMENT
+ * (lora_kv4_attend does not write its rows); a page id outside [0, n_pages)
+ * sets LORA_DEV_BAD_PAGE, and its positions count as masked.
+ */
+typedef struct {
+    const int32_t* q_starts;    /* [dev] [n_seqs+1]; q_starts[0] == 0, q_starts[n_seqs] == n_rows */
+    const int32_t* ctx_lens;    /* [dev] [n_seqs] */
+    const int32_t* block_table; /* [dev] [n_seqs][ld_table] page ids */
+    int ld_table;               /* at least ceil(max_ctx_len / page_size) */
+    int n_seqs;
+    int n_rows;
+    int max_q_len;              /* host values; upper bounds, which pick the kernel form */
+    int max_ctx_len;            /* and size the grids */
+} lora_kv4_batch_t;
+
+/* Bytes of one page's block of one kv head; 0 for a page size or head
+ * dimension the cache does not have. */
+size_t lora_kv4_block_bytes(int page_size, int head_dim);
+
+/* Most position axes of a rotary embedding (time, height, width). */
+#define LORA_MAX_ROPE_AXES 3
+
+/*
+ * Rotary embedding and cache append of the rows of a fused q/k/v
+ * projection.  Of every row t, the heads q (n_heads), k and v (n_kv each)
+ * start at columns q_off, k_off and v_off of x.  The first rot_dim
+ * dimensions of each q and k head are rotated in pairs (i, i + rot_dim/2):
+ *   a' = a cos - b sin,  b' = b cos + a sin
+ * with (cos, sin) = rope[pos][i], where pos is the row's position on the
+ * axis that pair i belongs to: the first axis_pairs[0] pairs turn with the
+ * first axis, the next axis_pairs[1] with the second, and so on (text: one
+ * axis; images and video: time, height and width).  q goes to q_out (bf16),
+ * k and v to the cache at the row's place.
+ * q_out      [dev] bf16 [n_rows][ld_q]; may be x + q_off itself
+ * x          [dev] bf16 [n_rows][ld_x]
+ * rope       [dev] fp32 [max_pos][rot_dim/2][2] (cos, sin); NULL with rot_dim 0
+ * positions  [dev] int32 [n_rows][ld_pos], n_axes per row; NULL: a row's
+ *            place in the cache, on every axis
+ * axis_pairs [host] n_axes entries, sum rot_dim/2
+ * Sums and products in fp32, each product rounded on its own, so that the
+ * cached bytes do not depend on how a compiler contracts them.
+ * A row without a place in the cache is skipped whole (its q_out is not
+ * written); so is, with LORA_DEV_BAD_POSITION, a row with a position
+ * outside [0, max_pos).  With LORA_DEV_BAD_PAGE, q_out alone is written.
+ * Two rows of a call that name the same place race.
+ * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL
+ * pointers, counts out of range, rot_dim without a table, n_axes outside
+ * 1..LORA_MAX_ROPE_AXES, a negative axis_pairs), LORA_ERR_SHAPE (slices
+ * past or overlapping in the row, rot_dim > head_dim, axis_pairs not
+ * summing to rot_dim/2, ld_pos < n_axes, a cache or block table too small),
+ * LORA_ERR_ALIGNMENT (as above; rot_dim a multiple of 16), LORA_ERR_CUDA.
+ */
+lora_status_t lora_kv4_append(lora_bf16_t* q_out, int ld_q, const lora_bf16_t* x, int ld_x, int n_heads, int q_off,
+                              int k_off, int v_off, const float* rope, int rot_dim, int max_pos,
+                              const int32_t* positions, int ld_pos, const int* axis_pairs, int n_axes,
+                              const lora_kv4_cache_t* cache, const lora_kv4_batch_t* batch, int32_t* dev_status,
+                              lora_stream_t stream);
+
+/*
+ * The cached keys and values of every row's place, as bf16_rne(code * step
+ * + low): k, v [dev] bf16 [n_rows][ld_k / ld_v], n_kv * head_dim columns.
+ * Rows without a place (or with a bad page) are not written.  With q_starts
+ * the running sum of ctx_lens it unpacks whole sequences, to move them to
+ * another cache or to compare.  Errors as lora_kv4_append.
+ */
+lora_status_t lora_kv4_read(lora_bf16_t* k, int ld_k, lora_bf16_t* v, int ld_v, const lora_kv4_cache_t* cache,
+                            const lora_kv4_batch_t* batch, int32_t* dev_status, lora_stream_t stream);
+
+/*
+ * Causal attention of the batch's rows over the cache.  q head h reads kv
+ * head h / (n_heads / n_kv).  The row at position p sees the positions
+ * j <= p, with window > 0 only those j > p - window:
+ *   out = sum_j softmax_j(scale * q . k_j) v_j
+ * over the cached values (code * step + low); a row that sees nothing gets
+ * zeros.  Masked positions, and the rest of a partly filled page, do not
+ * reach the result whatever their bytes hold.
+ * out, q    [dev] bf16 [n_rows][ld_out], [n_rows][ld_q], n_heads * head_dim
+ *           columns; out may be q itself
+ * scale     finite, usually 1 / sqrt(head_dim)
+ * workspace [dev] at least lora_kv4_attend_workspace_bytes(...) bytes,
+ *           256-byte aligned; scratch, calls that may overlap need their own
+ * Sums, maxima and products accumulate in fp32; the softmax weights are
+ * rounded to fp16 for the product with V, q is taken to fp16 after scaling
+ * each row by a power of two (exact but for elements 2^-22 below the row's
+ * largest), cached values to fp16.
+ * Errors (before anything is enqueued): as lora_kv4_append, plus
+ * LORA_ERR_SHAPE (n_heads not a multiple of n_kv, more than 64 q heads to a
+ * kv head), LORA_ERR_WORKSPACE, LORA_ERR_INVALID_ARG (scale not finite,
+ * window < 0).
+ */
+lora_status_t lora_kv4_attend(lora_bf16_t* out, int ld_out, const lora_bf16_t* q, int ld_q, int n_heads, float scale,
+                              int window, const lora_kv4_cache_t* cache, const lora_kv4_batch_t* batch,
+                              void* workspace, size_t ws_bytes, int32_t* dev_status, lora_stream_t stream);
+
+/* Workspace bytes of lora_kv4_attend for these heads and batches of at most
+ * max_q_len rows to a sequence; 0 for counts it rejects. */
+size_t lora_kv4_attend_workspace_bytes(int n_heads, int n_kv, int head_dim, int max_q_len);
 
 /* ------------------------------------------------------------------ *
  *  Adapter slots: GPU slots fed from a host cache of prepared adapters

@@ -25,6 +25,9 @@ LORA_APPLY_X_READY = 0x1
 LORA_APPLY_NO_PDL = 0x2
 LORA_APPLY_Y_READY = 0x4
 LORA_DEV_TIMEOUT = 0x4
+LORA_DEV_BAD_PAGE = 0x8
+LORA_DEV_BAD_POSITION = 0x10
+LORA_MAX_ROPE_AXES = 3
 
 STATUS = {
     0: "LORA_OK", 1: "LORA_ERR_INVALID_ARG", 2: "LORA_ERR_SHAPE",
@@ -40,6 +43,8 @@ EXPORTS = (
     "lora_kernel_launch_count", "lora_apply_noalloc", "lora_merge", "lora_merge_batch", "lora_linear",
     "lora_slots_create", "lora_slots_destroy", "lora_slots_register", "lora_slots_acquire",
     "lora_slots_slot_of", "lora_slots_stats",
+    "lora_rms_norm", "lora_kv4_block_bytes", "lora_kv4_append", "lora_kv4_read", "lora_kv4_attend",
+    "lora_kv4_attend_workspace_bytes",
 )
 LORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -62,6 +67,17 @@ class lora_meta_t(ctypes.Structure):
                 ("max_seg_len", ctypes.c_int),
                 ("perm", ctypes.c_void_p), ("gseg_starts", ctypes.c_void_p), ("gseg_slot", ctypes.c_void_p),
                 ("n_gsegs", ctypes.c_int), ("max_gseg_len", ctypes.c_int)]
+
+
+class lora_kv4_cache_t(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("page_stride", ctypes.c_int64), ("n_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("n_kv", ctypes.c_int), ("head_dim", ctypes.c_int)]
+
+
+class lora_kv4_batch_t(ctypes.Structure):
+    _fields_ = [("q_starts", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int), ("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int),
+                ("max_q_len", ctypes.c_int), ("max_ctx_len", ctypes.c_int)]
 
 
 _lib = None
@@ -98,12 +114,19 @@ def load(path: str | None = None):
         "lora_slots_acquire": [P, P, i32, P, P],
         "lora_slots_slot_of": [P, ctypes.c_int64],
         "lora_slots_stats": [P, P],
+        "lora_rms_norm": [P, i32, P, i32, P, i32, i32, P, i32, P, i32, P, i32, P, i32, i32, ctypes.c_float, P],
+        "lora_kv4_block_bytes": [i32, i32],
+        "lora_kv4_append": [P, i32, P, i32, i32, i32, i32, i32, P, i32, i32, P, i32, P, i32, P, P, P, P],
+        "lora_kv4_read": [P, i32, P, i32, P, P, P, P],
+        "lora_kv4_attend": [P, i32, P, i32, i32, ctypes.c_float, i32, P, P, P, sz, P, P],
+        "lora_kv4_attend_workspace_bytes": [i32, i32, i32, i32],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = ctypes.c_int
-    lib.lora_apply_workspace_bytes.restype = ctypes.c_size_t
+    for name in ("lora_apply_workspace_bytes", "lora_kv4_block_bytes", "lora_kv4_attend_workspace_bytes"):
+        getattr(lib, name).restype = ctypes.c_size_t
     lib.lora_status_string.restype = ctypes.c_char_p
     lib.lora_kernel_launch_count.argtypes = []
     lib.lora_kernel_launch_count.restype = ctypes.c_uint64
@@ -133,7 +156,8 @@ def _ld(t) -> int:
     return int(t.stride(0))
 
 
-_DTYPES = {"bf16": "torch.bfloat16", "f32": "torch.float32", "i32": "torch.int32"}
+_DTYPES = {"bf16": "torch.bfloat16", "f32": "torch.float32", "i32": "torch.int32", "u8": "torch.uint8",
+           "e4m3": "torch.float8_e4m3fn"}
 
 
 def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
@@ -152,6 +176,16 @@ def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
     if mat and (t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)):
         raise ValueError(f"{name} must be 2-D with unit column stride")
     return t.data_ptr()
+
+
+def _ld0(t) -> int:
+    return 0 if t is None else int(t.stride(0))
+
+
+def _rows(name: str, t, batch, cols: int = 0):
+    """A row-major operand with the batch's rows and at least cols columns."""
+    if t.dim() != 2 or t.shape[0] < batch.c.n_rows or t.shape[1] < cols:
+        raise ValueError(f"{name} must be 2-D with {batch.c.n_rows} rows and {cols} columns at least")
 
 
 def _stream(stream) -> int:
@@ -267,6 +301,82 @@ def lora_merge_batch(Ws, As, Bs, sign, *, stream=None):
     r_slot = int(As[0].shape[0]) if n else 8
     _check("lora_merge_batch", load().lora_merge_batch(n, arr_w, ld, out, h_in, arr_a, arr_b, r_slot, int(sign),
                                                        _stream(stream)))
+
+
+def lora_rms_norm(x, weight, eps, *, residual=None, residual_out=None, y=None, y8=None, scales=None, group=0,
+                  stream=None):
+    """h = bf16(x + residual) -> residual_out; n = h / sqrt(mean(h^2) + eps) * weight
+    -> y (bf16) and/or y8 (float8_e4m3fn) with fp32 scales [n_rows][groups], one
+    per `group` (128) columns or, with group 0, per row."""
+    n_rows, width = x.shape
+    if int(weight.numel()) != width or not weight.is_contiguous():
+        raise ValueError(f"weight must hold {width} contiguous values")
+    for name, t, cols in (("residual", residual, width), ("residual_out", residual_out, width), ("y", y, width),
+                          ("y8", y8, width), ("scales", scales, (width + group - 1) // group if group > 0 else 1)):
+        if t is not None and (t.dim() != 2 or t.shape[0] != n_rows or t.shape[1] < cols):
+            raise ValueError(f"{name} must be [{n_rows}][{cols}]")
+    _check("lora_rms_norm", load().lora_rms_norm(
+        _dev(y, "y", "bf16", True), _ld0(y), _dev(y8, "y8", "e4m3", True), _ld0(y8), _dev(scales, "scales", "f32", True),
+        _ld0(scales), group, _dev(residual_out, "residual_out", "bf16", True), _ld0(residual_out),
+        _dev(x, "x", "bf16", True), _ld(x), _dev(residual, "residual", "bf16", True), _ld0(residual),
+        _dev(weight, "weight", "bf16"), n_rows, width, eps, _stream(stream)))
+
+
+def lora_kv4_block_bytes(page_size, head_dim) -> int:
+    return int(load().lora_kv4_block_bytes(page_size, head_dim))
+
+
+def lora_kv4_append(q_out, x, cache, batch, *, n_heads, q_off, k_off, v_off, rope=None, positions=None,
+                    axis_pairs=None, dev_status=None, stream=None):
+    """Rotates q (-> q_out) and k of the fused rows x and stores k and v in
+    `cache` (store.KV4Cache) at the places `batch` (store.KV4Batch) gives.
+    rope: fp32 [max_pos][pairs][2] (cos, sin) or None; positions: int32
+    [n_rows][n_axes] or None; axis_pairs: pairs of each axis (default: all
+    on one axis)."""
+    _rows("x", x, batch)
+    _rows("q_out", q_out, batch, n_heads * cache.c.head_dim)
+    rot = max_pos = n_axes = 0
+    axes = None
+    if rope is not None:
+        if rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
+            raise ValueError("rope must be contiguous [max_pos][pairs][2]")
+        max_pos, rot = int(rope.shape[0]), 2 * int(rope.shape[1])
+        pairs = [rot // 2] if axis_pairs is None else list(axis_pairs)
+        n_axes = len(pairs)
+        axes = (ctypes.c_int * max(1, n_axes))(*pairs)
+        if positions is not None:
+            _rows("positions", positions, batch, n_axes)
+    _check("lora_kv4_append", load().lora_kv4_append(
+        _dev(q_out, "q_out", "bf16", True), _ld(q_out), _dev(x, "x", "bf16", True), _ld(x), n_heads, q_off, k_off, v_off,
+        _dev(rope, "rope", "f32"), rot, max_pos, _dev(positions, "positions", "i32", True), _ld0(positions),
+        axes, n_axes, ctypes.byref(cache.c), ctypes.byref(batch.c), _dev(dev_status, "dev_status", "i32"),
+        _stream(stream)))
+
+
+def lora_kv4_read(k, v, cache, batch, *, dev_status=None, stream=None):
+    """k, v [n_rows][n_kv * head_dim] <- the cached values of the rows' places."""
+    width = cache.c.n_kv * cache.c.head_dim
+    _rows("k", k, batch, width)
+    _rows("v", v, batch, width)
+    _check("lora_kv4_read", load().lora_kv4_read(
+        _dev(k, "k", "bf16", True), _ld(k), _dev(v, "v", "bf16", True), _ld(v), ctypes.byref(cache.c),
+        ctypes.byref(batch.c), _dev(dev_status, "dev_status", "i32"), _stream(stream)))
+
+
+def lora_kv4_attend(out, q, cache, batch, workspace, *, n_heads, scale, window=0, dev_status=None, stream=None):
+    """out [n_rows][n_heads * head_dim] <- causal attention of q over the cache
+    (the last `window` positions, 0: all)."""
+    width = n_heads * cache.c.head_dim
+    _rows("out", out, batch, width)
+    _rows("q", q, batch, width)
+    _check("lora_kv4_attend", load().lora_kv4_attend(
+        _dev(out, "out", "bf16", True), _ld(out), _dev(q, "q", "bf16", True), _ld(q), n_heads, scale, window,
+        ctypes.byref(cache.c), ctypes.byref(batch.c), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _dev(dev_status, "dev_status", "i32"), _stream(stream)))
+
+
+def lora_kv4_attend_workspace_bytes(n_heads, n_kv, head_dim, max_q_len) -> int:
+    return int(load().lora_kv4_attend_workspace_bytes(n_heads, n_kv, head_dim, max_q_len))
 
 
 class lora_slot_stats_t(ctypes.Structure):

@@ -1,0 +1,276 @@
+// kv4_append.cu -- rotary embedding of q and k with up to three position
+// axes, 4-bit quantisation of k and v into their pages, and the way back.
+//
+// A row is one CTA.  A team of head_dim / 16 lanes holds a head, sixteen dims
+// a lane, as two chunks of eight; in the rotated part the chunks are the two
+// halves of eight pairs, so a rotation needs no exchange.  The team's lanes
+// hold the same pairs for every head they take, so a lane reads its (cos,
+// sin) once per row.  A group's minimum and maximum cross the team by
+// shuffles.  Bound: HBM (the row in, q and a quarter of k and v out).
+#include <algorithm>
+
+#include "kv4.h"
+#include "tc_common.cuh"
+
+namespace lora {
+
+namespace {
+
+using kv4::Batch;
+using kv4::Cache;
+using kv4::Seq;
+
+// Minimum and maximum that keep a NaN.
+__device__ __forceinline__ float min_nan(float a, float b)
+{
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float* f)
+{
+    f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
+    f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
+}
+__device__ __forceinline__ uint4 pack8(const float* f)
+{
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+// Eight codes of a chunk, one per nibble.  Step and lowest value are rounded
+// to fp16 first (fewer bits to read back per token; the codes are taken
+// against the rounded ones, so that rounding only moves the grid).
+__device__ __forceinline__ uint32_t codes8(const float* f, float inv, float low)
+{
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(f[i], low), inv)), 0.f), 15.f);
+        w |= static_cast<uint32_t>(c) << (4 * i);
+    }
+    return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(128) kv4_append_kernel(AppendArgs a)
+{
+    constexpr int kLanes = D / 16, kGroups = D / kv4::kGroup;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int row = blockIdx.x, lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes, teams = blockDim.x / kLanes;
+    const int s = kv4::find_seq_warp(a.batch.q_starts, a.batch.n_seqs, row);
+    Seq q;
+    if (!kv4::load_seq(a.batch, s, q, threadIdx.x == 0 ? a.status : nullptr) || row < q.row0 || row >= q.row0 + q.n) return;
+    const int p = q.ctx - q.n + (row - q.row0);
+    if (p < 0) return;
+
+    // this lane's chunks: dims [d0, d0 + 8) and [d1, d1 + 8)
+    const int half = a.rot_dim >> 1, rot_lanes = half >> 3;
+    const bool turns = lane < rot_lanes;
+    const int d0 = turns ? 8 * lane : a.rot_dim + 16 * (lane - rot_lanes);
+    const int d1 = turns ? half + d0 : d0 + 8;
+    int at[LORA_MAX_ROPE_AXES];
+#pragma unroll
+    for (int x = 0; x < LORA_MAX_ROPE_AXES; ++x) at[x] = 0;
+    bool bad = false;
+    if (a.rot_dim) {
+#pragma unroll
+        for (int x = 0; x < LORA_MAX_ROPE_AXES; ++x) {
+            if (x >= a.n_axes) break;
+            at[x] = a.positions ? __ldg(a.positions + static_cast<long long>(row) * a.ld_pos + x) : p;
+            bad |= static_cast<unsigned>(at[x]) >= static_cast<unsigned>(a.max_pos);
+        }
+    }
+    if (bad) {
+        if (threadIdx.x == 0) flag(a.status, LORA_DEV_BAD_POSITION);
+        return;
+    }
+    float cs[8], sn[8];
+    if (turns) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int pair = d0 + i;
+            const int pos = pair < a.axis_end[0] ? at[0] : pair < a.axis_end[1] ? at[1] : at[2];
+            const float2 t = __ldg(reinterpret_cast<const float2*>(a.rope) + static_cast<long long>(pos) * half + pair);
+            cs[i] = t.x;
+            sn[i] = t.y;
+        }
+    }
+    const int page = kv4::page_of(a.cache, a.batch, s, p, threadIdx.x == 0 ? a.status : nullptr);
+    const int off = p & (a.cache.page_size - 1), ps = a.cache.page_size;
+
+    const bf16_t* x = a.x + static_cast<long long>(row) * a.ld_x;
+    const int n_kv = a.cache.n_kv, total = a.n_heads + 2 * n_kv;
+    // Every lane of a warp makes the same number of rounds (the shuffles
+    // below need them all).
+    for (int first = 0; first < total; first += teams) {
+        const int head = first + team;
+        const bool live = head < total;
+        const int kind = !live || head < a.n_heads ? 0 : head < a.n_heads + n_kv ? 1 : 2;   // q, k, v
+        const int h = kind == 0 ? head : kind == 1 ? head - a.n_heads : head - a.n_heads - n_kv;
+        const int col = (kind == 0 ? a.q_off : kind == 1 ? a.k_off : a.v_off) + h * D;
+        float f0[8], f1[8];
+        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
+        if (live) {
+            u0 = *reinterpret_cast<const uint4*>(x + col + d0);
+            u1 = *reinterpret_cast<const uint4*>(x + col + d1);
+        }
+        unpack8(u0, f0);
+        unpack8(u1, f1);
+        if (turns && kind != 2) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float lo = f0[i], hi = f1[i];
+                f0[i] = __fsub_rn(__fmul_rn(lo, cs[i]), __fmul_rn(hi, sn[i]));
+                f1[i] = __fadd_rn(__fmul_rn(hi, cs[i]), __fmul_rn(lo, sn[i]));
+            }
+        }
+        float lo[kGroups], hi[kGroups];
+        if (kind) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {   // saturation that keeps a NaN
+                f0[i] = max_nan(min_nan(f0[i], kv4::kMaxAbs), -kv4::kMaxAbs);
+                f1[i] = max_nan(min_nan(f1[i], kv4::kMaxAbs), -kv4::kMaxAbs);
+            }
+        }
+        const float inf = __int_as_float(0x7F800000);
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            lo[g] = inf;
+            hi[g] = -inf;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (d0 / kv4::kGroup == g) {
+                    lo[g] = min_nan(lo[g], f0[i]);
+                    hi[g] = max_nan(hi[g], f0[i]);
+                }
+                if (d1 / kv4::kGroup == g) {
+                    lo[g] = min_nan(lo[g], f1[i]);
+                    hi[g] = max_nan(hi[g], f1[i]);
+                }
+            }
+#pragma unroll
+            for (int o = kLanes / 2; o > 0; o >>= 1) {
+                lo[g] = min_nan(lo[g], __shfl_xor_sync(0xFFFFFFFFu, lo[g], o));
+                hi[g] = max_nan(hi[g], __shfl_xor_sync(0xFFFFFFFFu, hi[g], o));
+            }
+        }
+        if (!live) continue;
+        if (kind == 0) {
+            bf16_t* o = a.q_out + static_cast<long long>(row) * a.ld_q + h * D;
+            *reinterpret_cast<uint4*>(o + d0) = pack8(f0);
+            *reinterpret_cast<uint4*>(o + d1) = pack8(f1);
+            continue;
+        }
+        if (page < 0) continue;
+        uint8_t* block = kv4::block_of(a.cache, page, h);
+        float low[kGroups], inv[kGroups];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+            const __half st = __float2half_rn(__fmul_rn(__fsub_rn(hi[g], lo[g]), 1.f / 15.f));
+            const __half lw = __float2half_rn(lo[g]);
+            const float stf = __half2float(st);
+            low[g] = __half2float(lw);
+            inv[g] = stf > 0.f ? __frcp_rn(stf) : 0.f;
+            if (lane == 0) {
+                if (kind == 1) {
+                    __half2* d = reinterpret_cast<__half2*>(block + kv4::k_params_off(ps, D)) + off * kGroups + g;
+                    *d = __halves2half2(st, lw);
+                } else {
+                    __half* d = reinterpret_cast<__half*>(block + kv4::v_params_off(ps, D)) +
+                                ((off >> 1) * kGroups + g) * 4 + (off & 1);
+                    d[0] = st;
+                    d[2] = lw;
+                }
+            }
+        }
+        const int g0 = d0 / kv4::kGroup, g1 = d1 / kv4::kGroup;
+        const uint32_t w0 = codes8(f0, g0 ? inv[kGroups - 1] : inv[0], g0 ? low[kGroups - 1] : low[0]);
+        const uint32_t w1 = codes8(f1, g1 ? inv[kGroups - 1] : inv[0], g1 ? low[kGroups - 1] : low[0]);
+        if (kind == 1) {
+            uint32_t* d = reinterpret_cast<uint32_t*>(block) + off * (D / 8);
+            d[kv4::k_word(d0 >> 3, D)] = w0;
+            d[kv4::k_word(d1 >> 3, D)] = w1;
+        } else {
+            // halves of two neighbouring words, at this position's parity
+            uint16_t* d = reinterpret_cast<uint16_t*>(block + kv4::v_codes_off(ps, D)) + (off >> 1) * (D / 2) + (off & 1);
+            d[2 * (d0 >> 2)] = static_cast<uint16_t>(w0);
+            d[2 * (d0 >> 2) + 2] = static_cast<uint16_t>(w0 >> 16);
+            d[2 * (d1 >> 2)] = static_cast<uint16_t>(w1);
+            d[2 * (d1 >> 2) + 2] = static_cast<uint16_t>(w1 >> 16);
+        }
+    }
+}
+
+// One row per CTA, eight dims a thread: k of every kv head, then v.
+template <int D>
+__global__ void __launch_bounds__(128) kv4_read_kernel(ReadArgs a)
+{
+    constexpr int kChunks = D / 8, kGroups = D / kv4::kGroup;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int row = blockIdx.x;
+    const int s = kv4::find_seq_warp(a.batch.q_starts, a.batch.n_seqs, row);
+    Seq q;
+    if (!kv4::load_seq(a.batch, s, q, threadIdx.x == 0 ? a.status : nullptr) || row < q.row0 || row >= q.row0 + q.n) return;
+    const int p = q.ctx - q.n + (row - q.row0);
+    if (p < 0) return;
+    const int page = kv4::page_of(a.cache, a.batch, s, p, threadIdx.x == 0 ? a.status : nullptr);
+    if (page < 0) return;
+    const int ps = a.cache.page_size, off = p & (ps - 1), n_kv = a.cache.n_kv;
+    for (int i = threadIdx.x; i < 2 * n_kv * kChunks; i += blockDim.x) {
+        const int c = i % kChunks, hh = i / kChunks, h = hh % n_kv, g = c / 8;
+        const uint8_t* block = kv4::block_of(a.cache, page, h);
+        uint32_t w;
+        float step, low;
+        if (hh < n_kv) {
+            w = reinterpret_cast<const uint32_t*>(block)[off * (D / 8) + kv4::k_word(c, D)];
+            const __half2 pr = reinterpret_cast<const __half2*>(block + kv4::k_params_off(ps, D))[off * kGroups + g];
+            step = __low2float(pr);
+            low = __high2float(pr);
+        } else {
+            const uint16_t* d = reinterpret_cast<const uint16_t*>(block + kv4::v_codes_off(ps, D)) + (off >> 1) * (D / 2) + (off & 1);
+            w = d[4 * c] | (static_cast<uint32_t>(d[4 * c + 2]) << 16);
+            const __half* pr = reinterpret_cast<const __half*>(block + kv4::v_params_off(ps, D)) +
+                               ((off >> 1) * kGroups + g) * 4 + (off & 1);
+            step = __half2float(pr[0]);
+            low = __half2float(pr[2]);
+        }
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = __fadd_rn(__fmul_rn(static_cast<float>((w >> (4 * j)) & 15u), step), low);
+        bf16_t* o = hh < n_kv ? a.k + static_cast<long long>(row) * a.ld_k : a.v + static_cast<long long>(row) * a.ld_v;
+        *reinterpret_cast<uint4*>(o + h * D + 8 * c) = pack8(f);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t stream)
+{
+    if (a.batch.n_rows == 0) return cudaSuccess;
+    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), 128, 0, stream);
+    const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_append_kernel<64>, a)
+                                                 : cudaLaunchKernelEx(&l.cfg, kv4_append_kernel<128>, a);
+    note_launch();
+    return e;
+}
+
+cudaError_t launch_kv4_read(const ReadArgs& a, cudaStream_t stream)
+{
+    if (a.batch.n_rows == 0) return cudaSuccess;
+    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), 128, 0, stream);
+    const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<64>, a)
+                                                 : cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<128>, a);
+    note_launch();
+    return e;
+}
+
+}  // namespace lora

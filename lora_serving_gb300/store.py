@@ -134,3 +134,70 @@ def linear(y: torch.Tensor, x: torch.Tensor, W: torch.Tensor, store: GroupStore,
     projection, W the group's stacked base weight [ld_y][h_in]."""
     abi.lora_linear(y, x, store.h_in, W, store.c_projs(), store.r_slot, store.n_slots, meta.c, workspace,
                     dev_status=dev_status, stream=stream)
+
+
+class KV4Cache:
+    """A paged 4-bit cache (layout: include/lora.h): device memory and the C
+    struct that describes it.  pages: uint8 [n_pages][n_kv][block bytes], or
+    a view of a larger buffer with another stride between pages (one page's
+    blocks contiguous); allocated when None."""
+
+    def __init__(self, n_pages: int, page_size: int, n_kv: int, head_dim: int, device="cuda", pages=None):
+        block = abi.lora_kv4_block_bytes(page_size, head_dim)
+        if not block:
+            raise ValueError(f"no 4-bit cache with pages of {page_size} and heads of {head_dim}")
+        if pages is None:
+            pages = torch.zeros(n_pages, n_kv, block, dtype=torch.uint8, device=device)
+        abi._dev(pages, "pages", "u8")
+        if tuple(pages.shape) != (n_pages, n_kv, block) or pages.stride(2) != 1 or (n_kv > 1 and pages.stride(1) != block):
+            raise ValueError(f"pages must be [{n_pages}][{n_kv}][{block}], contiguous within a page")
+        self.pages = pages
+        self.n_pages, self.page_size, self.n_kv, self.head_dim = n_pages, page_size, n_kv, head_dim
+        stride = pages.stride(0) if n_pages > 1 else n_kv * block
+        self.c = abi.lora_kv4_cache_t(pages.data_ptr(), stride, n_pages, page_size, n_kv, head_dim)
+
+
+class KV4Batch:
+    """Where a batch's rows stand in a cache: device int32 q_starts [n_seqs+1],
+    ctx_lens [n_seqs] and block_table [n_seqs][pages], with the host's upper
+    bounds.  The tensors may be refilled between calls (and replays of a
+    captured graph) as long as the bounds hold."""
+
+    def __init__(self, q_starts, ctx_lens, block_table, *, n_rows: int, max_q_len: int, max_ctx_len: int):
+        n_seqs = int(ctx_lens.numel())
+        for name, t, n in (("q_starts", q_starts, n_seqs + 1), ("ctx_lens", ctx_lens, n_seqs)):
+            if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
+                raise ValueError(f"{name} must hold {n} adjacent entries")
+        if block_table.shape[0] != n_seqs:
+            raise ValueError(f"block_table must have {n_seqs} rows")
+        self.q_starts, self.ctx_lens, self.block_table = q_starts, ctx_lens, block_table
+        # the C side checks ld_table against max_ctx_len: with a stride wider
+        # than the row it would pass a table that is too narrow
+        ld = int(block_table.shape[1])
+        if n_seqs > 1 and int(block_table.stride(0)) != ld:
+            raise ValueError("block_table must be contiguous")
+        self.c = abi.lora_kv4_batch_t(abi._dev(q_starts, "q_starts", "i32"), abi._dev(ctx_lens, "ctx_lens", "i32"),
+                                      abi._dev(block_table, "block_table", "i32", True), ld, n_seqs,
+                                      int(n_rows), int(max_q_len), int(max_ctx_len))
+
+    @classmethod
+    def from_lens(cls, q_lens, ctx_lens, block_table, device="cuda"):
+        """From host lists: rows and positions (the rows' own included) of each sequence."""
+        q, ctx = np.asarray(q_lens, np.int32), np.asarray(ctx_lens, np.int32)
+        starts = np.concatenate([[0], np.cumsum(q)]).astype(np.int32)
+        up = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(device)  # noqa: E731
+        return cls(up(starts), up(ctx), up(np.asarray(block_table)), n_rows=int(starts[-1]),
+                   max_q_len=int(q.max(initial=0)), max_ctx_len=int(ctx.max(initial=0)))
+
+
+def kv4_workspace(cache: KV4Cache, n_heads: int, batch: KV4Batch, device="cuda") -> torch.Tensor:
+    """A workspace for lora_kv4_attend over batches within this one's bounds."""
+    nbytes = abi.lora_kv4_attend_workspace_bytes(n_heads, cache.n_kv, cache.head_dim, batch.c.max_q_len)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def rope_table(max_pos: int, pairs: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """fp32 [max_pos][pairs][2]: (cos, sin) of pos * base^(-i / pairs), angles in fp64."""
+    f = base ** (-torch.arange(pairs, dtype=torch.float64) / pairs)
+    a = torch.arange(max_pos, dtype=torch.float64)[:, None] * f
+    return torch.stack([a.cos(), a.sin()], -1).to(torch.float32).to(device)
