@@ -94,6 +94,7 @@ struct AttendArgs {
     size_t ws_bytes;
     int32_t* status;
 };
+constexpr int kMaxSeqs = 4096;   // sequences of one attention call (their running sum lies in shared memory)
 size_t kv4_attend_workspace(int n_heads, int n_kv, int head_dim, int max_q_len);
 cudaError_t launch_kv4_attend(const AttendArgs& a, cudaStream_t stream);
 

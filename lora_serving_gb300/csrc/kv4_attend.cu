@@ -3,7 +3,7 @@
 // One warp per (row, q head), a position at a time: each lane holds
 // head_dim / 32 dims of q and of the running sum, the score is a warp sum,
 // and the softmax keeps its running maximum and sum in fp32.
-#include "kv4.h"
+#include "kv4_attend.cuh"
 #include "tc_common.cuh"
 
 namespace lora {
@@ -69,11 +69,13 @@ __global__ void __launch_bounds__(128) kv4_attend_kernel(AttendArgs a)
 
 }  // namespace
 
-size_t kv4_attend_workspace(int, int, int, int) { return 256; }
+size_t kv4_attend_workspace(int n_heads, int n_kv, int head_dim, int max_q_len) { return kv4_few_workspace(head_dim, 32); }
 
 cudaError_t launch_kv4_attend(const AttendArgs& a, cudaStream_t stream)
 {
     if (a.batch.n_rows == 0) return cudaSuccess;
+    const int rows = a.batch.max_q_len * (a.n_heads / a.cache.n_kv);
+    if (rows <= 32) return launch_kv4_few(a, rows, stream);
     const long long warps = static_cast<long long>(a.batch.n_rows) * a.n_heads;
     PdlLaunch l(dim3(static_cast<unsigned>((warps + 3) / 4)), 128, 0, stream);
     const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_attend_kernel<64>, a)

@@ -1,0 +1,80 @@
+// kv4_attend.cuh -- what the attention kernels share: the way work is cut
+// into equal ranges over the batch, and the fragments' small instructions.
+#pragma once
+
+#include "kv4.h"
+
+namespace lora {
+namespace kv4 {
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// m16n8k16, fp16 x fp16 -> fp32.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements held as an mma fragment.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return as_u32(__floats2half2_rn(lo, hi)); }
+
+// Four pairs of codes of a word as fp16: pair i is (nibble i, nibble 4 + i).
+// A nibble OR-ed into the mantissa of 1024 is 1024 + code (low nibble of a
+// byte) or 1024 + 16 code (high nibble); both steps below are exact.
+__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask)
+{
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));   // (w & mask) | 1024
+    return r;
+}
+// Odd pairs keep their factor of 16 (the other operand of the product carries 1/16).
+__device__ __forceinline__ void codes_x16(uint32_t w, uint32_t (&c)[4])
+{
+    const __half2 k = __float2half2_rn(-1024.f);
+    const uint32_t y = w >> 8;
+    c[0] = as_u32(__hadd2(as_h2(pick(w, 0x000F000Fu)), k));
+    c[1] = as_u32(__hadd2(as_h2(pick(w, 0x00F000F0u)), k));
+    c[2] = as_u32(__hadd2(as_h2(pick(y, 0x000F000Fu)), k));
+    c[3] = as_u32(__hadd2(as_h2(pick(y, 0x00F000F0u)), k));
+}
+// code * step + low, one fp16 rounding.
+__device__ __forceinline__ void values(uint32_t w, __half2 step, __half2 low, uint32_t (&v)[4])
+{
+    const __half2 k = __float2half2_rn(-1024.f), s = __float2half2_rn(1.f / 16), k16 = __float2half2_rn(-64.f);
+    const uint32_t y = w >> 8;
+    v[0] = as_u32(__hfma2(__hadd2(as_h2(pick(w, 0x000F000Fu)), k), step, low));
+    v[1] = as_u32(__hfma2(__hfma2(as_h2(pick(w, 0x00F000F0u)), s, k16), step, low));
+    v[2] = as_u32(__hfma2(__hadd2(as_h2(pick(y, 0x000F000Fu)), k), step, low));
+    v[3] = as_u32(__hfma2(__hfma2(as_h2(pick(y, 0x00F000F0u)), s, k16), step, low));
+}
+
+// Whether an fp16 pair holds an infinity or a NaN.
+__device__ __forceinline__ bool not_finite(uint32_t h2)
+{
+    return (h2 & 0x7C00u) == 0x7C00u || (h2 & 0x7C000000u) == 0x7C000000u;
+}
+
+}  // namespace kv4
+
+cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, cudaStream_t stream);
+size_t kv4_few_workspace(int head_dim, int rows);
+
+}  // namespace lora

@@ -1,0 +1,617 @@
+// kv4_few.cu -- attention of few query rows (single tokens, drafts) over the
+// paged 4-bit cache: the cache's bytes are the cost, so every byte is read
+// once and the codes are unpacked in registers.
+//
+// Work.  A unit is (sequence, kv head): up to 8 NT query rows (rows x heads
+// of the group) over the sequence's tiles of 16 positions.  All units' tiles
+// laid end to end are cut into equal ranges, one per CTA, whatever the
+// lengths; a range may begin or end inside a unit, which then leaves partial
+// results that a second kernel joins in a fixed order.  A CTA's warps take
+// the tiles of a unit in turn and join over shared memory at its end.
+//
+// Tile.  A warp multiplies on mma.sync m16n8k16 with positions as M and query
+// rows as N, so that groups of up to 8 heads waste nothing:
+//   S[16 positions][8 rows] = codes(K) q^T, per group of 64 dims, then
+//   score = sum_g step_g S_g + low_g sum(q_g)         (K is never rounded)
+//   O[dims][8 rows] += V^T P, V = code * step + low in fp16, P in fp16.
+// The K layout puts the 16 bytes that a lane feeds to its fragments side by
+// side, the V layout pairs two positions in one 32-bit operand, and P goes
+// from the first product's layout to the second's by a register transpose.
+// The running maximum moves only when a score passes it by 2^8 (a vote per
+// tile), so most tiles rescale nothing.
+// A warp copies its own tiles ahead with cp.async into a ring of its own and
+// meets no other warp until the unit ends.
+#include <algorithm>
+
+#include "kv4_attend.cuh"
+#include "tc_common.cuh"
+
+namespace lora {
+
+namespace {
+
+using namespace kv4;
+
+constexpr int kWarps = 8, kThreads = 32 * kWarps;
+constexpr int kTile = 16;          // positions per tile
+constexpr int kStages = 4;         // tiles in a warp's ring
+constexpr int kMinTiles = kWarps;  // a CTA's range holds a tile for each warp
+constexpr float kSlack = 8.f;      // log2 by which a score may pass the running maximum
+constexpr float kLift = 7.f;       // weights carry 2^7: at most 2^15, and fp16 holds them down to 2^-31 of the largest
+
+template <int D>
+struct Shape {
+    static constexpr int kGroups = D / kGroup;
+    static constexpr int kWords = D / 32;                 // words of a lane per position (K) and per pair (V)
+    static constexpr int kCodeBytes = kTile * D / 2;
+    static constexpr int kParamBytes = kTile * 4 * kGroups;
+    static constexpr int kStage = 2 * kCodeBytes + 2 * kParamBytes;
+};
+
+// The smallest number of CTAs' ranges and where range b begins.
+__device__ __forceinline__ int ranges(int total, int ctas) { return min(ctas, max(1, total / kMinTiles)); }
+__device__ __forceinline__ int range_at(int total, int n, int b)
+{
+    return static_cast<int>(static_cast<long long>(total) * b / n);
+}
+
+// First tile, and tiles, that a sequence's rows see.
+__device__ __forceinline__ int first_tile(const Seq& q, int window)
+{
+    return window > 0 ? max(0, q.ctx - q.n - window + 1) / kTile : 0;
+}
+__device__ __forceinline__ int tiles_of(const Seq& q, int window)
+{
+    return max(1, (q.ctx + kTile - 1) / kTile - first_tile(q, window));   // at least one: its rows get their zeros
+}
+
+// Running sum over the sequences of tiles x kv heads, in shared memory.
+__device__ void scan_units(const AttendArgs& a, int few_rows, int group, int* prefix, int* warp_sums, int32_t* status)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int base = 0;
+    for (int s0 = 0; s0 < a.batch.n_seqs; s0 += kThreads) {
+        const int s = s0 + tid;
+        int v = 0;
+        if (s < a.batch.n_seqs) {
+            Seq q;
+            if (load_seq(a.batch, s, q, status) && q.n > 0 && q.n * group <= few_rows) v = tiles_of(q, a.window) * a.cache.n_kv;
+        }
+        int sum = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (lane == 31) warp_sums[warp] = sum;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += warp_sums[w];
+            all += warp_sums[w];
+        }
+        if (s < a.batch.n_seqs) prefix[s + 1] = base + before + sum;
+        base += all;
+        __syncthreads();
+    }
+    if (tid == 0) prefix[0] = 0;
+    __syncthreads();
+}
+
+// The unit that holds linear tile x (< total).
+struct Unit {
+    int s, h, u0, tiles;   // sequence, kv head, linear index of its first tile, tiles
+    Seq q;
+};
+__device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, int x)
+{
+    int lo = 0, hi = a.batch.n_seqs - 1;   // last s with prefix[s] <= x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    Unit u;
+    u.s = lo;
+    u.tiles = (prefix[lo + 1] - prefix[lo]) / a.cache.n_kv;
+    u.h = (x - prefix[lo]) / u.tiles;
+    u.u0 = prefix[lo] + u.h * u.tiles;
+    load_seq(a.batch, lo, u.q, nullptr);
+    return u;
+}
+
+// Partial result of a range's piece of a unit: rows x D sums, then the rows'
+// maxima and sums of weights.  Slot 0: the unit began in an earlier range;
+// slot 1: it began in this one and goes on.
+__device__ __forceinline__ float* partial(void* ws, int range, int slot, int rows, int D)
+{
+    return static_cast<float*>(ws) + (static_cast<long long>(range) * 2 + slot) * (static_cast<long long>(rows) * (D + 2));
+}
+
+template <int D, int NT>
+struct Smem {
+    using S = Shape<D>;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kRing = kWarps * kStages * S::kStage;
+    static constexpr int kRed = kWarps * kRows * (D + 2) * 4;
+    static constexpr int kFixed = kRing + kRed + 64;
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(AttendArgs a, int few_rows)
+{
+    using S = Shape<D>;
+    using M = Smem<D, NT>;
+    constexpr int kRows = M::kRows, kGroups = S::kGroups, kWords = S::kWords;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    uint8_t* ring = smem + warp * kStages * S::kStage;
+    float* red = reinterpret_cast<float*>(smem + M::kRing);   // [warp][row][D], then [warp][row] maxima, sums
+    float* red_m = red + kWarps * kRows * D;
+    float* red_l = red_m + kWarps * kRows;
+    int* warp_sums = reinterpret_cast<int*>(smem + M::kRing + M::kRed);
+    int* prefix = warp_sums + 16;
+
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
+    scan_units(a, few_rows, group, prefix, warp_sums, blockIdx.x == 0 ? a.status : nullptr);
+    const int total = prefix[a.batch.n_seqs];
+    if (total == 0) return;
+    const int n_ranges = ranges(total, gridDim.x), b = blockIdx.x;
+    if (b >= n_ranges) return;
+    const int end = range_at(total, n_ranges, b + 1);
+
+    for (int x = range_at(total, n_ranges, b); x < end;) {
+        const Unit u = unit_at(a, prefix, x);
+        const int t0 = x - u.u0, t1 = min(u.tiles, end - u.u0);
+        x = u.u0 + t1;
+        const int tile0 = first_tile(u.q, a.window), rows = u.q.n * group;
+        const int p0 = u.q.ctx - u.q.n;   // position of the first row
+        const int32_t* table = a.batch.block_table + static_cast<long long>(u.s) * a.batch.ld_table;
+
+        // ---- the ring: tile i of this warp is t0 + warp + i * kWarps
+        const int n_mine = max(0, (t1 - t0 - warp + kWarps - 1) / kWarps);
+        unsigned has = 0;   // stages that hold a tile
+        auto page_at = [&](int i) -> int {
+            const int pos = (tile0 + t0 + warp + i * kWarps) * kTile;
+            if (i >= n_mine || pos >= u.q.ctx) return -1;
+            return __ldg(table + (pos >> a.cache.page_shift));
+        };
+        int page_next = page_at(0);
+        auto issue = [&](int i) {
+            const int page = page_next, st = i % kStages;
+            page_next = page_at(i + 1);
+            has &= ~(1u << st);
+            if (i < n_mine) {
+                const int pos = (tile0 + t0 + warp + i * kWarps) * kTile;
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages)) {
+                    has |= 1u << st;
+                    const int off = pos & (ps - 1);
+                    const uint8_t* block = block_of(a.cache, page, u.h);
+                    uint8_t* dst = ring + st * S::kStage;
+                    const uint8_t* kc = block + off * (D / 2);
+                    const uint8_t* vc = kc + v_codes_off(ps, D);
+#pragma unroll
+                    for (int c = 0; c < S::kCodeBytes / 512; ++c) {
+                        const int o = 512 * c + 16 * lane;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst + o)), "l"(kc + o) : "memory");
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst + S::kCodeBytes + o)), "l"(vc + o) : "memory");
+                    }
+                    const int pl = lane & 15;
+                    if (pl < S::kParamBytes / 16) {
+                        const int v = lane >> 4;
+                        const uint8_t* src = block + (v ? v_params_off(ps, D) : k_params_off(ps, D)) + off * 4 * kGroups + 16 * pl;
+                        uint8_t* d = dst + 2 * S::kCodeBytes + v * S::kParamBytes + 16 * pl;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(d)), "l"(src) : "memory");
+                    }
+                } else if (pos < u.q.ctx && lane == 0) {
+                    flag(a.status, LORA_DEV_BAD_PAGE);
+                }
+            }
+            asm volatile("cp.async.commit_group;\n" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+        // ---- q as fragments: row n = 8 nt + g, dims 32 w + 8 t + (0..7)
+        uint32_t qf[NT][kWords][4];     // pairs (dims e, e + 4); odd pairs carry 1/16
+        float mult[NT][2], qsum[NT][kGroups][2];   // of rows 2t, 2t + 1
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = 8 * nt + g;
+            uint4 raw[kWords];
+            float top = 0.f;
+            const bf16_t* qp = a.q + static_cast<long long>(u.q.row0 + r / group) * a.ld_q + (u.h * group + r % group) * D + 8 * t;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                raw[w] = r < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
+                const uint32_t part[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(part[e])), fabsf(bf16_hi(part[e]))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            // a power of two that takes the row's largest into [2^7, 2^8)
+            const int e = static_cast<int>(__float_as_uint(top) >> 23);
+            const int fe = min(261 - e, 253);
+            const float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
+            const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
+            float sum[kGroups];
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) sum[gr] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                const float f[8] = {bf16_lo(raw[w].x) * up, bf16_hi(raw[w].x) * up, bf16_lo(raw[w].y) * up, bf16_hi(raw[w].y) * up,
+                                    bf16_lo(raw[w].z) * up, bf16_hi(raw[w].z) * up, bf16_lo(raw[w].w) * up, bf16_hi(raw[w].w) * up};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float k = (i & 1) ? 1.f / 16 : 1.f;
+                    qf[nt][w][i] = pack_f16x2(f[i] * k, f[i + 4] * k);
+                    sum[w / 2] += f[i] + f[i + 4];
+                }
+            }
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+                sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 1);
+                sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 2);
+            }
+            const float m = a.scale * 1.4426950408889634f * down;   // scores in log2
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                mult[nt][c] = __shfl_sync(0xFFFFFFFFu, m, 8 * t + 4 * c);
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr) qsum[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, sum[gr], 8 * t + 4 * c);
+            }
+        }
+        int last[NT][2];   // position of rows 2t, 2t + 1: the last one they see
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) last[nt][c] = p0 + (8 * nt + 2 * t + c) / group;
+
+        float acc[D / 16][NT][4];
+        float top[NT][2], sum[NT][2];
+        const float inf = __int_as_float(0x7F800000);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) acc[m][nt][c] = 0.f;
+            top[nt][0] = top[nt][1] = -inf;
+            sum[nt][0] = sum[nt][1] = 0.f;
+        }
+
+        for (int i = 0; i < n_mine; ++i) {
+            asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
+            __syncwarp();
+            const int st = i % kStages;
+            const uint8_t* src = ring + st * S::kStage;
+            const bool live = (has >> st) & 1u;
+            issue(i + kStages - 1);
+            if (!live) continue;
+            const int j0 = (tile0 + t0 + warp + i * kWarps) * kTile;   // the tile's first position
+            // every row sees every position?
+            const bool inner = j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + u.q.n - 1 - a.window);
+
+            // ---- scores
+            float sc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
+            uint32_t kw[2][kWords];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint8_t* p = src + (g + 8 * r) * (D / 2) + t * (4 * kWords);
+                if (kWords == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(p);
+                    kw[r][0] = v.x; kw[r][1] = v.y; kw[r][kWords - 2] = v.z; kw[r][kWords - 1] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(p);
+                    kw[r][0] = v.x; kw[r][1] = v.y;
+                }
+            }
+            const __half2* kp = reinterpret_cast<const __half2*>(src + 2 * S::kCodeBytes);
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+                float d[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) d[nt][c] = 0.f;
+#pragma unroll
+                for (int w = 2 * gr; w < 2 * gr + 2; ++w) {
+                    uint32_t lo[4], hi[4];
+                    codes_x16(kw[0][w], lo);
+                    codes_x16(kw[1][w], hi);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1]);
+                        mma_f16(d[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][w][2], qf[nt][w][3]);
+                    }
+                }
+                const float2 p0f = __half22float2(kp[g * kGroups + gr]), p1f = __half22float2(kp[(g + 8) * kGroups + gr]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    sc[nt][0] = fmaf(p0f.x, d[nt][0], fmaf(p0f.y, qsum[nt][gr][0], sc[nt][0]));
+                    sc[nt][1] = fmaf(p0f.x, d[nt][1], fmaf(p0f.y, qsum[nt][gr][1], sc[nt][1]));
+                    sc[nt][2] = fmaf(p1f.x, d[nt][2], fmaf(p1f.y, qsum[nt][gr][0], sc[nt][2]));
+                    sc[nt][3] = fmaf(p1f.x, d[nt][3], fmaf(p1f.y, qsum[nt][gr][1], sc[nt][3]));
+                }
+            }
+            bool up = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    sc[nt][c] *= mult[nt][c & 1];
+                    if (!inner) {
+                        const int j = j0 + g + 8 * (c >> 1), p = last[nt][c & 1];
+                        if (j > p || (a.window > 0 && j <= p - a.window)) sc[nt][c] = -inf;
+                    }
+                    up |= sc[nt][c] > top[nt][c & 1] + kSlack;
+                }
+            if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float m = fmaxf(sc[nt][c], sc[nt][c + 2]);
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                        m = fmaxf(m, top[nt][c]);
+                        const float keep = m == -inf ? 1.f : ex2(top[nt][c] - m);
+                        top[nt][c] = m;
+                        sum[nt][c] *= keep;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            acc[k][nt][c] *= keep;
+                            acc[k][nt][c + 2] *= keep;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float m = top[nt][c & 1];
+                    w[c] = ex2(sc[nt][c] - (m == -inf ? 0.f : m - kLift));
+                    sum[nt][c & 1] += w[c];
+                }
+                pf[nt][0] = transpose8(pack_f16x2(w[0], w[1]));
+                pf[nt][1] = transpose8(pack_f16x2(w[2], w[3]));
+            }
+
+            // ---- values: dims g * D/8 + 4 i + e of positions (2t, 2t+1) and (2t+8, 2t+9)
+            const int vg = g * (D / 8) / kGroup;
+            uint32_t step[2], low[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint2 v = *reinterpret_cast<const uint2*>(src + 2 * S::kCodeBytes + S::kParamBytes + ((t + 4 * r) * kGroups + vg) * 8);
+                step[r] = v.x;
+                low[r] = v.y;
+            }
+            bool poison = false;
+            if (!inner) {
+                // positions that no row sees count as zeros whatever they hold
+                const int j_end = u.q.ctx, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int j = j0 + 2 * t + 8 * r;
+                    const uint32_t keep = (j >= j_begin && j < j_end ? 0xFFFFu : 0u) | (j + 1 >= j_begin && j + 1 < j_end ? 0xFFFF0000u : 0u);
+                    step[r] &= keep;
+                    low[r] &= keep;
+                    poison |= not_finite(step[r]) || not_finite(low[r]);
+                }
+                // a NaN that some rows see and others do not: taken out here, put back below for those that see it
+                if (__any_sync(0xFFFFFFFFu, poison)) {
+                    poison = true;
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        uint32_t bad = 0;
+                        if (not_finite(step[r] & 0xFFFFu) || not_finite(low[r] & 0xFFFFu)) bad |= 0xFFFFu;
+                        if (not_finite(step[r] & 0xFFFF0000u) || not_finite(low[r] & 0xFFFF0000u)) bad |= 0xFFFF0000u;
+                        step[r] &= ~bad;
+                        low[r] &= ~bad;
+                    }
+                }
+            }
+            uint32_t vw[2][kWords];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint8_t* p = src + S::kCodeBytes + (t + 4 * r) * D + g * (4 * kWords);
+                if (kWords == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(p);
+                    vw[r][0] = v.x; vw[r][1] = v.y; vw[r][kWords - 2] = v.z; vw[r][kWords - 1] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(p);
+                    vw[r][0] = v.x; vw[r][1] = v.y;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                uint32_t a0[4], a1[4];
+                values(vw[0][w], as_h2(step[0]), as_h2(low[0]), a0);
+                values(vw[1][w], as_h2(step[1]), as_h2(low[1]), a1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[nt][0], pf[nt][1]);
+                    mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[nt][0], pf[nt][1]);
+                }
+            }
+            if (poison) {
+                const __half* vp = reinterpret_cast<const __half*>(src + 2 * S::kCodeBytes + S::kParamBytes);
+                for (int k = 0; k < kTile; ++k) {
+                    const __half* p = vp + ((k >> 1) * kGroups + vg) * 4 + (k & 1);
+                    const float nan = __half2float(p[0]) * 0.f + __half2float(p[2]) * 0.f;   // 0 where both are finite
+                    if (nan == 0.f) continue;
+                    const int j = j0 + k;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int p = last[nt][c];
+                            if (j > p || (a.window > 0 && j <= p - a.window) || j >= u.q.ctx) continue;
+#pragma unroll
+                            for (int m = 0; m < D / 16; ++m) {
+                                acc[m][nt][c] += nan;
+                                acc[m][nt][c + 2] += nan;
+                            }
+                        }
+                }
+            }
+        }
+
+        // ---- join the warps
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float l = sum[nt][c];
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+                l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+                const int r = 8 * nt + 2 * t + c;
+                if (g == 0) {
+                    red_m[warp * kRows + r] = top[nt][c];
+                    red_l[warp * kRows + r] = l;
+                }
+#pragma unroll
+                for (int w = 0; w < kWords; ++w)
+                    *reinterpret_cast<float4*>(red + (warp * kRows + r) * D + g * (D / 8) + 4 * w) =
+                        make_float4(acc[2 * w][nt][c], acc[2 * w][nt][c + 2], acc[2 * w + 1][nt][c], acc[2 * w + 1][nt][c + 2]);
+            }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == u.tiles;
+        float* out_p = partial(a.ws, b, t0 == 0 ? 1 : 0, kRows, D);
+        for (int e = tid; e < rows * (D / 4); e += kThreads) {
+            const int r = e / (D / 4), d = e % (D / 4) * 4;
+            float m = -inf;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_m[w * kRows + r]);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            float l = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float k = m == -inf ? 0.f : ex2(red_m[w * kRows + r] - m);
+                const float4 v = *reinterpret_cast<const float4*>(red + (w * kRows + r) * D + d);
+                o.x = fmaf(v.x, k, o.x);
+                o.y = fmaf(v.y, k, o.y);
+                o.z = fmaf(v.z, k, o.z);
+                o.w = fmaf(v.w, k, o.w);
+                l = fmaf(red_l[w * kRows + r], k, l);
+            }
+            if (whole) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.q.row0 + r / group) * a.ld_out +
+                                          (u.h * group + r % group) * D + d) = v;
+            } else {
+                *reinterpret_cast<float4*>(out_p + r * D + d) = o;
+                if (d == 0) {
+                    out_p[kRows * D + r] = m;
+                    out_p[kRows * D + kRows + r] = l;
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Joins the pieces of the unit that begins in range b and goes on, in order.
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads) kv4_few_join_kernel(AttendArgs a, int few_rows, int ctas)
+{
+    constexpr int kRows = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    int* warp_sums = reinterpret_cast<int*>(smem);
+    int* prefix = warp_sums + 16;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int group = a.n_heads / a.cache.n_kv;
+    scan_units(a, few_rows, group, prefix, warp_sums, nullptr);
+    const int total = prefix[a.batch.n_seqs];
+    if (total == 0) return;
+    const int n_ranges = ranges(total, ctas), b = blockIdx.x;
+    if (b >= n_ranges) return;
+    const int end = range_at(total, n_ranges, b + 1);
+    const Unit u = unit_at(a, prefix, end - 1);
+    const int u1 = u.u0 + u.tiles;
+    if (u1 <= end || u.u0 < range_at(total, n_ranges, b)) return;
+    int last = b + 1;
+    while (range_at(total, n_ranges, last + 1) < u1) ++last;
+    const float inf = __int_as_float(0x7F800000);
+    for (int e = threadIdx.x; e < u.q.n * group * (D / 4); e += kThreads) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4;
+        float m = -inf, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = b; k <= last; ++k) m = fmaxf(m, partial(a.ws, k, k == b, kRows, D)[kRows * D + r]);
+        for (int k = b; k <= last; ++k) {
+            const float* p = partial(a.ws, k, k == b, kRows, D);
+            const float w = m == -inf ? 0.f : ex2(p[kRows * D + r] - m);
+            const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
+            o.x = fmaf(v.x, w, o.x);
+            o.y = fmaf(v.y, w, o.y);
+            o.z = fmaf(v.z, w, o.z);
+            o.w = fmaf(v.w, w, o.w);
+            l = fmaf(p[kRows * D + kRows + r], w, l);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.q.row0 + r / group) * a.ld_out + (u.h * group + r % group) * D + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+}
+
+constexpr int kMaxSmem = 227 * 1024;
+static_assert(Smem<128, 4>::kRing + Smem<128, 4>::kRed + (17 + kMaxSeqs) * 4 <= kMaxSmem, "shared memory");
+constexpr int kMaxCtas = 2 * 160;   // ranges that the workspace has room for
+
+template <int D, int NT>
+cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
+{
+    const size_t scan = (16 + a.batch.n_seqs + 1) * sizeof(int);
+    const size_t smem = Smem<D, NT>::kRing + Smem<D, NT>::kRed + scan;
+    static bool attr_set = false;
+    cudaError_t e = cudaSuccess;
+    if (!attr_set) {
+        e = cudaFuncSetAttribute(kv4_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        if (e != cudaSuccess) return e;
+        attr_set = true;
+    }
+    const int ctas = std::min(kMaxCtas, device_sms() * (NT == 1 ? 2 : 1));
+    PdlLaunch l(dim3(ctas), kThreads, smem, stream);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    PdlLaunch j(dim3(ctas), kThreads, scan, stream);
+    e = cudaLaunchKernelEx(&j.cfg, kv4_few_join_kernel<D, NT>, a, few_rows, ctas);
+    note_launch();
+    return e;
+}
+
+}  // namespace
+
+size_t kv4_few_workspace(int head_dim, int rows)
+{
+    const int r = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+    return static_cast<size_t>(kMaxCtas) * 2 * r * (head_dim + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, cudaStream_t stream)
+{
+    if (a.cache.head_dim == 64) {
+        if (few_rows <= 8) return run<64, 1>(a, few_rows, stream);
+        if (few_rows <= 16) return run<64, 2>(a, few_rows, stream);
+        return run<64, 4>(a, few_rows, stream);
+    }
+    if (few_rows <= 8) return run<128, 1>(a, few_rows, stream);
+    if (few_rows <= 16) return run<128, 2>(a, few_rows, stream);
+    return run<128, 4>(a, few_rows, stream);
+}
+
+}  // namespace lora

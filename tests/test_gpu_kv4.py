@@ -403,8 +403,10 @@ def test_attend_device_faults(q_len):
     out.fill_(5.0)
     abi.lora_kv4_attend(out, q, cache, batch, ws, n_heads=H, scale=0.1, dev_status=st)
     assert abi.lora_read_device_status(st) == abi.LORA_DEV_BAD_SEGMENT
-    assert torch.equal(out[rows[0]], clean[rows[0]]) and torch.equal(out[rows[1]], clean[rows[1]])
     assert (out[rows[2]] == 5).all()
+    # the others' work is cut into other ranges without it: right within the tolerance, not bit for bit
+    want, tol = R.attend(R.f64(q).reshape(-1, H, D), K, V, case[0], case[1], table, page, 0.1)
+    _close(R.f64(out).reshape(-1, H, D)[:2 * q_len], want[:2 * q_len], tol[:2 * q_len])
 
 
 def test_attend_nan_in_a_visible_place_stays_in_its_head():
