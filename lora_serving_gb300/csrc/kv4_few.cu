@@ -3,11 +3,13 @@
 // once and the codes are unpacked in registers.
 //
 // Work.  A unit is (sequence, kv head): up to 8 NT query rows (rows x heads
-// of the group) over the sequence's tiles of 16 positions.  All units' tiles
-// laid end to end are cut into equal ranges, one per CTA, whatever the
-// lengths; a range may begin or end inside a unit, which then leaves partial
-// results that a second kernel joins in a fixed order.  A CTA's warps take
-// the tiles of a unit in turn and join over shared memory at its end.
+// of the group) over the sequence's tiles of 16 positions.  All units laid
+// end to end are cut into equal ranges, one per warp, whatever the lengths; a
+// unit counts kUnitCost tiles more than it has, for its start.  A warp that
+// has a whole unit writes its result; a unit cut by a range's end leaves
+// partial results, which the CTA joins over shared memory where its warps
+// have the whole unit, and a second kernel, in a fixed order, where other
+// CTAs have a part.
 //
 // Tile.  A warp multiplies on mma.sync m16n8k16 with positions as M and query
 // rows as N, so that groups of up to 8 heads waste nothing:
@@ -20,7 +22,7 @@
 // The running maximum moves only when a score passes it by 2^8 (a vote per
 // tile), so most tiles rescale nothing.
 // A warp copies its own tiles ahead with cp.async into a ring of its own and
-// meets no other warp until the unit ends.
+// meets no other warp until its range ends.
 #include <algorithm>
 
 #include "kv4_attend.cuh"
@@ -32,27 +34,37 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTile = 16;          // positions per tile
-constexpr int kStages = 4;         // tiles in a warp's ring
-constexpr int kMinTiles = kWarps;  // a CTA's range holds a tile for each warp
+constexpr int kUnitCost = 3;       // a unit's start (tables, q, the first copies), in tiles
+constexpr int kMinRange = 4;       // a warp's range, at least: a tile and the unit's start
 constexpr float kSlack = 8.f;      // log2 by which a score may pass the running maximum
 constexpr float kLift = 7.f;       // weights carry 2^7: at most 2^15, and fp16 holds them down to 2^-31 of the largest
 
-template <int D>
+// Sizes of one form: head dimension D, up to 8 NT query rows to a unit.
+template <int D, int NT>
 struct Shape {
     static constexpr int kGroups = D / kGroup;
     static constexpr int kWords = D / 32;                 // words of a lane per position (K) and per pair (V)
     static constexpr int kCodeBytes = kTile * D / 2;
     static constexpr int kParamBytes = kTile * 4 * kGroups;
     static constexpr int kStage = 2 * kCodeBytes + 2 * kParamBytes;
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kPartial = kRows * (D + 2);      // floats of a partial result: sums, maxima, sums of weights
+    // The ring is at least a partial result long: a warp's last one takes
+    // the ring's place.
+    static constexpr int kStages = D == 64 || NT == 4 ? 8 : 4;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int kWarps = D == 128 && NT == 4 ? 6 : 8;
+    static constexpr int kThreads = 32 * kWarps;
+    static constexpr int kSmem = kWarps * (kRing + 4 * kPartial) + 256;   // and the running sum of the sequences
+    static_assert(kRing >= 4 * kPartial, "ring");
 };
 
-// The smallest number of CTAs' ranges and where range b begins.
-__device__ __forceinline__ int ranges(int total, int ctas) { return min(ctas, max(1, total / kMinTiles)); }
-__device__ __forceinline__ int range_at(int total, int n, int b)
+// Ranges are one per warp; range w of n begins here.
+__device__ __forceinline__ int range_count(int total, int warps) { return min(warps, max(1, total / kMinRange)); }
+__device__ __forceinline__ int range_at(int total, int n, int w)
 {
-    return static_cast<int>(static_cast<long long>(total) * b / n);
+    return static_cast<int>(static_cast<long long>(total) * min(w, n) / n);
 }
 
 // First tile, and tiles, that a sequence's rows see.
@@ -65,17 +77,18 @@ __device__ __forceinline__ int tiles_of(const Seq& q, int window)
     return max(1, (q.ctx + kTile - 1) / kTile - first_tile(q, window));   // at least one: its rows get their zeros
 }
 
-// Running sum over the sequences of tiles x kv heads, in shared memory.
+// Running sum over the sequences of (tiles + kUnitCost) x kv heads, in shared memory.
+template <int kWarps>
 __device__ void scan_units(const AttendArgs& a, int few_rows, int group, int* prefix, int* warp_sums, int32_t* status)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int base = 0;
-    for (int s0 = 0; s0 < a.batch.n_seqs; s0 += kThreads) {
+    for (int s0 = 0; s0 < a.batch.n_seqs; s0 += 32 * kWarps) {
         const int s = s0 + tid;
         int v = 0;
         if (s < a.batch.n_seqs) {
             Seq q;
-            if (load_seq(a.batch, s, q, status) && q.n > 0 && q.n * group <= few_rows) v = tiles_of(q, a.window) * a.cache.n_kv;
+            if (load_seq(a.batch, s, q, status) && q.n > 0 && q.n * group <= few_rows) v = (tiles_of(q, a.window) + kUnitCost) * a.cache.n_kv;
         }
         int sum = v;
 #pragma unroll
@@ -99,9 +112,9 @@ __device__ void scan_units(const AttendArgs& a, int few_rows, int group, int* pr
     __syncthreads();
 }
 
-// The unit that holds linear tile x (< total).
+// The unit that holds place x (< total) of the line.
 struct Unit {
-    int s, h, u0, tiles;   // sequence, kv head, linear index of its first tile, tiles
+    int s, h, u0, len;   // sequence, kv head, its first place, places (kUnitCost, then its tiles)
     Seq q;
 };
 __device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, int x)
@@ -113,68 +126,71 @@ __device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, 
     }
     Unit u;
     u.s = lo;
-    u.tiles = (prefix[lo + 1] - prefix[lo]) / a.cache.n_kv;
-    u.h = (x - prefix[lo]) / u.tiles;
-    u.u0 = prefix[lo] + u.h * u.tiles;
+    u.len = (prefix[lo + 1] - prefix[lo]) / a.cache.n_kv;
+    u.h = (x - prefix[lo]) / u.len;
+    u.u0 = prefix[lo] + u.h * u.len;
     load_seq(a.batch, lo, u.q, nullptr);
     return u;
 }
 
-// Partial result of a range's piece of a unit: rows x D sums, then the rows'
-// maxima and sums of weights.  Slot 0: the unit began in an earlier range;
-// slot 1: it began in this one and goes on.
-__device__ __forceinline__ float* partial(void* ws, int range, int slot, int rows, int D)
+// A warp's partial result in shared memory.  Slot 0: of the unit that began
+// before the warp's range; slot 1: of the last one, which goes on after it.
+struct Piece {
+    int u0;               // the unit's first place; -1: none
+    int ends;             // whether the unit ends with this piece
+    int h, row0, rows, u1;
+};
+
+// What the workspace holds: a record for each CTA of the unit that begins in
+// it and goes on after it, then two partial results for each CTA (slots as a
+// warp's).
+struct Record {
+    int rows, row0, h, last;   // rows 0: none; the unit's pieces lie in CTAs [this, last]
+};
+constexpr int kMaxCtas = 2 * 160;   // CTAs that the workspace has room for
+constexpr size_t kRecordBytes = kMaxCtas * sizeof(Record);
+__device__ __forceinline__ float* partial(void* ws, int cta, int slot, int floats)
 {
-    return static_cast<float*>(ws) + (static_cast<long long>(range) * 2 + slot) * (static_cast<long long>(rows) * (D + 2));
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kRecordBytes) + (static_cast<long long>(cta) * 2 + slot) * floats;
 }
 
 template <int D, int NT>
-struct Smem {
-    using S = Shape<D>;
-    static constexpr int kRows = 8 * NT;
-    static constexpr int kRing = kWarps * kStages * S::kStage;
-    static constexpr int kRed = kWarps * kRows * (D + 2) * 4;
-    static constexpr int kFixed = kRing + kRed + 64;
-};
-
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(AttendArgs a, int few_rows)
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(AttendArgs a, int few_rows)
 {
-    using S = Shape<D>;
-    using M = Smem<D, NT>;
-    constexpr int kRows = M::kRows, kGroups = S::kGroups, kWords = S::kWords;
+    using S = Shape<D, NT>;
+    constexpr int kRows = S::kRows, kGroups = S::kGroups, kWords = S::kWords, kStages = S::kStages, kWarps = S::kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ Piece pieces[kWarps][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    uint8_t* ring = smem + warp * kStages * S::kStage;
-    float* red = reinterpret_cast<float*>(smem + M::kRing);   // [warp][row][D], then [warp][row] maxima, sums
-    float* red_m = red + kWarps * kRows * D;
-    float* red_l = red_m + kWarps * kRows;
-    int* warp_sums = reinterpret_cast<int*>(smem + M::kRing + M::kRed);
+    uint8_t* ring = smem + warp * S::kRing;
+    float* first_slot = reinterpret_cast<float*>(smem + kWarps * S::kRing);   // [warp] partial results of slot 0
+    int* warp_sums = reinterpret_cast<int*>(smem + kWarps * (S::kRing + 4 * S::kPartial));
     int* prefix = warp_sums + 16;
 
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
-    scan_units(a, few_rows, group, prefix, warp_sums, blockIdx.x == 0 ? a.status : nullptr);
+    scan_units<kWarps>(a, few_rows, group, prefix, warp_sums, blockIdx.x == 0 ? a.status : nullptr);
     const int total = prefix[a.batch.n_seqs];
-    if (total == 0) return;
-    const int n_ranges = ranges(total, gridDim.x), b = blockIdx.x;
-    if (b >= n_ranges) return;
-    const int end = range_at(total, n_ranges, b + 1);
+    const int n_ranges = range_count(total, gridDim.x * kWarps), b = blockIdx.x;
+    const int begin = range_at(total, n_ranges, b * kWarps + warp), end = range_at(total, n_ranges, b * kWarps + warp + 1);
+    if (lane < 2) pieces[warp][lane].u0 = -1;
+    const float inf = __int_as_float(0x7F800000);
 
-    for (int x = range_at(total, n_ranges, b); x < end;) {
+    for (int x = begin; x < end;) {
         const Unit u = unit_at(a, prefix, x);
-        const int t0 = x - u.u0, t1 = min(u.tiles, end - u.u0);
-        x = u.u0 + t1;
+        const int t0 = max(0, x - u.u0 - kUnitCost), t1 = max(0, min(u.len, end - u.u0) - kUnitCost);
+        x = min(end, u.u0 + u.len);
+        if (t0 == t1) continue;   // only the unit's start lies in the range
         const int tile0 = first_tile(u.q, a.window), rows = u.q.n * group;
         const int p0 = u.q.ctx - u.q.n;   // position of the first row
         const int32_t* table = a.batch.block_table + static_cast<long long>(u.s) * a.batch.ld_table;
 
-        // ---- the ring: tile i of this warp is t0 + warp + i * kWarps
-        const int n_mine = max(0, (t1 - t0 - warp + kWarps - 1) / kWarps);
+        // ---- the ring: tiles t0 + i
+        const int n_mine = t1 - t0;
         unsigned has = 0;   // stages that hold a tile
         auto page_at = [&](int i) -> int {
-            const int pos = (tile0 + t0 + warp + i * kWarps) * kTile;
+            const int pos = (tile0 + t0 + i) * kTile;
             if (i >= n_mine || pos >= u.q.ctx) return -1;
             return __ldg(table + (pos >> a.cache.page_shift));
         };
@@ -184,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(Atte
             page_next = page_at(i + 1);
             has &= ~(1u << st);
             if (i < n_mine) {
-                const int pos = (tile0 + t0 + warp + i * kWarps) * kTile;
+                const int pos = (tile0 + t0 + i) * kTile;
                 if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages)) {
                     has |= 1u << st;
                     const int off = pos & (ps - 1);
@@ -272,7 +288,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(Atte
 
         float acc[D / 16][NT][4];
         float top[NT][2], sum[NT][2];
-        const float inf = __int_as_float(0x7F800000);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(Atte
             const bool live = (has >> st) & 1u;
             issue(i + kStages - 1);
             if (!live) continue;
-            const int j0 = (tile0 + t0 + warp + i * kWarps) * kTile;   // the tile's first position
+            const int j0 = (tile0 + t0 + i) * kTile;   // the tile's first position
             // every row sees every position?
             const bool inner = j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + u.q.n - 1 - a.window);
 
@@ -467,7 +482,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(Atte
             }
         }
 
-        // ---- join the warps
+        // ---- the unit's rows, or a partial result
+        const bool whole = t0 == 0 && t1 == u.len - kUnitCost;
+        __syncwarp();   // every lane is done with the ring
+        float* slot = t0 > 0 ? first_slot + warp * S::kPartial : reinterpret_cast<float*>(ring);
+        if (!whole && lane == 0) pieces[warp][t0 > 0 ? 0 : 1] = Piece{u.u0, t1 == u.len - kUnitCost, u.h, u.q.row0, rows, u.u0 + u.len};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -477,82 +496,105 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(Atte
                 l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
                 l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
                 const int r = 8 * nt + 2 * t + c;
-                if (g == 0) {
-                    red_m[warp * kRows + r] = top[nt][c];
-                    red_l[warp * kRows + r] = l;
+                if (r >= rows) continue;
+                if (whole) {
+                    const float k = l == 0.f ? 0.f : 1.f / l;
+                    bf16_t* o = a.out + static_cast<long long>(u.q.row0 + r / group) * a.ld_out + (u.h * group + r % group) * D + g * (D / 8);
+#pragma unroll
+                    for (int w = 0; w < kWords; w += 2)
+                        *reinterpret_cast<uint4*>(o + 4 * w) =
+                            make_uint4(pack_bf16x2(acc[2 * w][nt][c] * k, acc[2 * w][nt][c + 2] * k),
+                                       pack_bf16x2(acc[2 * w + 1][nt][c] * k, acc[2 * w + 1][nt][c + 2] * k),
+                                       pack_bf16x2(acc[2 * w + 2][nt][c] * k, acc[2 * w + 2][nt][c + 2] * k),
+                                       pack_bf16x2(acc[2 * w + 3][nt][c] * k, acc[2 * w + 3][nt][c + 2] * k));
+                } else {
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w)
+                        *reinterpret_cast<float4*>(slot + r * D + g * (D / 8) + 4 * w) =
+                            make_float4(acc[2 * w][nt][c], acc[2 * w][nt][c + 2], acc[2 * w + 1][nt][c], acc[2 * w + 1][nt][c + 2]);
+                    if (g == 0) {
+                        slot[kRows * D + r] = top[nt][c];
+                        slot[kRows * D + kRows + r] = l;
+                    }
                 }
-#pragma unroll
-                for (int w = 0; w < kWords; ++w)
-                    *reinterpret_cast<float4*>(red + (warp * kRows + r) * D + g * (D / 8) + 4 * w) =
-                        make_float4(acc[2 * w][nt][c], acc[2 * w][nt][c + 2], acc[2 * w + 1][nt][c], acc[2 * w + 1][nt][c + 2]);
             }
-        __syncthreads();
-        const bool whole = t0 == 0 && t1 == u.tiles;
-        float* out_p = partial(a.ws, b, t0 == 0 ? 1 : 0, kRows, D);
-        for (int e = tid; e < rows * (D / 4); e += kThreads) {
+    }
+    __syncthreads();
+
+    // ---- join the CTA's partial results, unit by unit
+    auto slot_of = [&](int w, int k) {
+        return k == 0 ? first_slot + w * S::kPartial : reinterpret_cast<const float*>(smem + w * S::kRing);
+    };
+    Record rec{0, 0, 0, 0};
+    for (int i = 0; i < 2 * kWarps;) {   // entry i: warp i / 2, slot i % 2; a unit's pieces follow each other
+        const Piece first = pieces[i >> 1][i & 1];
+        const int i0 = i++;
+        if (first.u0 < 0) continue;
+        int ends = first.ends;
+        for (; i < 2 * kWarps; ++i) {
+            const Piece& p = pieces[i >> 1][i & 1];
+            if (p.u0 >= 0 && p.u0 != first.u0) break;
+            if (p.u0 == first.u0) ends = p.ends;
+        }
+        const bool starts = i0 & 1;
+        float* to = partial(a.ws, b, starts, S::kPartial);
+        for (int e = tid; e < first.rows * (D / 4); e += S::kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
-            float m = -inf;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_m[w * kRows + r]);
+            float m = -inf, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float k = m == -inf ? 0.f : ex2(red_m[w * kRows + r] - m);
-                const float4 v = *reinterpret_cast<const float4*>(red + (w * kRows + r) * D + d);
-                o.x = fmaf(v.x, k, o.x);
-                o.y = fmaf(v.y, k, o.y);
-                o.z = fmaf(v.z, k, o.z);
-                o.w = fmaf(v.w, k, o.w);
-                l = fmaf(red_l[w * kRows + r], k, l);
+            for (int k = i0; k < i; ++k)
+                if (pieces[k >> 1][k & 1].u0 >= 0) m = fmaxf(m, slot_of(k >> 1, k & 1)[kRows * D + r]);
+            for (int k = i0; k < i; ++k) {
+                if (pieces[k >> 1][k & 1].u0 < 0) continue;
+                const float* p = slot_of(k >> 1, k & 1);
+                const float w = m == -inf ? 0.f : ex2(p[kRows * D + r] - m);
+                const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
+                o.x = fmaf(v.x, w, o.x);
+                o.y = fmaf(v.y, w, o.y);
+                o.z = fmaf(v.z, w, o.z);
+                o.w = fmaf(v.w, w, o.w);
+                l = fmaf(p[kRows * D + kRows + r], w, l);
             }
-            if (whole) {
+            if (starts && ends) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint2 v = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-                *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.q.row0 + r / group) * a.ld_out +
-                                          (u.h * group + r % group) * D + d) = v;
+                *reinterpret_cast<uint2*>(a.out + static_cast<long long>(first.row0 + r / group) * a.ld_out + (first.h * group + r % group) * D + d) =
+                    make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
             } else {
-                *reinterpret_cast<float4*>(out_p + r * D + d) = o;
+                *reinterpret_cast<float4*>(to + r * D + d) = o;
                 if (d == 0) {
-                    out_p[kRows * D + r] = m;
-                    out_p[kRows * D + kRows + r] = l;
+                    to[kRows * D + r] = m;
+                    to[kRows * D + kRows + r] = l;
                 }
             }
         }
-        __syncthreads();
+        if (starts && !ends) {
+            rec = Record{first.rows, first.row0, first.h, b};
+            while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, (rec.last + 1) * kWarps) < first.u1) ++rec.last;
+        }
     }
+    if (tid == 0) static_cast<Record*>(a.ws)[b] = rec;
 }
 
-// Joins the pieces of the unit that begins in range b and goes on, in order.
+// Joins the pieces of the unit that begins in CTA b's ranges and goes on, in order.
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads) kv4_few_join_kernel(AttendArgs a, int few_rows, int ctas)
+__global__ void __launch_bounds__(256) kv4_few_join_kernel(AttendArgs a)
 {
-    constexpr int kRows = 8 * NT;
-    extern __shared__ __align__(128) uint8_t smem[];
-    int* warp_sums = reinterpret_cast<int*>(smem);
-    int* prefix = warp_sums + 16;
+    using S = Shape<D, NT>;
+    constexpr int kRows = S::kRows;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    const int group = a.n_heads / a.cache.n_kv;
-    scan_units(a, few_rows, group, prefix, warp_sums, nullptr);
-    const int total = prefix[a.batch.n_seqs];
-    if (total == 0) return;
-    const int n_ranges = ranges(total, ctas), b = blockIdx.x;
-    if (b >= n_ranges) return;
-    const int end = range_at(total, n_ranges, b + 1);
-    const Unit u = unit_at(a, prefix, end - 1);
-    const int u1 = u.u0 + u.tiles;
-    if (u1 <= end || u.u0 < range_at(total, n_ranges, b)) return;
-    int last = b + 1;
-    while (range_at(total, n_ranges, last + 1) < u1) ++last;
+    const int b = blockIdx.x, group = a.n_heads / a.cache.n_kv;
+    const Record u = static_cast<const Record*>(a.ws)[b];
     const float inf = __int_as_float(0x7F800000);
-    for (int e = threadIdx.x; e < u.q.n * group * (D / 4); e += kThreads) {
+    for (int e = threadIdx.x; e < u.rows * (D / 4); e += blockDim.x) {
         const int r = e / (D / 4), d = e % (D / 4) * 4;
         float m = -inf, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = b; k <= last; ++k) m = fmaxf(m, partial(a.ws, k, k == b, kRows, D)[kRows * D + r]);
-        for (int k = b; k <= last; ++k) {
-            const float* p = partial(a.ws, k, k == b, kRows, D);
+#pragma unroll 4
+        for (int k = b; k <= u.last; ++k) m = fmaxf(m, partial(a.ws, k, k == b, S::kPartial)[kRows * D + r]);
+#pragma unroll 4
+        for (int k = b; k <= u.last; ++k) {
+            const float* p = partial(a.ws, k, k == b, S::kPartial);
             const float w = m == -inf ? 0.f : ex2(p[kRows * D + r] - m);
             const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
             o.x = fmaf(v.x, w, o.x);
@@ -562,34 +604,32 @@ __global__ void __launch_bounds__(kThreads) kv4_few_join_kernel(AttendArgs a, in
             l = fmaf(p[kRows * D + kRows + r], w, l);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.q.row0 + r / group) * a.ld_out + (u.h * group + r % group) * D + d) =
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.row0 + r / group) * a.ld_out + (u.h * group + r % group) * D + d) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
 }
 
 constexpr int kMaxSmem = 227 * 1024;
-static_assert(Smem<128, 4>::kRing + Smem<128, 4>::kRed + (17 + kMaxSeqs) * 4 <= kMaxSmem, "shared memory");
-constexpr int kMaxCtas = 2 * 160;   // ranges that the workspace has room for
+static_assert(Shape<128, 4>::kSmem + 4 * kMaxSeqs <= kMaxSmem, "shared memory");
 
 template <int D, int NT>
 cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
 {
-    const size_t scan = (16 + a.batch.n_seqs + 1) * sizeof(int);
-    const size_t smem = Smem<D, NT>::kRing + Smem<D, NT>::kRed + scan;
+    using S = Shape<D, NT>;
     static bool attr_set = false;
     cudaError_t e = cudaSuccess;
     if (!attr_set) {
-        e = cudaFuncSetAttribute(kv4_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        e = cudaFuncSetAttribute(kv4_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
     const int ctas = std::min(kMaxCtas, device_sms() * (NT == 1 ? 2 : 1));
-    PdlLaunch l(dim3(ctas), kThreads, smem, stream);
+    PdlLaunch l(dim3(ctas), S::kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
     e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows);
     if (e != cudaSuccess) return e;
     note_launch();
-    PdlLaunch j(dim3(ctas), kThreads, scan, stream);
-    e = cudaLaunchKernelEx(&j.cfg, kv4_few_join_kernel<D, NT>, a, few_rows, ctas);
+    PdlLaunch j(dim3(ctas), 256, 0, stream);
+    e = cudaLaunchKernelEx(&j.cfg, kv4_few_join_kernel<D, NT>, a);
     note_launch();
     return e;
 }
@@ -599,7 +639,7 @@ cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
 size_t kv4_few_workspace(int head_dim, int rows)
 {
     const int r = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-    return static_cast<size_t>(kMaxCtas) * 2 * r * (head_dim + 2) * sizeof(float);
+    return kRecordBytes + static_cast<size_t>(kMaxCtas) * 2 * r * (head_dim + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, cudaStream_t stream)
