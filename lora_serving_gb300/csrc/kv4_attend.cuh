@@ -1,5 +1,5 @@
-// kv4_attend.cuh -- what the attention kernels share: the way work is cut
-// into equal ranges over the batch, and the fragments' small instructions.
+// kv4_attend.cuh -- what the attention kernels share: finding a place in the
+// batch's work, and the small steps from codes to fp16 operands.
 #pragma once
 
 #include "kv4.h"
@@ -72,8 +72,48 @@ __device__ __forceinline__ bool not_finite(uint32_t h2)
     return (h2 & 0x7C00u) == 0x7C00u || (h2 & 0x7C000000u) == 0x7C000000u;
 }
 
+// Running sum over the sequences of count(s), in shared memory (prefix: one
+// entry more than sequences; sums: one per warp), by the whole CTA.
+template <int kWarps, class F>
+__device__ __forceinline__ void scan_seqs(int n_seqs, int* prefix, int* sums, F count)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int base = 0;
+    if (tid == 0) prefix[0] = 0;
+    for (int s0 = 0; s0 < n_seqs; s0 += 32 * kWarps) {
+        const int s = s0 + tid;
+        int sum = s < n_seqs ? count(s) : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+            if (lane >= o) sum += up;
+        }
+        if (lane == 31) sums[warp] = sum;
+        __syncthreads();
+        int before = base;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            before += w < warp ? sums[w] : 0;
+            base += sums[w];
+        }
+        if (s < n_seqs) prefix[s + 1] = before + sum;
+        __syncthreads();
+    }
+}
+// The last s with prefix[s] <= x.
+__device__ __forceinline__ int seq_at(const int* prefix, int n_seqs, int x)
+{
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
 }  // namespace kv4
 
+cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, cudaStream_t stream);
 cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, cudaStream_t stream);
 size_t kv4_few_workspace(int head_dim, int rows);
 

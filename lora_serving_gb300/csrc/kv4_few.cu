@@ -77,41 +77,6 @@ __device__ __forceinline__ int tiles_of(const Seq& q, int window)
     return max(1, (q.ctx + kTile - 1) / kTile - first_tile(q, window));   // at least one: its rows get their zeros
 }
 
-// Running sum over the sequences of (tiles + kUnitCost) x kv heads, in shared memory.
-template <int kWarps>
-__device__ void scan_units(const AttendArgs& a, int few_rows, int group, int* prefix, int* warp_sums, int32_t* status)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int base = 0;
-    for (int s0 = 0; s0 < a.batch.n_seqs; s0 += 32 * kWarps) {
-        const int s = s0 + tid;
-        int v = 0;
-        if (s < a.batch.n_seqs) {
-            Seq q;
-            if (load_seq(a.batch, s, q, status) && q.n > 0 && q.n * group <= few_rows) v = (tiles_of(q, a.window) + kUnitCost) * a.cache.n_kv;
-        }
-        int sum = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-            if (lane >= o) sum += up;
-        }
-        if (lane == 31) warp_sums[warp] = sum;
-        __syncthreads();
-        int before = 0, all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) before += warp_sums[w];
-            all += warp_sums[w];
-        }
-        if (s < a.batch.n_seqs) prefix[s + 1] = base + before + sum;
-        base += all;
-        __syncthreads();
-    }
-    if (tid == 0) prefix[0] = 0;
-    __syncthreads();
-}
-
 // The unit that holds place x (< total) of the line.
 struct Unit {
     int s, h, u0, len;   // sequence, kv head, its first place, places (kUnitCost, then its tiles)
@@ -119,11 +84,7 @@ struct Unit {
 };
 __device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, int x)
 {
-    int lo = 0, hi = a.batch.n_seqs - 1;   // last s with prefix[s] <= x
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= x) lo = mid; else hi = mid - 1;
-    }
+    const int lo = seq_at(prefix, a.batch.n_seqs, x);
     Unit u;
     u.s = lo;
     u.len = (prefix[lo + 1] - prefix[lo]) / a.cache.n_kv;
@@ -170,7 +131,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
-    scan_units<kWarps>(a, few_rows, group, prefix, warp_sums, blockIdx.x == 0 ? a.status : nullptr);
+    scan_seqs<kWarps>(a.batch.n_seqs, prefix, warp_sums, [&](int s) {
+        Seq q;
+        const bool ok = load_seq(a.batch, s, q, blockIdx.x == 0 ? a.status : nullptr);
+        return ok && q.n > 0 && q.n * group <= few_rows ? (tiles_of(q, a.window) + kUnitCost) * a.cache.n_kv : 0;
+    });
     const int total = prefix[a.batch.n_seqs];
     const int n_ranges = range_count(total, gridDim.x * kWarps), b = blockIdx.x;
     const int begin = range_at(total, n_ranges, b * kWarps + warp), end = range_at(total, n_ranges, b * kWarps + warp + 1);
