@@ -12,6 +12,7 @@ import ctypes
 import os
 
 import numpy as np
+import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora.so")
@@ -156,8 +157,8 @@ def _ld(t) -> int:
     return int(t.stride(0))
 
 
-_DTYPES = {"bf16": "torch.bfloat16", "f32": "torch.float32", "i32": "torch.int32", "u8": "torch.uint8",
-           "e4m3": "torch.float8_e4m3fn"}
+_DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
+           "e4m3": torch.float8_e4m3fn}
 
 
 def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
@@ -171,27 +172,43 @@ def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
         return _p(t)
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and str(t.dtype) != _DTYPES[dtype]:
+    if dtype is not None and t.dtype is not _DTYPES[dtype]:
         raise ValueError(f"{name} must be {_DTYPES[dtype]}, got {t.dtype}")
     if mat and (t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1)):
         raise ValueError(f"{name} must be 2-D with unit column stride")
     return t.data_ptr()
 
 
-def _ld0(t) -> int:
-    return 0 if t is None else int(t.stride(0))
+def _mat(t, name: str, dtype, n_rows: int, cols: int):
+    """(pointer, leading dimension) of a row-major kernel operand: a CUDA
+    tensor of this element type with n_rows rows and cols columns at least
+    and unit column stride.  None: (NULL, 0)."""
+    if t is None:
+        return 0, 0
+    if not t.is_cuda or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < n_rows or shape[1] < cols:
+        raise ValueError(f"{name} must be 2-D with {n_rows} rows and {cols} columns at least, got {tuple(shape)}")
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), ld
 
 
-def _rows(name: str, t, batch, cols: int = 0):
-    """A row-major operand with the batch's rows and at least cols columns."""
-    if t.dim() != 2 or t.shape[0] < batch.c.n_rows or t.shape[1] < cols:
-        raise ValueError(f"{name} must be 2-D with {batch.c.n_rows} rows and {cols} columns at least")
+try:   # the current stream's handle without a Stream object around it (3 us of a call's 10)
+    _raw_stream, _cur_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+    def _current_stream() -> int:
+        return _raw_stream(_cur_device()) if torch.cuda.is_initialized() else torch.cuda.current_stream().cuda_stream
+except AttributeError:
+    def _current_stream() -> int:
+        return torch.cuda.current_stream().cuda_stream
 
 
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -303,23 +320,27 @@ def lora_merge_batch(Ws, As, Bs, sign, *, stream=None):
                                                        _stream(stream)))
 
 
+_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
+
+
 def lora_rms_norm(x, weight, eps, *, residual=None, residual_out=None, y=None, y8=None, scales=None, group=0,
                   stream=None):
     """h = bf16(x + residual) -> residual_out; n = h / sqrt(mean(h^2) + eps) * weight
     -> y (bf16) and/or y8 (float8_e4m3fn) with fp32 scales [n_rows][groups], one
     per `group` (128) columns or, with group 0, per row."""
     n_rows, width = x.shape
-    if int(weight.numel()) != width or not weight.is_contiguous():
+    if weight.numel() != width or not weight.is_contiguous():
         raise ValueError(f"weight must hold {width} contiguous values")
-    for name, t, cols in (("residual", residual, width), ("residual_out", residual_out, width), ("y", y, width),
-                          ("y8", y8, width), ("scales", scales, (width + group - 1) // group if group > 0 else 1)):
-        if t is not None and (t.dim() != 2 or t.shape[0] != n_rows or t.shape[1] < cols):
-            raise ValueError(f"{name} must be [{n_rows}][{cols}]")
-    _check("lora_rms_norm", load().lora_rms_norm(
-        _dev(y, "y", "bf16", True), _ld0(y), _dev(y8, "y8", "e4m3", True), _ld0(y8), _dev(scales, "scales", "f32", True),
-        _ld0(scales), group, _dev(residual_out, "residual_out", "bf16", True), _ld0(residual_out),
-        _dev(x, "x", "bf16", True), _ld(x), _dev(residual, "residual", "bf16", True), _ld0(residual),
-        _dev(weight, "weight", "bf16"), n_rows, width, eps, _stream(stream)))
+    y_p, ld_y = _mat(y, "y", _BF16, n_rows, width)
+    y8_p, ld_y8 = _mat(y8, "y8", _E4M3, n_rows, width)
+    s_p, ld_s = _mat(scales, "scales", _F32, n_rows, (width + group - 1) // group if group > 0 else 1)
+    ro_p, ld_ro = _mat(residual_out, "residual_out", _BF16, n_rows, width)
+    x_p, ld_x = _mat(x, "x", _BF16, n_rows, width)
+    r_p, ld_r = _mat(residual, "residual", _BF16, n_rows, width)
+    st = load().lora_rms_norm(y_p, ld_y, y8_p, ld_y8, s_p, ld_s, group, ro_p, ld_ro, x_p, ld_x, r_p, ld_r,
+                              _dev(weight, "weight", "bf16"), n_rows, width, eps, _stream(stream))
+    if st:
+        raise LoraError("lora_rms_norm", st)
 
 
 def lora_kv4_block_bytes(page_size, head_dim) -> int:
@@ -333,46 +354,48 @@ def lora_kv4_append(q_out, x, cache, batch, *, n_heads, q_off, k_off, v_off, rop
     rope: fp32 [max_pos][pairs][2] (cos, sin) or None; positions: int32
     [n_rows][n_axes] or None; axis_pairs: pairs of each axis (default: all
     on one axis)."""
-    _rows("x", x, batch)
-    _rows("q_out", q_out, batch, n_heads * cache.c.head_dim)
-    rot = max_pos = n_axes = 0
+    n = batch.c.n_rows
+    q_p, ld_q = _mat(q_out, "q_out", _BF16, n, n_heads * cache.c.head_dim)
+    x_p, ld_x = _mat(x, "x", _BF16, n, 0)
+    rot = max_pos = n_axes = pos_p = ld_pos = 0
     axes = None
     if rope is not None:
         if rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
             raise ValueError("rope must be contiguous [max_pos][pairs][2]")
-        max_pos, rot = int(rope.shape[0]), 2 * int(rope.shape[1])
-        pairs = [rot // 2] if axis_pairs is None else list(axis_pairs)
+        max_pos, rot = rope.shape[0], 2 * rope.shape[1]
+        pairs = (rot // 2,) if axis_pairs is None else axis_pairs
         n_axes = len(pairs)
         axes = (ctypes.c_int * max(1, n_axes))(*pairs)
-        if positions is not None:
-            _rows("positions", positions, batch, n_axes)
-    _check("lora_kv4_append", load().lora_kv4_append(
-        _dev(q_out, "q_out", "bf16", True), _ld(q_out), _dev(x, "x", "bf16", True), _ld(x), n_heads, q_off, k_off, v_off,
-        _dev(rope, "rope", "f32"), rot, max_pos, _dev(positions, "positions", "i32", True), _ld0(positions),
-        axes, n_axes, ctypes.byref(cache.c), ctypes.byref(batch.c), _dev(dev_status, "dev_status", "i32"),
-        _stream(stream)))
+        pos_p, ld_pos = _mat(positions, "positions", _I32, n, n_axes)
+    st = load().lora_kv4_append(q_p, ld_q, x_p, ld_x, n_heads, q_off, k_off, v_off, _dev(rope, "rope", "f32"), rot,
+                                max_pos, pos_p, ld_pos, axes, n_axes, cache.ref, batch.ref,
+                                _dev(dev_status, "dev_status", "i32"), _stream(stream))
+    if st:
+        raise LoraError("lora_kv4_append", st)
 
 
 def lora_kv4_read(k, v, cache, batch, *, dev_status=None, stream=None):
     """k, v [n_rows][n_kv * head_dim] <- the cached values of the rows' places."""
     width = cache.c.n_kv * cache.c.head_dim
-    _rows("k", k, batch, width)
-    _rows("v", v, batch, width)
-    _check("lora_kv4_read", load().lora_kv4_read(
-        _dev(k, "k", "bf16", True), _ld(k), _dev(v, "v", "bf16", True), _ld(v), ctypes.byref(cache.c),
-        ctypes.byref(batch.c), _dev(dev_status, "dev_status", "i32"), _stream(stream)))
+    k_p, ld_k = _mat(k, "k", _BF16, batch.c.n_rows, width)
+    v_p, ld_v = _mat(v, "v", _BF16, batch.c.n_rows, width)
+    st = load().lora_kv4_read(k_p, ld_k, v_p, ld_v, cache.ref, batch.ref, _dev(dev_status, "dev_status", "i32"),
+                              _stream(stream))
+    if st:
+        raise LoraError("lora_kv4_read", st)
 
 
 def lora_kv4_attend(out, q, cache, batch, workspace, *, n_heads, scale, window=0, dev_status=None, stream=None):
     """out [n_rows][n_heads * head_dim] <- causal attention of q over the cache
     (the last `window` positions, 0: all)."""
     width = n_heads * cache.c.head_dim
-    _rows("out", out, batch, width)
-    _rows("q", q, batch, width)
-    _check("lora_kv4_attend", load().lora_kv4_attend(
-        _dev(out, "out", "bf16", True), _ld(out), _dev(q, "q", "bf16", True), _ld(q), n_heads, scale, window,
-        ctypes.byref(cache.c), ctypes.byref(batch.c), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _dev(dev_status, "dev_status", "i32"), _stream(stream)))
+    out_p, ld_out = _mat(out, "out", _BF16, batch.c.n_rows, width)
+    q_p, ld_q = _mat(q, "q", _BF16, batch.c.n_rows, width)
+    st = load().lora_kv4_attend(out_p, ld_out, q_p, ld_q, n_heads, scale, window, cache.ref, batch.ref,
+                                _dev(workspace, "workspace"), workspace.nbytes,
+                                _dev(dev_status, "dev_status", "i32"), _stream(stream))
+    if st:
+        raise LoraError("lora_kv4_attend", st)
 
 
 def lora_kv4_attend_workspace_bytes(n_heads, n_kv, head_dim, max_q_len) -> int:
