@@ -20,6 +20,8 @@ using kv4::Batch;
 using kv4::Cache;
 using kv4::Seq;
 
+constexpr int kThreads = 128;
+
 // Minimum and maximum that keep a NaN.
 __device__ __forceinline__ float min_nan(float a, float b)
 {
@@ -44,22 +46,40 @@ __device__ __forceinline__ uint4 pack8(const float* f)
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
 }
 
+// rint(c) for c in [0, 2^22), as the low bits of c + 1.5 * 2^23 hold it.
+constexpr float kMagic = 12582912.f;
+
 // Eight codes of a chunk, one per nibble.  Step and lowest value are rounded
 // to fp16 first (fewer bits to read back per token; the codes are taken
-// against the rounded ones, so that rounding only moves the grid).
+// against the rounded ones, so that rounding only moves the grid).  Four
+// codes at a time are put together in fp32, exactly: conversions to integers
+// run at a quarter of the rate of the fp32 pipe.
 __device__ __forceinline__ uint32_t codes8(const float* f, float inv, float low)
 {
-    uint32_t w = 0;
+    uint32_t half[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        float c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = __fadd_rn(fminf(fmaxf(__fmul_rn(__fsub_rn(f[4 * k + i], low), inv), 0.f), 15.f), kMagic) - kMagic;
+        half[k] = __float_as_uint(fmaf(fmaf(c[3], 16.f, c[2]), 256.f, fmaf(c[1], 16.f, c[0])) + kMagic) & 0xFFFFu;
+    }
+    return half[0] | (half[1] << 16);
+}
+
+__device__ __forceinline__ void rotate8(float* a, float* b, const float* cs, const float* sn)
+{
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(f[i], low), inv)), 0.f), 15.f);
-        w |= static_cast<uint32_t>(c) << (4 * i);
+        const float lo = a[i], hi = b[i];
+        a[i] = __fsub_rn(__fmul_rn(lo, cs[i]), __fmul_rn(hi, sn[i]));
+        b[i] = __fadd_rn(__fmul_rn(hi, cs[i]), __fmul_rn(lo, sn[i]));
     }
-    return w;
 }
 
 template <int D>
-__global__ void __launch_bounds__(128) kv4_append_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kThreads, 8) kv4_append_kernel(AppendArgs a)
 {
     constexpr int kLanes = D / 16, kGroups = D / kv4::kGroup;
     tc::grid_dep_wait();
@@ -107,82 +127,68 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(AppendArgs a)
     const int off = p & (a.cache.page_size - 1), ps = a.cache.page_size;
 
     const bf16_t* x = a.x + static_cast<long long>(row) * a.ld_x;
-    const int n_kv = a.cache.n_kv, total = a.n_heads + 2 * n_kv;
-    // Every lane of a warp makes the same number of rounds (the shuffles
-    // below need them all).
-    for (int first = 0; first < total; first += teams) {
-        const int head = first + team;
-        const bool live = head < total;
-        const int kind = !live || head < a.n_heads ? 0 : head < a.n_heads + n_kv ? 1 : 2;   // q, k, v
-        const int h = kind == 0 ? head : kind == 1 ? head - a.n_heads : head - a.n_heads - n_kv;
-        const int col = (kind == 0 ? a.q_off : kind == 1 ? a.k_off : a.v_off) + h * D;
+    const int n_kv = a.cache.n_kv;
+    for (int h = team; h < a.n_heads; h += teams) {
         float f0[8], f1[8];
-        uint4 u0 = make_uint4(0, 0, 0, 0), u1 = u0;
-        if (live) {
-            u0 = *reinterpret_cast<const uint4*>(x + col + d0);
-            u1 = *reinterpret_cast<const uint4*>(x + col + d1);
-        }
-        unpack8(u0, f0);
-        unpack8(u1, f1);
-        if (turns && kind != 2) {
+        unpack8(*reinterpret_cast<const uint4*>(x + a.q_off + h * D + d0), f0);
+        unpack8(*reinterpret_cast<const uint4*>(x + a.q_off + h * D + d1), f1);
+        if (turns) rotate8(f0, f1, cs, sn);
+        bf16_t* o = a.q_out + static_cast<long long>(row) * a.ld_q + h * D;
+        *reinterpret_cast<uint4*>(o + d0) = pack8(f0);
+        *reinterpret_cast<uint4*>(o + d1) = pack8(f1);
+    }
+    if (page < 0) return;
+    const float inf = __int_as_float(0x7F800000);
+    const int g0 = d0 / kv4::kGroup, g1 = d1 / kv4::kGroup;
+    // Every lane of a warp makes the same number of rounds (the shuffles
+    // below need them all); a team past the last head does nothing with its.
+    for (int first = 0; first < 2 * n_kv; first += teams) {
+        const int head = first + team;
+        const bool live = head < 2 * n_kv, is_k = head < n_kv;
+        const int h = is_k ? head : head - n_kv;
+        const bf16_t* src = x + (is_k ? a.k_off : a.v_off) + (live ? h : 0) * D;
+        float f0[8], f1[8];
+        unpack8(*reinterpret_cast<const uint4*>(src + d0), f0);
+        unpack8(*reinterpret_cast<const uint4*>(src + d1), f1);
+        if (is_k && turns) rotate8(f0, f1, cs, sn);
+        // each chunk's ends, then its group's; a NaN stays
+        float lo[2] = {inf, inf}, hi[2] = {-inf, -inf};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float lo = f0[i], hi = f1[i];
-                f0[i] = __fsub_rn(__fmul_rn(lo, cs[i]), __fmul_rn(hi, sn[i]));
-                f1[i] = __fadd_rn(__fmul_rn(hi, cs[i]), __fmul_rn(lo, sn[i]));
-            }
+        for (int i = 0; i < 8; ++i) {
+            f0[i] = max_nan(min_nan(f0[i], kv4::kMaxAbs), -kv4::kMaxAbs);
+            f1[i] = max_nan(min_nan(f1[i], kv4::kMaxAbs), -kv4::kMaxAbs);
+            lo[0] = min_nan(lo[0], f0[i]);
+            hi[0] = max_nan(hi[0], f0[i]);
+            lo[1] = min_nan(lo[1], f1[i]);
+            hi[1] = max_nan(hi[1], f1[i]);
         }
-        float lo[kGroups], hi[kGroups];
-        if (kind) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {   // saturation that keeps a NaN
-                f0[i] = max_nan(min_nan(f0[i], kv4::kMaxAbs), -kv4::kMaxAbs);
-                f1[i] = max_nan(min_nan(f1[i], kv4::kMaxAbs), -kv4::kMaxAbs);
-            }
+        if (kGroups == 1) {
+            lo[0] = min_nan(lo[0], lo[1]);
+            hi[0] = max_nan(hi[0], hi[1]);
+        } else if (g0 == g1) {   // both chunks in one group: the other one's neutral
+            const float l = min_nan(lo[0], lo[1]), m = max_nan(hi[0], hi[1]);
+            lo[0] = g0 ? inf : l;
+            lo[1] = g0 ? l : inf;
+            hi[0] = g0 ? -inf : m;
+            hi[1] = g0 ? m : -inf;
         }
-        const float inf = __int_as_float(0x7F800000);
+        float low[kGroups], inv[kGroups];
+        uint8_t* block = kv4::block_of(a.cache, page, live ? h : 0);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-            lo[g] = inf;
-            hi[g] = -inf;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (d0 / kv4::kGroup == g) {
-                    lo[g] = min_nan(lo[g], f0[i]);
-                    hi[g] = max_nan(hi[g], f0[i]);
-                }
-                if (d1 / kv4::kGroup == g) {
-                    lo[g] = min_nan(lo[g], f1[i]);
-                    hi[g] = max_nan(hi[g], f1[i]);
-                }
-            }
 #pragma unroll
             for (int o = kLanes / 2; o > 0; o >>= 1) {
                 lo[g] = min_nan(lo[g], __shfl_xor_sync(0xFFFFFFFFu, lo[g], o));
                 hi[g] = max_nan(hi[g], __shfl_xor_sync(0xFFFFFFFFu, hi[g], o));
             }
-        }
-        if (!live) continue;
-        if (kind == 0) {
-            bf16_t* o = a.q_out + static_cast<long long>(row) * a.ld_q + h * D;
-            *reinterpret_cast<uint4*>(o + d0) = pack8(f0);
-            *reinterpret_cast<uint4*>(o + d1) = pack8(f1);
-            continue;
-        }
-        if (page < 0) continue;
-        uint8_t* block = kv4::block_of(a.cache, page, h);
-        float low[kGroups], inv[kGroups];
-#pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
             const __half st = __float2half_rn(__fmul_rn(__fsub_rn(hi[g], lo[g]), 1.f / 15.f));
             const __half lw = __float2half_rn(lo[g]);
             const float stf = __half2float(st);
             low[g] = __half2float(lw);
             inv[g] = stf > 0.f ? __frcp_rn(stf) : 0.f;
-            if (lane == 0) {
-                if (kind == 1) {
-                    __half2* d = reinterpret_cast<__half2*>(block + kv4::k_params_off(ps, D)) + off * kGroups + g;
-                    *d = __halves2half2(st, lw);
+            if (live && lane == 0) {
+                if (is_k) {
+                    reinterpret_cast<__half2*>(block + kv4::k_params_off(ps, D))[off * kGroups + g] = __halves2half2(st, lw);
                 } else {
                     __half* d = reinterpret_cast<__half*>(block + kv4::v_params_off(ps, D)) +
                                 ((off >> 1) * kGroups + g) * 4 + (off & 1);
@@ -191,10 +197,10 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(AppendArgs a)
                 }
             }
         }
-        const int g0 = d0 / kv4::kGroup, g1 = d1 / kv4::kGroup;
         const uint32_t w0 = codes8(f0, g0 ? inv[kGroups - 1] : inv[0], g0 ? low[kGroups - 1] : low[0]);
         const uint32_t w1 = codes8(f1, g1 ? inv[kGroups - 1] : inv[0], g1 ? low[kGroups - 1] : low[0]);
-        if (kind == 1) {
+        if (!live) continue;
+        if (is_k) {
             uint32_t* d = reinterpret_cast<uint32_t*>(block) + off * (D / 8);
             d[kv4::k_word(d0 >> 3, D)] = w0;
             d[kv4::k_word(d1 >> 3, D)] = w1;
@@ -211,7 +217,7 @@ __global__ void __launch_bounds__(128) kv4_append_kernel(AppendArgs a)
 
 // One row per CTA, eight dims a thread: k of every kv head, then v.
 template <int D>
-__global__ void __launch_bounds__(128) kv4_read_kernel(ReadArgs a)
+__global__ void __launch_bounds__(kThreads, 16) kv4_read_kernel(ReadArgs a)
 {
     constexpr int kChunks = D / 8, kGroups = D / kv4::kGroup;
     tc::grid_dep_wait();
@@ -245,7 +251,8 @@ __global__ void __launch_bounds__(128) kv4_read_kernel(ReadArgs a)
         }
         float f[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = __fadd_rn(__fmul_rn(static_cast<float>((w >> (4 * j)) & 15u), step), low);
+        for (int j = 0; j < 8; ++j)   // 2^23 + code, less 2^23; code * step is exact
+            f[j] = fmaf(__uint_as_float(((w >> (4 * j)) & 15u) | 0x4B000000u) - 8388608.f, step, low);
         bf16_t* o = hh < n_kv ? a.k + static_cast<long long>(row) * a.ld_k : a.v + static_cast<long long>(row) * a.ld_v;
         *reinterpret_cast<uint4*>(o + h * D + 8 * c) = pack8(f);
     }
@@ -256,7 +263,7 @@ __global__ void __launch_bounds__(128) kv4_read_kernel(ReadArgs a)
 cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t stream)
 {
     if (a.batch.n_rows == 0) return cudaSuccess;
-    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), 128, 0, stream);
+    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), kThreads, 0, stream);
     const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_append_kernel<64>, a)
                                                  : cudaLaunchKernelEx(&l.cfg, kv4_append_kernel<128>, a);
     note_launch();
@@ -266,7 +273,7 @@ cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t stream)
 cudaError_t launch_kv4_read(const ReadArgs& a, cudaStream_t stream)
 {
     if (a.batch.n_rows == 0) return cudaSuccess;
-    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), 128, 0, stream);
+    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), kThreads, 0, stream);
     const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<64>, a)
                                                  : cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<128>, a);
     note_launch();
