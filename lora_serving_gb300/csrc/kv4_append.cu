@@ -21,6 +21,7 @@ using kv4::Cache;
 using kv4::Seq;
 
 constexpr int kThreads = 128;
+constexpr int kWarpRows = 2432;   // 16 warps on each of 152 SMs
 
 // Minimum and maximum that keep a NaN.
 __device__ __forceinline__ float min_nan(float a, float b)
@@ -48,6 +49,11 @@ __device__ __forceinline__ uint4 pack8(const float* f)
 
 // rint(c) for c in [0, 2^22), as the low bits of c + 1.5 * 2^23 hold it.
 constexpr float kMagic = 12582912.f;
+
+__device__ __forceinline__ void prefetch_row(const bf16_t* p, int n, int i, int threads)
+{
+    for (; i * 64 < n; i += threads) asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p + i * 64));
+}
 
 // Eight codes of a chunk, one per nibble.  Step and lowest value are rounded
 // to fp16 first (fewer bits to read back per token; the codes are taken
@@ -79,15 +85,27 @@ __device__ __forceinline__ void rotate8(float* a, float* b, const float* cs, con
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 8) kv4_append_kernel(AppendArgs a)
+__global__ void __launch_bounds__(kThreads, 8) kv4_append_kernel(AppendArgs a, int per_row)
 {
     constexpr int kLanes = D / 16, kGroups = D / kv4::kGroup;
+    const int row = blockIdx.x * (kThreads / per_row) + threadIdx.x / per_row, of_row = threadIdx.x % per_row;
+    const int lane = of_row % kLanes, team = of_row / kLanes, teams = per_row / kLanes;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    const int row = blockIdx.x, lane = threadIdx.x % kLanes, team = threadIdx.x / kLanes, teams = blockDim.x / kLanes;
+    if (row >= a.batch.n_rows) return;
+    // the row's lines are on their way while the tables are read
+    prefetch_row(a.x + static_cast<long long>(row) * a.ld_x + a.q_off, a.n_heads * D, of_row, per_row);
+    prefetch_row(a.x + static_cast<long long>(row) * a.ld_x + a.k_off, a.cache.n_kv * D, of_row, per_row);
+    prefetch_row(a.x + static_cast<long long>(row) * a.ld_x + a.v_off, a.cache.n_kv * D, of_row, per_row);
+    int at[LORA_MAX_ROPE_AXES] = {0, 0, 0};
+    if (a.rot_dim && a.positions) {
+#pragma unroll
+        for (int x = 0; x < LORA_MAX_ROPE_AXES; ++x)
+            if (x < a.n_axes) at[x] = __ldg(a.positions + static_cast<long long>(row) * a.ld_pos + x);
+    }
     const int s = kv4::find_seq_warp(a.batch.q_starts, a.batch.n_seqs, row);
     Seq q;
-    if (!kv4::load_seq(a.batch, s, q, threadIdx.x == 0 ? a.status : nullptr) || row < q.row0 || row >= q.row0 + q.n) return;
+    if (!kv4::load_seq(a.batch, s, q, of_row == 0 ? a.status : nullptr) || row < q.row0 || row >= q.row0 + q.n) return;
     const int p = q.ctx - q.n + (row - q.row0);
     if (p < 0) return;
 
@@ -96,20 +114,17 @@ __global__ void __launch_bounds__(kThreads, 8) kv4_append_kernel(AppendArgs a)
     const bool turns = lane < rot_lanes;
     const int d0 = turns ? 8 * lane : a.rot_dim + 16 * (lane - rot_lanes);
     const int d1 = turns ? half + d0 : d0 + 8;
-    int at[LORA_MAX_ROPE_AXES];
-#pragma unroll
-    for (int x = 0; x < LORA_MAX_ROPE_AXES; ++x) at[x] = 0;
     bool bad = false;
     if (a.rot_dim) {
 #pragma unroll
         for (int x = 0; x < LORA_MAX_ROPE_AXES; ++x) {
             if (x >= a.n_axes) break;
-            at[x] = a.positions ? __ldg(a.positions + static_cast<long long>(row) * a.ld_pos + x) : p;
+            if (!a.positions) at[x] = p;
             bad |= static_cast<unsigned>(at[x]) >= static_cast<unsigned>(a.max_pos);
         }
     }
     if (bad) {
-        if (threadIdx.x == 0) flag(a.status, LORA_DEV_BAD_POSITION);
+        if (of_row == 0) flag(a.status, LORA_DEV_BAD_POSITION);
         return;
     }
     float cs[8], sn[8];
@@ -123,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 8) kv4_append_kernel(AppendArgs a)
             sn[i] = t.y;
         }
     }
-    const int page = kv4::page_of(a.cache, a.batch, s, p, threadIdx.x == 0 ? a.status : nullptr);
+    const int page = kv4::page_of(a.cache, a.batch, s, p, of_row == 0 ? a.status : nullptr);
     const int off = p & (a.cache.page_size - 1), ps = a.cache.page_size;
 
     const bf16_t* x = a.x + static_cast<long long>(row) * a.ld_x;
@@ -215,69 +230,81 @@ __global__ void __launch_bounds__(kThreads, 8) kv4_append_kernel(AppendArgs a)
     }
 }
 
-// One row per CTA, eight dims a thread: k of every kv head, then v.
+// Eight dims a thread: k of every kv head, then v.
 template <int D>
-__global__ void __launch_bounds__(kThreads, 16) kv4_read_kernel(ReadArgs a)
+__global__ void __launch_bounds__(kThreads, 8) kv4_read_kernel(ReadArgs a, int per_row)
 {
     constexpr int kChunks = D / 8, kGroups = D / kv4::kGroup;
+    const int row = blockIdx.x * (kThreads / per_row) + threadIdx.x / per_row, of_row = threadIdx.x % per_row;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    const int row = blockIdx.x;
+    if (row >= a.batch.n_rows) return;
     const int s = kv4::find_seq_warp(a.batch.q_starts, a.batch.n_seqs, row);
     Seq q;
-    if (!kv4::load_seq(a.batch, s, q, threadIdx.x == 0 ? a.status : nullptr) || row < q.row0 || row >= q.row0 + q.n) return;
+    if (!kv4::load_seq(a.batch, s, q, of_row == 0 ? a.status : nullptr) || row < q.row0 || row >= q.row0 + q.n) return;
     const int p = q.ctx - q.n + (row - q.row0);
     if (p < 0) return;
-    const int page = kv4::page_of(a.cache, a.batch, s, p, threadIdx.x == 0 ? a.status : nullptr);
+    const int page = kv4::page_of(a.cache, a.batch, s, p, of_row == 0 ? a.status : nullptr);
     if (page < 0) return;
     const int ps = a.cache.page_size, off = p & (ps - 1), n_kv = a.cache.n_kv;
-    for (int i = threadIdx.x; i < 2 * n_kv * kChunks; i += blockDim.x) {
-        const int c = i % kChunks, hh = i / kChunks, h = hh % n_kv, g = c / 8;
-        const uint8_t* block = kv4::block_of(a.cache, page, h);
-        uint32_t w;
-        float step, low;
-        if (hh < n_kv) {
-            w = reinterpret_cast<const uint32_t*>(block)[off * (D / 8) + kv4::k_word(c, D)];
-            const __half2 pr = reinterpret_cast<const __half2*>(block + kv4::k_params_off(ps, D))[off * kGroups + g];
-            step = __low2float(pr);
-            low = __high2float(pr);
-        } else {
-            const uint16_t* d = reinterpret_cast<const uint16_t*>(block + kv4::v_codes_off(ps, D)) + (off >> 1) * (D / 2) + (off & 1);
-            w = d[4 * c] | (static_cast<uint32_t>(d[4 * c + 2]) << 16);
-            const __half* pr = reinterpret_cast<const __half*>(block + kv4::v_params_off(ps, D)) +
-                               ((off >> 1) * kGroups + g) * 4 + (off & 1);
-            step = __half2float(pr[0]);
-            low = __half2float(pr[2]);
-        }
+    // this thread's eight dims of every head it takes
+    const int c = of_row % kChunks, g = c / 8, step_h = per_row / kChunks;
+    const long long head_bytes = kv4::block_bytes(ps, D);
+    const uint8_t* block = kv4::block_of(a.cache, page, of_row / kChunks);
+    const uint8_t* kc = block + off * (D / 2) + 4 * kv4::k_word(c, D);
+    const uint8_t* kp = block + kv4::k_params_off(ps, D) + 4 * (off * kGroups + g);
+    const uint8_t* vc = block + kv4::v_codes_off(ps, D) + (off >> 1) * D + 2 * (off & 1) + 8 * c;
+    const uint8_t* vp = block + kv4::v_params_off(ps, D) + ((off >> 1) * kGroups + g) * 8 + 2 * (off & 1);
+    bf16_t* ko = a.k + static_cast<long long>(row) * a.ld_k + 8 * c;
+    bf16_t* vo = a.v + static_cast<long long>(row) * a.ld_v + 8 * c;
+    auto out8 = [](uint32_t w, float step, float low) {
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)   // 2^23 + code, less 2^23; code * step is exact
             f[j] = fmaf(__uint_as_float(((w >> (4 * j)) & 15u) | 0x4B000000u) - 8388608.f, step, low);
-        bf16_t* o = hh < n_kv ? a.k + static_cast<long long>(row) * a.ld_k : a.v + static_cast<long long>(row) * a.ld_v;
-        *reinterpret_cast<uint4*>(o + h * D + 8 * c) = pack8(f);
+        return pack8(f);
+    };
+#pragma unroll 4
+    for (int h = of_row / kChunks; h < n_kv; h += step_h) {
+        const uint32_t kw = *reinterpret_cast<const uint32_t*>(kc);
+        const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(kp));
+        const uint32_t vw = *reinterpret_cast<const uint16_t*>(vc) | (static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(vc + 4)) << 16);
+        const float vs = __half2float(*reinterpret_cast<const __half*>(vp)), vl = __half2float(*reinterpret_cast<const __half*>(vp + 4));
+        *reinterpret_cast<uint4*>(ko + h * D) = out8(kw, kf.x, kf.y);
+        *reinterpret_cast<uint4*>(vo + h * D) = out8(vw, vs, vl);
+        kc += step_h * head_bytes;
+        kp += step_h * head_bytes;
+        vc += step_h * head_bytes;
+        vp += step_h * head_bytes;
     }
+}
+
+// Threads of a row: a CTA's four warps, or one where there are rows enough
+// to fill the SMs' warps all the same (its tables are then read once for
+// four times the work).
+int threads_per_row(int n_rows) { return n_rows >= kWarpRows ? 32 : kThreads; }
+
+template <class Args>
+cudaError_t launch(void (*kernel)(Args, int), const Args& a, cudaStream_t stream)
+{
+    if (a.batch.n_rows == 0) return cudaSuccess;
+    const int per_row = threads_per_row(a.batch.n_rows), rows = kThreads / per_row;
+    PdlLaunch l(dim3(static_cast<unsigned>((a.batch.n_rows + rows - 1) / rows)), kThreads, 0, stream);
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kernel, a, per_row);
+    note_launch();
+    return e;
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const AppendArgs& a, cudaStream_t stream)
 {
-    if (a.batch.n_rows == 0) return cudaSuccess;
-    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), kThreads, 0, stream);
-    const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_append_kernel<64>, a)
-                                                 : cudaLaunchKernelEx(&l.cfg, kv4_append_kernel<128>, a);
-    note_launch();
-    return e;
+    return a.cache.head_dim == 64 ? launch(kv4_append_kernel<64>, a, stream) : launch(kv4_append_kernel<128>, a, stream);
 }
 
 cudaError_t launch_kv4_read(const ReadArgs& a, cudaStream_t stream)
 {
-    if (a.batch.n_rows == 0) return cudaSuccess;
-    PdlLaunch l(dim3(static_cast<unsigned>(a.batch.n_rows)), kThreads, 0, stream);
-    const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<64>, a)
-                                                 : cudaLaunchKernelEx(&l.cfg, kv4_read_kernel<128>, a);
-    note_launch();
-    return e;
+    return a.cache.head_dim == 64 ? launch(kv4_read_kernel<64>, a, stream) : launch(kv4_read_kernel<128>, a, stream);
 }
 
 }  // namespace lora
