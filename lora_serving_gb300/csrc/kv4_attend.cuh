@@ -38,22 +38,33 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) { return as_u
 
 // Four pairs of codes of a word as fp16: pair i is (nibble i, nibble 4 + i).
 // A nibble OR-ed into the mantissa of 1024 is 1024 + code (low nibble of a
-// byte) or 1024 + 16 code (high nibble); both steps below are exact.
+// byte, even pairs) or 1024 + 16 code (high nibble, odd pairs).
 __device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t mask)
 {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xea;\n" : "=r"(r) : "r"(w), "r"(mask), "r"(0x64006400u));   // (w & mask) | 1024
     return r;
 }
-// Odd pairs keep their factor of 16 (the other operand of the product carries 1/16).
-__device__ __forceinline__ void codes_x16(uint32_t w, uint32_t (&c)[4])
+__device__ __forceinline__ void codes_1024(uint32_t w, uint32_t (&c)[4])
 {
-    const __half2 k = __float2half2_rn(-1024.f);
     const uint32_t y = w >> 8;
-    c[0] = as_u32(__hadd2(as_h2(pick(w, 0x000F000Fu)), k));
-    c[1] = as_u32(__hadd2(as_h2(pick(w, 0x00F000F0u)), k));
-    c[2] = as_u32(__hadd2(as_h2(pick(y, 0x000F000Fu)), k));
-    c[3] = as_u32(__hadd2(as_h2(pick(y, 0x00F000F0u)), k));
+    c[0] = pick(w, 0x000F000Fu);
+    c[1] = pick(w, 0x00F000F0u);
+    c[2] = pick(y, 0x000F000Fu);
+    c[3] = pick(y, 0x00F000F0u);
+}
+// kWords adjacent words of shared memory.
+template <int kWords>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[kWords])
+{
+    static_assert(kWords == 2 || kWords == 4, "words");
+    if (kWords == 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        w[0] = v.x; w[1] = v.y; w[kWords - 2] = v.z; w[kWords - 1] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        w[0] = v.x; w[1] = v.y;
+    }
 }
 // code * step + low, one fp16 rounding.
 __device__ __forceinline__ void values(uint32_t w, __half2 step, __half2 low, uint32_t (&v)[4])

@@ -3,7 +3,7 @@
 // once and the codes are unpacked in registers.
 //
 // Work.  A unit is (sequence, kv head): up to 8 NT query rows (rows x heads
-// of the group) over the sequence's tiles of 16 positions.  All units laid
+// of the group) over the sequence's tiles of 32 positions.  All units laid
 // end to end are cut into equal ranges, one per warp, whatever the lengths; a
 // unit counts kUnitCost tiles more than it has, for its start.  A warp that
 // has a whole unit writes its result; a unit cut by a range's end leaves
@@ -16,6 +16,8 @@
 //   S[16 positions][8 rows] = codes(K) q^T, per group of 64 dims, then
 //   score = sum_g step_g S_g + low_g sum(q_g)         (K is never rounded)
 //   O[dims][8 rows] += V^T P, V = code * step + low in fp16, P in fp16.
+// K's codes go in as 1024 + code, one instruction from the nibbles; the
+// product's accumulator starts at -1024 sum(q), which takes the 1024 out.
 // The K layout puts the 16 bytes that a lane feeds to its fragments side by
 // side, the V layout pairs two positions in one 32-bit operand, and P goes
 // from the first product's layout to the second's by a register transpose.
@@ -34,9 +36,10 @@ namespace {
 
 using namespace kv4;
 
-constexpr int kTile = 16;          // positions per tile
-constexpr int kUnitCost = 3;       // a unit's start (tables, q, the first copies), in tiles
-constexpr int kMinRange = 4;       // a warp's range, at least: a tile and the unit's start
+constexpr int kTile = 32;          // positions per tile: two halves of 16, the products' M
+constexpr int kHalf = 16;
+constexpr int kUnitCost = 2;       // a unit's start (tables, q, the first copies), in tiles
+constexpr int kMinRange = 3;       // a warp's range, at least: a tile and the unit's start
 constexpr float kSlack = 8.f;      // log2 by which a score may pass the running maximum
 constexpr float kLift = 7.f;       // weights carry 2^7: at most 2^15, and fp16 holds them down to 2^-31 of the largest
 
@@ -45,16 +48,21 @@ template <int D, int NT>
 struct Shape {
     static constexpr int kGroups = D / kGroup;
     static constexpr int kWords = D / 32;                 // words of a lane per position (K) and per pair (V)
-    static constexpr int kCodeBytes = kTile * D / 2;
-    static constexpr int kParamBytes = kTile * 4 * kGroups;
-    static constexpr int kStage = 2 * kCodeBytes + 2 * kParamBytes;
+    static constexpr int kCodeBytes = kHalf * D / 2;      // of K or V, of half a tile
+    static constexpr int kParamBytes = kHalf * 4 * kGroups;
+    // a stage: K codes, V codes, K params, V params, each of both halves
+    static constexpr int kVAt = 2 * kCodeBytes, kKpAt = 4 * kCodeBytes, kVpAt = kKpAt + 2 * kParamBytes;
+    static constexpr int kStage = kVpAt + 2 * kParamBytes;
     static constexpr int kRows = 8 * NT;
     static constexpr int kPartial = kRows * (D + 2);      // floats of a partial result: sums, maxima, sums of weights
+    // One row group's registers leave room for two CTAs on an SM, of six
+    // warps (168 registers; eight of 128 spill with heads of 128).
+    static constexpr int kCtas = NT == 1 ? 2 : 1;
+    static constexpr int kWarps = D == 128 && NT != 2 ? 6 : 8;
     // The ring is at least a partial result long: a warp's last one takes
     // the ring's place.
-    static constexpr int kStages = D == 64 || NT == 4 ? 8 : 4;
+    static constexpr int kStages = D == 128 && NT == 1 ? 3 : 4;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kWarps = D == 128 && NT == 4 ? 6 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * (kRing + 4 * kPartial) + 256;   // and the running sum of the sequences
     static_assert(kRing >= 4 * kPartial, "ring");
@@ -115,8 +123,13 @@ __device__ __forceinline__ float* partial(void* ws, int cta, int slot, int float
     return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kRecordBytes) + (static_cast<long long>(cta) * 2 + slot) * floats;
 }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_few_kernel(AttendArgs a, int few_rows)
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_few_kernel(AttendArgs a, int few_rows)
 {
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kGroups = S::kGroups, kWords = S::kWords, kStages = S::kStages, kWarps = S::kWarps;
@@ -152,42 +165,48 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
         const int32_t* table = a.batch.block_table + static_cast<long long>(u.s) * a.batch.ld_table;
 
         // ---- the ring: tiles t0 + i
-        const int n_mine = t1 - t0;
-        unsigned has = 0;   // stages that hold a tile
-        auto page_at = [&](int i) -> int {
-            const int pos = (tile0 + t0 + i) * kTile;
-            if (i >= n_mine || pos >= u.q.ctx) return -1;
-            return __ldg(table + (pos >> a.cache.page_shift));
-        };
-        int page_next = page_at(0);
+        const int n_mine = t1 - t0, pos0 = (tile0 + t0) * kTile;
+        const uint8_t* head_pages = a.cache.pages + static_cast<long long>(u.h) * block_bytes(ps, D);
+        const bool split = ps < kTile;   // a tile is two pages
+        unsigned has = 0;                // stages' halves that hold positions
+        auto page_at = [&](int pos) -> int { return pos < u.q.ctx ? __ldg(table + (pos >> a.cache.page_shift)) : -1; };
+        int next0 = n_mine > 0 ? page_at(pos0) : -1, next1 = n_mine > 0 && split ? page_at(pos0 + kHalf) : -1;
         auto issue = [&](int i) {
-            const int page = page_next, st = i % kStages;
-            page_next = page_at(i + 1);
-            has &= ~(1u << st);
+            const int pos = pos0 + i * kTile, st = i % kStages;
+            const int page0 = next0, page1 = split ? next1 : page0;
+            if (i + 1 < n_mine) {
+                next0 = page_at(pos + kTile);
+                if (split) next1 = page_at(pos + kTile + kHalf);
+            }
+            has &= ~(3u << (2 * st));
             if (i < n_mine) {
-                const int pos = (tile0 + t0 + i) * kTile;
-                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages)) {
-                    has |= 1u << st;
-                    const int off = pos & (ps - 1);
-                    const uint8_t* block = block_of(a.cache, page, u.h);
-                    uint8_t* dst = ring + st * S::kStage;
-                    const uint8_t* kc = block + off * (D / 2);
-                    const uint8_t* vc = kc + v_codes_off(ps, D);
+                const bool ok0 = static_cast<unsigned>(page0) < static_cast<unsigned>(a.cache.n_pages);
+                const bool ok1 = static_cast<unsigned>(page1) < static_cast<unsigned>(a.cache.n_pages) && pos + kHalf < u.q.ctx;
+                has |= (ok0 ? 1u : 0u) << (2 * st) | (ok1 ? 2u : 0u) << (2 * st);
+                if (lane == 0 && ((!ok0 && pos < u.q.ctx) || (!ok1 && pos + kHalf < u.q.ctx))) flag(a.status, LORA_DEV_BAD_PAGE);
+                const int off0 = pos & (ps - 1), off1 = (pos + kHalf) & (ps - 1);
+                const uint8_t* b0 = head_pages + static_cast<long long>(page0) * a.cache.page_stride;
+                const uint8_t* b1 = head_pages + static_cast<long long>(page1) * a.cache.page_stride;
+                const uint32_t dst = tc::smem_u32(ring + st * S::kStage) + 16 * lane;
+                const uint8_t* s0 = b0 + off0 * (D / 2) + 16 * lane;
+                const uint8_t* s1 = b1 + off1 * (D / 2) + 16 * lane;
 #pragma unroll
-                    for (int c = 0; c < S::kCodeBytes / 512; ++c) {
-                        const int o = 512 * c + 16 * lane;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst + o)), "l"(kc + o) : "memory");
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(dst + S::kCodeBytes + o)), "l"(vc + o) : "memory");
+                for (int c = 0; c < S::kCodeBytes; c += 512) {
+                    if (ok0) {
+                        copy16(dst + c, s0 + c);
+                        copy16(dst + S::kVAt + c, s0 + v_codes_off(ps, D) + c);
                     }
-                    const int pl = lane & 15;
-                    if (pl < S::kParamBytes / 16) {
-                        const int v = lane >> 4;
-                        const uint8_t* src = block + (v ? v_params_off(ps, D) : k_params_off(ps, D)) + off * 4 * kGroups + 16 * pl;
-                        uint8_t* d = dst + 2 * S::kCodeBytes + v * S::kParamBytes + 16 * pl;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(d)), "l"(src) : "memory");
+                    if (ok1) {
+                        copy16(dst + S::kCodeBytes + c, s1 + c);
+                        copy16(dst + S::kVAt + S::kCodeBytes + c, s1 + v_codes_off(ps, D) + c);
                     }
-                } else if (pos < u.q.ctx && lane == 0) {
-                    flag(a.status, LORA_DEV_BAD_PAGE);
+                }
+                // params: eight lanes to a half of K's, then of V's
+                const int pl = lane & 7, second = (lane >> 3) & 1;
+                if (pl < S::kParamBytes / 16 && (second ? ok1 : ok0)) {
+                    const uint8_t* src = (second ? b1 + off1 * 4 * kGroups : b0 + off0 * 4 * kGroups) +
+                                         (lane & 16 ? v_params_off(ps, D) : k_params_off(ps, D)) + 16 * pl;
+                    copy16(tc::smem_u32(ring + st * S::kStage) + S::kKpAt + (lane >> 3) * S::kParamBytes + 16 * pl, src);
                 }
             }
             asm volatile("cp.async.commit_group;\n" ::: "memory");
@@ -197,7 +216,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
 
         // ---- q as fragments: row n = 8 nt + g, dims 32 w + 8 t + (0..7)
         uint32_t qf[NT][kWords][4];     // pairs (dims e, e + 4); odd pairs carry 1/16
-        float mult[NT][2], qsum[NT][kGroups][2];   // of rows 2t, 2t + 1
+        float mult[NT][2], qsum[NT][kGroups][2], qoff[NT][kGroups][2];   // of rows 2t, 2t + 1
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int r = 8 * nt + g;
@@ -218,9 +237,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
             const int fe = min(261 - e, 253);
             const float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
             const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
-            float sum[kGroups];
+            // sums of the fp16 values as the product takes them: of q, and of 1024 times the operand
+            float sum[kGroups], ofs[kGroups];
 #pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) sum[gr] = 0.f;
+            for (int gr = 0; gr < kGroups; ++gr) sum[gr] = ofs[gr] = 0.f;
 #pragma unroll
             for (int w = 0; w < kWords; ++w) {
                 const float f[8] = {bf16_lo(raw[w].x) * up, bf16_hi(raw[w].x) * up, bf16_lo(raw[w].y) * up, bf16_hi(raw[w].y) * up,
@@ -229,20 +249,27 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
                 for (int i = 0; i < 4; ++i) {
                     const float k = (i & 1) ? 1.f / 16 : 1.f;
                     qf[nt][w][i] = pack_f16x2(f[i] * k, f[i + 4] * k);
-                    sum[w / 2] += f[i] + f[i + 4];
+                    const float2 h = __half22float2(as_h2(qf[nt][w][i]));
+                    sum[w / 2] = fmaf(h.x + h.y, (i & 1) ? 16.f : 1.f, sum[w / 2]);
+                    ofs[w / 2] = fmaf(h.x + h.y, -1024.f, ofs[w / 2]);
                 }
             }
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
                 sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 1);
                 sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 2);
+                ofs[gr] += __shfl_xor_sync(0xFFFFFFFFu, ofs[gr], 1);
+                ofs[gr] += __shfl_xor_sync(0xFFFFFFFFu, ofs[gr], 2);
             }
             const float m = a.scale * 1.4426950408889634f * down;   // scores in log2
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 mult[nt][c] = __shfl_sync(0xFFFFFFFFu, m, 8 * t + 4 * c);
 #pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr) qsum[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, sum[gr], 8 * t + 4 * c);
+                for (int gr = 0; gr < kGroups; ++gr) {
+                    qsum[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, sum[gr], 8 * t + 4 * c);
+                    qoff[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, ofs[gr], 8 * t + 4 * c);
+                }
             }
         }
         int last[NT][2];   // position of rows 2t, 2t + 1: the last one they see
@@ -268,57 +295,51 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
             __syncwarp();
             const int st = i % kStages;
             const uint8_t* src = ring + st * S::kStage;
-            const bool live = (has >> st) & 1u;
+            const unsigned live = (has >> (2 * st)) & 3u;   // its halves
             issue(i + kStages - 1);
             if (!live) continue;
-            const int j0 = (tile0 + t0 + i) * kTile;   // the tile's first position
+            const int j0 = pos0 + i * kTile;   // the tile's first position
             // every row sees every position?
-            const bool inner = j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + u.q.n - 1 - a.window);
+            const bool inner = live == 3u && j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + u.q.n - 1 - a.window);
 
             // ---- scores
-            float sc[NT][4];
+            float sc[2][NT][4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
-            uint32_t kw[2][kWords];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint8_t* p = src + (g + 8 * r) * (D / 2) + t * (4 * kWords);
-                if (kWords == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(p);
-                    kw[r][0] = v.x; kw[r][1] = v.y; kw[r][kWords - 2] = v.z; kw[r][kWords - 1] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p);
-                    kw[r][0] = v.x; kw[r][1] = v.y;
-                }
-            }
-            const __half2* kp = reinterpret_cast<const __half2*>(src + 2 * S::kCodeBytes);
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) {
-                float d[NT][4];
+            for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) d[nt][c] = 0.f;
+                    for (int c = 0; c < 4; ++c) sc[hf][nt][c] = 0.f;
+                uint32_t kw[2][kWords];
 #pragma unroll
-                for (int w = 2 * gr; w < 2 * gr + 2; ++w) {
-                    uint32_t lo[4], hi[4];
-                    codes_x16(kw[0][w], lo);
-                    codes_x16(kw[1][w], hi);
+                for (int r = 0; r < 2; ++r) load_words<kWords>(src + hf * S::kCodeBytes + (g + 8 * r) * (D / 2) + t * (4 * kWords), kw[r]);
+                const __half2* kp = reinterpret_cast<const __half2*>(src + S::kKpAt + hf * S::kParamBytes);
+#pragma unroll
+                for (int gr = 0; gr < kGroups; ++gr) {
+                    float d[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) d[nt][c] = qoff[nt][gr][c & 1];
+#pragma unroll
+                    for (int w = 2 * gr; w < 2 * gr + 2; ++w) {
+                        uint32_t lo[4], hi[4];
+                        codes_1024(kw[0][w], lo);
+                        codes_1024(kw[1][w], hi);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma_f16(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1]);
+                            mma_f16(d[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][w][2], qf[nt][w][3]);
+                        }
+                    }
+                    const float2 k0 = __half22float2(kp[g * kGroups + gr]), k1 = __half22float2(kp[(g + 8) * kGroups + gr]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1]);
-                        mma_f16(d[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][w][2], qf[nt][w][3]);
+                        sc[hf][nt][0] = fmaf(k0.x, d[nt][0], fmaf(k0.y, qsum[nt][gr][0], sc[hf][nt][0]));
+                        sc[hf][nt][1] = fmaf(k0.x, d[nt][1], fmaf(k0.y, qsum[nt][gr][1], sc[hf][nt][1]));
+                        sc[hf][nt][2] = fmaf(k1.x, d[nt][2], fmaf(k1.y, qsum[nt][gr][0], sc[hf][nt][2]));
+                        sc[hf][nt][3] = fmaf(k1.x, d[nt][3], fmaf(k1.y, qsum[nt][gr][1], sc[hf][nt][3]));
                     }
-                }
-                const float2 p0f = __half22float2(kp[g * kGroups + gr]), p1f = __half22float2(kp[(g + 8) * kGroups + gr]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sc[nt][0] = fmaf(p0f.x, d[nt][0], fmaf(p0f.y, qsum[nt][gr][0], sc[nt][0]));
-                    sc[nt][1] = fmaf(p0f.x, d[nt][1], fmaf(p0f.y, qsum[nt][gr][1], sc[nt][1]));
-                    sc[nt][2] = fmaf(p1f.x, d[nt][2], fmaf(p1f.y, qsum[nt][gr][0], sc[nt][2]));
-                    sc[nt][3] = fmaf(p1f.x, d[nt][3], fmaf(p1f.y, qsum[nt][gr][1], sc[nt][3]));
                 }
             }
             bool up = false;
@@ -326,19 +347,22 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    sc[nt][c] *= mult[nt][c & 1];
-                    if (!inner) {
-                        const int j = j0 + g + 8 * (c >> 1), p = last[nt][c & 1];
-                        if (j > p || (a.window > 0 && j <= p - a.window)) sc[nt][c] = -inf;
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        sc[hf][nt][c] *= mult[nt][c & 1];
+                        if (!inner) {
+                            const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[nt][c & 1];
+                            if (j > p || (a.window > 0 && j <= p - a.window) || !((live >> hf) & 1u)) sc[hf][nt][c] = -inf;
+                        }
                     }
-                    up |= sc[nt][c] > top[nt][c & 1] + kSlack;
+                    up |= fmaxf(sc[0][nt][c], sc[1][nt][c]) > top[nt][c & 1] + kSlack;
                 }
             if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float m = fmaxf(sc[nt][c], sc[nt][c + 2]);
+                        float m = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][c + 2]), fmaxf(sc[1][nt][c], sc[1][nt][c + 2]));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
@@ -353,90 +377,82 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
                         }
                     }
             }
-            uint32_t pf[NT][2];
+            uint32_t pf[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
+                float off[2];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float m = top[nt][c & 1];
-                    w[c] = ex2(sc[nt][c] - (m == -inf ? 0.f : m - kLift));
-                    sum[nt][c & 1] += w[c];
+                for (int c = 0; c < 2; ++c) off[c] = top[nt][c] == -inf ? 0.f : top[nt][c] - kLift;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    float w[4];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) w[c] = ex2(sc[hf][nt][c] - off[c & 1]);
+                    sum[nt][0] += w[0] + w[2];
+                    sum[nt][1] += w[1] + w[3];
+                    pf[hf][nt][0] = transpose8(pack_f16x2(w[0], w[1]));
+                    pf[hf][nt][1] = transpose8(pack_f16x2(w[2], w[3]));
                 }
-                pf[nt][0] = transpose8(pack_f16x2(w[0], w[1]));
-                pf[nt][1] = transpose8(pack_f16x2(w[2], w[3]));
             }
 
-            // ---- values: dims g * D/8 + 4 i + e of positions (2t, 2t+1) and (2t+8, 2t+9)
+            // ---- values: dims g * D/8 + 4 w + e of positions (2t, 2t+1) and (2t+8, 2t+9) of each half
             const int vg = g * (D / 8) / kGroup;
-            uint32_t step[2], low[2];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint2 v = *reinterpret_cast<const uint2*>(src + 2 * S::kCodeBytes + S::kParamBytes + ((t + 4 * r) * kGroups + vg) * 8);
-                step[r] = v.x;
-                low[r] = v.y;
-            }
             bool poison = false;
-            if (!inner) {
-                // positions that no row sees count as zeros whatever they hold
-                const int j_end = u.q.ctx, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                uint32_t step[2], low[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int j = j0 + 2 * t + 8 * r;
-                    const uint32_t keep = (j >= j_begin && j < j_end ? 0xFFFFu : 0u) | (j + 1 >= j_begin && j + 1 < j_end ? 0xFFFF0000u : 0u);
-                    step[r] &= keep;
-                    low[r] &= keep;
-                    poison |= not_finite(step[r]) || not_finite(low[r]);
+                    const uint2 v = *reinterpret_cast<const uint2*>(src + S::kVpAt + hf * S::kParamBytes + ((t + 4 * r) * kGroups + vg) * 8);
+                    step[r] = v.x;
+                    low[r] = v.y;
                 }
-                // a NaN that some rows see and others do not: taken out here, put back below for those that see it
-                if (__any_sync(0xFFFFFFFFu, poison)) {
-                    poison = true;
+                if (!inner) {
+                    // positions that no row sees count as zeros whatever they hold, and a value that is
+                    // not finite is taken out here and put back below for the rows that see it
+                    const int j_end = (live >> hf) & 1u ? u.q.ctx : 0, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
+                        const int j = j0 + kHalf * hf + 2 * t + 8 * r;
+                        const uint32_t keep = (j >= j_begin && j < j_end ? 0xFFFFu : 0u) | (j + 1 >= j_begin && j + 1 < j_end ? 0xFFFF0000u : 0u);
+                        step[r] &= keep;
+                        low[r] &= keep;
                         uint32_t bad = 0;
                         if (not_finite(step[r] & 0xFFFFu) || not_finite(low[r] & 0xFFFFu)) bad |= 0xFFFFu;
                         if (not_finite(step[r] & 0xFFFF0000u) || not_finite(low[r] & 0xFFFF0000u)) bad |= 0xFFFF0000u;
                         step[r] &= ~bad;
                         low[r] &= ~bad;
+                        poison |= bad != 0;
+                    }
+                }
+                uint32_t vw[2][kWords];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) load_words<kWords>(src + S::kVAt + hf * S::kCodeBytes + (t + 4 * r) * D + g * (4 * kWords), vw[r]);
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    uint32_t a0[4], a1[4];
+                    values(vw[0][w], as_h2(step[0]), as_h2(low[0]), a0);
+                    values(vw[1][w], as_h2(step[1]), as_h2(low[1]), a1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[hf][nt][0], pf[hf][nt][1]);
+                        mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[hf][nt][0], pf[hf][nt][1]);
                     }
                 }
             }
-            uint32_t vw[2][kWords];
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const uint8_t* p = src + S::kCodeBytes + (t + 4 * r) * D + g * (4 * kWords);
-                if (kWords == 4) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(p);
-                    vw[r][0] = v.x; vw[r][1] = v.y; vw[r][kWords - 2] = v.z; vw[r][kWords - 1] = v.w;
-                } else {
-                    const uint2 v = *reinterpret_cast<const uint2*>(p);
-                    vw[r][0] = v.x; vw[r][1] = v.y;
-                }
-            }
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                uint32_t a0[4], a1[4];
-                values(vw[0][w], as_h2(step[0]), as_h2(low[0]), a0);
-                values(vw[1][w], as_h2(step[1]), as_h2(low[1]), a1);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[nt][0], pf[nt][1]);
-                    mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[nt][0], pf[nt][1]);
-                }
-            }
-            if (poison) {
-                const __half* vp = reinterpret_cast<const __half*>(src + 2 * S::kCodeBytes + S::kParamBytes);
+            if (!inner && __any_sync(0xFFFFFFFFu, poison)) {
                 for (int k = 0; k < kTile; ++k) {
-                    const __half* p = vp + ((k >> 1) * kGroups + vg) * 4 + (k & 1);
-                    const float nan = __half2float(p[0]) * 0.f + __half2float(p[2]) * 0.f;   // 0 where both are finite
-                    if (nan == 0.f) continue;
+                    if (!((live >> (k / kHalf)) & 1u)) continue;
                     const int j = j0 + k;
+                    const __half* p = reinterpret_cast<const __half*>(src + S::kVpAt + (k / kHalf) * S::kParamBytes) +
+                                      (((k % kHalf) >> 1) * kGroups + vg) * 4 + (k & 1);
+                    const float nan = __half2float(p[0]) * 0.f + __half2float(p[2]) * 0.f;   // 0 where both are finite
+                    if (nan == 0.f || j >= u.q.ctx) continue;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            const int p = last[nt][c];
-                            if (j > p || (a.window > 0 && j <= p - a.window) || j >= u.q.ctx) continue;
+                            if (j > last[nt][c] || (a.window > 0 && j <= last[nt][c] - a.window)) continue;
 #pragma unroll
                             for (int m = 0; m < D / 16; ++m) {
                                 acc[m][nt][c] += nan;
@@ -449,6 +465,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, NT == 1 ? 2 : 1) kv4_f
 
         // ---- the unit's rows, or a partial result
         const bool whole = t0 == 0 && t1 == u.len - kUnitCost;
+        asm volatile("cp.async.wait_all;\n" ::: "memory");
         __syncwarp();   // every lane is done with the ring
         float* slot = t0 > 0 ? first_slot + warp * S::kPartial : reinterpret_cast<float*>(ring);
         if (!whole && lane == 0) pieces[warp][t0 > 0 ? 0 : 1] = Piece{u.u0, t1 == u.len - kUnitCost, u.h, u.q.row0, rows, u.u0 + u.len};
@@ -588,7 +605,7 @@ cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    const int ctas = std::min(kMaxCtas, device_sms() * (NT == 1 ? 2 : 1));
+    const int ctas = std::min(kMaxCtas, device_sms() * S::kCtas);
     PdlLaunch l(dim3(ctas), S::kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
     e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows);
     if (e != cudaSuccess) return e;
