@@ -58,10 +58,10 @@ struct Shape {
     // One row group's registers leave room for two CTAs on an SM, of six
     // warps (168 registers; eight of 128 spill with heads of 128).
     static constexpr int kCtas = NT == 1 ? 2 : 1;
-    static constexpr int kWarps = D == 128 && NT != 2 ? 6 : 8;
+    static constexpr int kWarps = D == 128 && NT == 4 ? 6 : 8;
     // The ring is at least a partial result long: a warp's last one takes
     // the ring's place.
-    static constexpr int kStages = D == 128 && NT == 1 ? 3 : 4;
+    static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
     static constexpr int kRing = kStages * kStage;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * (kRing + 4 * kPartial) + 256;   // and the running sum of the sequences
@@ -302,14 +302,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
             // every row sees every position?
             const bool inner = live == 3u && j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + u.q.n - 1 - a.window);
 
-            // ---- scores
-            float sc[2][NT][4];
+            const int vg = g * (D / 8) / kGroup;
+            bool poison = false;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
+                // ---- scores
+                const bool there = (live >> hf) & 1u;
+                float sc[NT][4];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) sc[hf][nt][c] = 0.f;
+                    for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
                 uint32_t kw[2][kWords];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) load_words<kWords>(src + hf * S::kCodeBytes + (g + 8 * r) * (D / 2) + t * (4 * kWords), kw[r]);
@@ -335,71 +338,58 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
                     const float2 k0 = __half22float2(kp[g * kGroups + gr]), k1 = __half22float2(kp[(g + 8) * kGroups + gr]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        sc[hf][nt][0] = fmaf(k0.x, d[nt][0], fmaf(k0.y, qsum[nt][gr][0], sc[hf][nt][0]));
-                        sc[hf][nt][1] = fmaf(k0.x, d[nt][1], fmaf(k0.y, qsum[nt][gr][1], sc[hf][nt][1]));
-                        sc[hf][nt][2] = fmaf(k1.x, d[nt][2], fmaf(k1.y, qsum[nt][gr][0], sc[hf][nt][2]));
-                        sc[hf][nt][3] = fmaf(k1.x, d[nt][3], fmaf(k1.y, qsum[nt][gr][1], sc[hf][nt][3]));
+                        sc[nt][0] = fmaf(k0.x, d[nt][0], fmaf(k0.y, qsum[nt][gr][0], sc[nt][0]));
+                        sc[nt][1] = fmaf(k0.x, d[nt][1], fmaf(k0.y, qsum[nt][gr][1], sc[nt][1]));
+                        sc[nt][2] = fmaf(k1.x, d[nt][2], fmaf(k1.y, qsum[nt][gr][0], sc[nt][2]));
+                        sc[nt][3] = fmaf(k1.x, d[nt][3], fmaf(k1.y, qsum[nt][gr][1], sc[nt][3]));
                     }
                 }
-            }
-            bool up = false;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        sc[hf][nt][c] *= mult[nt][c & 1];
-                        if (!inner) {
-                            const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[nt][c & 1];
-                            if (j > p || (a.window > 0 && j <= p - a.window) || !((live >> hf) & 1u)) sc[hf][nt][c] = -inf;
-                        }
-                    }
-                    up |= fmaxf(sc[0][nt][c], sc[1][nt][c]) > top[nt][c & 1] + kSlack;
-                }
-            if (__any_sync(0xFFFFFFFFu, up)) {
+                bool up = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float m = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][c + 2]), fmaxf(sc[1][nt][c], sc[1][nt][c + 2]));
-                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                        m = fmaxf(m, top[nt][c]);
-                        const float keep = m == -inf ? 1.f : ex2(top[nt][c] - m);
-                        top[nt][c] = m;
-                        sum[nt][c] *= keep;
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            acc[k][nt][c] *= keep;
-                            acc[k][nt][c + 2] *= keep;
+                    for (int c = 0; c < 4; ++c) {
+                        sc[nt][c] *= mult[nt][c & 1];
+                        if (!inner) {
+                            const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[nt][c & 1];
+                            if (j > p || (a.window > 0 && j <= p - a.window) || !there) sc[nt][c] = -inf;
                         }
+                        up |= sc[nt][c] > top[nt][c & 1] + kSlack;
                     }
-            }
-            uint32_t pf[2][NT][2];
+                if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float off[2];
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) off[c] = top[nt][c] == -inf ? 0.f : top[nt][c] - kLift;
+                        for (int c = 0; c < 2; ++c) {
+                            float m = fmaxf(sc[nt][c], sc[nt][c + 2]);
+                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                            m = fmaxf(m, top[nt][c]);
+                            const float keep = m == -inf ? 1.f : ex2(top[nt][c] - m);
+                            top[nt][c] = m;
+                            sum[nt][c] *= keep;
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
+                            for (int k = 0; k < D / 16; ++k) {
+                                acc[k][nt][c] *= keep;
+                                acc[k][nt][c + 2] *= keep;
+                            }
+                        }
+                }
+                uint32_t pf[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
                     float w[4];
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) w[c] = ex2(sc[hf][nt][c] - off[c & 1]);
-                    sum[nt][0] += w[0] + w[2];
-                    sum[nt][1] += w[1] + w[3];
-                    pf[hf][nt][0] = transpose8(pack_f16x2(w[0], w[1]));
-                    pf[hf][nt][1] = transpose8(pack_f16x2(w[2], w[3]));
+                    for (int c = 0; c < 4; ++c) {
+                        w[c] = ex2(sc[nt][c] - (top[nt][c & 1] == -inf ? 0.f : top[nt][c & 1] - kLift));
+                        sum[nt][c & 1] += w[c];
+                    }
+                    pf[nt][0] = transpose8(pack_f16x2(w[0], w[1]));
+                    pf[nt][1] = transpose8(pack_f16x2(w[2], w[3]));
                 }
-            }
 
-            // ---- values: dims g * D/8 + 4 w + e of positions (2t, 2t+1) and (2t+8, 2t+9) of each half
-            const int vg = g * (D / 8) / kGroup;
-            bool poison = false;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
+                // ---- values: dims g * D/8 + 4 w + e of positions (2t, 2t+1) and (2t+8, 2t+9)
                 uint32_t step[2], low[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
@@ -410,7 +400,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
                 if (!inner) {
                     // positions that no row sees count as zeros whatever they hold, and a value that is
                     // not finite is taken out here and put back below for the rows that see it
-                    const int j_end = (live >> hf) & 1u ? u.q.ctx : 0, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
+                    const int j_end = there ? u.q.ctx : 0, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
                         const int j = j0 + kHalf * hf + 2 * t + 8 * r;
@@ -435,8 +425,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
                     values(vw[1][w], as_h2(step[1]), as_h2(low[1]), a1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[hf][nt][0], pf[hf][nt][1]);
-                        mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[hf][nt][0], pf[hf][nt][1]);
+                        mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[nt][0], pf[nt][1]);
+                        mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[nt][0], pf[nt][1]);
                     }
                 }
             }
