@@ -18,6 +18,7 @@
 // order 0 4 1 5 2 6 3 7; Q is laid out in the same order instead of undoing
 // it, a sum over dims not minding.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4_attend.cuh"
 #include "tc_common.cuh"
@@ -31,7 +32,12 @@ using namespace kv4;
 constexpr int kRowsPerTile = 128, kRowsPerItem = 256;
 constexpr int kTok = 128;                  // positions of a tile
 constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackWarps;
-constexpr int kWarps = kMmaWarp + 1, kThreads = 32 * kWarps;
+constexpr int kWarps = 16, kThreads = 32 * kWarps;   // the MMA warp's three neighbours only scan
+// Registers: 128 a thread at launch; the softmax warps, which hold a row's
+// weights and the scores on their way, take what the others give up:
+// 256 * 184 + 128 * 96 + 128 * 48 = 512 * 128.
+constexpr int kSoftRegs = 184, kUnpackRegs = 96, kMmaRegs = 48;
+static_assert(2 * kSoftRegs + kUnpackRegs + kMmaRegs <= 4 * 128, "registers");
 constexpr float kSlack = 8.f, kLift = 7.f; // as in the kernel for few rows
 constexpr uint32_t kTmemCols = 512;
 
@@ -71,6 +77,85 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r)
         "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// 16 columns of this warp's lanes, without waiting for them ...
+__device__ __forceinline__ void tmem_ld16_start(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+// ... and the wait for every load so far; the registers pass through it, so that no use moves ahead of it.
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld32_start(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
+}
+
+// tc::mbar_wait in line: a call would cost the warps with a register budget
+// of their own their registers.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity)
+{
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = tc::gtime();
+    while (!tc::mbar_try_wait_suspend(bar, parity))
+        if (tc::gtime() - t0 > tc::kTimeoutNs) return false;
+    return true;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+          "l"(*reinterpret_cast<unsigned long long*>(&c)));
+    return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;\n"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+    return *reinterpret_cast<float2*>(&d);
+}
+
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 struct Barriers {
@@ -165,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
         };
 
         if (warp < kSoftWarps) {
+            more_registers<kSoftRegs>();
             const int x = warp >> 2, r = x * kRowsPerTile + (tid & 127);   // row of the item
             // ---- Q: one row to a thread, taken to fp16 with a power of two, into the swizzled tile
             const int row = block0 + r;
@@ -211,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 uint32_t sick = 0;   // groups of dims in which this row sees a value that is not finite
                 bool ok = true;
                 for (int j = 0; j < n_tiles; ++j) {
-                    if (!tc::mbar_wait(&bar.s_full[x], j & 1)) { ok = false; break; }
+                    if (!wait_for(&bar.s_full[x], j & 1)) { ok = false; break; }
                     tc::tc_fence_after();
                     const uint4 hid4 = notes.hidden[j & 3];
                     const uint32_t hid[4] = {hid4.x, hid4.y, hid4.z, hid4.w};
@@ -219,60 +305,68 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     const int c0 = (tile0 + j) * kTok;
                     // this row sees columns [c_lo, c_hi) of the tile
                     const int c_hi = pos + 1 - c0, c_lo = a.window > 0 ? pos + 1 - a.window - c0 : 0;
-                    float m = -inf;
+                    // Weights against the running maximum as it stands; where a score passes it by 2^8
+                    // (always in the first tile) the maximum moves, O is rescaled and they are taken again.
+                    uint32_t p[kTok / 2];
+                    float2 part[2];
+                    for (;;) {
+                        const float off = top == -inf ? 0.f : kLift - top;
+                        const float2 mult2 = make_float2(mult, mult), off2 = make_float2(off, off);
+                        float m[4] = {-inf, -inf, -inf, -inf};
+                        part[0] = part[1] = make_float2(0.f, 0.f);
+                        auto weigh = [&](auto masked) {
+                            constexpr bool kMasked = decltype(masked)::value;
+                            uint32_t v[2][32];
+                            tmem_ld32_start(ts, v[0]);
 #pragma unroll
-                    for (int c = 0; c < kTok; c += 32) {
-                        float v[32];
-                        tc::tmem_ld32(ts + c, v);
-                        if (!all) {
-                            const uint32_t see = bits_in(c_lo - c, c_hi - c) & ~hid[c >> 5];
+                            for (int c = 0; c < kTok / 32; ++c) {
+                                uint32_t(&w)[32] = v[c & 1];
+                                tmem_ld32_wait(w);
+                                if (c + 1 < kTok / 32) tmem_ld32_start(ts + 32 * (c + 1), v[(c + 1) & 1]);
+                                const uint32_t see = kMasked ? bits_in(c_lo - 32 * c, c_hi - 32 * c) & ~hid[c] : 0u;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((see >> e) & 1u)) v[e] = -inf;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) m = fmaxf(m, v[e]);
-                    }
-                    m *= mult;
-                    if (m != m) m = -inf;   // 0 * -inf: nothing seen, or no scale
-                    if (__any_sync(0xFFFFFFFFu, m > top + kSlack)) {
-                        const float next = fmaxf(m, top);
+                                for (int e = 0; e < 32; e += 2) {
+                                    float2 x2 = make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+                                    if (kMasked) {
+                                        if (!((see >> e) & 1u)) x2.x = -inf;
+                                        if (!((see >> e) & 2u)) x2.y = -inf;
+                                    }
+                                    m[(e >> 1) & 3] = fmaxf(m[(e >> 1) & 3], fmaxf(x2.x, x2.y));
+                                    float2 y = fma2(x2, mult2, off2);
+                                    y.x = ex2(y.x);
+                                    y.y = ex2(y.y);
+                                    if (kMasked) {   // 0 * -inf with a scale of 0
+                                        if (!((see >> e) & 1u)) y.x = 0.f;
+                                        if (!((see >> e) & 2u)) y.y = 0.f;
+                                    }
+                                    part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], y);
+                                    p[16 * c + (e >> 1)] = pack_f16x2(y.x, y.y);
+                                }
+                            }
+                        };
+                        if (all) weigh(std::false_type{}); else weigh(std::true_type{});
+                        float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mult;
+                        if (high != high) high = -inf;   // 0 * -inf: nothing seen
+                        if (!__any_sync(0xFFFFFFFFu, high > top + kSlack)) break;
+                        const float next = fmaxf(high, top);
                         const float keep = next == -inf ? 1.f : ex2(top - next);
                         top = next;
                         sum *= keep;
                         if (j > 0) {
 #pragma unroll
                             for (int c = 0; c < D; c += 16) {
-                                float v[16];
-                                tc::tmem_ld16(to + c, v);
                                 uint32_t w[16];
+                                tmem_ld16_start(to + c, w);
+                                tmem_ld16_wait(w);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(v[e] * keep);
+                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
                                 tmem_st16(to + c, w);
                             }
                         }
                     }
-                    const float off = top == -inf ? 0.f : kLift - top;
+                    sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
 #pragma unroll
-                    for (int c = 0; c < kTok; c += 32) {
-                        float v[32];
-                        tc::tmem_ld32(ts + c, v);
-                        uint32_t p[16];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = ex2(fmaf(v[e], mult, off));
-                        if (!all) {
-                            const uint32_t see = bits_in(c_lo - c, c_hi - c) & ~hid[c >> 5];
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (!((see >> e) & 1u)) v[e] = 0.f;
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            sum += v[2 * e] + v[2 * e + 1];
-                            p[e] = pack_f16x2(v[2 * e], v[2 * e + 1]);
-                        }
-                        tmem_st16(ts + (c >> 1), p);
-                    }
+                    for (int c = 0; c < kTok / 2; c += 16) tmem_st16(ts + c, p + c);
                     if (notes.any_sick[j & 3] && !inner(j, p0, p1)) {
                         for (int g = 0; g < kGroups; ++g)
                             for (int c = 0; c < kTok; c += 32)
@@ -284,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     if (lane == 0) tc::mbar_arrive(&bar.p_full[x]);
                 }
                 // ---- the result
-                if (ok) ok = tc::mbar_wait(&bar.o_full[x], 0);
+                if (ok) ok = wait_for(&bar.o_full[x], 0);
                 tc::tc_fence_after();
                 if (ok) {
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -308,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             }
         } else if (warp < kMmaWarp) {
             // ---- unpacking: K one position to a thread, V eight positions x 16 dims
+            fewer_registers<kUnpackRegs>();
             const int u = tid - 32 * kSoftWarps;
             const int tok8 = u & 15, quad = u >> 4;            // quad: 16 dims of V
             const bool has_v = quad < D / 16;
@@ -385,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             bool ok = true;
             for (int j = 0; j < n_tiles && ok; ++j) {
                 const int st = j & 1;
-                if (j >= 2) ok = tc::mbar_wait(&bar.k_free[st], ((j >> 1) & 1) ^ 1);
+                if (j >= 2) ok = wait_for(&bar.k_free[st], ((j >> 1) & 1) ^ 1);
                 uint8_t* kd = k_s + st * S::kKTile + u * 128;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
@@ -422,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 if (lane == 0) tc::mbar_arrive(&bar.k_full[st]);
                 if (j + 1 < n_tiles) load_k(j + 1);
 
-                if (ok && j >= 2) ok = tc::mbar_wait(&bar.v_free[st], ((j >> 1) & 1) ^ 1);
+                if (ok && j >= 2) ok = wait_for(&bar.v_free[st], ((j >> 1) & 1) ^ 1);
                 if (has_v) {
                     uint8_t* vd = v_s + st * S::kVTile + (tok8 >> 3) * (D * 128);
                     const uint32_t* raw = reinterpret_cast<const uint32_t*>(vr);
@@ -447,8 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             if (!ok) failed = 1;
         } else {
             // ---- the products
-            tc::named_barrier(1, 32 * (kSoftWarps + 1));
-            if (lane == 0) {
+            fewer_registers<kMmaRegs>();
+            if (warp == kMmaWarp) tc::named_barrier(1, 32 * (kSoftWarps + 1));
+            if (warp == kMmaWarp && lane == 0) {
                 constexpr uint32_t id_s = idesc_f16(kRowsPerTile, kTok), id_o = idesc_f16(kRowsPerTile, D);
                 const uint32_t qa = tc::smem_u32(q_s), ka = tc::smem_u32(k_s), va = tc::smem_u32(v_s);
                 auto scores = [&](int x, int st) {
