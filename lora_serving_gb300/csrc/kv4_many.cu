@@ -4,15 +4,19 @@
 // Work.  An item is (sequence, kv head, 256 query rows), rows being a
 // sequence's positions x the heads of the group, so that the heads that
 // share a kv head share its tiles.  Two tiles of 128 rows take turns on the
-// tensor cores: while one's scores go through the softmax, the other's
-// products run.
+// tensor cores.
 //
-// Tile of 128 positions.  Four warps unpack the tile's codes to fp16 values
-// in shared memory, K as [position][dim] and V transposed as
-// [dim][position], both in the 128-byte-swizzled K-major form; one thread
+// Tile of 64 positions.  Two warps unpack K's codes to fp16 values in shared
+// memory, as [position][dim], two warps V's, transposed as [dim][position],
+// both in the 128-byte-swizzled K-major form; one thread per tile of rows
 // issues S = Q K^T (fp32 in tensor memory) and O += P V, P being read from
-// tensor memory, where it takes the place of S.  Four warps per tile of rows do
-// the softmax, one row to a thread: no row needs another thread's numbers.
+// tensor memory, where it takes the place of S.  Four warps per tile of rows
+// do the softmax, one row to a thread: no row needs another thread's numbers.
+// Each tile of rows has two score buffers, so that the product for the tile
+// after next runs while the softmax is at the next: with one buffer of 128
+// positions, product, hand-over and softmax followed one another, and 1024
+// rows over 32 k positions (64 heads of 128) took 1193 us.  One issuing thread per tile of rows,
+// because issuing blocks: with one for both, its barriers' time was not hidden.
 // The running maximum moves only when a score passes it by 2^8, so O is
 // seldom rescaled.  The dims of a K word come out of their nibbles in the
 // order 0 4 1 5 2 6 3 7; Q is laid out in the same order instead of undoing
@@ -30,14 +34,11 @@ namespace {
 using namespace kv4;
 
 constexpr int kRowsPerTile = 128, kRowsPerItem = 256;
-constexpr int kTok = 128;                  // positions of a tile
-constexpr int kSoftWarps = 8, kUnpackWarps = 4, kMmaWarp = kSoftWarps + kUnpackWarps;
-constexpr int kWarps = 16, kThreads = 32 * kWarps;   // the MMA warp's three neighbours only scan
-// Registers: 128 a thread at launch; the softmax warps, which hold a row's
-// weights and the scores on their way, take what the others give up:
-// 256 * 184 + 128 * 96 + 128 * 48 = 512 * 128.
-constexpr int kSoftRegs = 184, kUnpackRegs = 96, kMmaRegs = 48;
-static_assert(2 * kSoftRegs + kUnpackRegs + kMmaRegs <= 4 * 128, "registers");
+constexpr int kTok = 64;                   // positions of a tile
+constexpr int kStages = 4;                 // tiles of K, and of V, in shared memory
+constexpr int kSoftWarps = 8, kVWarp = 10, kMmaWarp = 12;
+constexpr int kWarps = 14, kThreads = 32 * kWarps;
+constexpr int kNotes = 8;                  // tiles of notes to the softmax (see Notes)
 constexpr float kSlack = 8.f, kLift = 7.f; // as in the kernel for few rows
 constexpr uint32_t kTmemCols = 512;
 
@@ -48,9 +49,9 @@ struct Shape {
     static constexpr int kQTile = kRowsPerTile * D * 2;   // bytes
     static constexpr int kKTile = kTok * D * 2;
     static constexpr int kVTile = D * kTok * 2;
-    static constexpr int kSmem = 2 * kQTile + 2 * kKTile + 2 * kVTile + 1024;   // and alignment
+    static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + 1024;   // and alignment
     // tensor memory columns
-    static constexpr uint32_t kS = 0, kO = 256;           // S (and P) of tile x at 128 x, O at 256 + D x
+    static constexpr uint32_t kS = 0, kO = 256;           // buffer b of S (and P) of tile x at 128 x + 64 b, O at 256 + D x
 };
 
 // kind::f16, fp16 x fp16 -> fp32, both operands K-major.
@@ -106,35 +107,36 @@ __device__ __forceinline__ void tmem_ld32_start(uint32_t addr, uint32_t (&r)[32]
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
 }
-__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32])
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+// Keeps uses of loaded registers behind the wait before it.
+__device__ __forceinline__ void after_wait(uint32_t (&r)[32])
 {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+    asm volatile(""
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                    "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
                    "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
                    "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-// tc::mbar_wait in line: a call would cost the warps with a register budget
-// of their own their registers.
+// Bounded waits, in line and timed by the SM's clock: a read of the global
+// timer, before the first poll, took longer than most waits here.
+constexpr long long kTimeoutClocks = 400000000;   // 0.2 s at 2 GHz
 __device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity)
 {
     if (tc::mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = tc::gtime();
-    while (!tc::mbar_try_wait_suspend(bar, parity))
-        if (tc::gtime() - t0 > tc::kTimeoutNs) return false;
+    const long long t0 = clock64();
+    while (!tc::mbar_try_wait(bar, parity))
+        if (clock64() - t0 > kTimeoutClocks) return false;
     return true;
 }
-
-template <int kRegs>
-__device__ __forceinline__ void more_registers()
+// Polling, for the thread that feeds the tensor cores.
+__device__ __forceinline__ bool wait_polling(uint64_t* bar, unsigned parity)
 {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
-}
-template <int kRegs>
-__device__ __forceinline__ void fewer_registers()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+    if (tc::mbar_test_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (!tc::mbar_test_wait(bar, parity))
+        if (clock64() - t0 > kTimeoutClocks) return false;
+    return true;
 }
 
 // Two fp32 operations in one instruction.
@@ -159,19 +161,22 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
 struct Barriers {
-    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], s_full[2], p_full[2], o_full[2];
+    uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
+    uint64_t s_full[2][2], p_full[2][2];   // [tile of rows][buffer]
+    uint64_t o_done[2];                    // a phase for each product with V but the last,
+    uint64_t o_full[2];                    // which has its own: a parity tells a phase only from its neighbours
 };
 
 // What the unpacking warps tell the softmax of a tile, a bit per position:
 // positions on a page that the cache does not have, and, where not every row
 // sees the whole tile, positions whose V is not finite in a group of dims.
-// Four tiles deep: a tile's entry is written again four tiles later, whose
-// stage is free only once both softmaxes are past the tile.
+// Tile j's entry is written again for tile j + 8: its stage of K is free once
+// both products for tile j + 4 are done, and these follow the softmax of tile j + 2.
 template <int kGroups>
 struct Notes {
-    uint4 hidden[4];
-    uint32_t any_sick[4];
-    uint32_t sick[4][kGroups][kTok / 32];
+    uint2 hidden[kNotes];
+    uint32_t any_sick[kNotes];
+    uint32_t sick[kNotes][kGroups][kTok / 32];
 };
 
 // Bits [lo, hi) of 32, whatever the bounds.
@@ -196,25 +201,30 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     uint8_t* smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* q_s = smem;
     uint8_t* k_s = smem + 2 * S::kQTile;
-    uint8_t* v_s = k_s + 2 * S::kKTile;
-    int* prefix = reinterpret_cast<int*>(v_s + 2 * S::kVTile);
+    uint8_t* v_s = k_s + kStages * S::kKTile;
+    int* prefix = reinterpret_cast<int*>(v_s + kStages * S::kVTile);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, kTmemCols);
     if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&bar.k_full[i], 2);   // two warps
+            tc::mbar_init(&bar.v_full[i], 2);
+            tc::mbar_init(&bar.k_free[i], 2);   // both tiles' products
+            tc::mbar_init(&bar.v_free[i], 2);
+        }
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(&bar.s_full[i >> 1][i & 1], 1);
+            tc::mbar_init(&bar.p_full[i >> 1][i & 1], 4);
+        }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bar.k_full[i], kUnpackWarps);
-            tc::mbar_init(&bar.v_full[i], kUnpackWarps);
-            tc::mbar_init(&bar.k_free[i], 1);
-            tc::mbar_init(&bar.v_free[i], 1);
-            tc::mbar_init(&bar.s_full[i], 1);
-            tc::mbar_init(&bar.p_full[i], 4);
+            tc::mbar_init(&bar.o_done[i], 1);
             tc::mbar_init(&bar.o_full[i], 1);
         }
         tc::mbar_init_fence();
         failed = 0;
     }
-    if (tid < 4) notes.any_sick[tid] = 0;
+    if (tid < kNotes) notes.any_sick[tid] = 0;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
 
@@ -250,7 +260,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
         };
 
         if (warp < kSoftWarps) {
-            more_registers<kSoftRegs>();
             const int x = warp >> 2, r = x * kRowsPerTile + (tid & 127);   // row of the item
             // ---- Q: one row to a thread, taken to fp16 with a power of two, into the swizzled tile
             const int row = block0 + r;
@@ -284,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 }
             }
             tc::fence_async_smem();
-            tc::named_barrier(1, 32 * (kSoftWarps + 1));   // Q is in place (the MMA warp waits too)
+            tc::named_barrier(1, 32 * (kSoftWarps + 2));   // Q is in place (the MMA warps wait too)
 
             // ---- softmax
             if (x < tiles_q) {
@@ -297,11 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 uint32_t sick = 0;   // groups of dims in which this row sees a value that is not finite
                 bool ok = true;
                 for (int j = 0; j < n_tiles; ++j) {
-                    if (!wait_for(&bar.s_full[x], j & 1)) { ok = false; break; }
+                    if (!wait_for(&bar.s_full[x][j & 1], (j >> 1) & 1)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const uint4 hid4 = notes.hidden[j & 3];
-                    const uint32_t hid[4] = {hid4.x, hid4.y, hid4.z, hid4.w};
-                    const bool all = inner(j, lo, hi) && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
+                    const uint2 hid2 = notes.hidden[j & (kNotes - 1)];
+                    const uint32_t hid[2] = {hid2.x, hid2.y}, tj = ts + 64 * (j & 1);
+                    const bool all = inner(j, lo, hi) && (hid2.x | hid2.y) == 0;
                     const int c0 = (tile0 + j) * kTok;
                     // this row sees columns [c_lo, c_hi) of the tile
                     const int c_hi = pos + 1 - c0, c_lo = a.window > 0 ? pos + 1 - a.window - c0 : 0;
@@ -316,17 +325,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         part[0] = part[1] = make_float2(0.f, 0.f);
                         auto weigh = [&](auto masked) {
                             constexpr bool kMasked = decltype(masked)::value;
-                            uint32_t v[2][32];
-                            tmem_ld32_start(ts, v[0]);
+                            uint32_t v[kTok / 32][32];
+#pragma unroll
+                            for (int c = 0; c < kTok / 32; ++c) tmem_ld32_start(tj + 32 * c, v[c]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < kTok / 32; ++c) after_wait(v[c]);
 #pragma unroll
                             for (int c = 0; c < kTok / 32; ++c) {
-                                uint32_t(&w)[32] = v[c & 1];
-                                tmem_ld32_wait(w);
-                                if (c + 1 < kTok / 32) tmem_ld32_start(ts + 32 * (c + 1), v[(c + 1) & 1]);
                                 const uint32_t see = kMasked ? bits_in(c_lo - 32 * c, c_hi - 32 * c) & ~hid[c] : 0u;
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    float2 x2 = make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+                                    float2 x2 = make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
                                     if (kMasked) {
                                         if (!((see >> e) & 1u)) x2.x = -inf;
                                         if (!((see >> e) & 2u)) x2.y = -inf;
@@ -353,6 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         top = next;
                         sum *= keep;
                         if (j > 0) {
+                            // once the last product with V is done: phase j - 1; phase j - 2 is over, since
+                            // this tile's scores were issued after it, and phase j awaits this row's weights
+                            if (!wait_for(&bar.o_done[x], (j - 1) & 1)) { ok = false; break; }
+                            tc::tc_fence_after();
 #pragma unroll
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t w[16];
@@ -364,18 +378,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                             }
                         }
                     }
+                    if (!ok) break;
                     sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
 #pragma unroll
-                    for (int c = 0; c < kTok / 2; c += 16) tmem_st16(ts + c, p + c);
-                    if (notes.any_sick[j & 3] && !inner(j, p0, p1)) {
+                    for (int c = 0; c < kTok / 2; c += 16) tmem_st16(tj + c, p + c);
+                    if (notes.any_sick[j & (kNotes - 1)] && !inner(j, p0, p1)) {
                         for (int g = 0; g < kGroups; ++g)
                             for (int c = 0; c < kTok; c += 32)
-                                if (notes.sick[j & 3][g][c >> 5] & bits_in(c_lo - c, c_hi - c) & ~hid[c >> 5]) sick |= 1u << g;
+                                if (notes.sick[j & (kNotes - 1)][g][c >> 5] & bits_in(c_lo - c, c_hi - c) & ~hid[c >> 5]) sick |= 1u << g;
                     }
                     tmem_wait_st();
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.p_full[x]);
+                    if (lane == 0) tc::mbar_arrive(&bar.p_full[x][j & 1]);
                 }
                 // ---- the result
                 if (ok) ok = wait_for(&bar.o_full[x], 0);
@@ -401,189 +416,192 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 }
             }
         } else if (warp < kMmaWarp) {
-            // ---- unpacking: K one position to a thread, V eight positions x 16 dims
-            fewer_registers<kUnpackRegs>();
-            const int u = tid - 32 * kSoftWarps;
-            const int tok8 = u & 15, quad = u >> 4;            // quad: 16 dims of V
-            const bool has_v = quad < D / 16;
-            uint4 kr[D / 32];
-            uint32_t kp[kGroups];
-            uint4 vr[4];
-            uint2 vp[4];
-            // bytes of a place, or null where no row sees it or its page is bad
-            auto place = [&](int p) -> const uint8_t* {
-                if (p >= j_end) return nullptr;
-                const int page = __ldg(table + (p >> a.cache.page_shift));
-                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.cache.n_pages)) {
-                    flag(a.status, LORA_DEV_BAD_PAGE);
-                    return nullptr;
-                }
-                return block_of(a.cache, page, h);
+            // ---- unpacking: two warps K, a position to a thread, two warps V, eight positions x 16 dims
+            const bool is_k = warp < kVWarp;
+            const int u = tid & 63;                             // K: position in the tile
+            const int tok8 = u & 7, quad = u >> 3;              // V: eight positions, 16 dims
+            const bool idle = !is_k && quad >= D / 16;
+            const int my_tok = is_k ? u : 8 * tok8;
+            struct Raw {
+                uint4 w[4];        // K: the row's words; V: four pairs' words
+                uint32_t par[8];   // K: the groups' (step, low); V: four pairs' (steps, lows)
+                uint32_t sick;     // K: groups in which the position's V is not finite
+                bool hidden;       // K: the position's page is bad
+                int page;          // of the tile to be loaded next
             };
-            bool hidden = false;    // this position's page is bad
-            uint32_t v_sick = 0;    // this position's groups with a V that is not finite
-            auto load_k = [&](int j) {
-                const int p = (tile0 + j) * kTok + u, off = p & (ps - 1);
-                const uint8_t* b = place(p);
+            auto page_at = [&](int j) -> int {   // -1: no row sees the place; -2: its page is bad
+                const int p = (tile0 + j) * kTok + my_tok;
+                if (j >= n_tiles || p >= j_end || idle) return -1;
+                const int page = __ldg(table + (p >> a.cache.page_shift));
+                return static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages) ? page : -2;
+            };
+            auto load = [&](Raw& r, int j) {
+                const int p = (tile0 + j) * kTok + my_tok, off = p & (ps - 1), page = r.page;
+                r.page = page_at(j + 2);
 #pragma unroll
-                for (int t = 0; t < D / 32; ++t) kr[t] = make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < 4; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int g = 0; g < kGroups; ++g) kp[g] = 0;
-                v_sick = 0;
-                hidden = b == nullptr && p < j_end;
-                if (b) {
+                for (int i = 0; i < 8; ++i) r.par[i] = 0;
+                r.sick = 0;
+                r.hidden = page == -2;
+                if (page == -2) flag(a.status, LORA_DEV_BAD_PAGE);
+                if (page < 0) return;
+                const uint8_t* b = block_of(a.cache, page, h);
+                if (is_k) {
 #pragma unroll
-                    for (int t = 0; t < D / 32; ++t) kr[t] = __ldg(reinterpret_cast<const uint4*>(b + off * (D / 2)) + t);
+                    for (int t = 0; t < D / 32; ++t) r.w[t] = __ldg(reinterpret_cast<const uint4*>(b + off * (D / 2)) + t);
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) kp[g] = __ldg(reinterpret_cast<const uint32_t*>(b + k_params_off(ps, D)) + off * kGroups + g);
+                    for (int g = 0; g < kGroups; ++g) r.par[g] = __ldg(reinterpret_cast<const uint32_t*>(b + k_params_off(ps, D)) + off * kGroups + g);
                     if (!inner(j, p0, p1)) {
 #pragma unroll
                         for (int g = 0; g < kGroups; ++g) {
                             const uint16_t* w = reinterpret_cast<const uint16_t*>(b + v_params_off(ps, D)) + ((off >> 1) * kGroups + g) * 4 + (off & 1);
-                            v_sick |= (not_finite(w[0]) || not_finite(w[2]) ? 1u : 0u) << g;
+                            r.sick |= (not_finite(w[0]) || not_finite(w[2]) ? 1u : 0u) << g;
                         }
                     }
-                }
-            };
-            auto load_v = [&](int j) {
-                const int p = (tile0 + j) * kTok + 8 * tok8, off = p & (ps - 1);
-                const uint8_t* b = has_v ? place(p) : nullptr;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    vr[i] = make_uint4(0, 0, 0, 0);
-                    vp[i] = make_uint2(0, 0);
-                }
-                if (b) {
+                } else {
                     const uint8_t* c = b + v_codes_off(ps, D) + (off >> 1) * D + 16 * quad;
                     const uint8_t* w = b + v_params_off(ps, D) + ((off >> 1) * kGroups + quad * 16 / kGroup) * 8;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        vr[i] = __ldg(reinterpret_cast<const uint4*>(c + i * D));
-                        vp[i] = __ldg(reinterpret_cast<const uint2*>(w + i * 8 * kGroups));
-                    }
-                    if (!inner(j, p0, p1)) {
-                        // positions past the last row's, and values that are not finite, count as zeros
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int at = p + 2 * i;
-                            uint32_t keep = (at < j_end ? 0xFFFFu : 0u) | (at + 1 < j_end ? 0xFFFF0000u : 0u);
-                            if (not_finite(vp[i].x & 0xFFFFu) || not_finite(vp[i].y & 0xFFFFu)) keep &= 0xFFFF0000u;
-                            if (not_finite(vp[i].x & 0xFFFF0000u) || not_finite(vp[i].y & 0xFFFF0000u)) keep &= 0xFFFFu;
-                            vp[i].x &= keep;
-                            vp[i].y &= keep;
-                        }
+                        r.w[i] = __ldg(reinterpret_cast<const uint4*>(c + i * D));
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(w + i * 8 * kGroups));
+                        r.par[2 * i] = v.x;
+                        r.par[2 * i + 1] = v.y;
                     }
                 }
             };
-            load_k(0);
-            load_v(0);
-            bool ok = true;
-            for (int j = 0; j < n_tiles && ok; ++j) {
-                const int st = j & 1;
-                if (j >= 2) ok = wait_for(&bar.k_free[st], ((j >> 1) & 1) ^ 1);
-                uint8_t* kd = k_s + st * S::kKTile + u * 128;
+            auto store_k = [&](const Raw& r, int j) {
+                uint8_t* kd = k_s + (j & (kStages - 1)) * S::kKTile + u * 128;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     // 16 bytes of the row hold words (t, 0..kWords-1)
                     uint32_t w[4];
                     if (kWords == 4) {
-                        w[0] = kr[t % (D / 32)].x; w[1] = kr[t % (D / 32)].y; w[2] = kr[t % (D / 32)].z; w[3] = kr[t % (D / 32)].w;
+                        w[0] = r.w[t].x; w[1] = r.w[t].y; w[2] = r.w[t].z; w[3] = r.w[t].w;
                     } else {
-                        const uint4 v = kr[(t >> 1) % (D / 32)];
-                        w[0] = t & 1 ? v.z : v.x; w[1] = t & 1 ? v.w : v.y;
+                        w[0] = t & 1 ? r.w[t >> 1].z : r.w[t >> 1].x;
+                        w[1] = t & 1 ? r.w[t >> 1].w : r.w[t >> 1].y;
                     }
 #pragma unroll
                     for (int i = 0; i < kWords; ++i) {
-                        const __half2 pr = as_h2(kp[i / 2]);
+                        const __half2 pr = as_h2(r.par[i / 2]);
                         uint32_t v[4];
                         values(w[i], __low2half2(pr), __high2half2(pr), v);
                         const int c = 4 * (i & 1) + t;
                         *reinterpret_cast<uint4*>(kd + (i >> 1) * (kTok * 128) + ((c ^ (u & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
-                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, hidden);
-                if (lane == 0) reinterpret_cast<uint32_t*>(&notes.hidden[j & 3])[u >> 5] = gone;
+                const int n = j & (kNotes - 1);
+                const uint32_t gone = __ballot_sync(0xFFFFFFFFu, r.hidden);
+                if (lane == 0) reinterpret_cast<uint32_t*>(&notes.hidden[n])[u >> 5] = gone;
                 if (!inner(j, p0, p1)) {
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
-                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, (v_sick >> g) & 1u);
-                        if (lane == 0) notes.sick[j & 3][g][u >> 5] = bits;
-                    }
-                    const bool any = __any_sync(0xFFFFFFFFu, v_sick != 0);
-                    if (lane == 0 && any) notes.any_sick[j & 3] = 1;   // stays set: the bits say what is there
-                }
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar.k_full[st]);
-                if (j + 1 < n_tiles) load_k(j + 1);
-
-                if (ok && j >= 2) ok = wait_for(&bar.v_free[st], ((j >> 1) & 1) ^ 1);
-                if (has_v) {
-                    uint8_t* vd = v_s + st * S::kVTile + (tok8 >> 3) * (D * 128);
-                    const uint32_t* raw = reinterpret_cast<const uint32_t*>(vr);
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        uint32_t v[4][4];   // [pair of positions][dim]
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) values(raw[4 * i + w], as_h2(vp[i].x), as_h2(vp[i].y), v[i]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int d = 16 * quad + 4 * w + e;
-                            *reinterpret_cast<uint4*>(vd + d * 128 + (((tok8 & 7) ^ (d & 7)) << 4)) =
-                                make_uint4(v[0][e], v[1][e], v[2][e], v[3][e]);
+                        const uint32_t bits = __ballot_sync(0xFFFFFFFFu, (r.sick >> g) & 1u);
+                        if (lane == 0) {
+                            notes.sick[n][g][u >> 5] = bits;
+                            if (bits) notes.any_sick[n] = 1;   // stays set: the bits say what is there
                         }
                     }
                 }
+            };
+            auto store_v = [&](Raw& r, int j) {
+                if (idle) return;
+                if (!inner(j, p0, p1)) {
+                    // positions past the last row's, and values that are not finite, count as zeros
+                    const int p = (tile0 + j) * kTok + my_tok;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = p + 2 * i;
+                        uint32_t& step = r.par[2 * i];
+                        uint32_t& low = r.par[2 * i + 1];
+                        uint32_t keep = (at < j_end ? 0xFFFFu : 0u) | (at + 1 < j_end ? 0xFFFF0000u : 0u);
+                        if (not_finite(step & 0xFFFFu) || not_finite(low & 0xFFFFu)) keep &= 0xFFFF0000u;
+                        if (not_finite(step & 0xFFFF0000u) || not_finite(low & 0xFFFF0000u)) keep &= 0xFFFFu;
+                        step &= keep;
+                        low &= keep;
+                    }
+                }
+                uint8_t* vd = v_s + (j & (kStages - 1)) * S::kVTile;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t v[4][4];   // [pair of positions][dim]
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t raw = w == 0 ? r.w[i].x : w == 1 ? r.w[i].y : w == 2 ? r.w[i].z : r.w[i].w;
+                        values(raw, as_h2(r.par[2 * i]), as_h2(r.par[2 * i + 1]), v[i]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int d = 16 * quad + 4 * w + e;
+                        *reinterpret_cast<uint4*>(vd + d * 128 + ((tok8 ^ (d & 7)) << 4)) = make_uint4(v[0][e], v[1][e], v[2][e], v[3][e]);
+                    }
+                }
+            };
+            uint64_t* full = is_k ? bar.k_full : bar.v_full;
+            uint64_t* free = is_k ? bar.k_free : bar.v_free;
+            auto step = [&](Raw& r, int j) -> bool {
+                const int st = j & (kStages - 1);
+                if (j >= kStages && !wait_for(&free[st], ((j / kStages) & 1) ^ 1)) return false;
+                if (is_k) store_k(r, j); else store_v(r, j);
                 tc::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&bar.v_full[st]);
-                if (j + 1 < n_tiles) load_v(j + 1);
+                if (lane == 0) tc::mbar_arrive(&full[st]);
+                if (j + 2 < n_tiles) load(r, j + 2);
+                return true;
+            };
+            // two tiles on their way, and the pages of the two after them
+            Raw r0, r1;
+            r0.page = page_at(0);
+            r1.page = page_at(1);
+            load(r0, 0);
+            load(r1, 1);
+            bool ok = true;
+            for (int j = 0; ok && j < n_tiles; j += 2) {
+                ok = step(r0, j);
+                if (ok && j + 1 < n_tiles) ok = step(r1, j + 1);
             }
             if (!ok) failed = 1;
         } else {
             // ---- the products
-            fewer_registers<kMmaRegs>();
-            if (warp == kMmaWarp) tc::named_barrier(1, 32 * (kSoftWarps + 1));
-            if (warp == kMmaWarp && lane == 0) {
+            const int x = warp - kMmaWarp;   // the tile of rows whose products this warp issues
+            tc::named_barrier(1, 32 * (kSoftWarps + 2));
+            if (x < tiles_q && lane == 0) {
                 constexpr uint32_t id_s = idesc_f16(kRowsPerTile, kTok), id_o = idesc_f16(kRowsPerTile, D);
-                const uint32_t qa = tc::smem_u32(q_s), ka = tc::smem_u32(k_s), va = tc::smem_u32(v_s);
-                auto scores = [&](int x, int st) {
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const uint32_t at = (k >> 2) * (128 * 128) + (k & 3) * 32;
-                        tc::mma_bf16(tmem + S::kS + 128 * x, tc::sdesc_sw128(qa + x * S::kQTile + at),
-                                     tc::sdesc_sw128(ka + st * S::kKTile + at), id_s, k > 0);
-                    }
-                    tc::mma_commit(&bar.s_full[x]);
+                const uint32_t s_t = tmem + S::kS + 128 * x, o_t = tmem + S::kO + D * x;
+                const uint64_t q_d = tc::sdesc_sw128(tc::smem_u32(q_s) + x * S::kQTile);
+                const uint64_t k_d = tc::sdesc_sw128(tc::smem_u32(k_s)), v_d = tc::sdesc_sw128(tc::smem_u32(v_s));
+                auto freed = [&](uint64_t* b) {
+                    tc::mma_commit(b);
+                    if (tiles_q == 1) tc::mma_commit(b);   // for the tile that is not there
                 };
-                bool ok = tc::mbar_wait_spin(&bar.k_full[0], 0);
-                tc::tc_fence_after();
-                for (int x = 0; ok && x < tiles_q; ++x) scores(x, 0);
-                if (ok) tc::mma_commit(&bar.k_free[0]);
-                for (int j = 0; ok && j < n_tiles; ++j) {
-                    const int st = j & 1, nx = (j + 1) & 1;
-                    ok = tc::mbar_wait_spin(&bar.v_full[st], (j >> 1) & 1);
-                    for (int x = 0; ok && x < tiles_q; ++x) {
-                        ok = tc::mbar_wait_spin(&bar.p_full[x], j & 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
+                auto scores = [&](int j) -> bool {
+                    const int st = j & (kStages - 1);
+                    if (!wait_polling(&bar.k_full[st], (j / kStages) & 1)) return false;
+                    tc::tc_fence_after();
+                    const uint64_t k_j = k_d + static_cast<uint64_t>(st * (S::kKTile >> 4));   // descriptors count 16 bytes
 #pragma unroll
-                        for (int k = 0; k < kTok / 16; ++k)
-                            mma_ts(tmem + S::kO + D * x, tmem + S::kS + 128 * x + 8 * k,
-                                   tc::sdesc_sw128(va + st * S::kVTile + (k >> 2) * (D * 128) + (k & 3) * 32), id_o, j > 0 || k > 0);
-                        if (x == tiles_q - 1) tc::mma_commit(&bar.v_free[st]);
-                        if (j + 1 < n_tiles) {
-                            if (x == 0) {
-                                ok = tc::mbar_wait_spin(&bar.k_full[nx], ((j + 1) >> 1) & 1);
-                                if (!ok) break;
-                                tc::tc_fence_after();
-                            }
-                            scores(x, nx);
-                            if (x == tiles_q - 1) tc::mma_commit(&bar.k_free[nx]);
-                        } else {
-                            tc::mma_commit(&bar.o_full[x]);
-                        }
-                    }
+                    for (int k = 0; k < D / 16; ++k)
+                        tc::mma_bf16(s_t + 64 * (j & 1), q_d + (((k >> 2) * (kRowsPerTile * 128) + (k & 3) * 32) >> 4),
+                                     k_j + (((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4), id_s, k > 0);
+                    tc::mma_commit(&bar.s_full[x][j & 1]);
+                    freed(&bar.k_free[st]);
+                    return true;
+                };
+                bool ok = scores(0) && (n_tiles < 2 || scores(1));
+                for (int j = 0; ok && j < n_tiles; ++j) {
+                    const int st = j & (kStages - 1);
+                    ok = wait_polling(&bar.v_full[st], (j / kStages) & 1) && wait_polling(&bar.p_full[x][j & 1], (j >> 1) & 1);
+                    if (!ok) break;
+                    tc::tc_fence_after();
+                    const uint64_t v_j = v_d + static_cast<uint64_t>(st * (S::kVTile >> 4));
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_ts(o_t, s_t + 64 * (j & 1) + 8 * k, v_j + ((k * 32) >> 4), id_o, j > 0 || k > 0);
+                    tc::mma_commit(j + 1 < n_tiles ? &bar.o_done[x] : &bar.o_full[x]);
+                    freed(&bar.v_free[st]);
+                    if (j + 2 < n_tiles) ok = scores(j + 2);
                 }
                 if (!ok) failed = 1;
             }
