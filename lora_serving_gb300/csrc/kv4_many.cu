@@ -6,17 +6,15 @@
 // share a kv head share its tiles.  Two tiles of 128 rows take turns on the
 // tensor cores.
 //
-// Tile of 64 positions.  Two warps unpack K's codes to fp16 values in shared
-// memory, as [position][dim], two warps V's, transposed as [dim][position],
+// Tile of 128 positions.  Four warps unpack K's codes to fp16 values in shared
+// memory, as [position][dim], four warps V's, transposed as [dim][position],
 // both in the 128-byte-swizzled K-major form; one thread per tile of rows
 // issues S = Q K^T (fp32 in tensor memory) and O += P V, P being read from
 // tensor memory, where it takes the place of S.  Four warps per tile of rows
 // do the softmax, one row to a thread: no row needs another thread's numbers.
-// Each tile of rows has two score buffers, so that the product for the tile
-// after next runs while the softmax is at the next: with one buffer of 128
-// positions, product, hand-over and softmax followed one another, and 1024
-// rows over 32 k positions (64 heads of 128) took 1193 us.  One issuing thread per tile of rows,
-// because issuing blocks: with one for both, its barriers' time was not hidden.
+// The issuing threads take turns: the tensor cores serve two threads in
+// alternation, which drew the tiles of rows into step, both waiting for their
+// products at the same time and then both at the softmax (4900 clocks a tile of 128 positions).
 // The running maximum moves only when a score passes it by 2^8, so O is
 // seldom rescaled.  The dims of a K word come out of their nibbles in the
 // order 0 4 1 5 2 6 3 7; Q is laid out in the same order instead of undoing
@@ -34,11 +32,16 @@ namespace {
 using namespace kv4;
 
 constexpr int kRowsPerTile = 128, kRowsPerItem = 256;
-constexpr int kTok = 64;                   // positions of a tile
-constexpr int kStages = 4;                 // tiles of K, and of V, in shared memory
-constexpr int kSoftWarps = 8, kVWarp = 10, kMmaWarp = 12;
-constexpr int kWarps = 14, kThreads = 32 * kWarps;
-constexpr int kNotes = 8;                  // tiles of notes to the softmax (see Notes)
+constexpr int kTok = 128;                  // positions of a tile
+constexpr int kStages = 2;                 // tiles of K, and of V, in shared memory
+constexpr int kSoftWarps = 8, kVWarp = 12, kMmaWarp = 16;
+constexpr int kWarps = 20, kThreads = 32 * kWarps;   // two MMA warps; their two neighbours only scan
+constexpr int kNotes = 4;                  // tiles of which the softmax has notes (see Notes)
+// Registers: 96 a thread at launch; the softmax warps, which hold a row's
+// scores and weights, take what the others give up:
+// 256 * 160 + 256 * 64 + 128 * 32 = 640 * 96.
+constexpr int kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
+static_assert(2 * kSoftRegs + 2 * kUnpackRegs + kMmaRegs <= 5 * 96, "registers");
 constexpr float kSlack = 8.f, kLift = 7.f; // as in the kernel for few rows
 constexpr uint32_t kTmemCols = 512;
 
@@ -48,10 +51,10 @@ struct Shape {
     static constexpr int kWords = D / 32;                 // K words of one lane of the cache's layout
     static constexpr int kQTile = kRowsPerTile * D * 2;   // bytes
     static constexpr int kKTile = kTok * D * 2;
-    static constexpr int kVTile = D * kTok * 2;
+    static constexpr int kVHalf = D * 64 * 2, kVTile = 2 * kVHalf;   // [64 positions each][dim][position]
     static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + 1024;   // and alignment
     // tensor memory columns
-    static constexpr uint32_t kS = 0, kO = 256;           // buffer b of S (and P) of tile x at 128 x + 64 b, O at 256 + D x
+    static constexpr uint32_t kS = 0, kO = 256;           // S (and P) of tile x at 128 x, O at 256 + D x
 };
 
 // kind::f16, fp16 x fp16 -> fp32, both operands K-major.
@@ -139,6 +142,24 @@ __device__ __forceinline__ bool wait_polling(uint64_t* bar, unsigned parity)
     return true;
 }
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
+}
+
+template <int kRegs>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegs));
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -162,19 +183,20 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 struct Barriers {
     uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
-    uint64_t s_full[2][2], p_full[2][2];   // [tile of rows][buffer]
-    uint64_t o_done[2];                    // a phase for each product with V but the last,
-    uint64_t o_full[2];                    // which has its own: a parity tells a phase only from its neighbours
+    uint64_t s_full[2], p_full[2];   // of a tile of rows
+    uint64_t o_full[2];
+    uint64_t turn[2];                // a tile of rows' products may be issued
 };
 
 // What the unpacking warps tell the softmax of a tile, a bit per position:
 // positions on a page that the cache does not have, and, where not every row
 // sees the whole tile, positions whose V is not finite in a group of dims.
-// Tile j's entry is written again for tile j + 8: its stage of K is free once
-// both products for tile j + 4 are done, and these follow the softmax of tile j + 2.
+// A tile's entry is written again four tiles later: that tile's stage of K is
+// free once both products of two tiles earlier are done, and these follow the
+// softmax of the tile before.
 template <int kGroups>
 struct Notes {
-    uint2 hidden[kNotes];
+    uint4 hidden[kNotes];
     uint32_t any_sick[kNotes];
     uint32_t sick[kNotes][kGroups][kTok / 32];
 };
@@ -203,23 +225,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     uint8_t* k_s = smem + 2 * S::kQTile;
     uint8_t* v_s = k_s + kStages * S::kKTile;
     int* prefix = reinterpret_cast<int*>(v_s + kStages * S::kVTile);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, kTmemCols);
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&bar.k_full[i], 2);   // two warps
-            tc::mbar_init(&bar.v_full[i], 2);
+            tc::mbar_init(&bar.k_full[i], 4);   // four warps
+            tc::mbar_init(&bar.v_full[i], 4);
             tc::mbar_init(&bar.k_free[i], 2);   // both tiles' products
             tc::mbar_init(&bar.v_free[i], 2);
         }
-        for (int i = 0; i < 4; ++i) {
-            tc::mbar_init(&bar.s_full[i >> 1][i & 1], 1);
-            tc::mbar_init(&bar.p_full[i >> 1][i & 1], 4);
-        }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(&bar.o_done[i], 1);
+            tc::mbar_init(&bar.s_full[i], 1);
+            tc::mbar_init(&bar.p_full[i], 4);
             tc::mbar_init(&bar.o_full[i], 1);
+            tc::mbar_init(&bar.turn[i], 1);
         }
         tc::mbar_init_fence();
         failed = 0;
@@ -260,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
         };
 
         if (warp < kSoftWarps) {
+            more_registers<kSoftRegs>();
             const int x = warp >> 2, r = x * kRowsPerTile + (tid & 127);   // row of the item
             // ---- Q: one row to a thread, taken to fp16 with a power of two, into the swizzled tile
             const int row = block0 + r;
@@ -306,11 +327,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 uint32_t sick = 0;   // groups of dims in which this row sees a value that is not finite
                 bool ok = true;
                 for (int j = 0; j < n_tiles; ++j) {
-                    if (!wait_for(&bar.s_full[x][j & 1], (j >> 1) & 1)) { ok = false; break; }
+                    if (!wait_for(&bar.s_full[x], j & 1)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const uint2 hid2 = notes.hidden[j & (kNotes - 1)];
-                    const uint32_t hid[2] = {hid2.x, hid2.y}, tj = ts + 64 * (j & 1);
-                    const bool all = inner(j, lo, hi) && (hid2.x | hid2.y) == 0;
+                    const int note = j & (kNotes - 1);
+                    const uint4 hid4 = notes.hidden[note];
+                    const uint32_t hid[4] = {hid4.x, hid4.y, hid4.z, hid4.w};
+                    const bool all = inner(j, lo, hi) && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
                     const int c0 = (tile0 + j) * kTok;
                     // this row sees columns [c_lo, c_hi) of the tile
                     const int c_hi = pos + 1 - c0, c_lo = a.window > 0 ? pos + 1 - a.window - c0 : 0;
@@ -325,18 +347,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         part[0] = part[1] = make_float2(0.f, 0.f);
                         auto weigh = [&](auto masked) {
                             constexpr bool kMasked = decltype(masked)::value;
-                            uint32_t v[kTok / 32][32];
-#pragma unroll
-                            for (int c = 0; c < kTok / 32; ++c) tmem_ld32_start(tj + 32 * c, v[c]);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < kTok / 32; ++c) after_wait(v[c]);
+                            uint32_t v[2][32];   // one load ahead of the arithmetic
+                            tmem_ld32_start(ts, v[0]);
 #pragma unroll
                             for (int c = 0; c < kTok / 32; ++c) {
+                                uint32_t(&w)[32] = v[c & 1];
+                                tmem_wait_ld();
+                                after_wait(w);
+                                if (c + 1 < kTok / 32) tmem_ld32_start(ts + 32 * (c + 1), v[(c + 1) & 1]);
                                 const uint32_t see = kMasked ? bits_in(c_lo - 32 * c, c_hi - 32 * c) & ~hid[c] : 0u;
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    float2 x2 = make_float2(__uint_as_float(v[c][e]), __uint_as_float(v[c][e + 1]));
+                                    float2 x2 = make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
                                     if (kMasked) {
                                         if (!((see >> e) & 1u)) x2.x = -inf;
                                         if (!((see >> e) & 2u)) x2.y = -inf;
@@ -362,11 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         const float keep = next == -inf ? 1.f : ex2(top - next);
                         top = next;
                         sum *= keep;
-                        if (j > 0) {
-                            // once the last product with V is done: phase j - 1; phase j - 2 is over, since
-                            // this tile's scores were issued after it, and phase j awaits this row's weights
-                            if (!wait_for(&bar.o_done[x], (j - 1) & 1)) { ok = false; break; }
-                            tc::tc_fence_after();
+                        if (j > 0) {   // the last product with V is done: this tile's scores were issued after it
 #pragma unroll
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t w[16];
@@ -378,19 +396,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                             }
                         }
                     }
-                    if (!ok) break;
                     sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
 #pragma unroll
-                    for (int c = 0; c < kTok / 2; c += 16) tmem_st16(tj + c, p + c);
-                    if (notes.any_sick[j & (kNotes - 1)] && !inner(j, p0, p1)) {
+                    for (int c = 0; c < kTok / 2; c += 16) tmem_st16(ts + c, p + c);
+                    if (notes.any_sick[note] && !inner(j, p0, p1)) {
                         for (int g = 0; g < kGroups; ++g)
                             for (int c = 0; c < kTok; c += 32)
-                                if (notes.sick[j & (kNotes - 1)][g][c >> 5] & bits_in(c_lo - c, c_hi - c) & ~hid[c >> 5]) sick |= 1u << g;
+                                if (notes.sick[note][g][c >> 5] & bits_in(c_lo - c, c_hi - c) & ~hid[c >> 5]) sick |= 1u << g;
                     }
                     tmem_wait_st();
                     tc::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&bar.p_full[x][j & 1]);
+                    if (lane == 0) tc::mbar_arrive(&bar.p_full[x]);
                 }
                 // ---- the result
                 if (ok) ok = wait_for(&bar.o_full[x], 0);
@@ -416,12 +433,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 }
             }
         } else if (warp < kMmaWarp) {
-            // ---- unpacking: two warps K, a position to a thread, two warps V, eight positions x 16 dims
+            // ---- unpacking: four warps K, a position to a thread, four warps V, eight positions x 16 dims
+            fewer_registers<kUnpackRegs>();
             const bool is_k = warp < kVWarp;
-            const int u = tid & 63;                             // K: position in the tile
-            const int tok8 = u & 7, quad = u >> 3;              // V: eight positions, 16 dims
+            const int u = tid & 127;                            // K: position in the tile
+            const int half = (u >> 5) & 1, t8 = u & 7;          // V: eight positions of a half of 64,
+            const int quad = ((u >> 6) << 2) | ((u >> 3) & 3);  // 16 dims; eight lanes of a dim write its 128 bytes
             const bool idle = !is_k && quad >= D / 16;
-            const int my_tok = is_k ? u : 8 * tok8;
+            const int my_tok = is_k ? u : 64 * half + 8 * t8;
             struct Raw {
                 uint4 w[4];        // K: the row's words; V: four pairs' words
                 uint32_t par[8];   // K: the groups' (step, low); V: four pairs' (steps, lows)
@@ -437,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             };
             auto load = [&](Raw& r, int j) {
                 const int p = (tile0 + j) * kTok + my_tok, off = p & (ps - 1), page = r.page;
-                r.page = page_at(j + 2);
+                r.page = page_at(j + 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -523,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         low &= keep;
                     }
                 }
-                uint8_t* vd = v_s + (j & (kStages - 1)) * S::kVTile;
+                uint8_t* vd = v_s + (j & (kStages - 1)) * S::kVTile + half * S::kVHalf;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     uint32_t v[4][4];   // [pair of positions][dim]
@@ -535,73 +554,81 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int d = 16 * quad + 4 * w + e;
-                        *reinterpret_cast<uint4*>(vd + d * 128 + ((tok8 ^ (d & 7)) << 4)) = make_uint4(v[0][e], v[1][e], v[2][e], v[3][e]);
+                        *reinterpret_cast<uint4*>(vd + d * 128 + ((t8 ^ (d & 7)) << 4)) = make_uint4(v[0][e], v[1][e], v[2][e], v[3][e]);
                     }
                 }
             };
             uint64_t* full = is_k ? bar.k_full : bar.v_full;
             uint64_t* free = is_k ? bar.k_free : bar.v_free;
-            auto step = [&](Raw& r, int j) -> bool {
+            // a tile on its way, and the page of the one after it
+            Raw r;
+            r.page = page_at(0);
+            load(r, 0);
+            for (int j = 0; j < n_tiles; ++j) {
                 const int st = j & (kStages - 1);
-                if (j >= kStages && !wait_for(&free[st], ((j / kStages) & 1) ^ 1)) return false;
+                if (j >= kStages && !wait_for(&free[st], ((j / kStages) & 1) ^ 1)) { failed = 1; break; }
                 if (is_k) store_k(r, j); else store_v(r, j);
                 tc::fence_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&full[st]);
-                if (j + 2 < n_tiles) load(r, j + 2);
-                return true;
-            };
-            // two tiles on their way, and the pages of the two after them
-            Raw r0, r1;
-            r0.page = page_at(0);
-            r1.page = page_at(1);
-            load(r0, 0);
-            load(r1, 1);
-            bool ok = true;
-            for (int j = 0; ok && j < n_tiles; j += 2) {
-                ok = step(r0, j);
-                if (ok && j + 1 < n_tiles) ok = step(r1, j + 1);
+                if (j + 1 < n_tiles) load(r, j + 1);
             }
-            if (!ok) failed = 1;
         } else {
             // ---- the products
+            // The whole warp runs the loop and one elected lane issues: values that the compiler knows to be
+            // the warp's own stay in uniform registers, where the instruction wants its operands.
+            fewer_registers<kMmaRegs>();
             const int x = warp - kMmaWarp;   // the tile of rows whose products this warp issues
-            tc::named_barrier(1, 32 * (kSoftWarps + 2));
-            if (x < tiles_q && lane == 0) {
+            if (x < 2) tc::named_barrier(1, 32 * (kSoftWarps + 2));
+            if (x < tiles_q) {
                 constexpr uint32_t id_s = idesc_f16(kRowsPerTile, kTok), id_o = idesc_f16(kRowsPerTile, D);
-                const uint32_t s_t = tmem + S::kS + 128 * x, o_t = tmem + S::kO + D * x;
+                const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+                const uint32_t s_t = t0 + S::kS + 128 * x, o_t = t0 + S::kO + D * x;
                 const uint64_t q_d = tc::sdesc_sw128(tc::smem_u32(q_s) + x * S::kQTile);
                 const uint64_t k_d = tc::sdesc_sw128(tc::smem_u32(k_s)), v_d = tc::sdesc_sw128(tc::smem_u32(v_s));
-                auto freed = [&](uint64_t* b) {
-                    tc::mma_commit(b);
-                    if (tiles_q == 1) tc::mma_commit(b);   // for the tile that is not there
-                };
+                const bool lead = elect_one();
+                // turn n of this tile of rows
+                auto my_turn = [&](int n) { return tiles_q == 1 || wait_polling(&bar.turn[x], n & 1); };
                 auto scores = [&](int j) -> bool {
                     const int st = j & (kStages - 1);
                     if (!wait_polling(&bar.k_full[st], (j / kStages) & 1)) return false;
                     tc::tc_fence_after();
-                    const uint64_t k_j = k_d + static_cast<uint64_t>(st * (S::kKTile >> 4));   // descriptors count 16 bytes
+                    if (lead) {
+                        const uint64_t k_j = k_d + static_cast<uint64_t>(st * (S::kKTile >> 4));   // descriptors count 16 bytes
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k)
-                        tc::mma_bf16(s_t + 64 * (j & 1), q_d + (((k >> 2) * (kRowsPerTile * 128) + (k & 3) * 32) >> 4),
-                                     k_j + (((k >> 2) * (kTok * 128) + (k & 3) * 32) >> 4), id_s, k > 0);
-                    tc::mma_commit(&bar.s_full[x][j & 1]);
-                    freed(&bar.k_free[st]);
+                        for (int k = 0; k < D / 16; ++k) {
+                            const int at = ((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4;
+                            tc::mma_bf16(s_t, q_d + at, k_j + at, id_s, k > 0);
+                        }
+                        tc::mma_commit(&bar.s_full[x]);
+                        tc::mma_commit(&bar.k_free[st]);
+                        if (tiles_q == 1) tc::mma_commit(&bar.k_free[st]);   // for the tile of rows that is not there
+                        else tc::mbar_arrive(&bar.turn[x ^ 1]);
+                    }
+                    __syncwarp();
                     return true;
                 };
-                bool ok = scores(0) && (n_tiles < 2 || scores(1));
+                bool ok = (x == 0 || my_turn(0)) && scores(0);
                 for (int j = 0; ok && j < n_tiles; ++j) {
                     const int st = j & (kStages - 1);
-                    ok = wait_polling(&bar.v_full[st], (j / kStages) & 1) && wait_polling(&bar.p_full[x][j & 1], (j >> 1) & 1);
+                    ok = wait_polling(&bar.v_full[st], (j / kStages) & 1) && wait_polling(&bar.p_full[x], j & 1) && my_turn(j + x);
                     if (!ok) break;
                     tc::tc_fence_after();
-                    const uint64_t v_j = v_d + static_cast<uint64_t>(st * (S::kVTile >> 4));
+                    if (lead) {
+                        const uint64_t v_j = v_d + static_cast<uint64_t>(st * (S::kVTile >> 4));
 #pragma unroll
-                    for (int k = 0; k < kTok / 16; ++k)
-                        mma_ts(o_t, s_t + 64 * (j & 1) + 8 * k, v_j + ((k * 32) >> 4), id_o, j > 0 || k > 0);
-                    tc::mma_commit(j + 1 < n_tiles ? &bar.o_done[x] : &bar.o_full[x]);
-                    freed(&bar.v_free[st]);
-                    if (j + 2 < n_tiles) ok = scores(j + 2);
+                        for (int k = 0; k < kTok / 16; ++k)
+                            mma_ts(o_t, s_t + 8 * k, v_j + (((k >> 2) * S::kVHalf + (k & 3) * 32) >> 4), id_o, j > 0 || k > 0);
+                        if (j + 1 < n_tiles) {
+                            tc::mma_commit(&bar.v_free[st]);
+                            if (tiles_q == 1) tc::mma_commit(&bar.v_free[st]);
+                        } else {
+                            tc::mma_commit(&bar.o_full[x]);
+                            if (tiles_q == 2) tc::mbar_arrive(&bar.turn[x ^ 1]);
+                        }
+                    }
+                    __syncwarp();
+                    if (j + 1 < n_tiles) ok = scores(j + 1);
                 }
                 if (!ok) failed = 1;
             }
