@@ -124,8 +124,11 @@ __device__ __forceinline__ int seq_at(const int* prefix, int n_seqs, int x)
 
 }  // namespace kv4
 
-cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, cudaStream_t stream);
-cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, cudaStream_t stream);
+// Sequences with at most few_rows query rows to a kv head (rows x heads of
+// the group), and the others; ws: the kernel's own workspace.
+cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream);
+cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream);
+size_t kv4_many_workspace(int head_dim);
 size_t kv4_few_workspace(int head_dim, int rows);
 
 }  // namespace lora

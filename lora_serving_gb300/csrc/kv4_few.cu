@@ -129,7 +129,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src)
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_few_kernel(AttendArgs a, int few_rows)
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_few_kernel(AttendArgs a, int few_rows, void* ws)
 {
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kGroups = S::kGroups, kWords = S::kWords, kStages = S::kStages, kWarps = S::kWarps;
@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
             if (p.u0 == first.u0) ends = p.ends;
         }
         const bool starts = i0 & 1;
-        float* to = partial(a.ws, b, starts, S::kPartial);
+        float* to = partial(ws, b, starts, S::kPartial);
         for (int e = tid; e < first.rows * (D / 4); e += S::kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = -inf, l = 0.f;
@@ -544,29 +544,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
             while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, (rec.last + 1) * kWarps) < first.u1) ++rec.last;
         }
     }
-    if (tid == 0) static_cast<Record*>(a.ws)[b] = rec;
+    if (tid == 0) static_cast<Record*>(ws)[b] = rec;
 }
 
 // Joins the pieces of the unit that begins in CTA b's ranges and goes on, in order.
 template <int D, int NT>
-__global__ void __launch_bounds__(256) kv4_few_join_kernel(AttendArgs a)
+__global__ void __launch_bounds__(256) kv4_few_join_kernel(AttendArgs a, void* ws)
 {
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
     const int b = blockIdx.x, group = a.n_heads / a.cache.n_kv;
-    const Record u = static_cast<const Record*>(a.ws)[b];
+    const Record u = static_cast<const Record*>(ws)[b];
     const float inf = __int_as_float(0x7F800000);
     for (int e = threadIdx.x; e < u.rows * (D / 4); e += blockDim.x) {
         const int r = e / (D / 4), d = e % (D / 4) * 4;
         float m = -inf, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int k = b; k <= u.last; ++k) m = fmaxf(m, partial(a.ws, k, k == b, S::kPartial)[kRows * D + r]);
+        for (int k = b; k <= u.last; ++k) m = fmaxf(m, partial(ws, k, k == b, S::kPartial)[kRows * D + r]);
 #pragma unroll 4
         for (int k = b; k <= u.last; ++k) {
-            const float* p = partial(a.ws, k, k == b, S::kPartial);
+            const float* p = partial(ws, k, k == b, S::kPartial);
             const float w = m == -inf ? 0.f : ex2(p[kRows * D + r] - m);
             const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
             o.x = fmaf(v.x, w, o.x);
@@ -585,7 +585,7 @@ constexpr int kMaxSmem = 227 * 1024;
 static_assert(Shape<128, 4>::kSmem + 4 * kMaxSeqs <= kMaxSmem, "shared memory");
 
 template <int D, int NT>
-cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
+cudaError_t run(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
 {
     using S = Shape<D, NT>;
     static bool attr_set = false;
@@ -597,11 +597,11 @@ cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
     }
     const int ctas = std::min(kMaxCtas, device_sms() * S::kCtas);
     PdlLaunch l(dim3(ctas), S::kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
-    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows, ws);
     if (e != cudaSuccess) return e;
     note_launch();
     PdlLaunch j(dim3(ctas), 256, 0, stream);
-    e = cudaLaunchKernelEx(&j.cfg, kv4_few_join_kernel<D, NT>, a);
+    e = cudaLaunchKernelEx(&j.cfg, kv4_few_join_kernel<D, NT>, a, ws);
     note_launch();
     return e;
 }
@@ -611,19 +611,19 @@ cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
 size_t kv4_few_workspace(int head_dim, int rows)
 {
     const int r = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-    return kRecordBytes + static_cast<size_t>(kMaxCtas) * 2 * r * (head_dim + 2) * sizeof(float);
+    return (kRecordBytes + static_cast<size_t>(kMaxCtas) * 2 * r * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
 }
 
-cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, cudaStream_t stream)
+cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
 {
     if (a.cache.head_dim == 64) {
-        if (few_rows <= 8) return run<64, 1>(a, few_rows, stream);
-        if (few_rows <= 16) return run<64, 2>(a, few_rows, stream);
-        return run<64, 4>(a, few_rows, stream);
+        if (few_rows <= 8) return run<64, 1>(a, few_rows, ws, stream);
+        if (few_rows <= 16) return run<64, 2>(a, few_rows, ws, stream);
+        return run<64, 4>(a, few_rows, ws, stream);
     }
-    if (few_rows <= 8) return run<128, 1>(a, few_rows, stream);
-    if (few_rows <= 16) return run<128, 2>(a, few_rows, stream);
-    return run<128, 4>(a, few_rows, stream);
+    if (few_rows <= 8) return run<128, 1>(a, few_rows, ws, stream);
+    if (few_rows <= 16) return run<128, 2>(a, few_rows, ws, stream);
+    return run<128, 4>(a, few_rows, ws, stream);
 }
 
 }  // namespace lora

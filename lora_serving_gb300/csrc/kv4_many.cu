@@ -4,7 +4,10 @@
 // Work.  An item is (sequence, kv head, 256 query rows), rows being a
 // sequence's positions x the heads of the group, so that the heads that
 // share a kv head share its tiles.  Two tiles of 128 rows take turns on the
-// tensor cores.
+// tensor cores.  All items' tiles of positions laid end to end are cut into
+// equal ranges, one per SM, an item counting kItemCost tiles more than it
+// has, for its start and end; an item cut by a range's end leaves partial
+// results, which a second kernel joins in a fixed order.
 //
 // Tile of 128 positions.  Four warps unpack K's codes to fp16 values in shared
 // memory, as [position][dim], four warps V's, transposed as [dim][position],
@@ -42,6 +45,8 @@ constexpr int kNotes = 4;                  // tiles of which the softmax has not
 // 256 * 160 + 256 * 64 + 128 * 32 = 640 * 96.
 constexpr int kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
 static_assert(2 * kSoftRegs + 2 * kUnpackRegs + kMmaRegs <= 5 * 96, "registers");
+constexpr int kItemCost = 2;               // an item's start and end, in tiles
+constexpr int kMinRange = 4;               // a CTA's range, at least
 constexpr float kSlack = 8.f, kLift = 7.f; // as in the kernel for few rows
 constexpr uint32_t kTmemCols = 512;
 
@@ -52,6 +57,7 @@ struct Shape {
     static constexpr int kQTile = kRowsPerTile * D * 2;   // bytes
     static constexpr int kKTile = kTok * D * 2;
     static constexpr int kVHalf = D * 64 * 2, kVTile = 2 * kVHalf;   // [64 positions each][dim][position]
+    static constexpr int kPartial = kRowsPerItem * (D + 2);   // floats of a partial result: sums, maxima, sums of weights
     static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + 1024;   // and alignment
     // tensor memory columns
     static constexpr uint32_t kS = 0, kO = 256;           // S (and P) of tile x at 128 x, O at 256 + D x
@@ -209,8 +215,116 @@ __device__ __forceinline__ uint32_t bits_in(int lo, int hi)
     return below_hi & ~below_lo;
 }
 
+// 256 query rows of a sequence: its rows [row0, row0 + rows) of positions x
+// heads, the positions of the first and the last, and the tiles they see.
+struct Block {
+    int row0, rows, p0, p1, tile0, tiles;
+};
+__device__ __forceinline__ Block block_at(const Seq& q, int i, int group, int window)
+{
+    Block b;
+    b.row0 = i * kRowsPerItem;
+    b.rows = min(kRowsPerItem, q.n * group - b.row0);
+    b.p0 = q.ctx - q.n + b.row0 / group;
+    b.p1 = q.ctx - q.n + (b.row0 + b.rows - 1) / group;
+    const int begin = window > 0 ? max(0, b.p0 - window + 1) : 0;
+    b.tile0 = begin / kTok;
+    b.tiles = max(1, (max(0, b.p1 + 1) + kTok - 1) / kTok - b.tile0);   // at least one: its rows get their zeros
+    return b;
+}
+
+// A range's part of an item.
+struct Piece {
+    int s, h;
+    Seq q;
+    Block b;
+    int tile0, tiles;    // the piece's tiles
+    bool starts, ends;   // whether the item begins, ends with it
+    int u1;              // where the item ends on the line
+};
+
+// Walks the pieces of a CTA's range.  The line goes by blocks of rows in the
+// order of the sequences, the kv heads of a block one after another.
+struct Walk {
+    const AttendArgs& a;
+    const int* prefix;   // blocks before each sequence
+    int group, x, end, s, i, at;   // x: place on the line; block i of sequence s begins at `at`
+    Seq q;
+    Block b;
+
+    __device__ __forceinline__ void set_block()
+    {
+        load_seq(a.batch, s, q, nullptr);
+        b = block_at(q, i, group, a.window);
+    }
+    // cost: places before each thread's share of the blocks, `share` blocks to a thread
+    __device__ __forceinline__ Walk(const AttendArgs& args, const int* pre, const int* cost, int share, int begin, int end_)
+        : a(args), prefix(pre), group(args.n_heads / args.cache.n_kv), x(begin), end(end_)
+    {
+        if (x >= end) return;
+        const int c = seq_at(cost, kThreads, x);
+        at = cost[c];
+        s = seq_at(prefix, a.batch.n_seqs, c * share);
+        i = c * share - prefix[s];
+        set_block();
+        while (x >= at + (b.tiles + kItemCost) * a.cache.n_kv) next_block();
+    }
+    __device__ __forceinline__ void next_block()
+    {
+        at += (b.tiles + kItemCost) * a.cache.n_kv;
+        if (prefix[s] + ++i == prefix[s + 1]) {
+            i = 0;
+            do ++s; while (prefix[s] == prefix[s + 1]);
+        }
+        set_block();
+    }
+    __device__ __forceinline__ bool next(Piece& p)
+    {
+        while (x < end) {
+            const int len = b.tiles + kItemCost;
+            if (x >= at + len * a.cache.n_kv) {
+                next_block();
+                continue;
+            }
+            p.h = (x - at) / len;
+            const int u0 = at + p.h * len;
+            const int t0 = max(0, x - u0 - kItemCost), t1 = max(0, min(len, end - u0) - kItemCost);
+            x = min(end, u0 + len);
+            if (t0 == t1) continue;   // only the item's start lies in the range
+            p.s = s;
+            p.q = q;
+            p.b = b;
+            p.tile0 = b.tile0 + t0;
+            p.tiles = t1 - t0;
+            p.starts = t0 == 0;
+            p.ends = t1 == b.tiles;
+            p.u1 = u0 + len;
+            return true;
+        }
+        return false;
+    }
+};
+__device__ __forceinline__ int range_count(int total, int ctas) { return min(ctas, max(1, total / kMinRange)); }
+__device__ __forceinline__ int range_at(int total, int n, int b)
+{
+    return static_cast<int>(static_cast<long long>(total) * min(b, n) / n);
+}
+
+// What the workspace holds: a record for each CTA of the item that begins in
+// its range and goes on after it, then two partial results for each CTA: of
+// the item that began before its range, and of the one that goes on after it.
+struct Record {
+    int rows, block_row0, seq_row0, h, last;   // rows 0: none; the item's pieces lie in CTAs [this, last]
+};
+constexpr int kMaxCtas = 160;   // CTAs that the workspace has room for
+constexpr size_t kRecordBytes = (kMaxCtas * sizeof(Record) + 255) / 256 * 256;
+__device__ __forceinline__ float* partial(void* ws, int cta, int slot, int floats)
+{
+    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kRecordBytes) + (static_cast<long long>(cta) * 2 + slot) * floats;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int few_rows)
+__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int few_rows, void* ws)
 {
     using S = Shape<D>;
     constexpr int kGroups = S::kGroups, kWords = S::kWords;
@@ -219,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     __shared__ Notes<kGroups> notes;
     __shared__ uint32_t tmem_base;
     __shared__ int sums[kWarps];
+    __shared__ int cost[kThreads + 1];
     __shared__ int failed;
     uint8_t* smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* q_s = smem;
@@ -248,92 +363,106 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     tc::grid_dep_wait();
     tc::grid_dep_launch();
 
-    // ---- this CTA's item
-    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size, n_kv = a.cache.n_kv;
+    // ---- this CTA's range: blocks before each sequence, then places before each thread's share of the blocks
+    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
     scan_seqs<kWarps>(a.batch.n_seqs, prefix, sums, [&](int s) {
         Seq q;
         const bool ok = load_seq(a.batch, s, q, blockIdx.x == 0 ? a.status : nullptr);
-        return ok && q.n * group > few_rows ? (q.n * group + kRowsPerItem - 1) / kRowsPerItem * n_kv : 0;
+        return ok && q.n * group > few_rows ? (q.n * group + kRowsPerItem - 1) / kRowsPerItem : 0;
+    });
+    __syncthreads();
+    const int blocks = prefix[a.batch.n_seqs], share = (blocks + kThreads - 1) / kThreads;
+    scan_seqs<kWarps>(kThreads, cost, sums, [&](int t) {
+        int sum = 0;
+        for (int f = t * share; f < min(blocks, (t + 1) * share); ++f) {
+            const int s = seq_at(prefix, a.batch.n_seqs, f);
+            Seq q;
+            load_seq(a.batch, s, q, nullptr);
+            sum += (block_at(q, f - prefix[s], group, a.window).tiles + kItemCost) * a.cache.n_kv;
+        }
+        return sum;
     });
     tc::tc_fence_before();
-    __syncthreads();   // barriers, the tensor memory's address, the running sum
+    __syncthreads();   // barriers, the tensor memory's address, the running sums
     tc::tc_fence_after();
-    const int item = blockIdx.x;
-    const bool work = item < prefix[a.batch.n_seqs];
+    const int total = cost[kThreads], n_ranges = range_count(total, gridDim.x);
+    const int begin = range_at(total, n_ranges, blockIdx.x), end = range_at(total, n_ranges, blockIdx.x + 1);
     const uint32_t tmem = tmem_base;
-    if (work) {
-        const int s = seq_at(prefix, a.batch.n_seqs, item);
-        Seq q;
-        load_seq(a.batch, s, q, nullptr);
-        const int of = (prefix[s + 1] - prefix[s]) / n_kv, in = item - prefix[s];
-        const int h = in % n_kv, block0 = (of - 1 - in / n_kv) * kRowsPerItem;   // the last rows see most: they come first
-        const int rows = min(kRowsPerItem, q.n * group - block0);                // of this item
-        const int tiles_q = rows > kRowsPerTile ? 2 : 1;
-        // positions of the item's first and last row, and the positions that any of them sees
-        const int p0 = q.ctx - q.n + block0 / group, p1 = q.ctx - q.n + (block0 + rows - 1) / group;
-        const int j_begin = a.window > 0 ? max(0, p0 - a.window + 1) : 0, j_end = max(0, p1 + 1);
-        const int tile0 = j_begin / kTok, n_tiles = max(1, (j_end + kTok - 1) / kTok - tile0);
-        const int32_t* table = a.batch.block_table + static_cast<long long>(s) * a.batch.ld_table;
-        auto inner = [&](int j, int lo, int hi) {   // rows at positions lo..hi see all of tile j
-            const int c = (tile0 + j) * kTok;
+    if (tid == 0) static_cast<Record*>(ws)[blockIdx.x].rows = 0;
+    if (begin < end) {
+        Walk walk(a, prefix, cost, share, begin, end);
+        Piece pc{};
+        // rows at positions lo..hi see all of the piece's tile j
+        auto inner = [&](int j, int lo, int hi) {
+            const int c = (pc.tile0 + j) * kTok;
             return c + kTok - 1 <= lo && (a.window == 0 || c > hi - a.window);
         };
 
         if (warp < kSoftWarps) {
             more_registers<kSoftRegs>();
-            const int x = warp >> 2, r = x * kRowsPerTile + (tid & 127);   // row of the item
-            // ---- Q: one row to a thread, taken to fp16 with a power of two, into the swizzled tile
-            const int row = block0 + r;
-            const bool live = r < rows;
-            const int pos = q.ctx - q.n + row / group;
-            float mult = 0.f;
-            if (x < tiles_q) {
-                const bf16_t* qp = a.q + static_cast<long long>(q.row0 + row / group) * a.ld_q + (h * group + row % group) * D;
-                float top = 0.f;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = live ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
-                    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+            const int x = warp >> 2;
+            const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 lanes of tensor memory, << 16
+            const uint32_t ts = tmem + lanes + S::kS + 128 * x, to = tmem + lanes + S::kO + D * x;
+            const float inf = __int_as_float(0x7F800000);
+            int tile = 0, mine = 0, items = 0;   // tiles so far; of this tile of rows; and its items
+            bool ok = true;
+            while (ok && walk.next(pc)) {
+                const int h = pc.h, n_tiles = pc.tiles, rows = pc.b.rows, p0 = pc.b.p0, p1 = pc.b.p1;
+                if (x * kRowsPerTile >= rows) {
+                    tile += n_tiles;
+                    continue;
+                }
+                const int r = x * kRowsPerTile + (tid & 127);   // row of the item
+                const int row = pc.b.row0 + r;
+                const bool live = r < rows;
+                const int token = row / group, pos = pc.q.ctx - pc.q.n + token, head = h * group + row - token * group;
+                // ---- Q: one row to a thread, taken to fp16 with a power of two, into the swizzled tile (the
+                // last item's products with it are done: its result has been read)
+                float mult;
+                {
+                    const bf16_t* qp = a.q + static_cast<long long>(pc.q.row0 + token) * a.ld_q + head * D;
+                    uint4 raw[D / 8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[e])), fabsf(bf16_hi(p[e]))));
+                    for (int c = 0; c < D / 8; ++c) raw[c] = live ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
+                    float top = 0.f;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint32_t p[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[e])), fabsf(bf16_hi(p[e]))));
+                    }
+                    const int fe = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
+                    float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
+                    const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
+                    mult = fabsf(a.scale) * 1.4426950408889634f * down;   // scores in log2, never a negative factor
+                    if (a.scale < 0.f) up = -up;
+                    const int rt = tid & 127;
+                    uint8_t* dst = q_s + x * S::kQTile + rt * 128;
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) {
+                        const uint4 v = raw[c];
+                        const float f[8] = {bf16_lo(v.x) * up, bf16_hi(v.x) * up, bf16_lo(v.y) * up, bf16_hi(v.y) * up,
+                                            bf16_lo(v.z) * up, bf16_hi(v.z) * up, bf16_lo(v.w) * up, bf16_hi(v.w) * up};
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * (kRowsPerTile * 128) + (((c & 7) ^ (rt & 7)) << 4)) =
+                            make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
+                    }
                 }
-                const int fe = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
-                float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
-                const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
-                mult = fabsf(a.scale) * 1.4426950408889634f * down;   // scores in log2, never a negative factor
-                if (a.scale < 0.f) up = -up;
-                uint8_t* dst = q_s + x * S::kQTile;
-                const int rt = tid & 127;
-#pragma unroll 4
-                for (int c = 0; c < D / 8; ++c) {
-                    const uint4 v = live ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
-                    const float f[8] = {bf16_lo(v.x) * up, bf16_hi(v.x) * up, bf16_lo(v.y) * up, bf16_hi(v.y) * up,
-                                        bf16_lo(v.z) * up, bf16_hi(v.z) * up, bf16_lo(v.w) * up, bf16_hi(v.w) * up};
-                    const uint4 o = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
-                    *reinterpret_cast<uint4*>(dst + (c >> 3) * (kRowsPerTile * 128) + rt * 128 + (((c & 7) ^ (rt & 7)) << 4)) = o;
-                }
-            }
-            tc::fence_async_smem();
-            tc::named_barrier(1, 32 * (kSoftWarps + 2));   // Q is in place (the MMA warps wait too)
+                tc::fence_async_smem();
+                tc::named_barrier(1 + x, 128 + 32);   // Q is in place (the tile's MMA warp waits too)
 
-            // ---- softmax
-            if (x < tiles_q) {
-                const int x0 = block0 + x * kRowsPerTile, x1 = block0 + min(rows, (x + 1) * kRowsPerTile) - 1;
-                const int lo = q.ctx - q.n + x0 / group, hi = q.ctx - q.n + x1 / group;
-                const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 lanes of tensor memory, << 16
-                const uint32_t ts = tmem + lanes + S::kS + 128 * x, to = tmem + lanes + S::kO + D * x;
-                const float inf = __int_as_float(0x7F800000);
+                // ---- softmax
+                const int x0 = pc.b.row0 + x * kRowsPerTile, x1 = pc.b.row0 + min(rows, (x + 1) * kRowsPerTile) - 1;
+                const int lo = pc.q.ctx - pc.q.n + x0 / group, hi = pc.q.ctx - pc.q.n + x1 / group;
                 float top = -inf, sum = 0.f;
                 uint32_t sick = 0;   // groups of dims in which this row sees a value that is not finite
-                bool ok = true;
                 for (int j = 0; j < n_tiles; ++j) {
-                    if (!wait_for(&bar.s_full[x], j & 1)) { ok = false; break; }
+                    if (!wait_for(&bar.s_full[x], (mine + j) & 1)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const int note = j & (kNotes - 1);
+                    const int note = (tile + j) & (kNotes - 1);
                     const uint4 hid4 = notes.hidden[note];
                     const uint32_t hid[4] = {hid4.x, hid4.y, hid4.z, hid4.w};
                     const bool all = inner(j, lo, hi) && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
-                    const int c0 = (tile0 + j) * kTok;
+                    const int c0 = (pc.tile0 + j) * kTok;
                     // this row sees columns [c_lo, c_hi) of the tile
                     const int c_hi = pos + 1 - c0, c_lo = a.window > 0 ? pos + 1 - a.window - c0 : 0;
                     // Weights against the running maximum as it stands; where a score passes it by 2^8
@@ -409,29 +538,48 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bar.p_full[x]);
                 }
-                // ---- the result
-                if (ok) ok = wait_for(&bar.o_full[x], 0);
+                // ---- the result, or a partial one
+                if (ok) ok = wait_for(&bar.o_full[x], items & 1);
+                if (!ok) break;
                 tc::tc_fence_after();
-                if (ok) {
-                    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                    bf16_t* o = a.out + static_cast<long long>(q.row0 + row / group) * a.ld_out + (h * group + row % group) * D;
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        float v[32];
-                        tc::tmem_ld32(to + c, v);
-                        const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
-                        if (live) {
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                *reinterpret_cast<uint4*>(o + c + e) =
-                                    make_uint4(pack_bf16x2(v[e] * k, v[e + 1] * k), pack_bf16x2(v[e + 2] * k, v[e + 3] * k),
-                                               pack_bf16x2(v[e + 4] * k, v[e + 5] * k), pack_bf16x2(v[e + 6] * k, v[e + 7] * k));
-                        }
-                    }
-                } else {
-                    failed = 1;
+                const bool whole = pc.starts && pc.ends;
+                const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
+                bf16_t* o = a.out + static_cast<long long>(pc.q.row0 + token) * a.ld_out + head * D;
+                float* part_o = partial(ws, blockIdx.x, pc.starts, S::kPartial);
+                if (!whole) {
+                    part_o[kRowsPerItem * D + r] = top;
+                    part_o[kRowsPerItem * (D + 1) + r] = sum;
                 }
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float v[32];
+                    tc::tmem_ld32(to + c, v);
+                    const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
+                    if (!live) continue;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(o + c + e) =
+                                make_uint4(pack_bf16x2(v[e] * k, v[e + 1] * k), pack_bf16x2(v[e + 2] * k, v[e + 3] * k),
+                                           pack_bf16x2(v[e + 4] * k, v[e + 5] * k), pack_bf16x2(v[e + 6] * k, v[e + 7] * k));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(part_o + r * D + c + e) = make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
+                    }
+                }
+                // the loads above are done before the next item's first product with V: its weights come after
+                tc::tc_fence_before();
+                if (tid == 0 && pc.starts && !pc.ends) {
+                    Record rec{rows, pc.b.row0, pc.q.row0, h, static_cast<int>(blockIdx.x)};
+                    while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, rec.last + 1) < pc.u1) ++rec.last;
+                    static_cast<Record*>(ws)[blockIdx.x] = rec;
+                }
+                tile += n_tiles;
+                mine += n_tiles;
+                ++items;
             }
+            if (!ok) failed = 1;
         } else if (warp < kMmaWarp) {
             // ---- unpacking: four warps K, a position to a thread, four warps V, eight positions x 16 dims
             fewer_registers<kUnpackRegs>();
@@ -448,14 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 bool hidden;       // K: the position's page is bad
                 int page;          // of the tile to be loaded next
             };
+            int p0 = 0, p1 = 0, j_end = 0;
+            const int32_t* table = nullptr;
             auto page_at = [&](int j) -> int {   // -1: no row sees the place; -2: its page is bad
-                const int p = (tile0 + j) * kTok + my_tok;
-                if (j >= n_tiles || p >= j_end || idle) return -1;
+                const int p = (pc.tile0 + j) * kTok + my_tok;
+                if (j >= pc.tiles || p >= j_end || idle) return -1;
                 const int page = __ldg(table + (p >> a.cache.page_shift));
                 return static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages) ? page : -2;
             };
             auto load = [&](Raw& r, int j) {
-                const int p = (tile0 + j) * kTok + my_tok, off = p & (ps - 1), page = r.page;
+                const int p = (pc.tile0 + j) * kTok + my_tok, off = p & (ps - 1), page = r.page;
                 r.page = page_at(j + 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
@@ -465,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 r.hidden = page == -2;
                 if (page == -2) flag(a.status, LORA_DEV_BAD_PAGE);
                 if (page < 0) return;
-                const uint8_t* b = block_of(a.cache, page, h);
+                const uint8_t* b = block_of(a.cache, page, pc.h);
                 if (is_k) {
 #pragma unroll
                     for (int t = 0; t < D / 32; ++t) r.w[t] = __ldg(reinterpret_cast<const uint4*>(b + off * (D / 2)) + t);
@@ -490,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     }
                 }
             };
-            auto store_k = [&](const Raw& r, int j) {
-                uint8_t* kd = k_s + (j & (kStages - 1)) * S::kKTile + u * 128;
+            auto store_k = [&](const Raw& r, int j, int n) {   // n: the tile's place among all of the range
+                uint8_t* kd = k_s + (n & (kStages - 1)) * S::kKTile + u * 128;
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     // 16 bytes of the row hold words (t, 0..kWords-1)
@@ -511,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         *reinterpret_cast<uint4*>(kd + (i >> 1) * (kTok * 128) + ((c ^ (u & 7)) << 4)) = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
-                const int n = j & (kNotes - 1);
+                n &= kNotes - 1;
                 const uint32_t gone = __ballot_sync(0xFFFFFFFFu, r.hidden);
                 if (lane == 0) reinterpret_cast<uint32_t*>(&notes.hidden[n])[u >> 5] = gone;
                 if (!inner(j, p0, p1)) {
@@ -525,11 +675,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     }
                 }
             };
-            auto store_v = [&](Raw& r, int j) {
+            auto store_v = [&](Raw& r, int j, int n) {
                 if (idle) return;
                 if (!inner(j, p0, p1)) {
                     // positions past the last row's, and values that are not finite, count as zeros
-                    const int p = (tile0 + j) * kTok + my_tok;
+                    const int p = (pc.tile0 + j) * kTok + my_tok;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = p + 2 * i;
@@ -542,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         low &= keep;
                     }
                 }
-                uint8_t* vd = v_s + (j & (kStages - 1)) * S::kVTile + half * S::kVHalf;
+                uint8_t* vd = v_s + (n & (kStages - 1)) * S::kVTile + half * S::kVHalf;
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     uint32_t v[4][4];   // [pair of positions][dim]
@@ -561,37 +711,47 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             uint64_t* full = is_k ? bar.k_full : bar.v_full;
             uint64_t* free = is_k ? bar.k_free : bar.v_free;
             // a tile on its way, and the page of the one after it
-            Raw r;
-            r.page = page_at(0);
-            load(r, 0);
-            for (int j = 0; j < n_tiles; ++j) {
-                const int st = j & (kStages - 1);
-                if (j >= kStages && !wait_for(&free[st], ((j / kStages) & 1) ^ 1)) { failed = 1; break; }
-                if (is_k) store_k(r, j); else store_v(r, j);
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&full[st]);
-                if (j + 1 < n_tiles) load(r, j + 1);
+            int n = 0;
+            bool ok = true;
+            while (ok && walk.next(pc)) {
+                p0 = pc.b.p0;
+                p1 = pc.b.p1;
+                j_end = max(0, p1 + 1);
+                table = a.batch.block_table + static_cast<long long>(pc.s) * a.batch.ld_table;
+                Raw r;
+                r.page = page_at(0);
+                load(r, 0);
+                for (int j = 0; j < pc.tiles; ++j, ++n) {
+                    const int st = n & (kStages - 1);
+                    if (n >= kStages && !wait_for(&free[st], ((n / kStages) & 1) ^ 1)) { ok = false; break; }
+                    if (is_k) store_k(r, j, n); else store_v(r, j, n);
+                    tc::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&full[st]);
+                    if (j + 1 < pc.tiles) load(r, j + 1);
+                }
             }
+            if (!ok) failed = 1;
         } else {
             // ---- the products
             // The whole warp runs the loop and one elected lane issues: values that the compiler knows to be
             // the warp's own stay in uniform registers, where the instruction wants its operands.
             fewer_registers<kMmaRegs>();
             const int x = warp - kMmaWarp;   // the tile of rows whose products this warp issues
-            if (x < 2) tc::named_barrier(1, 32 * (kSoftWarps + 2));
-            if (x < tiles_q) {
+            if (x < 2) {
                 constexpr uint32_t id_s = idesc_f16(kRowsPerTile, kTok), id_o = idesc_f16(kRowsPerTile, D);
                 const uint32_t t0 = __shfl_sync(0xFFFFFFFFu, tmem, 0);
                 const uint32_t s_t = t0 + S::kS + 128 * x, o_t = t0 + S::kO + D * x;
                 const uint64_t q_d = tc::sdesc_sw128(tc::smem_u32(q_s) + x * S::kQTile);
                 const uint64_t k_d = tc::sdesc_sw128(tc::smem_u32(k_s)), v_d = tc::sdesc_sw128(tc::smem_u32(v_s));
                 const bool lead = elect_one();
-                // turn n of this tile of rows
-                auto my_turn = [&](int n) { return tiles_q == 1 || wait_polling(&bar.turn[x], n & 1); };
-                auto scores = [&](int j) -> bool {
-                    const int st = j & (kStages - 1);
-                    if (!wait_polling(&bar.k_full[st], (j / kStages) & 1)) return false;
+                int n = 0, mine = 0, turns = 0;   // tiles so far; of this tile of rows; its turns
+                bool both = false;
+                auto my_turn = [&]() { return !both || wait_polling(&bar.turn[x], turns++ & 1); };
+                auto your_turn = [&]() { if (both) tc::mbar_arrive(&bar.turn[x ^ 1]); };
+                auto scores = [&](int t) -> bool {   // t: the tile's place among all of the range
+                    const int st = t & (kStages - 1);
+                    if (!wait_polling(&bar.k_full[st], (t / kStages) & 1)) return false;
                     tc::tc_fence_after();
                     if (lead) {
                         const uint64_t k_j = k_d + static_cast<uint64_t>(st * (S::kKTile >> 4));   // descriptors count 16 bytes
@@ -602,33 +762,51 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         }
                         tc::mma_commit(&bar.s_full[x]);
                         tc::mma_commit(&bar.k_free[st]);
-                        if (tiles_q == 1) tc::mma_commit(&bar.k_free[st]);   // for the tile of rows that is not there
-                        else tc::mbar_arrive(&bar.turn[x ^ 1]);
+                        your_turn();
                     }
                     __syncwarp();
                     return true;
                 };
-                bool ok = (x == 0 || my_turn(0)) && scores(0);
-                for (int j = 0; ok && j < n_tiles; ++j) {
-                    const int st = j & (kStages - 1);
-                    ok = wait_polling(&bar.v_full[st], (j / kStages) & 1) && wait_polling(&bar.p_full[x], j & 1) && my_turn(j + x);
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    if (lead) {
-                        const uint64_t v_j = v_d + static_cast<uint64_t>(st * (S::kVTile >> 4));
-#pragma unroll
-                        for (int k = 0; k < kTok / 16; ++k)
-                            mma_ts(o_t, s_t + 8 * k, v_j + (((k >> 2) * S::kVHalf + (k & 3) * 32) >> 4), id_o, j > 0 || k > 0);
-                        if (j + 1 < n_tiles) {
-                            tc::mma_commit(&bar.v_free[st]);
-                            if (tiles_q == 1) tc::mma_commit(&bar.v_free[st]);
-                        } else {
-                            tc::mma_commit(&bar.o_full[x]);
-                            if (tiles_q == 2) tc::mbar_arrive(&bar.turn[x ^ 1]);
+                bool ok = true, first = true;   // first: no turn has been taken
+                while (ok && walk.next(pc)) {
+                    const int n_tiles = pc.tiles;
+                    both = pc.b.rows > kRowsPerTile;
+                    if (x == 1 && !both) {
+                        // the stages pass this tile of rows by, in step (a parity tells a phase only from its neighbours)
+                        for (int j = 0; ok && j < n_tiles; ++j, ++n) {
+                            const int st = n & (kStages - 1);
+                            ok = wait_polling(&bar.k_full[st], (n / kStages) & 1);
+                            if (lead) tc::mbar_arrive(&bar.k_free[st]);
+                            ok = ok && wait_polling(&bar.v_full[st], (n / kStages) & 1);
+                            if (lead) tc::mbar_arrive(&bar.v_free[st]);
                         }
+                        continue;
                     }
-                    __syncwarp();
-                    if (j + 1 < n_tiles) ok = scores(j + 1);
+                    tc::named_barrier(1 + x, 128 + 32);
+                    // the first tile of rows goes first; later items wait for the turn that the last one left over
+                    ok = ((x == 0 && first) || my_turn()) && scores(n);
+                    if (both) first = false;
+                    for (int j = 0; ok && j < n_tiles; ++j) {
+                        const int st = (n + j) & (kStages - 1);
+                        ok = wait_polling(&bar.v_full[st], ((n + j) / kStages) & 1) && wait_polling(&bar.p_full[x], (mine + j) & 1) && my_turn();
+                        if (!ok) break;
+                        tc::tc_fence_after();
+                        if (lead) {
+                            const uint64_t v_j = v_d + static_cast<uint64_t>(st * (S::kVTile >> 4));
+#pragma unroll
+                            for (int k = 0; k < kTok / 16; ++k)
+                                mma_ts(o_t, s_t + 8 * k, v_j + (((k >> 2) * S::kVHalf + (k & 3) * 32) >> 4), id_o, j > 0 || k > 0);
+                            tc::mma_commit(&bar.v_free[st]);
+                            if (j + 1 == n_tiles) {
+                                tc::mma_commit(&bar.o_full[x]);
+                                your_turn();
+                            }
+                        }
+                        __syncwarp();
+                        if (j + 1 < n_tiles) ok = scores(n + j + 1);
+                    }
+                    n += n_tiles;
+                    mine += n_tiles;
                 }
                 if (!ok) failed = 1;
             }
@@ -638,14 +816,49 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     tc::tc_fence_before();
     __syncthreads();
     if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
-    if (tid == 0 && work && failed) flag(a.status, LORA_DEV_TIMEOUT);
+    if (tid == 0 && failed) flag(a.status, LORA_DEV_TIMEOUT);
+}
+
+// Joins the pieces of the item that begins in CTA b's range and goes on, in
+// order: four CTAs to a record, a quarter of the rows each.
+template <int D>
+__global__ void __launch_bounds__(256) kv4_many_join_kernel(AttendArgs a, void* ws)
+{
+    using S = Shape<D>;
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int b = blockIdx.x >> 2, group = a.n_heads / a.cache.n_kv;
+    const Record u = static_cast<const Record*>(ws)[b];
+    const float inf = __int_as_float(0x7F800000);
+    for (int e = (blockIdx.x & 3) * 256 + threadIdx.x; e < u.rows * (D / 4); e += 1024) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4;
+        float m = -inf, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = b; k <= u.last; ++k) m = fmaxf(m, partial(ws, k, k == b, S::kPartial)[kRowsPerItem * D + r]);
+#pragma unroll 4
+        for (int k = b; k <= u.last; ++k) {
+            const float* p = partial(ws, k, k == b, S::kPartial);
+            const float w = m == -inf ? 0.f : ex2(p[kRowsPerItem * D + r] - m);
+            const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
+            o.x = fmaf(v.x, w, o.x);
+            o.y = fmaf(v.y, w, o.y);
+            o.z = fmaf(v.z, w, o.z);
+            o.w = fmaf(v.w, w, o.w);
+            l = fmaf(p[kRowsPerItem * (D + 1) + r], w, l);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int row = u.block_row0 + r;
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.seq_row0 + row / group) * a.ld_out + (u.h * group + row % group) * D + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
 }
 
 template <int D>
-cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
+cudaError_t run(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
 {
     using S = Shape<D>;
-    constexpr int kMaxSmem = 226 * 1024;
+    constexpr int kMaxSmem = 220 * 1024;
     static_assert(S::kSmem + 4 * (kMaxSeqs + 1) <= kMaxSmem, "shared memory");
     static bool attr_set = false;
     if (!attr_set) {
@@ -653,20 +866,27 @@ cudaError_t run(const AttendArgs& a, int few_rows, cudaStream_t stream)
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    const int group = a.n_heads / a.cache.n_kv;
-    // an upper bound on the items: a sequence's last block may be short
-    const long long items = (static_cast<long long>(a.batch.n_rows) * group / kRowsPerItem + a.batch.n_seqs) * a.cache.n_kv;
-    PdlLaunch l(dim3(static_cast<unsigned>(items)), kThreads, S::kSmem + 4 * (a.batch.n_seqs + 1), stream);
-    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D>, a, few_rows);
+    const int ctas = std::min(kMaxCtas, device_sms());
+    PdlLaunch l(dim3(ctas), kThreads, S::kSmem + 4 * (a.batch.n_seqs + 1), stream);
+    cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D>, a, few_rows, ws);
+    if (e != cudaSuccess) return e;
+    note_launch();
+    PdlLaunch j(dim3(4 * ctas), 256, 0, stream);
+    e = cudaLaunchKernelEx(&j.cfg, kv4_many_join_kernel<D>, a, ws);
     note_launch();
     return e;
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, cudaStream_t stream)
+size_t kv4_many_workspace(int head_dim)
 {
-    return a.cache.head_dim == 64 ? run<64>(a, few_rows, stream) : run<128>(a, few_rows, stream);
+    return (kRecordBytes + static_cast<size_t>(kMaxCtas) * 2 * kRowsPerItem * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
+}
+
+cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
+{
+    return a.cache.head_dim == 64 ? run<64>(a, few_rows, ws, stream) : run<128>(a, few_rows, ws, stream);
 }
 
 }  // namespace lora
