@@ -45,8 +45,8 @@ constexpr int kNotes = 4;                  // tiles of which the softmax has not
 // 256 * 160 + 256 * 64 + 128 * 32 = 640 * 96.
 constexpr int kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
 static_assert(2 * kSoftRegs + 2 * kUnpackRegs + kMmaRegs <= 5 * 96, "registers");
-constexpr int kItemCost = 2;               // an item's start and end, in tiles
-constexpr int kMinRange = 4;               // a CTA's range, at least
+constexpr int kItemCost = 4;               // an item's start and end, in tiles
+constexpr int kMinRange = 6;               // a CTA's range, at least
 constexpr float kSlack = 8.f, kLift = 7.f; // as in the kernel for few rows
 constexpr uint32_t kTmemCols = 512;
 
@@ -404,6 +404,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 lanes of tensor memory, << 16
             const uint32_t ts = tmem + lanes + S::kS + 128 * x, to = tmem + lanes + S::kO + D * x;
             const float inf = __int_as_float(0x7F800000);
+            // f(token of the sequence, column of q and out, place in the swizzled tile) for every 16 bytes of
+            // the warp's 32 rows, a row to 2 D / 16 neighbouring lanes
+            auto warp_rows = [&](const Piece& p, uint8_t* tile_s, auto f) {
+                constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+                const int c = lane % kLanes;
+                int r = (x * 4 + (warp & 3)) * 32 + lane / kLanes;
+                int t = (p.b.row0 + r) / group, hh = p.b.row0 + r - t * group;
+#pragma unroll 4
+                for (int i = 0; i < 32; i += kStep, r += kStep) {
+                    if (r < p.b.rows) {
+                        const int rt = r & 127;
+                        f(static_cast<long long>(t), (p.h * group + hh) * D + 8 * c,
+                          tile_s + (c >> 3) * (kRowsPerTile * 128) + rt * 128 + (((c & 7) ^ (rt & 7)) << 4));
+                    }
+                    for (hh += kStep; hh >= group; hh -= group) ++t;
+                }
+            };
             int tile = 0, mine = 0, items = 0;   // tiles so far; of this tile of rows; and its items
             bool ok = true;
             while (ok && walk.next(pc)) {
@@ -415,15 +432,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 const int r = x * kRowsPerTile + (tid & 127);   // row of the item
                 const int row = pc.b.row0 + r;
                 const bool live = r < rows;
-                const int token = row / group, pos = pc.q.ctx - pc.q.n + token, head = h * group + row - token * group;
+                const int pos = pc.q.ctx - pc.q.n + row / group;
                 // ---- Q: one row to a thread, taken to fp16 with a power of two, into the swizzled tile (the
                 // last item's products with it are done: its result has been read)
                 float mult;
                 {
-                    const bf16_t* qp = a.q + static_cast<long long>(pc.q.row0 + token) * a.ld_q + head * D;
+                    // the warp's rows come in whole lines (16 bytes of 32 rows to an instruction cost as many
+                    // lines as rows), then each thread takes its own
+                    warp_rows(pc, q_s + x * S::kQTile, [&](long long token_row, int col, uint8_t* at) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(at)),
+                                     "l"(a.q + (pc.q.row0 + token_row) * a.ld_q + col)
+                                     : "memory");
+                    });
+                    asm volatile("cp.async.wait_all;\n" ::: "memory");
+                    __syncwarp();
+                    const int rt = tid & 127;
+                    uint8_t* dst = q_s + x * S::kQTile + rt * 128;
+                    auto at = [&](int c) { return reinterpret_cast<uint4*>(dst + (c >> 3) * (kRowsPerTile * 128) + (((c & 7) ^ (rt & 7)) << 4)); };
                     uint4 raw[D / 8];
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) raw[c] = live ? *reinterpret_cast<const uint4*>(qp + 8 * c) : make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < D / 8; ++c) raw[c] = live ? *at(c) : make_uint4(0, 0, 0, 0);
                     float top = 0.f;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
@@ -436,15 +464,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
                     mult = fabsf(a.scale) * 1.4426950408889634f * down;   // scores in log2, never a negative factor
                     if (a.scale < 0.f) up = -up;
-                    const int rt = tid & 127;
-                    uint8_t* dst = q_s + x * S::kQTile + rt * 128;
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
                         const uint4 v = raw[c];
                         const float f[8] = {bf16_lo(v.x) * up, bf16_hi(v.x) * up, bf16_lo(v.y) * up, bf16_hi(v.y) * up,
                                             bf16_lo(v.z) * up, bf16_hi(v.z) * up, bf16_lo(v.w) * up, bf16_hi(v.w) * up};
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * (kRowsPerTile * 128) + (((c & 7) ^ (rt & 7)) << 4)) =
-                            make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
+                        *at(c) = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
                     }
                 }
                 tc::fence_async_smem();
@@ -543,29 +568,40 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 if (!ok) break;
                 tc::tc_fence_after();
                 const bool whole = pc.starts && pc.ends;
-                const float inv = !whole ? 1.f : sum == 0.f ? 0.f : 1.f / sum;
-                bf16_t* o = a.out + static_cast<long long>(pc.q.row0 + token) * a.ld_out + head * D;
-                float* part_o = partial(ws, blockIdx.x, pc.starts, S::kPartial);
-                if (!whole) {
-                    part_o[kRowsPerItem * D + r] = top;
-                    part_o[kRowsPerItem * (D + 1) + r] = sum;
-                }
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                if (whole) {   // through the place of Q, whose products are done, to whole lines
+                    const int rt = tid & 127;
+                    uint8_t* dst = q_s + x * S::kQTile + rt * 128;
 #pragma unroll
-                for (int c = 0; c < D; c += 32) {
-                    float v[32];
-                    tc::tmem_ld32(to + c, v);
-                    const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
-                    if (!live) continue;
-                    if (whole) {
+                    for (int c = 0; c < D; c += 32) {
+                        float v[32];
+                        tc::tmem_ld32(to + c, v);
+                        const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4*>(o + c + e) =
+                        for (int e = 0; e < 32; e += 8) {
+                            const int ch = (c + e) >> 3;
+                            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kRowsPerTile * 128) + (((ch & 7) ^ (rt & 7)) << 4)) =
                                 make_uint4(pack_bf16x2(v[e] * k, v[e + 1] * k), pack_bf16x2(v[e + 2] * k, v[e + 3] * k),
                                            pack_bf16x2(v[e + 4] * k, v[e + 5] * k), pack_bf16x2(v[e + 6] * k, v[e + 7] * k));
-                    } else {
+                        }
+                    }
+                    __syncwarp();
+                    warp_rows(pc, q_s + x * S::kQTile, [&](long long token_row, int col, uint8_t* at) {
+                        *reinterpret_cast<uint4*>(a.out + (pc.q.row0 + token_row) * a.ld_out + col) = *reinterpret_cast<uint4*>(at);
+                    });
+                    __syncwarp();
+                } else {
+                    float* part_o = partial(ws, blockIdx.x, pc.starts, S::kPartial);
+                    part_o[kRowsPerItem * D + r] = top;
+                    part_o[kRowsPerItem * (D + 1) + r] = sum;
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        float v[32];
+                        tc::tmem_ld32(to + c, v);
+                        const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : 1.f;
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(part_o + r * D + c + e) = make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
+                            if (live) *reinterpret_cast<float4*>(part_o + r * D + c + e) = make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
                     }
                 }
                 // the loads above are done before the next item's first product with V: its weights come after
@@ -718,6 +754,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 p1 = pc.b.p1;
                 j_end = max(0, p1 + 1);
                 table = a.batch.block_table + static_cast<long long>(pc.s) * a.batch.ld_table;
+                if (is_k) {   // these warps are ahead of the softmax: Q's lines are on their way when it comes for them
+                    for (int i = u; i < pc.b.rows * (D / 64); i += 128) {
+                        const int row = pc.b.row0 + i / (D / 64), t = row / group;
+                        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(a.q + static_cast<long long>(pc.q.row0 + t) * a.ld_q +
+                                                                       (pc.h * group + row - t * group) * D + 64 * (i % (D / 64))));
+                    }
+                }
                 Raw r;
                 r.page = page_at(0);
                 load(r, 0);
@@ -788,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     if (both) first = false;
                     for (int j = 0; ok && j < n_tiles; ++j) {
                         const int st = (n + j) & (kStages - 1);
-                        ok = wait_polling(&bar.v_full[st], ((n + j) / kStages) & 1) && wait_polling(&bar.p_full[x], (mine + j) & 1) && my_turn();
+                        ok = wait_polling(&bar.v_full[st], ((n + j) / kStages) & 1) && my_turn() && wait_polling(&bar.p_full[x], (mine + j) & 1);
                         if (!ok) break;
                         tc::tc_fence_after();
                         if (lead) {
