@@ -42,8 +42,8 @@ constexpr int kWarps = 20, kThreads = 32 * kWarps;   // two MMA warps; their two
 constexpr int kNotes = 4;                  // tiles of which the softmax has notes (see Notes)
 // Registers: 96 a thread at launch; the softmax warps, which hold a row's
 // scores and weights, take what the others give up:
-// 256 * 160 + 256 * 64 + 128 * 32 = 640 * 96.
-constexpr int kSoftRegs = 160, kUnpackRegs = 64, kMmaRegs = 32;
+// 256 * 144 + 256 * 80 + 128 * 32 <= 640 * 96.
+constexpr int kSoftRegs = 144, kUnpackRegs = 80, kMmaRegs = 32;
 static_assert(2 * kSoftRegs + 2 * kUnpackRegs + kMmaRegs <= 5 * 96, "registers");
 constexpr int kItemCost = 4;               // an item's start and end, in tiles
 constexpr int kMinRange = 6;               // a CTA's range, at least
@@ -404,21 +404,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 lanes of tensor memory, << 16
             const uint32_t ts = tmem + lanes + S::kS + 128 * x, to = tmem + lanes + S::kO + D * x;
             const float inf = __int_as_float(0x7F800000);
-            // f(token of the sequence, column of q and out, place in the swizzled tile) for every 16 bytes of
-            // the warp's 32 rows, a row to 2 D / 16 neighbouring lanes
-            auto warp_rows = [&](const Piece& p, uint8_t* tile_s, auto f) {
+            // f(which, element of a matrix with this leading dimension, place in the swizzled tile) for every 16 bytes
+            // of the warp's 32 rows, a row to D / 8 neighbouring lanes
+            auto warp_rows = [&](const Piece& p, int ld, uint8_t* tile_s, auto f) {
                 constexpr int kLanes = D / 8, kStep = 32 / kLanes;
                 const int c = lane % kLanes;
                 int r = (x * 4 + (warp & 3)) * 32 + lane / kLanes;
-                int t = (p.b.row0 + r) / group, hh = p.b.row0 + r - t * group;
-#pragma unroll 4
-                for (int i = 0; i < 32; i += kStep, r += kStep) {
-                    if (r < p.b.rows) {
-                        const int rt = r & 127;
-                        f(static_cast<long long>(t), (p.h * group + hh) * D + 8 * c,
-                          tile_s + (c >> 3) * (kRowsPerTile * 128) + rt * 128 + (((c & 7) ^ (rt & 7)) << 4));
+                const int t = (p.b.row0 + r) / group, dt = kStep / group, dh = kStep - dt * group;
+                int hh = p.b.row0 + r - t * group;
+                long long at = static_cast<long long>(p.q.row0 + t) * ld + (p.h * group + hh) * D + 8 * c;
+                const int on = dt * ld + dh * D, wrap = ld - group * D;   // to the next row, and where that is the next token's
+                uint8_t* place = tile_s + (c >> 3) * (kRowsPerTile * 128) + (r & 127) * 128;
+#pragma unroll
+                for (int i = 0; i < 32; i += kStep) {
+                    if (r < p.b.rows) f(i / kStep, at, place + (((c & 7) ^ (r & 7)) << 4));
+                    r += kStep;
+                    place += kStep * 128;
+                    hh += dh;
+                    at += on;
+                    if (hh >= group) {
+                        hh -= group;
+                        at += wrap;
                     }
-                    for (hh += kStep; hh >= group; hh -= group) ++t;
                 }
             };
             int tile = 0, mine = 0, items = 0;   // tiles so far; of this tile of rows; and its items
@@ -439,10 +446,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 {
                     // the warp's rows come in whole lines (16 bytes of 32 rows to an instruction cost as many
                     // lines as rows), then each thread takes its own
-                    warp_rows(pc, q_s + x * S::kQTile, [&](long long token_row, int col, uint8_t* at) {
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(at)),
-                                     "l"(a.q + (pc.q.row0 + token_row) * a.ld_q + col)
-                                     : "memory");
+                    warp_rows(pc, a.ld_q, q_s + x * S::kQTile, [&](int, long long e, uint8_t* at) {
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(at)), "l"(a.q + e) : "memory");
                     });
                     asm volatile("cp.async.wait_all;\n" ::: "memory");
                     __syncwarp();
@@ -452,13 +457,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     uint4 raw[D / 8];
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) raw[c] = live ? *at(c) : make_uint4(0, 0, 0, 0);
-                    float top = 0.f;
+                    __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) {
                         const uint32_t p[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(p[e])), fabsf(bf16_hi(p[e]))));
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t u = p[e] & 0x7FFF7FFFu;
+                            top2 = __hmax2(top2, *reinterpret_cast<const __nv_bfloat162*>(&u));
+                        }
                     }
+                    const float top = fmaxf(__low2float(top2), __high2float(top2));
                     const int fe = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
                     float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
                     const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
@@ -490,8 +499,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     const int c0 = (pc.tile0 + j) * kTok;
                     // this row sees columns [c_lo, c_hi) of the tile
                     const int c_hi = pos + 1 - c0, c_lo = a.window > 0 ? pos + 1 - a.window - c0 : 0;
-                    // Weights against the running maximum as it stands; where a score passes it by 2^8
-                    // (always in the first tile) the maximum moves, O is rescaled and they are taken again.
+                    auto highest = [&](const float (&m)[4]) {
+                        const float h = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mult;
+                        return h != h ? -inf : h;   // 0 * -inf: nothing seen
+                    };
+                    if (j == 0) {   // the first tile's maximum
+                        float m[4] = {-inf, -inf, -inf, -inf};
+#pragma unroll 1
+                        for (int c = 0; c < kTok / 32; ++c) {
+                            uint32_t w[32];
+                            tmem_ld32_start(ts + 32 * c, w);
+                            tmem_wait_ld();
+                            after_wait(w);
+                            const uint32_t see = bits_in(c_lo - 32 * c, c_hi - 32 * c) & ~(c == 0 ? hid[0] : c == 1 ? hid[1] : c == 2 ? hid[2] : hid[3]);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], (see >> e) & 1u ? __uint_as_float(w[e]) : -inf);
+                        }
+                        top = highest(m);
+                    }
+                    // Weights against the running maximum as it stands; where a score passes it by 2^8 the
+                    // maximum moves, O is rescaled and they are taken again.
                     uint32_t p[kTok / 2];
                     float2 part[2];
                     for (;;) {
@@ -531,14 +558,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                             }
                         };
                         if (all) weigh(std::false_type{}); else weigh(std::true_type{});
-                        float high = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mult;
-                        if (high != high) high = -inf;   // 0 * -inf: nothing seen
+                        const float high = highest(m);
                         if (!__any_sync(0xFFFFFFFFu, high > top + kSlack)) break;
                         const float next = fmaxf(high, top);
                         const float keep = next == -inf ? 1.f : ex2(top - next);
                         top = next;
                         sum *= keep;
-                        if (j > 0) {   // the last product with V is done: this tile's scores were issued after it
+                        {   // (the last product with V is done: this tile's scores were issued after it)
 #pragma unroll
                             for (int c = 0; c < D; c += 16) {
                                 uint32_t w[16];
@@ -572,23 +598,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 if (whole) {   // through the place of Q, whose products are done, to whole lines
                     const int rt = tid & 127;
                     uint8_t* dst = q_s + x * S::kQTile + rt * 128;
+                    uint32_t v[2][32];   // one load ahead of the arithmetic
+                    tmem_ld32_start(to, v[0]);
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        float v[32];
-                        tc::tmem_ld32(to + c, v);
-                        const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t(&w)[32] = v[c & 1];
+                        tmem_wait_ld();
+                        after_wait(w);
+                        if (c + 1 < D / 32) tmem_ld32_start(to + 32 * (c + 1), v[(c + 1) & 1]);
+                        const float k = (sick >> (32 * c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
+                        auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(w[e]) * k, __uint_as_float(w[e + 1]) * k); };
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
-                            const int ch = (c + e) >> 3;
+                            const int ch = (32 * c + e) >> 3;
                             *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kRowsPerTile * 128) + (((ch & 7) ^ (rt & 7)) << 4)) =
-                                make_uint4(pack_bf16x2(v[e] * k, v[e + 1] * k), pack_bf16x2(v[e + 2] * k, v[e + 3] * k),
-                                           pack_bf16x2(v[e + 4] * k, v[e + 5] * k), pack_bf16x2(v[e + 6] * k, v[e + 7] * k));
+                                make_uint4(pair(e), pair(e + 2), pair(e + 4), pair(e + 6));
                         }
                     }
                     __syncwarp();
-                    warp_rows(pc, q_s + x * S::kQTile, [&](long long token_row, int col, uint8_t* at) {
-                        *reinterpret_cast<uint4*>(a.out + (pc.q.row0 + token_row) * a.ld_out + col) = *reinterpret_cast<uint4*>(at);
-                    });
+                    warp_rows(pc, a.ld_out, q_s + x * S::kQTile, [&](int, long long e, uint8_t* at) { *reinterpret_cast<uint4*>(a.out + e) = *reinterpret_cast<uint4*>(at); });
                     __syncwarp();
                 } else {
                     float* part_o = partial(ws, blockIdx.x, pc.starts, S::kPartial);
