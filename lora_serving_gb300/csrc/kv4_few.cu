@@ -39,7 +39,7 @@ using namespace kv4;
 constexpr int kTile = 32;          // positions per tile: two halves of 16, the products' M
 constexpr int kHalf = 16;
 constexpr int kUnitCost = 2;       // a unit's start (tables, q, the first copies), in tiles
-constexpr int kMinRange = 3;       // a warp's range, at least: a tile and the unit's start
+constexpr float kNone = -3e38f;    // the running maximum before any score (finite, so that no difference is NaN)
 constexpr float kSlack = 8.f;      // log2 by which a score may pass the running maximum
 constexpr float kLift = 7.f;       // weights carry 2^7: at most 2^15, and fp16 holds them down to 2^-31 of the largest
 
@@ -69,7 +69,7 @@ struct Shape {
 };
 
 // Ranges are one per warp; range w of n begins here.
-__device__ __forceinline__ int range_count(int total, int warps) { return min(warps, max(1, total / kMinRange)); }
+__device__ __forceinline__ int range_count(int total, int warps) { return min(warps, max(1, total)); }
 __device__ __forceinline__ int range_at(int total, int n, int w)
 {
     return static_cast<int>(static_cast<long long>(total) * min(w, n) / n);
@@ -128,14 +128,366 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
+// A warp's running result of a unit: fragments of the sums, and the maximum
+// and the lane's part of the sum of weights of rows 2t, 2t + 1.
+template <int D, int NT>
+struct Sums {
+    float acc[D / 16][NT][4], top[NT][2], sum[NT][2];
+};
+
+// One warp: `n_mine` tiles from tile `tile` of sequence s, kv head h.
+template <int D, int NT>
+__device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring, int s, int h, const Seq& q, int tile, int n_mine,
+                                             Sums<D, NT>& out)
+{
+    using S = Shape<D, NT>;
+    constexpr int kGroups = S::kGroups, kWords = S::kWords, kStages = S::kStages;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size, rows = q.n * group;
+    const int p0 = q.ctx - q.n;   // position of the first row
+    const int32_t* table = a.batch.block_table + static_cast<long long>(s) * a.batch.ld_table;
+    const float inf = __int_as_float(0x7F800000);
+
+    // ---- the ring
+    const int pos0 = tile * kTile;
+    const uint8_t* head_pages = a.cache.pages + static_cast<long long>(h) * block_bytes(ps, D);
+    const bool split = ps < kTile;   // a tile is two pages
+    unsigned has = 0;                // stages' halves that hold positions
+    auto page_at = [&](int pos) -> int { return pos < q.ctx ? __ldg(table + (pos >> a.cache.page_shift)) : -1; };
+    int next0 = n_mine > 0 ? page_at(pos0) : -1, next1 = n_mine > 0 && split ? page_at(pos0 + kHalf) : -1;
+    auto issue = [&](int i) {
+        const int pos = pos0 + i * kTile, st = i % kStages;
+        const int page0 = next0, page1 = split ? next1 : page0;
+        if (i + 1 < n_mine) {
+            next0 = page_at(pos + kTile);
+            if (split) next1 = page_at(pos + kTile + kHalf);
+        }
+        has &= ~(3u << (2 * st));
+        if (i < n_mine) {
+            const bool ok0 = static_cast<unsigned>(page0) < static_cast<unsigned>(a.cache.n_pages);
+            const bool ok1 = static_cast<unsigned>(page1) < static_cast<unsigned>(a.cache.n_pages) && pos + kHalf < q.ctx;
+            has |= (ok0 ? 1u : 0u) << (2 * st) | (ok1 ? 2u : 0u) << (2 * st);
+            if (lane == 0 && ((!ok0 && pos < q.ctx) || (!ok1 && pos + kHalf < q.ctx))) flag(a.status, LORA_DEV_BAD_PAGE);
+            const int off0 = pos & (ps - 1), off1 = (pos + kHalf) & (ps - 1);
+            const uint8_t* b0 = head_pages + static_cast<long long>(page0) * a.cache.page_stride;
+            const uint8_t* b1 = head_pages + static_cast<long long>(page1) * a.cache.page_stride;
+            const uint32_t dst = tc::smem_u32(ring + st * S::kStage) + 16 * lane;
+            const uint8_t* s0 = b0 + off0 * (D / 2) + 16 * lane;
+            const uint8_t* s1 = b1 + off1 * (D / 2) + 16 * lane;
+#pragma unroll
+            for (int c = 0; c < S::kCodeBytes; c += 512) {
+                if (ok0) {
+                    copy16(dst + c, s0 + c);
+                    copy16(dst + S::kVAt + c, s0 + v_codes_off(ps, D) + c);
+                }
+                if (ok1) {
+                    copy16(dst + S::kCodeBytes + c, s1 + c);
+                    copy16(dst + S::kVAt + S::kCodeBytes + c, s1 + v_codes_off(ps, D) + c);
+                }
+            }
+            // params: eight lanes to a half of K's, then of V's
+            const int pl = lane & 7, second = (lane >> 3) & 1;
+            if (pl < S::kParamBytes / 16 && (second ? ok1 : ok0)) {
+                const uint8_t* src = (second ? b1 + off1 * 4 * kGroups : b0 + off0 * 4 * kGroups) +
+                                     (lane & 16 ? v_params_off(ps, D) : k_params_off(ps, D)) + 16 * pl;
+                copy16(tc::smem_u32(ring + st * S::kStage) + S::kKpAt + (lane >> 3) * S::kParamBytes + 16 * pl, src);
+            }
+        }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // ---- q as fragments: row n = 8 nt + g, dims 32 w + 8 t + (0..7)
+    uint32_t qf[NT][kWords][4];     // pairs (dims e, e + 4); odd pairs carry 1/16
+    float mult[NT][2], qsum[NT][kGroups][2], qoff[NT][kGroups][2];   // of rows 2t, 2t + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = 8 * nt + g;
+        uint4 raw[kWords];
+        float top = 0.f;
+        const bf16_t* qp = a.q + static_cast<long long>(q.row0 + r / group) * a.ld_q + (h * group + r % group) * D + 8 * t;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            raw[w] = r < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
+            const uint32_t part[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(part[e])), fabsf(bf16_hi(part[e]))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        // a power of two that takes the row's largest into [2^7, 2^8)
+        const int e = static_cast<int>(__float_as_uint(top) >> 23);
+        const int fe = min(261 - e, 253);
+        const float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
+        const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
+        // sums of the fp16 values as the product takes them: of q, and of 1024 times the operand
+        float sum[kGroups], ofs[kGroups];
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) sum[gr] = ofs[gr] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+            const float f[8] = {bf16_lo(raw[w].x) * up, bf16_hi(raw[w].x) * up, bf16_lo(raw[w].y) * up, bf16_hi(raw[w].y) * up,
+                                bf16_lo(raw[w].z) * up, bf16_hi(raw[w].z) * up, bf16_lo(raw[w].w) * up, bf16_hi(raw[w].w) * up};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float k = (i & 1) ? 1.f / 16 : 1.f;
+                qf[nt][w][i] = pack_f16x2(f[i] * k, f[i + 4] * k);
+                const float2 h = __half22float2(as_h2(qf[nt][w][i]));
+                sum[w / 2] = fmaf(h.x + h.y, (i & 1) ? 16.f : 1.f, sum[w / 2]);
+                ofs[w / 2] = fmaf(h.x + h.y, -1024.f, ofs[w / 2]);
+            }
+        }
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+            sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 1);
+            sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 2);
+            ofs[gr] += __shfl_xor_sync(0xFFFFFFFFu, ofs[gr], 1);
+            ofs[gr] += __shfl_xor_sync(0xFFFFFFFFu, ofs[gr], 2);
+        }
+        const float m = a.scale * 1.4426950408889634f * down;   // scores in log2
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            mult[nt][c] = __shfl_sync(0xFFFFFFFFu, m, 8 * t + 4 * c);
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+                qsum[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, sum[gr], 8 * t + 4 * c);
+                qoff[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, ofs[gr], 8 * t + 4 * c);
+            }
+        }
+    }
+    int last[NT][2];   // position of rows 2t, 2t + 1: the last one they see
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) last[nt][c] = p0 + (8 * nt + 2 * t + c) / group;
+
+    float (&acc)[D / 16][NT][4] = out.acc;
+    float (&top)[NT][2] = out.top, (&sum)[NT][2] = out.sum;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[m][nt][c] = 0.f;
+        top[nt][0] = top[nt][1] = kNone;
+        sum[nt][0] = sum[nt][1] = 0.f;
+    }
+
+    for (int i = 0; i < n_mine; ++i) {
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
+        __syncwarp();
+        const int st = i % kStages;
+        const uint8_t* src = ring + st * S::kStage;
+        const unsigned live = (has >> (2 * st)) & 3u;   // its halves
+        issue(i + kStages - 1);
+        if (!live) continue;
+        const int j0 = pos0 + i * kTile;   // the tile's first position
+        // every row sees every position?
+        const bool inner = live == 3u && j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + q.n - 1 - a.window);
+
+        const int vg = g * (D / 8) / kGroup;
+        bool poison = false;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            // ---- scores
+            const bool there = (live >> hf) & 1u;
+            float sc[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
+            uint32_t kw[2][kWords];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) load_words<kWords>(src + hf * S::kCodeBytes + (g + 8 * r) * (D / 2) + t * (4 * kWords), kw[r]);
+            const __half2* kp = reinterpret_cast<const __half2*>(src + S::kKpAt + hf * S::kParamBytes);
+#pragma unroll
+            for (int gr = 0; gr < kGroups; ++gr) {
+                float d[NT][4];
+#pragma unroll
+                for (int w = 2 * gr; w < 2 * gr + 2; ++w) {
+                    uint32_t lo[4], hi[4];
+                    codes_1024(kw[0][w], lo);
+                    codes_1024(kw[1][w], hi);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (w == 2 * gr)
+                            mma_f16_from(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1], qoff[nt][gr][0], qoff[nt][gr][1]);
+                        else
+                            mma_f16(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1]);
+                        mma_f16(d[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][w][2], qf[nt][w][3]);
+                    }
+                }
+                const float2 k0 = __half22float2(kp[g * kGroups + gr]), k1 = __half22float2(kp[(g + 8) * kGroups + gr]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    sc[nt][0] = fmaf(k0.x, d[nt][0], fmaf(k0.y, qsum[nt][gr][0], sc[nt][0]));
+                    sc[nt][1] = fmaf(k0.x, d[nt][1], fmaf(k0.y, qsum[nt][gr][1], sc[nt][1]));
+                    sc[nt][2] = fmaf(k1.x, d[nt][2], fmaf(k1.y, qsum[nt][gr][0], sc[nt][2]));
+                    sc[nt][3] = fmaf(k1.x, d[nt][3], fmaf(k1.y, qsum[nt][gr][1], sc[nt][3]));
+                }
+            }
+            bool up = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    sc[nt][c] *= mult[nt][c & 1];
+                    if (!inner) {
+                        const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[nt][c & 1];
+                        if (j > p || (a.window > 0 && j <= p - a.window) || !there) sc[nt][c] = -inf;
+                    }
+                    up |= sc[nt][c] > top[nt][c & 1] + kSlack;
+                }
+            if (__any_sync(0xFFFFFFFFu, up)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float m = fmaxf(sc[nt][c], sc[nt][c + 2]);
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                        m = fmaxf(m, top[nt][c]);
+                        const float keep = ex2(top[nt][c] - m);
+                        top[nt][c] = m;
+                        sum[nt][c] *= keep;
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            acc[k][nt][c] *= keep;
+                            acc[k][nt][c + 2] *= keep;
+                        }
+                    }
+            }
+            uint32_t pf[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float w[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    w[c] = ex2(sc[nt][c] - (top[nt][c & 1] - kLift));
+                    sum[nt][c & 1] += w[c];
+                }
+                pf[nt][0] = transpose8(pack_f16x2(w[0], w[1]));
+                pf[nt][1] = transpose8(pack_f16x2(w[2], w[3]));
+            }
+
+            // ---- values: dims g * D/8 + 4 w + e of positions (2t, 2t+1) and (2t+8, 2t+9)
+            uint32_t step[2], low[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint2 v = *reinterpret_cast<const uint2*>(src + S::kVpAt + hf * S::kParamBytes + ((t + 4 * r) * kGroups + vg) * 8);
+                step[r] = v.x;
+                low[r] = v.y;
+            }
+            if (!inner) {
+                // positions that no row sees count as zeros whatever they hold, and a value that is
+                // not finite is taken out here and put back below for the rows that see it
+                const int j_end = there ? q.ctx : 0, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int j = j0 + kHalf * hf + 2 * t + 8 * r;
+                    const uint32_t keep = (j >= j_begin && j < j_end ? 0xFFFFu : 0u) | (j + 1 >= j_begin && j + 1 < j_end ? 0xFFFF0000u : 0u);
+                    step[r] &= keep;
+                    low[r] &= keep;
+                    uint32_t bad = 0;
+                    if (not_finite(step[r] & 0xFFFFu) || not_finite(low[r] & 0xFFFFu)) bad |= 0xFFFFu;
+                    if (not_finite(step[r] & 0xFFFF0000u) || not_finite(low[r] & 0xFFFF0000u)) bad |= 0xFFFF0000u;
+                    step[r] &= ~bad;
+                    low[r] &= ~bad;
+                    poison |= bad != 0;
+                }
+            }
+            uint32_t vw[2][kWords];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) load_words<kWords>(src + S::kVAt + hf * S::kCodeBytes + (t + 4 * r) * D + g * (4 * kWords), vw[r]);
+#pragma unroll
+            for (int w = 0; w < kWords; ++w) {
+                uint32_t a0[4], a1[4];
+                values(vw[0][w], as_h2(step[0]), as_h2(low[0]), a0);
+                values(vw[1][w], as_h2(step[1]), as_h2(low[1]), a1);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[nt][0], pf[nt][1]);
+                    mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[nt][0], pf[nt][1]);
+                }
+            }
+        }
+        if (!inner && __any_sync(0xFFFFFFFFu, poison)) {
+            for (int k = 0; k < kTile; ++k) {
+                if (!((live >> (k / kHalf)) & 1u)) continue;
+                const int j = j0 + k;
+                const __half* p = reinterpret_cast<const __half*>(src + S::kVpAt + (k / kHalf) * S::kParamBytes) +
+                                  (((k % kHalf) >> 1) * kGroups + vg) * 4 + (k & 1);
+                const float nan = __half2float(p[0]) * 0.f + __half2float(p[2]) * 0.f;   // 0 where both are finite
+                if (nan == 0.f || j >= q.ctx) continue;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        if (j > last[nt][c] || (a.window > 0 && j <= last[nt][c] - a.window)) continue;
+#pragma unroll
+                        for (int m = 0; m < D / 16; ++m) {
+                            acc[m][nt][c] += nan;
+                            acc[m][nt][c + 2] += nan;
+                        }
+                    }
+            }
+        }
+    }
+
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    __syncwarp();   // every lane is done with the ring
+}
+
+// The unit's rows (slot null), or a partial result.
+template <int D, int NT>
+__device__ __forceinline__ void put(const AttendArgs& a, int h, const Seq& q, const Sums<D, NT>& o, float* slot)
+{
+    using S = Shape<D, NT>;
+    constexpr int kRows = S::kRows, kWords = S::kWords;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, group = a.n_heads / a.cache.n_kv;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float l = o.sum[nt][c];
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+            const int r = 8 * nt + 2 * t + c;
+            if (r >= q.n * group) continue;
+            if (!slot) {
+                const float k = l == 0.f ? 0.f : 1.f / l;
+                bf16_t* d = a.out + static_cast<long long>(q.row0 + r / group) * a.ld_out + (h * group + r % group) * D + g * (D / 8);
+#pragma unroll
+                for (int w = 0; w < kWords; w += 2)
+                    *reinterpret_cast<uint4*>(d + 4 * w) =
+                        make_uint4(pack_bf16x2(o.acc[2 * w][nt][c] * k, o.acc[2 * w][nt][c + 2] * k),
+                                   pack_bf16x2(o.acc[2 * w + 1][nt][c] * k, o.acc[2 * w + 1][nt][c + 2] * k),
+                                   pack_bf16x2(o.acc[2 * w + 2][nt][c] * k, o.acc[2 * w + 2][nt][c + 2] * k),
+                                   pack_bf16x2(o.acc[2 * w + 3][nt][c] * k, o.acc[2 * w + 3][nt][c + 2] * k));
+            } else {
+#pragma unroll
+                for (int w = 0; w < kWords; ++w)
+                    *reinterpret_cast<float4*>(slot + r * D + g * (D / 8) + 4 * w) =
+                        make_float4(o.acc[2 * w][nt][c], o.acc[2 * w][nt][c + 2], o.acc[2 * w + 1][nt][c], o.acc[2 * w + 1][nt][c + 2]);
+                if (g == 0) {
+                    slot[kRows * D + r] = o.top[nt][c];
+                    slot[kRows * D + kRows + r] = l;
+                }
+            }
+        }
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_few_kernel(AttendArgs a, int few_rows, void* ws)
 {
     using S = Shape<D, NT>;
-    constexpr int kRows = S::kRows, kGroups = S::kGroups, kWords = S::kWords, kStages = S::kStages, kWarps = S::kWarps;
+    constexpr int kRows = S::kRows, kWarps = S::kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Piece pieces[kWarps][2];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint8_t* ring = smem + warp * S::kRing;
     float* first_slot = reinterpret_cast<float*>(smem + kWarps * S::kRing);   // [warp] partial results of slot 0
     int* warp_sums = reinterpret_cast<int*>(smem + kWarps * (S::kRing + 4 * S::kPartial));
@@ -143,7 +495,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
 
     tc::grid_dep_wait();
     tc::grid_dep_launch();
-    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
+    const int group = a.n_heads / a.cache.n_kv;
     scan_seqs<kWarps>(a.batch.n_seqs, prefix, warp_sums, [&](int s) {
         Seq q;
         const bool ok = load_seq(a.batch, s, q, blockIdx.x == 0 ? a.status : nullptr);
@@ -160,336 +512,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
         const int t0 = max(0, x - u.u0 - kUnitCost), t1 = max(0, min(u.len, end - u.u0) - kUnitCost);
         x = min(end, u.u0 + u.len);
         if (t0 == t1) continue;   // only the unit's start lies in the range
-        const int tile0 = first_tile(u.q, a.window), rows = u.q.n * group;
-        const int p0 = u.q.ctx - u.q.n;   // position of the first row
-        const int32_t* table = a.batch.block_table + static_cast<long long>(u.s) * a.batch.ld_table;
-
-        // ---- the ring: tiles t0 + i
-        const int n_mine = t1 - t0, pos0 = (tile0 + t0) * kTile;
-        const uint8_t* head_pages = a.cache.pages + static_cast<long long>(u.h) * block_bytes(ps, D);
-        const bool split = ps < kTile;   // a tile is two pages
-        unsigned has = 0;                // stages' halves that hold positions
-        auto page_at = [&](int pos) -> int { return pos < u.q.ctx ? __ldg(table + (pos >> a.cache.page_shift)) : -1; };
-        int next0 = n_mine > 0 ? page_at(pos0) : -1, next1 = n_mine > 0 && split ? page_at(pos0 + kHalf) : -1;
-        auto issue = [&](int i) {
-            const int pos = pos0 + i * kTile, st = i % kStages;
-            const int page0 = next0, page1 = split ? next1 : page0;
-            if (i + 1 < n_mine) {
-                next0 = page_at(pos + kTile);
-                if (split) next1 = page_at(pos + kTile + kHalf);
-            }
-            has &= ~(3u << (2 * st));
-            if (i < n_mine) {
-                const bool ok0 = static_cast<unsigned>(page0) < static_cast<unsigned>(a.cache.n_pages);
-                const bool ok1 = static_cast<unsigned>(page1) < static_cast<unsigned>(a.cache.n_pages) && pos + kHalf < u.q.ctx;
-                has |= (ok0 ? 1u : 0u) << (2 * st) | (ok1 ? 2u : 0u) << (2 * st);
-                if (lane == 0 && ((!ok0 && pos < u.q.ctx) || (!ok1 && pos + kHalf < u.q.ctx))) flag(a.status, LORA_DEV_BAD_PAGE);
-                const int off0 = pos & (ps - 1), off1 = (pos + kHalf) & (ps - 1);
-                const uint8_t* b0 = head_pages + static_cast<long long>(page0) * a.cache.page_stride;
-                const uint8_t* b1 = head_pages + static_cast<long long>(page1) * a.cache.page_stride;
-                const uint32_t dst = tc::smem_u32(ring + st * S::kStage) + 16 * lane;
-                const uint8_t* s0 = b0 + off0 * (D / 2) + 16 * lane;
-                const uint8_t* s1 = b1 + off1 * (D / 2) + 16 * lane;
-#pragma unroll
-                for (int c = 0; c < S::kCodeBytes; c += 512) {
-                    if (ok0) {
-                        copy16(dst + c, s0 + c);
-                        copy16(dst + S::kVAt + c, s0 + v_codes_off(ps, D) + c);
-                    }
-                    if (ok1) {
-                        copy16(dst + S::kCodeBytes + c, s1 + c);
-                        copy16(dst + S::kVAt + S::kCodeBytes + c, s1 + v_codes_off(ps, D) + c);
-                    }
-                }
-                // params: eight lanes to a half of K's, then of V's
-                const int pl = lane & 7, second = (lane >> 3) & 1;
-                if (pl < S::kParamBytes / 16 && (second ? ok1 : ok0)) {
-                    const uint8_t* src = (second ? b1 + off1 * 4 * kGroups : b0 + off0 * 4 * kGroups) +
-                                         (lane & 16 ? v_params_off(ps, D) : k_params_off(ps, D)) + 16 * pl;
-                    copy16(tc::smem_u32(ring + st * S::kStage) + S::kKpAt + (lane >> 3) * S::kParamBytes + 16 * pl, src);
-                }
-            }
-            asm volatile("cp.async.commit_group;\n" ::: "memory");
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) issue(i);
-
-        // ---- q as fragments: row n = 8 nt + g, dims 32 w + 8 t + (0..7)
-        uint32_t qf[NT][kWords][4];     // pairs (dims e, e + 4); odd pairs carry 1/16
-        float mult[NT][2], qsum[NT][kGroups][2], qoff[NT][kGroups][2];   // of rows 2t, 2t + 1
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = 8 * nt + g;
-            uint4 raw[kWords];
-            float top = 0.f;
-            const bf16_t* qp = a.q + static_cast<long long>(u.q.row0 + r / group) * a.ld_q + (u.h * group + r % group) * D + 8 * t;
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                raw[w] = r < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
-                const uint32_t part[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(part[e])), fabsf(bf16_hi(part[e]))));
-            }
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-            // a power of two that takes the row's largest into [2^7, 2^8)
-            const int e = static_cast<int>(__float_as_uint(top) >> 23);
-            const int fe = min(261 - e, 253);
-            const float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
-            const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
-            // sums of the fp16 values as the product takes them: of q, and of 1024 times the operand
-            float sum[kGroups], ofs[kGroups];
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) sum[gr] = ofs[gr] = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) {
-                const float f[8] = {bf16_lo(raw[w].x) * up, bf16_hi(raw[w].x) * up, bf16_lo(raw[w].y) * up, bf16_hi(raw[w].y) * up,
-                                    bf16_lo(raw[w].z) * up, bf16_hi(raw[w].z) * up, bf16_lo(raw[w].w) * up, bf16_hi(raw[w].w) * up};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float k = (i & 1) ? 1.f / 16 : 1.f;
-                    qf[nt][w][i] = pack_f16x2(f[i] * k, f[i + 4] * k);
-                    const float2 h = __half22float2(as_h2(qf[nt][w][i]));
-                    sum[w / 2] = fmaf(h.x + h.y, (i & 1) ? 16.f : 1.f, sum[w / 2]);
-                    ofs[w / 2] = fmaf(h.x + h.y, -1024.f, ofs[w / 2]);
-                }
-            }
-#pragma unroll
-            for (int gr = 0; gr < kGroups; ++gr) {
-                sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 1);
-                sum[gr] += __shfl_xor_sync(0xFFFFFFFFu, sum[gr], 2);
-                ofs[gr] += __shfl_xor_sync(0xFFFFFFFFu, ofs[gr], 1);
-                ofs[gr] += __shfl_xor_sync(0xFFFFFFFFu, ofs[gr], 2);
-            }
-            const float m = a.scale * 1.4426950408889634f * down;   // scores in log2
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                mult[nt][c] = __shfl_sync(0xFFFFFFFFu, m, 8 * t + 4 * c);
-#pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr) {
-                    qsum[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, sum[gr], 8 * t + 4 * c);
-                    qoff[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, ofs[gr], 8 * t + 4 * c);
-                }
-            }
-        }
-        int last[NT][2];   // position of rows 2t, 2t + 1: the last one they see
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) last[nt][c] = p0 + (8 * nt + 2 * t + c) / group;
-
-        float acc[D / 16][NT][4];
-        float top[NT][2], sum[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) acc[m][nt][c] = 0.f;
-            top[nt][0] = top[nt][1] = -inf;
-            sum[nt][0] = sum[nt][1] = 0.f;
-        }
-
-        for (int i = 0; i < n_mine; ++i) {
-            asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
-            __syncwarp();
-            const int st = i % kStages;
-            const uint8_t* src = ring + st * S::kStage;
-            const unsigned live = (has >> (2 * st)) & 3u;   // its halves
-            issue(i + kStages - 1);
-            if (!live) continue;
-            const int j0 = pos0 + i * kTile;   // the tile's first position
-            // every row sees every position?
-            const bool inner = live == 3u && j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + u.q.n - 1 - a.window);
-
-            const int vg = g * (D / 8) / kGroup;
-            bool poison = false;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                // ---- scores
-                const bool there = (live >> hf) & 1u;
-                float sc[NT][4];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
-                uint32_t kw[2][kWords];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) load_words<kWords>(src + hf * S::kCodeBytes + (g + 8 * r) * (D / 2) + t * (4 * kWords), kw[r]);
-                const __half2* kp = reinterpret_cast<const __half2*>(src + S::kKpAt + hf * S::kParamBytes);
-#pragma unroll
-                for (int gr = 0; gr < kGroups; ++gr) {
-                    float d[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) d[nt][c] = qoff[nt][gr][c & 1];
-#pragma unroll
-                    for (int w = 2 * gr; w < 2 * gr + 2; ++w) {
-                        uint32_t lo[4], hi[4];
-                        codes_1024(kw[0][w], lo);
-                        codes_1024(kw[1][w], hi);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma_f16(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1]);
-                            mma_f16(d[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][w][2], qf[nt][w][3]);
-                        }
-                    }
-                    const float2 k0 = __half22float2(kp[g * kGroups + gr]), k1 = __half22float2(kp[(g + 8) * kGroups + gr]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        sc[nt][0] = fmaf(k0.x, d[nt][0], fmaf(k0.y, qsum[nt][gr][0], sc[nt][0]));
-                        sc[nt][1] = fmaf(k0.x, d[nt][1], fmaf(k0.y, qsum[nt][gr][1], sc[nt][1]));
-                        sc[nt][2] = fmaf(k1.x, d[nt][2], fmaf(k1.y, qsum[nt][gr][0], sc[nt][2]));
-                        sc[nt][3] = fmaf(k1.x, d[nt][3], fmaf(k1.y, qsum[nt][gr][1], sc[nt][3]));
-                    }
-                }
-                bool up = false;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        sc[nt][c] *= mult[nt][c & 1];
-                        if (!inner) {
-                            const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[nt][c & 1];
-                            if (j > p || (a.window > 0 && j <= p - a.window) || !there) sc[nt][c] = -inf;
-                        }
-                        up |= sc[nt][c] > top[nt][c & 1] + kSlack;
-                    }
-                if (__any_sync(0xFFFFFFFFu, up)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            float m = fmaxf(sc[nt][c], sc[nt][c + 2]);
-                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-                            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                            m = fmaxf(m, top[nt][c]);
-                            const float keep = m == -inf ? 1.f : ex2(top[nt][c] - m);
-                            top[nt][c] = m;
-                            sum[nt][c] *= keep;
-#pragma unroll
-                            for (int k = 0; k < D / 16; ++k) {
-                                acc[k][nt][c] *= keep;
-                                acc[k][nt][c + 2] *= keep;
-                            }
-                        }
-                }
-                uint32_t pf[NT][2];
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float w[4];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        w[c] = ex2(sc[nt][c] - (top[nt][c & 1] == -inf ? 0.f : top[nt][c & 1] - kLift));
-                        sum[nt][c & 1] += w[c];
-                    }
-                    pf[nt][0] = transpose8(pack_f16x2(w[0], w[1]));
-                    pf[nt][1] = transpose8(pack_f16x2(w[2], w[3]));
-                }
-
-                // ---- values: dims g * D/8 + 4 w + e of positions (2t, 2t+1) and (2t+8, 2t+9)
-                uint32_t step[2], low[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const uint2 v = *reinterpret_cast<const uint2*>(src + S::kVpAt + hf * S::kParamBytes + ((t + 4 * r) * kGroups + vg) * 8);
-                    step[r] = v.x;
-                    low[r] = v.y;
-                }
-                if (!inner) {
-                    // positions that no row sees count as zeros whatever they hold, and a value that is
-                    // not finite is taken out here and put back below for the rows that see it
-                    const int j_end = there ? u.q.ctx : 0, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int j = j0 + kHalf * hf + 2 * t + 8 * r;
-                        const uint32_t keep = (j >= j_begin && j < j_end ? 0xFFFFu : 0u) | (j + 1 >= j_begin && j + 1 < j_end ? 0xFFFF0000u : 0u);
-                        step[r] &= keep;
-                        low[r] &= keep;
-                        uint32_t bad = 0;
-                        if (not_finite(step[r] & 0xFFFFu) || not_finite(low[r] & 0xFFFFu)) bad |= 0xFFFFu;
-                        if (not_finite(step[r] & 0xFFFF0000u) || not_finite(low[r] & 0xFFFF0000u)) bad |= 0xFFFF0000u;
-                        step[r] &= ~bad;
-                        low[r] &= ~bad;
-                        poison |= bad != 0;
-                    }
-                }
-                uint32_t vw[2][kWords];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) load_words<kWords>(src + S::kVAt + hf * S::kCodeBytes + (t + 4 * r) * D + g * (4 * kWords), vw[r]);
-#pragma unroll
-                for (int w = 0; w < kWords; ++w) {
-                    uint32_t a0[4], a1[4];
-                    values(vw[0][w], as_h2(step[0]), as_h2(low[0]), a0);
-                    values(vw[1][w], as_h2(step[1]), as_h2(low[1]), a1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[nt][0], pf[nt][1]);
-                        mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[nt][0], pf[nt][1]);
-                    }
-                }
-            }
-            if (!inner && __any_sync(0xFFFFFFFFu, poison)) {
-                for (int k = 0; k < kTile; ++k) {
-                    if (!((live >> (k / kHalf)) & 1u)) continue;
-                    const int j = j0 + k;
-                    const __half* p = reinterpret_cast<const __half*>(src + S::kVpAt + (k / kHalf) * S::kParamBytes) +
-                                      (((k % kHalf) >> 1) * kGroups + vg) * 4 + (k & 1);
-                    const float nan = __half2float(p[0]) * 0.f + __half2float(p[2]) * 0.f;   // 0 where both are finite
-                    if (nan == 0.f || j >= u.q.ctx) continue;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            if (j > last[nt][c] || (a.window > 0 && j <= last[nt][c] - a.window)) continue;
-#pragma unroll
-                            for (int m = 0; m < D / 16; ++m) {
-                                acc[m][nt][c] += nan;
-                                acc[m][nt][c + 2] += nan;
-                            }
-                        }
-                }
-            }
-        }
-
-        // ---- the unit's rows, or a partial result
+        Sums<D, NT> o;
+        attend_tiles<D, NT>(a, ring, u.s, u.h, u.q, first_tile(u.q, a.window) + t0, t1 - t0, o);
         const bool whole = t0 == 0 && t1 == u.len - kUnitCost;
-        asm volatile("cp.async.wait_all;\n" ::: "memory");
-        __syncwarp();   // every lane is done with the ring
         float* slot = t0 > 0 ? first_slot + warp * S::kPartial : reinterpret_cast<float*>(ring);
-        if (!whole && lane == 0) pieces[warp][t0 > 0 ? 0 : 1] = Piece{u.u0, t1 == u.len - kUnitCost, u.h, u.q.row0, rows, u.u0 + u.len};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                float l = sum[nt][c];
-                l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
-                l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-                l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-                const int r = 8 * nt + 2 * t + c;
-                if (r >= rows) continue;
-                if (whole) {
-                    const float k = l == 0.f ? 0.f : 1.f / l;
-                    bf16_t* o = a.out + static_cast<long long>(u.q.row0 + r / group) * a.ld_out + (u.h * group + r % group) * D + g * (D / 8);
-#pragma unroll
-                    for (int w = 0; w < kWords; w += 2)
-                        *reinterpret_cast<uint4*>(o + 4 * w) =
-                            make_uint4(pack_bf16x2(acc[2 * w][nt][c] * k, acc[2 * w][nt][c + 2] * k),
-                                       pack_bf16x2(acc[2 * w + 1][nt][c] * k, acc[2 * w + 1][nt][c + 2] * k),
-                                       pack_bf16x2(acc[2 * w + 2][nt][c] * k, acc[2 * w + 2][nt][c + 2] * k),
-                                       pack_bf16x2(acc[2 * w + 3][nt][c] * k, acc[2 * w + 3][nt][c + 2] * k));
-                } else {
-#pragma unroll
-                    for (int w = 0; w < kWords; ++w)
-                        *reinterpret_cast<float4*>(slot + r * D + g * (D / 8) + 4 * w) =
-                            make_float4(acc[2 * w][nt][c], acc[2 * w][nt][c + 2], acc[2 * w + 1][nt][c], acc[2 * w + 1][nt][c + 2]);
-                    if (g == 0) {
-                        slot[kRows * D + r] = top[nt][c];
-                        slot[kRows * D + kRows + r] = l;
-                    }
-                }
-            }
+        if (!whole && lane == 0)
+            pieces[warp][t0 > 0 ? 0 : 1] = Piece{u.u0, t1 == u.len - kUnitCost, u.h, u.q.row0, u.q.n * group, u.u0 + u.len};
+        put<D, NT>(a, u.h, u.q, o, whole ? nullptr : slot);
     }
     __syncthreads();
 
@@ -498,27 +527,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
         return k == 0 ? first_slot + w * S::kPartial : reinterpret_cast<const float*>(smem + w * S::kRing);
     };
     Record rec{0, 0, 0, 0};
-    for (int i = 0; i < 2 * kWarps;) {   // entry i: warp i / 2, slot i % 2; a unit's pieces follow each other
-        const Piece first = pieces[i >> 1][i & 1];
-        const int i0 = i++;
-        if (first.u0 < 0) continue;
-        int ends = first.ends;
-        for (; i < 2 * kWarps; ++i) {
-            const Piece& p = pieces[i >> 1][i & 1];
-            if (p.u0 >= 0 && p.u0 != first.u0) break;
-            if (p.u0 == first.u0) ends = p.ends;
-        }
+    // entry i: warp i / 2, slot i % 2; a unit's pieces follow each other
+    const int entry_u0 = lane < 2 * kWarps ? pieces[lane >> 1][lane & 1].u0 : -1;
+    for (unsigned left = __ballot_sync(0xFFFFFFFFu, entry_u0 >= 0); left;) {
+        const int i0 = __ffs(left) - 1;
+        const unsigned set = __ballot_sync(0xFFFFFFFFu, entry_u0 == __shfl_sync(0xFFFFFFFFu, entry_u0, i0));
+        left &= ~set;
+        const Piece first = pieces[i0 >> 1][i0 & 1];
+        const int last = 31 - __clz(set), ends = pieces[last >> 1][last & 1].ends;
         const bool starts = i0 & 1;
         float* to = partial(ws, b, starts, S::kPartial);
         for (int e = tid; e < first.rows * (D / 4); e += S::kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = -inf, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int k = i0; k < i; ++k)
-                if (pieces[k >> 1][k & 1].u0 >= 0) m = fmaxf(m, slot_of(k >> 1, k & 1)[kRows * D + r]);
-            for (int k = i0; k < i; ++k) {
-                if (pieces[k >> 1][k & 1].u0 < 0) continue;
-                const float* p = slot_of(k >> 1, k & 1);
+            for (unsigned k = set; k; k &= k - 1) m = fmaxf(m, slot_of((__ffs(k) - 1) >> 1, (__ffs(k) - 1) & 1)[kRows * D + r]);
+            for (unsigned k = set; k; k &= k - 1) {
+                const float* p = slot_of((__ffs(k) - 1) >> 1, (__ffs(k) - 1) & 1);
                 const float w = m == -inf ? 0.f : ex2(p[kRows * D + r] - m);
                 const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
                 o.x = fmaf(v.x, w, o.x);
@@ -545,6 +570,91 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
         }
     }
     if (tid == 0) static_cast<Record*>(ws)[b] = rec;
+}
+
+// The form for a few short units: a cluster of kCluster CTAs per unit, each
+// warp an equal share of its tiles, joined over the CTAs' shared memory.  One
+// launch, and no tables of the batch's work to build first.
+constexpr int kCluster = 8;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_unit_kernel(AttendArgs a, int few_rows)
+{
+    using S = Shape<D, NT>;
+    constexpr int kRows = S::kRows, kWarps = S::kWarps;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, rank = static_cast<int>(cluster_rank());
+    uint8_t* ring = smem + warp * S::kRing;
+    float* mine = reinterpret_cast<float*>(smem + kWarps * S::kRing);   // the CTA's partial result: sums, then (maximum, sum of weights)
+    const int unit = blockIdx.x / kCluster, s = unit / a.cache.n_kv, h = unit - s * a.cache.n_kv;
+    const int group = a.n_heads / a.cache.n_kv;
+    const float inf = __int_as_float(0x7F800000);
+
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    Seq q;
+    // (the whole cluster leaves, or none of it)
+    if (!load_seq(a.batch, s, q, rank == 0 && h == 0 && tid == 0 ? a.status : nullptr) || q.n == 0 || q.n * group > few_rows) return;
+    const int tiles = tiles_of(q, a.window);
+    auto share = [&](int w) { return static_cast<int>(static_cast<long long>(tiles) * w / (kCluster * kWarps)); };   // first tile of warp w of the cluster
+    const int t0 = share(rank * kWarps + warp), t1 = share(rank * kWarps + warp + 1);
+    if (t0 < t1) {
+        Sums<D, NT> o;
+        attend_tiles<D, NT>(a, ring, s, h, q, first_tile(q, a.window) + t0, t1 - t0, o);
+        put<D, NT>(a, h, q, o, reinterpret_cast<float*>(ring));
+    }
+    __syncthreads();
+    const int work = q.n * group * (D / 4);
+    for (int e = tid; e < work; e += S::kThreads) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4;
+        float m = -inf, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < kWarps; ++w)
+            if (share(rank * kWarps + w) < share(rank * kWarps + w + 1)) m = fmaxf(m, reinterpret_cast<const float*>(smem + w * S::kRing)[kRows * D + r]);
+        for (int w = 0; w < kWarps; ++w) {
+            if (share(rank * kWarps + w) == share(rank * kWarps + w + 1)) continue;
+            const float* p = reinterpret_cast<const float*>(smem + w * S::kRing);
+            const float k = m == -inf ? 0.f : ex2(p[kRows * D + r] - m);
+            const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
+            o.x = fmaf(v.x, k, o.x);
+            o.y = fmaf(v.y, k, o.y);
+            o.z = fmaf(v.z, k, o.z);
+            o.w = fmaf(v.w, k, o.w);
+            l = fmaf(p[kRows * D + kRows + r], k, l);
+        }
+        *reinterpret_cast<float4*>(mine + r * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(mine + kRows * D + 2 * r) = make_float2(m, l);
+    }
+    cluster_arrive();
+    cluster_wait();
+    for (int e = rank * S::kThreads + tid; e < work; e += kCluster * S::kThreads) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4;
+        float2 ml[kCluster];
+        float4 v[kCluster];
+#pragma unroll
+        for (int k = 0; k < kCluster; ++k) {
+            ml[k] = ld_dsmem_f2(map_rank(tc::smem_u32(mine + kRows * D + 2 * r), k));
+            v[k] = ld_dsmem_f4(map_rank(tc::smem_u32(mine + r * D + d), k));
+        }
+        float m = -inf, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kCluster; ++k) m = fmaxf(m, ml[k].x);
+#pragma unroll
+        for (int k = 0; k < kCluster; ++k) {   // (a CTA without tiles left zeros)
+            const float w = m == -inf ? 0.f : ex2(ml[k].x - m);
+            o.x = fmaf(v[k].x, w, o.x);
+            o.y = fmaf(v[k].y, w, o.y);
+            o.z = fmaf(v[k].z, w, o.z);
+            o.w = fmaf(v[k].w, w, o.w);
+            l = fmaf(ml[k].y, w, l);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(q.row0 + r / group) * a.ld_out + (h * group + r % group) * D + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+    cluster_arrive();
+    cluster_wait();   // no CTA leaves while another reads its result
 }
 
 // Joins the pieces of the unit that begins in CTA b's ranges and goes on, in order.
@@ -581,6 +691,7 @@ __global__ void __launch_bounds__(256) kv4_few_join_kernel(AttendArgs a, void* w
     }
 }
 
+constexpr int kUnitTiles = 16;
 constexpr int kMaxSmem = 227 * 1024;
 static_assert(Shape<128, 4>::kSmem + 4 * kMaxSeqs <= kMaxSmem, "shared memory");
 
@@ -592,10 +703,43 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream
     cudaError_t e = cudaSuccess;
     if (!attr_set) {
         e = cudaFuncSetAttribute(kv4_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kv4_unit_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
     const int ctas = std::min(kMaxCtas, device_sms() * S::kCtas);
+    // Units that all have a cluster on the GPU at once, with at most kUnitTiles tiles to a warp: a cluster each.
+    // Measured both ways (us, heads of 128 in groups of 4, cluster / ranges): one sequence of 1000, 8000, 32000
+    // positions 6.3 / 9.9, 10.9 / 24.5, 28 / 32; four sequences 6.8 / 12.1, 14.6 / 20.9, 40 / 44; but two waves
+    // of clusters (16 rows to a unit, two sequences of 1000) 16.3 / 15.6, and at more positions the ranges,
+    // which every SM takes part in.
+    const long long units = static_cast<long long>(a.batch.n_seqs) * a.cache.n_kv;
+    if (a.batch.max_ctx_len <= kTile * kUnitTiles * kCluster * S::kWarps) {
+        static int room = -1;   // clusters on the GPU at once
+        PdlLaunch l(dim3(static_cast<unsigned>(units * kCluster)), S::kThreads, S::kSmem, stream);
+        cudaLaunchAttribute attr[2];
+        attr[0] = l.attr[0];
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = kCluster;
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        l.cfg.attrs = attr;
+        l.cfg.numAttrs = 2;
+        if (room < 0) {
+            int n = 0;
+            cudaLaunchConfig_t one = l.cfg;   // the query does without the other attribute
+            one.gridDim = dim3(kCluster);
+            one.attrs = attr + 1;
+            one.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, kv4_unit_kernel<D, NT>, &one);
+            if (e != cudaSuccess) return e;
+            room = n;
+        }
+        if (units <= room) {
+            e = cudaLaunchKernelEx(&l.cfg, kv4_unit_kernel<D, NT>, a, few_rows);
+            note_launch();
+            return e;
+        }
+    }
     PdlLaunch l(dim3(ctas), S::kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
     e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows, ws);
     if (e != cudaSuccess) return e;
