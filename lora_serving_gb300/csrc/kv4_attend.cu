@@ -1,7 +1,9 @@
-// kv4_attend.cu -- which kernel takes which rows of lora_kv4_attend.
+// kv4_attend.cu -- which kernel takes which rows of lora_kv4_attend, and the
+// joining of what their ranges' ends cut.
 #include <algorithm>
 
 #include "kv4_attend.cuh"
+#include "tc_common.cuh"
 
 namespace lora {
 
@@ -20,6 +22,46 @@ int few_limit(int group, int max_q_len)
     return group <= 8 ? 8 : group <= 16 ? 16 : group <= kFewRows ? kFewRows : 0;
 }
 
+// Joins the pieces behind each record, in order: kQuads 16-byte pieces of a
+// row's sums to a thread, as many CTAs to a record as its slot's rows need.
+constexpr int kJoinThreads = 256, kQuads = 1;
+__host__ __device__ constexpr int join_ctas(int rows, int D) { return (rows * (D / 4) + kJoinThreads * kQuads - 1) / (kJoinThreads * kQuads); }
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv4::Partials p0, kv4::Partials p1)
+{
+    tc::grid_dep_wait();
+    tc::grid_dep_launch();
+    const int n0 = p0.ctas * join_ctas(p0.rows, D);
+    const bool second = static_cast<int>(blockIdx.x) >= n0;
+    const kv4::Partials& p = second ? p1 : p0;
+    const int per = join_ctas(p.rows, D), x = blockIdx.x - (second ? n0 : 0), b = x / per, group = a.n_heads / a.cache.n_kv;
+    const kv4::Record u = p.records[b];
+    const float inf = __int_as_float(0x7F800000);
+    for (int e = (x - b * per) * kJoinThreads + threadIdx.x; e < u.rows * (D / 4); e += per * kJoinThreads) {
+        const int r = e / (D / 4), d = e % (D / 4) * 4;
+        float m = -inf, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = b; k <= u.last; ++k) m = fmaxf(m, p.slot(k, k == b, D)[p.rows * D + r]);
+#pragma unroll 4
+        for (int k = b; k <= u.last; ++k) {
+            const float* s = p.slot(k, k == b, D);
+            const float w = m == -inf ? 0.f : kv4::ex2(s[p.rows * D + r] - m);
+            const float4 v = *reinterpret_cast<const float4*>(s + r * D + d);
+            o.x = fmaf(v.x, w, o.x);
+            o.y = fmaf(v.y, w, o.y);
+            o.z = fmaf(v.z, w, o.z);
+            o.w = fmaf(v.w, w, o.w);
+            l = fmaf(s[p.rows * (D + 1) + r], w, l);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int row = u.block_row0 + r;
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.seq_row0 + row / group) * a.ld_out + (u.h * group + row % group) * D + d) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    }
+}
+
 }  // namespace
 
 // The kernels' workspaces lie one after the other.
@@ -32,13 +74,18 @@ size_t kv4_attend_workspace(int n_heads, int n_kv, int head_dim, int max_q_len)
 cudaError_t launch_kv4_attend(const AttendArgs& a, cudaStream_t stream)
 {
     if (a.batch.n_rows == 0 || a.batch.max_q_len == 0) return cudaSuccess;
-    const int group = a.n_heads / a.cache.n_kv, few = few_limit(group, a.batch.max_q_len);
-    if (static_cast<long long>(group) * a.batch.max_q_len > few) {
-        void* ws = static_cast<uint8_t*>(a.ws) + kv4_few_workspace(a.cache.head_dim, few);
-        const cudaError_t e = launch_kv4_many(a, few, ws, stream);
-        if (e != cudaSuccess) return e;
-    }
-    return few ? launch_kv4_few(a, few, a.ws, stream) : cudaSuccess;
+    const int group = a.n_heads / a.cache.n_kv, D = a.cache.head_dim, few = few_limit(group, a.batch.max_q_len);
+    const bool many = static_cast<long long>(group) * a.batch.max_q_len > few;
+    kv4::Partials p0{}, p1{};
+    cudaError_t e = cudaSuccess;
+    if (many) e = launch_kv4_many(a, few, static_cast<uint8_t*>(a.ws) + kv4_few_workspace(D, few), &p0, stream);
+    if (e == cudaSuccess && few) e = launch_kv4_few(a, few, a.ws, many, &p1, stream);
+    const int ctas = p0.ctas * join_ctas(p0.rows, D) + p1.ctas * join_ctas(p1.rows, D);
+    if (e != cudaSuccess || ctas == 0) return e;
+    PdlLaunch l(dim3(ctas), kJoinThreads, 0, stream);
+    e = D == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_join_kernel<64>, a, p0, p1) : cudaLaunchKernelEx(&l.cfg, kv4_join_kernel<128>, a, p0, p1);
+    note_launch();
+    return e;
 }
 
 }  // namespace lora

@@ -132,12 +132,41 @@ __device__ __forceinline__ int seq_at(const int* prefix, int n_seqs, int x)
     return lo;
 }
 
+// Partial results.  Work is cut into equal ranges, one per CTA; what a range's
+// end cuts leaves partial results: `rows` x D sums of weighted values, then the
+// rows' maxima (log2) and sums of weights.  Slot 0 of a CTA: of what began
+// before its range; slot 1: of what begins in it and goes on after it, which
+// has a record.
+struct Record {
+    int rows, block_row0, seq_row0, h, last;   // rows 0: none; the pieces lie in CTAs [this, last]
+};
+struct Partials {
+    Record* records;
+    float* sums;
+    int ctas, rows;   // ranges; rows of a slot
+    __device__ __forceinline__ float* slot(int cta, int i, int D) const
+    {
+        return sums + (static_cast<long long>(cta) * 2 + i) * (static_cast<long long>(rows) * (D + 2));
+    }
+};
+// Where they lie in a workspace, and its bytes (a multiple of 256).
+inline Partials partials_at(void* ws, int ctas, int rows)
+{
+    return Partials{static_cast<Record*>(ws), reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + (ctas * sizeof(Record) + 255) / 256 * 256), ctas, rows};
+}
+inline size_t partials_bytes(int ctas, int rows, int D)
+{
+    return ((ctas * sizeof(Record) + 255) / 256 * 256 + static_cast<size_t>(ctas) * 2 * rows * (D + 2) * sizeof(float) + 255) / 256 * 256;
+}
+
 }  // namespace kv4
 
 // Sequences with at most few_rows query rows to a kv head (rows x heads of
-// the group), and the others; ws: the kernel's own workspace.
-cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream);
-cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream);
+// the group), and the others; ws: the kernel's own workspace.  *left: the
+// partial results to be joined (ctas 0: none).  after: the launch before it
+// is the other kernel's of the same call, which it need not wait for.
+cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, bool after, kv4::Partials* left, cudaStream_t stream);
+cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, kv4::Partials* left, cudaStream_t stream);
 size_t kv4_many_workspace(int head_dim);
 size_t kv4_few_workspace(int head_dim, int rows);
 

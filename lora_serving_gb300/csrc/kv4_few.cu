@@ -110,18 +110,7 @@ struct Piece {
     int h, row0, rows, u1;
 };
 
-// What the workspace holds: a record for each CTA of the unit that begins in
-// it and goes on after it, then two partial results for each CTA (slots as a
-// warp's).
-struct Record {
-    int rows, row0, h, last;   // rows 0: none; the unit's pieces lie in CTAs [this, last]
-};
 constexpr int kMaxCtas = 2 * 160;   // CTAs that the workspace has room for
-constexpr size_t kRecordBytes = kMaxCtas * sizeof(Record);
-__device__ __forceinline__ float* partial(void* ws, int cta, int slot, int floats)
-{
-    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kRecordBytes) + (static_cast<long long>(cta) * 2 + slot) * floats;
-}
 
 __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src)
 {
@@ -481,7 +470,7 @@ __device__ __forceinline__ void put(const AttendArgs& a, int h, const Seq& q, co
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_few_kernel(AttendArgs a, int few_rows, void* ws)
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_few_kernel(AttendArgs a, int few_rows, Partials left, bool after)
 {
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kWarps = S::kWarps;
@@ -493,7 +482,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
     int* warp_sums = reinterpret_cast<int*>(smem + kWarps * (S::kRing + 4 * S::kPartial));
     int* prefix = warp_sums + 16;
 
-    tc::grid_dep_wait();
+    if (!after) tc::grid_dep_wait();
     tc::grid_dep_launch();
     const int group = a.n_heads / a.cache.n_kv;
     scan_seqs<kWarps>(a.batch.n_seqs, prefix, warp_sums, [&](int s) {
@@ -526,17 +515,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
     auto slot_of = [&](int w, int k) {
         return k == 0 ? first_slot + w * S::kPartial : reinterpret_cast<const float*>(smem + w * S::kRing);
     };
-    Record rec{0, 0, 0, 0};
+    Record rec{0, 0, 0, 0, 0};
     // entry i: warp i / 2, slot i % 2; a unit's pieces follow each other
     const int entry_u0 = lane < 2 * kWarps ? pieces[lane >> 1][lane & 1].u0 : -1;
-    for (unsigned left = __ballot_sync(0xFFFFFFFFu, entry_u0 >= 0); left;) {
-        const int i0 = __ffs(left) - 1;
+    for (unsigned todo = __ballot_sync(0xFFFFFFFFu, entry_u0 >= 0); todo;) {
+        const int i0 = __ffs(todo) - 1;
         const unsigned set = __ballot_sync(0xFFFFFFFFu, entry_u0 == __shfl_sync(0xFFFFFFFFu, entry_u0, i0));
-        left &= ~set;
+        todo &= ~set;
         const Piece first = pieces[i0 >> 1][i0 & 1];
         const int last = 31 - __clz(set), ends = pieces[last >> 1][last & 1].ends;
         const bool starts = i0 & 1;
-        float* to = partial(ws, b, starts, S::kPartial);
+        float* to = left.slot(b, starts, D);
         for (int e = tid; e < first.rows * (D / 4); e += S::kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = -inf, l = 0.f;
@@ -565,11 +554,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
             }
         }
         if (starts && !ends) {
-            rec = Record{first.rows, first.row0, first.h, b};
+            rec = Record{first.rows, 0, first.row0, first.h, b};
             while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, (rec.last + 1) * kWarps) < first.u1) ++rec.last;
         }
     }
-    if (tid == 0) static_cast<Record*>(ws)[b] = rec;
+    if (tid == 0) left.records[b] = rec;
+    if (after) tc::grid_dep_wait();   // no kernel completes before the one before it
 }
 
 // The form for a few short units: a cluster of kCluster CTAs per unit, each
@@ -578,7 +568,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
 constexpr int kCluster = 8;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_unit_kernel(AttendArgs a, int few_rows)
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_unit_kernel(AttendArgs a, int few_rows, bool after)
 {
     using S = Shape<D, NT>;
     constexpr int kRows = S::kRows, kWarps = S::kWarps;
@@ -590,11 +580,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
     const int group = a.n_heads / a.cache.n_kv;
     const float inf = __int_as_float(0x7F800000);
 
-    tc::grid_dep_wait();
+    if (!after) tc::grid_dep_wait();
     tc::grid_dep_launch();
     Seq q;
-    // (the whole cluster leaves, or none of it)
-    if (!load_seq(a.batch, s, q, rank == 0 && h == 0 && tid == 0 ? a.status : nullptr) || q.n == 0 || q.n * group > few_rows) return;
+    const bool ok = load_seq(a.batch, s, q, rank == 0 && h == 0 && tid == 0 ? a.status : nullptr);
+    if (after) tc::grid_dep_wait();   // no kernel completes before the one before it
+    if (!ok || q.n == 0 || q.n * group > few_rows) return;   // the whole cluster leaves, or none of it
     const int tiles = tiles_of(q, a.window);
     auto share = [&](int w) { return static_cast<int>(static_cast<long long>(tiles) * w / (kCluster * kWarps)); };   // first tile of warp w of the cluster
     const int t0 = share(rank * kWarps + warp), t1 = share(rank * kWarps + warp + 1);
@@ -657,46 +648,12 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
     cluster_wait();   // no CTA leaves while another reads its result
 }
 
-// Joins the pieces of the unit that begins in CTA b's ranges and goes on, in order.
-template <int D, int NT>
-__global__ void __launch_bounds__(256) kv4_few_join_kernel(AttendArgs a, void* ws)
-{
-    using S = Shape<D, NT>;
-    constexpr int kRows = S::kRows;
-    tc::grid_dep_wait();
-    tc::grid_dep_launch();
-    const int b = blockIdx.x, group = a.n_heads / a.cache.n_kv;
-    const Record u = static_cast<const Record*>(ws)[b];
-    const float inf = __int_as_float(0x7F800000);
-    for (int e = threadIdx.x; e < u.rows * (D / 4); e += blockDim.x) {
-        const int r = e / (D / 4), d = e % (D / 4) * 4;
-        float m = -inf, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = b; k <= u.last; ++k) m = fmaxf(m, partial(ws, k, k == b, S::kPartial)[kRows * D + r]);
-#pragma unroll 4
-        for (int k = b; k <= u.last; ++k) {
-            const float* p = partial(ws, k, k == b, S::kPartial);
-            const float w = m == -inf ? 0.f : ex2(p[kRows * D + r] - m);
-            const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
-            o.x = fmaf(v.x, w, o.x);
-            o.y = fmaf(v.y, w, o.y);
-            o.z = fmaf(v.z, w, o.z);
-            o.w = fmaf(v.w, w, o.w);
-            l = fmaf(p[kRows * D + kRows + r], w, l);
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.row0 + r / group) * a.ld_out + (u.h * group + r % group) * D + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    }
-}
-
 constexpr int kUnitTiles = 16;
 constexpr int kMaxSmem = 227 * 1024;
 static_assert(Shape<128, 4>::kSmem + 4 * kMaxSeqs <= kMaxSmem, "shared memory");
 
 template <int D, int NT>
-cudaError_t run(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
+cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partials* left, cudaStream_t stream)
 {
     using S = Shape<D, NT>;
     static bool attr_set = false;
@@ -735,39 +692,33 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream
             room = n;
         }
         if (units <= room) {
-            e = cudaLaunchKernelEx(&l.cfg, kv4_unit_kernel<D, NT>, a, few_rows);
+            left->ctas = 0;
+            e = cudaLaunchKernelEx(&l.cfg, kv4_unit_kernel<D, NT>, a, few_rows, after);
             note_launch();
             return e;
         }
     }
     PdlLaunch l(dim3(ctas), S::kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
-    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows, ws);
-    if (e != cudaSuccess) return e;
-    note_launch();
-    PdlLaunch j(dim3(ctas), 256, 0, stream);
-    e = cudaLaunchKernelEx(&j.cfg, kv4_few_join_kernel<D, NT>, a, ws);
+    *left = partials_at(ws, ctas, S::kRows);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows, *left, after);
     note_launch();
     return e;
 }
 
 }  // namespace
 
-size_t kv4_few_workspace(int head_dim, int rows)
-{
-    const int r = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-    return (kRecordBytes + static_cast<size_t>(kMaxCtas) * 2 * r * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
-}
+size_t kv4_few_workspace(int head_dim, int rows) { return partials_bytes(kMaxCtas, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, head_dim); }
 
-cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
+cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, bool after, Partials* left, cudaStream_t stream)
 {
     if (a.cache.head_dim == 64) {
-        if (few_rows <= 8) return run<64, 1>(a, few_rows, ws, stream);
-        if (few_rows <= 16) return run<64, 2>(a, few_rows, ws, stream);
-        return run<64, 4>(a, few_rows, ws, stream);
+        if (few_rows <= 8) return run<64, 1>(a, few_rows, ws, after, left, stream);
+        if (few_rows <= 16) return run<64, 2>(a, few_rows, ws, after, left, stream);
+        return run<64, 4>(a, few_rows, ws, after, left, stream);
     }
-    if (few_rows <= 8) return run<128, 1>(a, few_rows, ws, stream);
-    if (few_rows <= 16) return run<128, 2>(a, few_rows, ws, stream);
-    return run<128, 4>(a, few_rows, ws, stream);
+    if (few_rows <= 8) return run<128, 1>(a, few_rows, ws, after, left, stream);
+    if (few_rows <= 16) return run<128, 2>(a, few_rows, ws, after, left, stream);
+    return run<128, 4>(a, few_rows, ws, after, left, stream);
 }
 
 }  // namespace lora

@@ -57,7 +57,6 @@ struct Shape {
     static constexpr int kQTile = kRowsPerTile * D * 2;   // bytes
     static constexpr int kKTile = kTok * D * 2;
     static constexpr int kVHalf = D * 64 * 2, kVTile = 2 * kVHalf;   // [64 positions each][dim][position]
-    static constexpr int kPartial = kRowsPerItem * (D + 2);   // floats of a partial result: sums, maxima, sums of weights
     static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + 1024;   // and alignment
     // tensor memory columns
     static constexpr uint32_t kS = 0, kO = 256;           // S (and P) of tile x at 128 x, O at 256 + D x
@@ -248,7 +247,7 @@ struct Piece {
 struct Walk {
     const AttendArgs& a;
     const int* prefix;   // blocks before each sequence
-    int group, x, end, s, i, at;   // x: place on the line; block i of sequence s begins at `at`
+    int group, share, x, end, s, i, at;   // share: places of a range; x: place on the line; block i of sequence s begins at `at`
     Seq q;
     Block b;
 
@@ -257,15 +256,15 @@ struct Walk {
         load_seq(a.batch, s, q, nullptr);
         b = block_at(q, i, group, a.window);
     }
-    // cost: places before each thread's share of the blocks, `share` blocks to a thread
-    __device__ __forceinline__ Walk(const AttendArgs& args, const int* pre, const int* cost, int share, int begin, int end_)
-        : a(args), prefix(pre), group(args.n_heads / args.cache.n_kv), x(begin), end(end_)
+    // cost: places before each thread's blocks, `per` blocks to a thread
+    __device__ __forceinline__ Walk(const AttendArgs& args, const int* pre, const int* cost, int per, int share_, int begin, int end_)
+        : a(args), prefix(pre), group(args.n_heads / args.cache.n_kv), share(share_), x(begin), end(end_)
     {
         if (x >= end) return;
         const int c = seq_at(cost, kThreads, x);
         at = cost[c];
-        s = seq_at(prefix, a.batch.n_seqs, c * share);
-        i = c * share - prefix[s];
+        s = seq_at(prefix, a.batch.n_seqs, c * per);
+        i = c * per - prefix[s];
         set_block();
         while (x >= at + (b.tiles + kItemCost) * a.cache.n_kv) next_block();
     }
@@ -288,9 +287,14 @@ struct Walk {
             }
             p.h = (x - at) / len;
             const int u0 = at + p.h * len;
-            const int t0 = max(0, x - u0 - kItemCost), t1 = max(0, min(len, end - u0) - kItemCost);
+            int t0 = max(0, x - u0 - kItemCost), t1 = max(0, min(len, end - u0) - kItemCost);
+            if (8 * len <= share) {
+                // An item that is short beside a range is not cut, since a cut costs partial results: it goes to
+                // the range that its middle lies in.
+                if (u0 + len / 2 < x || u0 + len / 2 >= end) t1 = t0; else { t0 = 0; t1 = b.tiles; }
+            }
             x = min(end, u0 + len);
-            if (t0 == t1) continue;   // only the item's start lies in the range
+            if (t0 == t1) continue;   // nothing of it, or only its start, lies in the range
             p.s = s;
             p.q = q;
             p.b = b;
@@ -310,21 +314,10 @@ __device__ __forceinline__ int range_at(int total, int n, int b)
     return static_cast<int>(static_cast<long long>(total) * min(b, n) / n);
 }
 
-// What the workspace holds: a record for each CTA of the item that begins in
-// its range and goes on after it, then two partial results for each CTA: of
-// the item that began before its range, and of the one that goes on after it.
-struct Record {
-    int rows, block_row0, seq_row0, h, last;   // rows 0: none; the item's pieces lie in CTAs [this, last]
-};
 constexpr int kMaxCtas = 160;   // CTAs that the workspace has room for
-constexpr size_t kRecordBytes = (kMaxCtas * sizeof(Record) + 255) / 256 * 256;
-__device__ __forceinline__ float* partial(void* ws, int cta, int slot, int floats)
-{
-    return reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kRecordBytes) + (static_cast<long long>(cta) * 2 + slot) * floats;
-}
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int few_rows, void* ws)
+__global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int few_rows, Partials left)
 {
     using S = Shape<D>;
     constexpr int kGroups = S::kGroups, kWords = S::kWords;
@@ -371,10 +364,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
         return ok && q.n * group > few_rows ? (q.n * group + kRowsPerItem - 1) / kRowsPerItem : 0;
     });
     __syncthreads();
-    const int blocks = prefix[a.batch.n_seqs], share = (blocks + kThreads - 1) / kThreads;
+    const int blocks = prefix[a.batch.n_seqs], per = (blocks + kThreads - 1) / kThreads;
     scan_seqs<kWarps>(kThreads, cost, sums, [&](int t) {
         int sum = 0;
-        for (int f = t * share; f < min(blocks, (t + 1) * share); ++f) {
+        for (int f = t * per; f < min(blocks, (t + 1) * per); ++f) {
             const int s = seq_at(prefix, a.batch.n_seqs, f);
             Seq q;
             load_seq(a.batch, s, q, nullptr);
@@ -388,9 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     const int total = cost[kThreads], n_ranges = range_count(total, gridDim.x);
     const int begin = range_at(total, n_ranges, blockIdx.x), end = range_at(total, n_ranges, blockIdx.x + 1);
     const uint32_t tmem = tmem_base;
-    if (tid == 0) static_cast<Record*>(ws)[blockIdx.x].rows = 0;
+    if (tid == 0) left.records[blockIdx.x].rows = 0;
     if (begin < end) {
-        Walk walk(a, prefix, cost, share, begin, end);
+        Walk walk(a, prefix, cost, per, total / n_ranges, begin, end);
         Piece pc{};
         // rows at positions lo..hi see all of the piece's tile j
         auto inner = [&](int j, int lo, int hi) {
@@ -619,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     warp_rows(pc, a.ld_out, q_s + x * S::kQTile, [&](int, long long e, uint8_t* at) { *reinterpret_cast<uint4*>(a.out + e) = *reinterpret_cast<uint4*>(at); });
                     __syncwarp();
                 } else {
-                    float* part_o = partial(ws, blockIdx.x, pc.starts, S::kPartial);
+                    float* part_o = left.slot(blockIdx.x, pc.starts, D);
                     part_o[kRowsPerItem * D + r] = top;
                     part_o[kRowsPerItem * (D + 1) + r] = sum;
 #pragma unroll
@@ -637,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 if (tid == 0 && pc.starts && !pc.ends) {
                     Record rec{rows, pc.b.row0, pc.q.row0, h, static_cast<int>(blockIdx.x)};
                     while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, rec.last + 1) < pc.u1) ++rec.last;
-                    static_cast<Record*>(ws)[blockIdx.x] = rec;
+                    left.records[blockIdx.x] = rec;
                 }
                 tile += n_tiles;
                 mine += n_tiles;
@@ -890,43 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     if (tid == 0 && failed) flag(a.status, LORA_DEV_TIMEOUT);
 }
 
-// Joins the pieces of the item that begins in CTA b's range and goes on, in
-// order: four CTAs to a record, a quarter of the rows each.
 template <int D>
-__global__ void __launch_bounds__(256) kv4_many_join_kernel(AttendArgs a, void* ws)
-{
-    using S = Shape<D>;
-    tc::grid_dep_wait();
-    tc::grid_dep_launch();
-    const int b = blockIdx.x >> 2, group = a.n_heads / a.cache.n_kv;
-    const Record u = static_cast<const Record*>(ws)[b];
-    const float inf = __int_as_float(0x7F800000);
-    for (int e = (blockIdx.x & 3) * 256 + threadIdx.x; e < u.rows * (D / 4); e += 1024) {
-        const int r = e / (D / 4), d = e % (D / 4) * 4;
-        float m = -inf, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = b; k <= u.last; ++k) m = fmaxf(m, partial(ws, k, k == b, S::kPartial)[kRowsPerItem * D + r]);
-#pragma unroll 4
-        for (int k = b; k <= u.last; ++k) {
-            const float* p = partial(ws, k, k == b, S::kPartial);
-            const float w = m == -inf ? 0.f : ex2(p[kRowsPerItem * D + r] - m);
-            const float4 v = *reinterpret_cast<const float4*>(p + r * D + d);
-            o.x = fmaf(v.x, w, o.x);
-            o.y = fmaf(v.y, w, o.y);
-            o.z = fmaf(v.z, w, o.z);
-            o.w = fmaf(v.w, w, o.w);
-            l = fmaf(p[kRowsPerItem * (D + 1) + r], w, l);
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int row = u.block_row0 + r;
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.seq_row0 + row / group) * a.ld_out + (u.h * group + row % group) * D + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    }
-}
-
-template <int D>
-cudaError_t run(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
+cudaError_t run(const AttendArgs& a, int few_rows, void* ws, Partials* left, cudaStream_t stream)
 {
     using S = Shape<D>;
     constexpr int kMaxSmem = 220 * 1024;
@@ -939,25 +897,19 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream
     }
     const int ctas = std::min(kMaxCtas, device_sms());
     PdlLaunch l(dim3(ctas), kThreads, S::kSmem + 4 * (a.batch.n_seqs + 1), stream);
-    cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D>, a, few_rows, ws);
-    if (e != cudaSuccess) return e;
-    note_launch();
-    PdlLaunch j(dim3(4 * ctas), 256, 0, stream);
-    e = cudaLaunchKernelEx(&j.cfg, kv4_many_join_kernel<D>, a, ws);
+    *left = partials_at(ws, ctas, kRowsPerItem);
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D>, a, few_rows, *left);
     note_launch();
     return e;
 }
 
 }  // namespace
 
-size_t kv4_many_workspace(int head_dim)
-{
-    return (kRecordBytes + static_cast<size_t>(kMaxCtas) * 2 * kRowsPerItem * (head_dim + 2) * sizeof(float) + 255) / 256 * 256;
-}
+size_t kv4_many_workspace(int head_dim) { return partials_bytes(kMaxCtas, kRowsPerItem, head_dim); }
 
-cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, cudaStream_t stream)
+cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, Partials* left, cudaStream_t stream)
 {
-    return a.cache.head_dim == 64 ? run<64>(a, few_rows, ws, stream) : run<128>(a, few_rows, ws, stream);
+    return a.cache.head_dim == 64 ? run<64>(a, few_rows, ws, left, stream) : run<128>(a, few_rows, ws, left, stream);
 }
 
 }  // namespace lora
