@@ -1,6 +1,7 @@
 // kv4_attend.cu -- which kernel takes which rows of lora_kv4_attend, and the
 // joining of what their ranges' ends cut.
 #include <algorithm>
+#include <cmath>
 
 #include "kv4_attend.cuh"
 #include "tc_common.cuh"
@@ -10,16 +11,26 @@ namespace lora {
 namespace {
 
 // Query rows to a kv head (a sequence's rows x the heads of a group) up to
-// which a sequence goes to the kernel for few rows.  Where all of a batch's
-// sequences are that short, all go there.  In a batch with longer ones the
-// single tokens still do, in the narrowest form that holds them.
-constexpr int kFewRows = 32;
+// which the kernel for few rows is the faster one whatever the lengths: it
+// takes 8 rows at a time over 32 positions in 0.9 ns of the GPU's time, the
+// tensor-memory kernel 256 rows over 128 positions in 11.5 ns.
+constexpr int kFewRows = 24;
 
-int few_limit(int group, int max_q_len)
+// The limit for a batch: all of its rows where the kernel for few rows takes
+// the shorter time by that account and the launches' fixed times (9 and 22 us:
+// so small batches of longer rows go to it too), otherwise kFewRows.
+// Measured both ways (us, 8 kv heads of 128, few / many): one sequence of 1000
+// positions with 256 rows 20 / 34, of 16000 with 40 rows 32 / 36 and with 64
+// 42 / 37; 32 of 1000 with 40 rows 51 / 61, of 8000 303 / 201.
+int few_limit(const AttendArgs& a)
 {
-    const long long rows = static_cast<long long>(group) * max_q_len;
-    if (rows <= kFewRows) return static_cast<int>(rows);
-    return group <= 8 ? 8 : group <= 16 ? 16 : group <= kFewRows ? kFewRows : 0;
+    const int group = a.n_heads / a.cache.n_kv;
+    const long long rows = static_cast<long long>(group) * a.batch.max_q_len;
+    const double units = static_cast<double>(a.batch.n_seqs) * a.cache.n_kv, ctx = a.batch.max_ctx_len;
+    const double few = 9e-6 + units * std::ceil(rows / 8.) * (ctx / 32 + 2) * 0.9e-9;
+    const double many = 22e-6 + units * std::ceil(rows / 256.) * (ctx / 128 + 4) * 11.5e-9;
+    if (rows <= kFewRows || few <= many) return static_cast<int>(std::min<long long>(rows, 1 << 30));
+    return group <= kFewRows ? kFewRows : 0;
 }
 
 // Joins the pieces behind each record, in order: kQuads 16-byte pieces of a
@@ -64,21 +75,21 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv
 
 }  // namespace
 
-// The kernels' workspaces lie one after the other.
+// The kernels' workspaces lie one after the other (which of them a batch's
+// longer rows go to depends on more than the arguments here).
 size_t kv4_attend_workspace(int n_heads, int n_kv, int head_dim, int max_q_len)
 {
-    const int group = n_heads / n_kv, few = few_limit(group, max_q_len);
-    return kv4_few_workspace(head_dim, few) + (static_cast<long long>(group) * max_q_len > few ? kv4_many_workspace(head_dim) : 0);
+    return kv4_few_workspace(head_dim) + (static_cast<long long>(n_heads / n_kv) * max_q_len > kFewRows ? kv4_many_workspace(head_dim) : 0);
 }
 
 cudaError_t launch_kv4_attend(const AttendArgs& a, cudaStream_t stream)
 {
     if (a.batch.n_rows == 0 || a.batch.max_q_len == 0) return cudaSuccess;
-    const int group = a.n_heads / a.cache.n_kv, D = a.cache.head_dim, few = few_limit(group, a.batch.max_q_len);
+    const int group = a.n_heads / a.cache.n_kv, D = a.cache.head_dim, few = few_limit(a);
     const bool many = static_cast<long long>(group) * a.batch.max_q_len > few;
     kv4::Partials p0{}, p1{};
     cudaError_t e = cudaSuccess;
-    if (many) e = launch_kv4_many(a, few, static_cast<uint8_t*>(a.ws) + kv4_few_workspace(D, few), &p0, stream);
+    if (many) e = launch_kv4_many(a, few, static_cast<uint8_t*>(a.ws) + kv4_few_workspace(D), &p0, stream);
     if (e == cudaSuccess && few) e = launch_kv4_few(a, few, a.ws, many, &p1, stream);
     const int ctas = p0.ctas * join_ctas(p0.rows, D) + p1.ctas * join_ctas(p1.rows, D);
     if (e != cudaSuccess || ctas == 0) return e;

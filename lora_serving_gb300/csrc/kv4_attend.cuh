@@ -168,6 +168,6 @@ inline size_t partials_bytes(int ctas, int rows, int D)
 cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, bool after, kv4::Partials* left, cudaStream_t stream);
 cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, kv4::Partials* left, cudaStream_t stream);
 size_t kv4_many_workspace(int head_dim);
-size_t kv4_few_workspace(int head_dim, int rows);
+size_t kv4_few_workspace(int head_dim);
 
 }  // namespace lora

@@ -2,8 +2,10 @@
 // paged 4-bit cache: the cache's bytes are the cost, so every byte is read
 // once and the codes are unpacked in registers.
 //
-// Work.  A unit is (sequence, kv head): up to 8 NT query rows (rows x heads
-// of the group) over the sequence's tiles of 32 positions.  All units laid
+// Work.  A unit is (sequence, kv head, slice of up to 8 query rows, rows
+// being a sequence's rows x the heads of the group) over the sequence's tiles
+// of 32 positions; the slices of a kv head lie next to each other, so that
+// the second one's bytes come from L2.  All units laid
 // end to end are cut into equal ranges, one per warp, whatever the lengths; a
 // unit counts kUnitCost tiles more than it has, for its start.  A warp that
 // has a whole unit writes its result; a unit cut by a range's end leaves
@@ -36,6 +38,13 @@ namespace {
 
 using namespace kv4;
 
+// Rows of a unit: one column block of the product.  Slices of 16 or 32 rows,
+// which unpack once for more rows, were slower for their registers: one CTA on
+// an SM (us, 32 requests of up to 1000 positions, rows of a kv head 16 / 32, by
+// slices of 8, 16, 32: heads of 128 16 / 21, 16 / 22, 29 / 33; of 64 13 / 17, 12 / 15, 15 / 17).
+constexpr int kRows = 8;
+// Two CTAs of eight warps on an SM: 128 registers a thread.
+constexpr int kCtas = 2, kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTile = 32;          // positions per tile: two halves of 16, the products' M
 constexpr int kHalf = 16;
 constexpr int kUnitCost = 2;       // a unit's start (tables, q, the first copies), in tiles
@@ -43,8 +52,8 @@ constexpr float kNone = -3e38f;    // the running maximum before any score (fini
 constexpr float kSlack = 8.f;      // log2 by which a score may pass the running maximum
 constexpr float kLift = 7.f;       // weights carry 2^7: at most 2^15, and fp16 holds them down to 2^-31 of the largest
 
-// Sizes of one form: head dimension D, up to 8 NT query rows to a unit.
-template <int D, int NT>
+// Sizes for head dimension D.
+template <int D>
 struct Shape {
     static constexpr int kGroups = D / kGroup;
     static constexpr int kWords = D / 32;                 // words of a lane per position (K) and per pair (V)
@@ -53,17 +62,11 @@ struct Shape {
     // a stage: K codes, V codes, K params, V params, each of both halves
     static constexpr int kVAt = 2 * kCodeBytes, kKpAt = 4 * kCodeBytes, kVpAt = kKpAt + 2 * kParamBytes;
     static constexpr int kStage = kVpAt + 2 * kParamBytes;
-    static constexpr int kRows = 8 * NT;
     static constexpr int kPartial = kRows * (D + 2);      // floats of a partial result: sums, maxima, sums of weights
-    // One row group's registers leave room for two CTAs on an SM, of six
-    // warps (168 registers; eight of 128 spill with heads of 128).
-    static constexpr int kCtas = NT == 1 ? 2 : 1;
-    static constexpr int kWarps = D == 128 && NT == 4 ? 6 : 8;
     // The ring is at least a partial result long: a warp's last one takes
     // the ring's place.
-    static constexpr int kStages = D == 128 && NT == 1 ? 2 : 4;
+    static constexpr int kStages = D == 128 ? 2 : 4;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kSmem = kWarps * (kRing + 4 * kPartial) + 256;   // and the running sum of the sequences
     static_assert(kRing >= 4 * kPartial, "ring");
 };
@@ -85,9 +88,13 @@ __device__ __forceinline__ int tiles_of(const Seq& q, int window)
     return max(1, (q.ctx + kTile - 1) / kTile - first_tile(q, window));   // at least one: its rows get their zeros
 }
 
-// The unit that holds place x (< total) of the line.
+// Slices of a sequence's rows, of kRows each.
+__device__ __forceinline__ int slices_of(const Seq& q, int group) { return (q.n * group + kRows - 1) / kRows; }
+
+// The unit that holds place x (< total) of the line: rows [row0, row0 + rows)
+// of positions x heads.
 struct Unit {
-    int s, h, u0, len;   // sequence, kv head, its first place, places (kUnitCost, then its tiles)
+    int s, h, row0, rows, u0, len;   // u0: its first place; len: its places (kUnitCost, then its tiles)
     Seq q;
 };
 __device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, int x)
@@ -95,10 +102,14 @@ __device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, 
     const int lo = seq_at(prefix, a.batch.n_seqs, x);
     Unit u;
     u.s = lo;
-    u.len = (prefix[lo + 1] - prefix[lo]) / a.cache.n_kv;
-    u.h = (x - prefix[lo]) / u.len;
-    u.u0 = prefix[lo] + u.h * u.len;
     load_seq(a.batch, lo, u.q, nullptr);
+    const int group = a.n_heads / a.cache.n_kv, slices = slices_of(u.q, group);
+    u.len = (prefix[lo + 1] - prefix[lo]) / (a.cache.n_kv * slices);
+    const int v = (x - prefix[lo]) / u.len;
+    u.u0 = prefix[lo] + v * u.len;
+    u.h = v / slices;
+    u.row0 = (v - u.h * slices) * kRows;
+    u.rows = min(kRows, u.q.n * group - u.row0);
     return u;
 }
 
@@ -107,7 +118,7 @@ __device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, 
 struct Piece {
     int u0;               // the unit's first place; -1: none
     int ends;             // whether the unit ends with this piece
-    int h, row0, rows, u1;
+    int h, seq_row0, row0, rows, u1;
 };
 
 constexpr int kMaxCtas = 2 * 160;   // CTAs that the workspace has room for
@@ -119,20 +130,21 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src)
 
 // A warp's running result of a unit: fragments of the sums, and the maximum
 // and the lane's part of the sum of weights of rows 2t, 2t + 1.
-template <int D, int NT>
+template <int D>
 struct Sums {
-    float acc[D / 16][NT][4], top[NT][2], sum[NT][2];
+    float acc[D / 16][4], top[2], sum[2];
 };
 
-// One warp: `n_mine` tiles from tile `tile` of sequence s, kv head h.
-template <int D, int NT>
-__device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring, int s, int h, const Seq& q, int tile, int n_mine,
-                                             Sums<D, NT>& out)
+// One warp: `n_mine` tiles from tile `tile` of sequence s, kv head h, for the
+// rows [row0, row0 + rows).
+template <int D>
+__device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring, int s, int h, const Seq& q, int row0, int rows, int tile, int n_mine,
+                                             Sums<D>& out)
 {
-    using S = Shape<D, NT>;
+    using S = Shape<D>;
     constexpr int kGroups = S::kGroups, kWords = S::kWords, kStages = S::kStages;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size, rows = q.n * group;
+    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
     const int p0 = q.ctx - q.n;   // position of the first row
     const int32_t* table = a.batch.block_table + static_cast<long long>(s) * a.batch.ld_table;
     const float inf = __int_as_float(0x7F800000);
@@ -187,18 +199,16 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) issue(i);
 
-    // ---- q as fragments: row n = 8 nt + g, dims 32 w + 8 t + (0..7)
-    uint32_t qf[NT][kWords][4];     // pairs (dims e, e + 4); odd pairs carry 1/16
-    float mult[NT][2], qsum[NT][kGroups][2], qoff[NT][kGroups][2];   // of rows 2t, 2t + 1
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = 8 * nt + g;
+    // ---- q as fragments: row g, dims 32 w + 8 t + (0..7)
+    uint32_t qf[kWords][4];     // pairs (dims e, e + 4); odd pairs carry 1/16
+    float mult[2], qsum[kGroups][2], qoff[kGroups][2];   // of rows 2t, 2t + 1
+    {
         uint4 raw[kWords];
         float top = 0.f;
-        const bf16_t* qp = a.q + static_cast<long long>(q.row0 + r / group) * a.ld_q + (h * group + r % group) * D + 8 * t;
+        const bf16_t* qp = a.q + static_cast<long long>(q.row0 + (row0 + g) / group) * a.ld_q + (h * group + (row0 + g) % group) * D + 8 * t;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
-            raw[w] = r < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
+            raw[w] = g < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
             const uint32_t part[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(part[e])), fabsf(bf16_hi(part[e]))));
@@ -221,8 +231,8 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float k = (i & 1) ? 1.f / 16 : 1.f;
-                qf[nt][w][i] = pack_f16x2(f[i] * k, f[i + 4] * k);
-                const float2 h = __half22float2(as_h2(qf[nt][w][i]));
+                qf[w][i] = pack_f16x2(f[i] * k, f[i + 4] * k);
+                const float2 h = __half22float2(as_h2(qf[w][i]));
                 sum[w / 2] = fmaf(h.x + h.y, (i & 1) ? 16.f : 1.f, sum[w / 2]);
                 ofs[w / 2] = fmaf(h.x + h.y, -1024.f, ofs[w / 2]);
             }
@@ -237,31 +247,26 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
         const float m = a.scale * 1.4426950408889634f * down;   // scores in log2
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            mult[nt][c] = __shfl_sync(0xFFFFFFFFu, m, 8 * t + 4 * c);
+            mult[c] = __shfl_sync(0xFFFFFFFFu, m, 8 * t + 4 * c);
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
-                qsum[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, sum[gr], 8 * t + 4 * c);
-                qoff[nt][gr][c] = __shfl_sync(0xFFFFFFFFu, ofs[gr], 8 * t + 4 * c);
+                qsum[gr][c] = __shfl_sync(0xFFFFFFFFu, sum[gr], 8 * t + 4 * c);
+                qoff[gr][c] = __shfl_sync(0xFFFFFFFFu, ofs[gr], 8 * t + 4 * c);
             }
         }
     }
-    int last[NT][2];   // position of rows 2t, 2t + 1: the last one they see
+    int last[2];   // position of rows 2t, 2t + 1: the last one they see
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) last[nt][c] = p0 + (8 * nt + 2 * t + c) / group;
+    for (int c = 0; c < 2; ++c) last[c] = p0 + (row0 + 2 * t + c) / group;
 
-    float (&acc)[D / 16][NT][4] = out.acc;
-    float (&top)[NT][2] = out.top, (&sum)[NT][2] = out.sum;
+    float (&acc)[D / 16][4] = out.acc;
+    float (&top)[2] = out.top, (&sum)[2] = out.sum;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int m = 0; m < D / 16; ++m)
 #pragma unroll
-        for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) acc[m][nt][c] = 0.f;
-        top[nt][0] = top[nt][1] = kNone;
-        sum[nt][0] = sum[nt][1] = 0.f;
-    }
+        for (int c = 0; c < 4; ++c) acc[m][c] = 0.f;
+    top[0] = top[1] = kNone;
+    sum[0] = sum[1] = 0.f;
 
     for (int i = 0; i < n_mine; ++i) {
         asm volatile("cp.async.wait_group %0;\n" ::"n"(kStages - 2) : "memory");
@@ -281,85 +286,70 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
         for (int hf = 0; hf < 2; ++hf) {
             // ---- scores
             const bool there = (live >> hf) & 1u;
-            float sc[NT][4];
+            float sc[4];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) sc[nt][c] = 0.f;
+            for (int c = 0; c < 4; ++c) sc[c] = 0.f;
             uint32_t kw[2][kWords];
 #pragma unroll
             for (int r = 0; r < 2; ++r) load_words<kWords>(src + hf * S::kCodeBytes + (g + 8 * r) * (D / 2) + t * (4 * kWords), kw[r]);
             const __half2* kp = reinterpret_cast<const __half2*>(src + S::kKpAt + hf * S::kParamBytes);
 #pragma unroll
             for (int gr = 0; gr < kGroups; ++gr) {
-                float d[NT][4];
+                float d[4];
 #pragma unroll
                 for (int w = 2 * gr; w < 2 * gr + 2; ++w) {
                     uint32_t lo[4], hi[4];
                     codes_1024(kw[0][w], lo);
                     codes_1024(kw[1][w], hi);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (w == 2 * gr)
-                            mma_f16_from(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1], qoff[nt][gr][0], qoff[nt][gr][1]);
-                        else
-                            mma_f16(d[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][w][0], qf[nt][w][1]);
-                        mma_f16(d[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][w][2], qf[nt][w][3]);
-                    }
+                    if (w == 2 * gr)
+                        mma_f16_from(d, lo[0], hi[0], lo[1], hi[1], qf[w][0], qf[w][1], qoff[gr][0], qoff[gr][1]);
+                    else
+                        mma_f16(d, lo[0], hi[0], lo[1], hi[1], qf[w][0], qf[w][1]);
+                    mma_f16(d, lo[2], hi[2], lo[3], hi[3], qf[w][2], qf[w][3]);
                 }
                 const float2 k0 = __half22float2(kp[g * kGroups + gr]), k1 = __half22float2(kp[(g + 8) * kGroups + gr]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    sc[nt][0] = fmaf(k0.x, d[nt][0], fmaf(k0.y, qsum[nt][gr][0], sc[nt][0]));
-                    sc[nt][1] = fmaf(k0.x, d[nt][1], fmaf(k0.y, qsum[nt][gr][1], sc[nt][1]));
-                    sc[nt][2] = fmaf(k1.x, d[nt][2], fmaf(k1.y, qsum[nt][gr][0], sc[nt][2]));
-                    sc[nt][3] = fmaf(k1.x, d[nt][3], fmaf(k1.y, qsum[nt][gr][1], sc[nt][3]));
-                }
+                sc[0] = fmaf(k0.x, d[0], fmaf(k0.y, qsum[gr][0], sc[0]));
+                sc[1] = fmaf(k0.x, d[1], fmaf(k0.y, qsum[gr][1], sc[1]));
+                sc[2] = fmaf(k1.x, d[2], fmaf(k1.y, qsum[gr][0], sc[2]));
+                sc[3] = fmaf(k1.x, d[3], fmaf(k1.y, qsum[gr][1], sc[3]));
             }
             bool up = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    sc[nt][c] *= mult[nt][c & 1];
-                    if (!inner) {
-                        const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[nt][c & 1];
-                        if (j > p || (a.window > 0 && j <= p - a.window) || !there) sc[nt][c] = -inf;
-                    }
-                    up |= sc[nt][c] > top[nt][c & 1] + kSlack;
+            for (int c = 0; c < 4; ++c) {
+                sc[c] *= mult[c & 1];
+                if (!inner) {
+                    const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[c & 1];
+                    if (j > p || (a.window > 0 && j <= p - a.window) || !there) sc[c] = -inf;
                 }
+                up |= sc[c] > top[c & 1] + kSlack;
+            }
             if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int c = 0; c < 2; ++c) {
+                    float m = fmaxf(sc[c], sc[c + 2]);
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+                    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+                    m = fmaxf(m, top[c]);
+                    const float keep = ex2(top[c] - m);
+                    top[c] = m;
+                    sum[c] *= keep;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float m = fmaxf(sc[nt][c], sc[nt][c + 2]);
-                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
-                        m = fmaxf(m, top[nt][c]);
-                        const float keep = ex2(top[nt][c] - m);
-                        top[nt][c] = m;
-                        sum[nt][c] *= keep;
-#pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            acc[k][nt][c] *= keep;
-                            acc[k][nt][c + 2] *= keep;
-                        }
+                    for (int k = 0; k < D / 16; ++k) {
+                        acc[k][c] *= keep;
+                        acc[k][c + 2] *= keep;
                     }
-            }
-            uint32_t pf[NT][2];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float w[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    w[c] = ex2(sc[nt][c] - (top[nt][c & 1] - kLift));
-                    sum[nt][c & 1] += w[c];
                 }
-                pf[nt][0] = transpose8(pack_f16x2(w[0], w[1]));
-                pf[nt][1] = transpose8(pack_f16x2(w[2], w[3]));
             }
+            uint32_t pf[2];
+            float w[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                w[c] = ex2(sc[c] - (top[c & 1] - kLift));
+                sum[c & 1] += w[c];
+            }
+            pf[0] = transpose8(pack_f16x2(w[0], w[1]));
+            pf[1] = transpose8(pack_f16x2(w[2], w[3]));
 
             // ---- values: dims g * D/8 + 4 w + e of positions (2t, 2t+1) and (2t+8, 2t+9)
             uint32_t step[2], low[2];
@@ -395,11 +385,8 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                 uint32_t a0[4], a1[4];
                 values(vw[0][w], as_h2(step[0]), as_h2(low[0]), a0);
                 values(vw[1][w], as_h2(step[1]), as_h2(low[1]), a1);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(acc[2 * w][nt], a0[0], a0[1], a1[0], a1[1], pf[nt][0], pf[nt][1]);
-                    mma_f16(acc[2 * w + 1][nt], a0[2], a0[3], a1[2], a1[3], pf[nt][0], pf[nt][1]);
-                }
+                mma_f16(acc[2 * w], a0[0], a0[1], a1[0], a1[1], pf[0], pf[1]);
+                mma_f16(acc[2 * w + 1], a0[2], a0[3], a1[2], a1[3], pf[0], pf[1]);
             }
         }
         if (!inner && __any_sync(0xFFFFFFFFu, poison)) {
@@ -411,16 +398,14 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                 const float nan = __half2float(p[0]) * 0.f + __half2float(p[2]) * 0.f;   // 0 where both are finite
                 if (nan == 0.f || j >= q.ctx) continue;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int c = 0; c < 2; ++c) {
+                    if (j > last[c] || (a.window > 0 && j <= last[c] - a.window)) continue;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        if (j > last[nt][c] || (a.window > 0 && j <= last[nt][c] - a.window)) continue;
-#pragma unroll
-                        for (int m = 0; m < D / 16; ++m) {
-                            acc[m][nt][c] += nan;
-                            acc[m][nt][c + 2] += nan;
-                        }
+                    for (int m = 0; m < D / 16; ++m) {
+                        acc[m][c] += nan;
+                        acc[m][c + 2] += nan;
                     }
+                }
             }
         }
     }
@@ -430,50 +415,47 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
 }
 
 // The unit's rows (slot null), or a partial result.
-template <int D, int NT>
-__device__ __forceinline__ void put(const AttendArgs& a, int h, const Seq& q, const Sums<D, NT>& o, float* slot)
+template <int D>
+__device__ __forceinline__ void put(const AttendArgs& a, int h, const Seq& q, int row0, int rows, const Sums<D>& o, float* slot)
 {
-    using S = Shape<D, NT>;
-    constexpr int kRows = S::kRows, kWords = S::kWords;
+    using S = Shape<D>;
+    constexpr int kWords = S::kWords;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, group = a.n_heads / a.cache.n_kv;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int c = 0; c < 2; ++c) {
+        float l = o.sum[c];
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
+        l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+        const int r = 2 * t + c;
+        if (r >= rows) continue;
+        if (!slot) {
+            const float k = l == 0.f ? 0.f : 1.f / l;
+            bf16_t* d = a.out + static_cast<long long>(q.row0 + (row0 + r) / group) * a.ld_out + (h * group + (row0 + r) % group) * D + g * (D / 8);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float l = o.sum[nt][c];
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
-            const int r = 8 * nt + 2 * t + c;
-            if (r >= q.n * group) continue;
-            if (!slot) {
-                const float k = l == 0.f ? 0.f : 1.f / l;
-                bf16_t* d = a.out + static_cast<long long>(q.row0 + r / group) * a.ld_out + (h * group + r % group) * D + g * (D / 8);
+            for (int w = 0; w < kWords; w += 2)
+                *reinterpret_cast<uint4*>(d + 4 * w) =
+                    make_uint4(pack_bf16x2(o.acc[2 * w][c] * k, o.acc[2 * w][c + 2] * k),
+                               pack_bf16x2(o.acc[2 * w + 1][c] * k, o.acc[2 * w + 1][c + 2] * k),
+                               pack_bf16x2(o.acc[2 * w + 2][c] * k, o.acc[2 * w + 2][c + 2] * k),
+                               pack_bf16x2(o.acc[2 * w + 3][c] * k, o.acc[2 * w + 3][c + 2] * k));
+        } else {
 #pragma unroll
-                for (int w = 0; w < kWords; w += 2)
-                    *reinterpret_cast<uint4*>(d + 4 * w) =
-                        make_uint4(pack_bf16x2(o.acc[2 * w][nt][c] * k, o.acc[2 * w][nt][c + 2] * k),
-                                   pack_bf16x2(o.acc[2 * w + 1][nt][c] * k, o.acc[2 * w + 1][nt][c + 2] * k),
-                                   pack_bf16x2(o.acc[2 * w + 2][nt][c] * k, o.acc[2 * w + 2][nt][c + 2] * k),
-                                   pack_bf16x2(o.acc[2 * w + 3][nt][c] * k, o.acc[2 * w + 3][nt][c + 2] * k));
-            } else {
-#pragma unroll
-                for (int w = 0; w < kWords; ++w)
-                    *reinterpret_cast<float4*>(slot + r * D + g * (D / 8) + 4 * w) =
-                        make_float4(o.acc[2 * w][nt][c], o.acc[2 * w][nt][c + 2], o.acc[2 * w + 1][nt][c], o.acc[2 * w + 1][nt][c + 2]);
-                if (g == 0) {
-                    slot[kRows * D + r] = o.top[nt][c];
-                    slot[kRows * D + kRows + r] = l;
-                }
+            for (int w = 0; w < kWords; ++w)
+                *reinterpret_cast<float4*>(slot + r * D + g * (D / 8) + 4 * w) =
+                    make_float4(o.acc[2 * w][c], o.acc[2 * w][c + 2], o.acc[2 * w + 1][c], o.acc[2 * w + 1][c + 2]);
+            if (g == 0) {
+                slot[kRows * D + r] = o.top[c];
+                slot[kRows * D + kRows + r] = l;
             }
         }
+    }
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_few_kernel(AttendArgs a, int few_rows, Partials left, bool after)
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, int few_rows, Partials left, bool after)
 {
-    using S = Shape<D, NT>;
-    constexpr int kRows = S::kRows, kWarps = S::kWarps;
+    using S = Shape<D>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Piece pieces[kWarps][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -488,7 +470,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
     scan_seqs<kWarps>(a.batch.n_seqs, prefix, warp_sums, [&](int s) {
         Seq q;
         const bool ok = load_seq(a.batch, s, q, blockIdx.x == 0 ? a.status : nullptr);
-        return ok && q.n > 0 && q.n * group <= few_rows ? (tiles_of(q, a.window) + kUnitCost) * a.cache.n_kv : 0;
+        return ok && q.n > 0 && q.n * group <= few_rows ? (tiles_of(q, a.window) + kUnitCost) * a.cache.n_kv * slices_of(q, group) : 0;
     });
     const int total = prefix[a.batch.n_seqs];
     const int n_ranges = range_count(total, gridDim.x * kWarps), b = blockIdx.x;
@@ -501,13 +483,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
         const int t0 = max(0, x - u.u0 - kUnitCost), t1 = max(0, min(u.len, end - u.u0) - kUnitCost);
         x = min(end, u.u0 + u.len);
         if (t0 == t1) continue;   // only the unit's start lies in the range
-        Sums<D, NT> o;
-        attend_tiles<D, NT>(a, ring, u.s, u.h, u.q, first_tile(u.q, a.window) + t0, t1 - t0, o);
+        Sums<D> o;
+        attend_tiles<D>(a, ring, u.s, u.h, u.q, u.row0, u.rows, first_tile(u.q, a.window) + t0, t1 - t0, o);
         const bool whole = t0 == 0 && t1 == u.len - kUnitCost;
         float* slot = t0 > 0 ? first_slot + warp * S::kPartial : reinterpret_cast<float*>(ring);
         if (!whole && lane == 0)
-            pieces[warp][t0 > 0 ? 0 : 1] = Piece{u.u0, t1 == u.len - kUnitCost, u.h, u.q.row0, u.q.n * group, u.u0 + u.len};
-        put<D, NT>(a, u.h, u.q, o, whole ? nullptr : slot);
+            pieces[warp][t0 > 0 ? 0 : 1] = Piece{u.u0, t1 == u.len - kUnitCost, u.h, u.q.row0, u.row0, u.rows, u.u0 + u.len};
+        put<D>(a, u.h, u.q, u.row0, u.rows, o, whole ? nullptr : slot);
     }
     __syncthreads();
 
@@ -526,7 +508,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
         const int last = 31 - __clz(set), ends = pieces[last >> 1][last & 1].ends;
         const bool starts = i0 & 1;
         float* to = left.slot(b, starts, D);
-        for (int e = tid; e < first.rows * (D / 4); e += S::kThreads) {
+        for (int e = tid; e < first.rows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = -inf, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -543,7 +525,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
             }
             if (starts && ends) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                *reinterpret_cast<uint2*>(a.out + static_cast<long long>(first.row0 + r / group) * a.ld_out + (first.h * group + r % group) * D + d) =
+                const int row = first.row0 + r;
+                *reinterpret_cast<uint2*>(a.out + static_cast<long long>(first.seq_row0 + row / group) * a.ld_out + (first.h * group + row % group) * D + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
             } else {
                 *reinterpret_cast<float4*>(to + r * D + d) = o;
@@ -554,7 +537,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
             }
         }
         if (starts && !ends) {
-            rec = Record{first.rows, 0, first.row0, first.h, b};
+            rec = Record{first.rows, first.row0, first.seq_row0, first.h, b};
             while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, (rec.last + 1) * kWarps) < first.u1) ++rec.last;
         }
     }
@@ -567,36 +550,36 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
 // launch, and no tables of the batch's work to build first.
 constexpr int kCluster = 8;
 
-template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) kv4_unit_kernel(AttendArgs a, int few_rows, bool after)
+template <int D>
+__global__ void __launch_bounds__(kThreads, kCtas) kv4_unit_kernel(AttendArgs a, int few_rows, bool after)
 {
-    using S = Shape<D, NT>;
-    constexpr int kRows = S::kRows, kWarps = S::kWarps;
+    using S = Shape<D>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, rank = static_cast<int>(cluster_rank());
     uint8_t* ring = smem + warp * S::kRing;
     float* mine = reinterpret_cast<float*>(smem + kWarps * S::kRing);   // the CTA's partial result: sums, then (maximum, sum of weights)
-    const int unit = blockIdx.x / kCluster, s = unit / a.cache.n_kv, h = unit - s * a.cache.n_kv;
-    const int group = a.n_heads / a.cache.n_kv;
+    const int group = a.n_heads / a.cache.n_kv, slices = (few_rows + kRows - 1) / kRows, per_seq = a.cache.n_kv * slices;
+    const int unit = blockIdx.x / kCluster, s = unit / per_seq, h = (unit - s * per_seq) / slices, row0 = (unit - s * per_seq - h * slices) * kRows;
     const float inf = __int_as_float(0x7F800000);
 
     if (!after) tc::grid_dep_wait();
     tc::grid_dep_launch();
     Seq q;
-    const bool ok = load_seq(a.batch, s, q, rank == 0 && h == 0 && tid == 0 ? a.status : nullptr);
+    const bool ok = load_seq(a.batch, s, q, rank == 0 && unit == s * per_seq && tid == 0 ? a.status : nullptr);
     if (after) tc::grid_dep_wait();   // no kernel completes before the one before it
-    if (!ok || q.n == 0 || q.n * group > few_rows) return;   // the whole cluster leaves, or none of it
+    const int rows = min(kRows, q.n * group - row0);
+    if (!ok || rows <= 0 || q.n * group > few_rows) return;   // the whole cluster leaves, or none of it
     const int tiles = tiles_of(q, a.window);
     auto share = [&](int w) { return static_cast<int>(static_cast<long long>(tiles) * w / (kCluster * kWarps)); };   // first tile of warp w of the cluster
     const int t0 = share(rank * kWarps + warp), t1 = share(rank * kWarps + warp + 1);
     if (t0 < t1) {
-        Sums<D, NT> o;
-        attend_tiles<D, NT>(a, ring, s, h, q, first_tile(q, a.window) + t0, t1 - t0, o);
-        put<D, NT>(a, h, q, o, reinterpret_cast<float*>(ring));
+        Sums<D> o;
+        attend_tiles<D>(a, ring, s, h, q, row0, rows, first_tile(q, a.window) + t0, t1 - t0, o);
+        put<D>(a, h, q, row0, rows, o, reinterpret_cast<float*>(ring));
     }
     __syncthreads();
-    const int work = q.n * group * (D / 4);
-    for (int e = tid; e < work; e += S::kThreads) {
+    const int work = rows * (D / 4);
+    for (int e = tid; e < work; e += kThreads) {
         const int r = e / (D / 4), d = e % (D / 4) * 4;
         float m = -inf, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -618,7 +601,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
     }
     cluster_arrive();
     cluster_wait();
-    for (int e = rank * S::kThreads + tid; e < work; e += kCluster * S::kThreads) {
+    for (int e = rank * kThreads + tid; e < work; e += kCluster * kThreads) {
         const int r = e / (D / 4), d = e % (D / 4) * 4;
         float2 ml[kCluster];
         float4 v[kCluster];
@@ -641,7 +624,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
             l = fmaf(ml[k].y, w, l);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(q.row0 + r / group) * a.ld_out + (h * group + r % group) * D + d) =
+        const int row = row0 + r;
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(q.row0 + row / group) * a.ld_out + (h * group + row % group) * D + d) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
     cluster_arrive();
@@ -650,30 +634,30 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, Shape<D, NT>::kCtas) k
 
 constexpr int kUnitTiles = 16;
 constexpr int kMaxSmem = 227 * 1024;
-static_assert(Shape<128, 4>::kSmem + 4 * kMaxSeqs <= kMaxSmem, "shared memory");
+static_assert(Shape<128>::kSmem + 4 * kMaxSeqs <= kMaxSmem, "shared memory");
 
-template <int D, int NT>
+template <int D>
 cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partials* left, cudaStream_t stream)
 {
-    using S = Shape<D, NT>;
+    using S = Shape<D>;
     static bool attr_set = false;
     cudaError_t e = cudaSuccess;
     if (!attr_set) {
-        e = cudaFuncSetAttribute(kv4_few_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kv4_unit_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        e = cudaFuncSetAttribute(kv4_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kv4_unit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
         if (e != cudaSuccess) return e;
         attr_set = true;
     }
-    const int ctas = std::min(kMaxCtas, device_sms() * S::kCtas);
+    const int ctas = std::min(kMaxCtas, device_sms() * kCtas);
     // Units that all have a cluster on the GPU at once, with at most kUnitTiles tiles to a warp: a cluster each.
     // Measured both ways (us, heads of 128 in groups of 4, cluster / ranges): one sequence of 1000, 8000, 32000
     // positions 6.3 / 9.9, 10.9 / 24.5, 28 / 32; four sequences 6.8 / 12.1, 14.6 / 20.9, 40 / 44; but two waves
     // of clusters (16 rows to a unit, two sequences of 1000) 16.3 / 15.6, and at more positions the ranges,
     // which every SM takes part in.
-    const long long units = static_cast<long long>(a.batch.n_seqs) * a.cache.n_kv;
-    if (a.batch.max_ctx_len <= kTile * kUnitTiles * kCluster * S::kWarps) {
+    const long long units = static_cast<long long>(a.batch.n_seqs) * a.cache.n_kv * ((few_rows + kRows - 1) / kRows);
+    if (a.batch.max_ctx_len <= kTile * kUnitTiles * kCluster * kWarps) {
         static int room = -1;   // clusters on the GPU at once
-        PdlLaunch l(dim3(static_cast<unsigned>(units * kCluster)), S::kThreads, S::kSmem, stream);
+        PdlLaunch l(dim3(static_cast<unsigned>(units * kCluster)), kThreads, S::kSmem, stream);
         cudaLaunchAttribute attr[2];
         attr[0] = l.attr[0];
         attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -687,38 +671,31 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partial
             one.gridDim = dim3(kCluster);
             one.attrs = attr + 1;
             one.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, kv4_unit_kernel<D, NT>, &one);
+            e = cudaOccupancyMaxActiveClusters(&n, kv4_unit_kernel<D>, &one);
             if (e != cudaSuccess) return e;
             room = n;
         }
         if (units <= room) {
             left->ctas = 0;
-            e = cudaLaunchKernelEx(&l.cfg, kv4_unit_kernel<D, NT>, a, few_rows, after);
+            e = cudaLaunchKernelEx(&l.cfg, kv4_unit_kernel<D>, a, few_rows, after);
             note_launch();
             return e;
         }
     }
-    PdlLaunch l(dim3(ctas), S::kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
-    *left = partials_at(ws, ctas, S::kRows);
-    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, NT>, a, few_rows, *left, after);
+    PdlLaunch l(dim3(ctas), kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
+    *left = partials_at(ws, ctas, kRows);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D>, a, few_rows, *left, after);
     note_launch();
     return e;
 }
 
 }  // namespace
 
-size_t kv4_few_workspace(int head_dim, int rows) { return partials_bytes(kMaxCtas, rows <= 8 ? 8 : rows <= 16 ? 16 : 32, head_dim); }
+size_t kv4_few_workspace(int head_dim) { return partials_bytes(kMaxCtas, kRows, head_dim); }
 
 cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, bool after, Partials* left, cudaStream_t stream)
 {
-    if (a.cache.head_dim == 64) {
-        if (few_rows <= 8) return run<64, 1>(a, few_rows, ws, after, left, stream);
-        if (few_rows <= 16) return run<64, 2>(a, few_rows, ws, after, left, stream);
-        return run<64, 4>(a, few_rows, ws, after, left, stream);
-    }
-    if (few_rows <= 8) return run<128, 1>(a, few_rows, ws, after, left, stream);
-    if (few_rows <= 16) return run<128, 2>(a, few_rows, ws, after, left, stream);
-    return run<128, 4>(a, few_rows, ws, after, left, stream);
+    return a.cache.head_dim == 64 ? run<64>(a, few_rows, ws, after, left, stream) : run<128>(a, few_rows, ws, after, left, stream);
 }
 
 }  // namespace lora

@@ -225,10 +225,21 @@ ATTENDS = [  # q_lens, ctx_lens, heads, kv, D, page, window
 ]
 
 
-def _attend(case, seed, q_scale=2.0, poison=True):
+# The host's bounds pick the kernel: exact ones send small batches to the
+# kernel for few rows, a cluster to a unit; loose ones send up to 24 rows of a
+# kv head to its form by ranges, more to the tensor-memory kernel.
+BOUNDS = ["exact", "loose"]
+LOOSE_CTX = 200000
+
+
+def _attend(case, seed, q_scale=2.0, poison=True, bounds="exact"):
     q_lens, ctx, H, KV, D, page, window = case
     rng = np.random.default_rng(seed)
     table, n_pages = _table(rng, ctx, page)
+    if bounds == "loose":
+        wide = np.full((len(ctx), -(-LOOSE_CTX // page)), -1, np.int32)
+        wide[:, :table.shape[1]] = table
+        table = wide
     pages = R.random_pages(rng, n_pages, KV, page, D)
     K, V = R.unpack(pages, page, D)
     if poison:   # what no row may see: infinities and NaN in every masked place
@@ -249,6 +260,9 @@ def _attend(case, seed, q_scale=2.0, poison=True):
     q = torch.from_numpy((q_scale * rng.standard_normal((T, H * D))).astype(np.float32)).bfloat16().cuda()
     cache = store.KV4Cache(n_pages, page, KV, D, pages=torch.from_numpy(pages).cuda())
     batch = store.KV4Batch.from_lens(q_lens, ctx, table)
+    if bounds == "loose":
+        batch.c.max_ctx_len = LOOSE_CTX
+        batch.c.max_q_len += 3
     return q, K, V, table, cache, batch
 
 
@@ -268,10 +282,11 @@ def _close(got, want, tol):
     assert (off <= tol).all(), (float((off / tol).max()), np.unravel_index(np.argmax(off / tol), off.shape))
 
 
+@pytest.mark.parametrize("bounds", BOUNDS)
 @pytest.mark.parametrize("case", ATTENDS, ids=range(len(ATTENDS)))
-def test_attend(case):
+def test_attend(case, bounds):
     q_lens, ctx, H, KV, D, page, window = case
-    q, K, V, table, cache, batch = _attend(case, 7 * H + D + len(ctx))
+    q, K, V, table, cache, batch = _attend(case, 7 * H + D + len(ctx), bounds=bounds)
     scale = 1 / math.sqrt(D)
     got = R.f64(_run(q, cache, batch, H, scale, window)).reshape(-1, H, D)
     want, tol = R.attend(R.f64(q).reshape(-1, H, D), K, V, q_lens, ctx, table, page, scale, window)
@@ -283,20 +298,22 @@ def test_attend(case):
 
 @pytest.mark.parametrize("q_len", [1, 4, 40])
 @pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
-def test_attend_scales(q_len, scale):
+@pytest.mark.parametrize("bounds", BOUNDS)
+def test_attend_scales(q_len, scale, bounds):
     """No score at all, a negative scale, and scores in the hundreds (one position takes all the weight)."""
     case = ([q_len, q_len], [300, 131], 8, 2, 128, 32, 0)
-    q, K, V, table, cache, batch = _attend(case, 5)
+    q, K, V, table, cache, batch = _attend(case, 5, bounds=bounds)
     got = R.f64(_run(q, cache, batch, 8, scale)).reshape(-1, 8, 128)
     want, tol = R.attend(R.f64(q).reshape(-1, 8, 128), K, V, case[0], case[1], table, 32, scale)
     _close(got, want, tol)
 
 
+@pytest.mark.parametrize("bounds", BOUNDS)
 @pytest.mark.parametrize("q_len", [1, 50])
-def test_attend_query_range(q_len):
+def test_attend_query_range(q_len, bounds):
     """Rows of zeros, and rows whose values lie outside fp16's range."""
     case = ([q_len, q_len], [200, 96], 4, 2, 64, 16, 0)
-    q, K, V, table, cache, batch = _attend(case, 6, q_scale=1.0)
+    q, K, V, table, cache, batch = _attend(case, 6, q_scale=1.0, bounds=bounds)
     q[0, :64] = 0
     q[0, 64:128] *= 1e-7
     q[0, 128:192] *= 1e6
@@ -306,12 +323,13 @@ def test_attend_query_range(q_len):
         _close(got, want[:1, h], tol[:1, h])
 
 
+@pytest.mark.parametrize("bounds", BOUNDS)
 @pytest.mark.parametrize("q_lens", [[1, 1, 1], [3, 1, 2], [60, 1, 45]])
-def test_attend_strides_alias_and_far_pages(q_lens):
+def test_attend_strides_alias_and_far_pages(q_lens, bounds):
     """q and out as slices of wider rows, out over q, and pages a gigabyte apart (offsets past 32 bits)."""
     ctx, H, KV, D, page = [130, 64, 99], 8, 2, 128, 32
     case = (q_lens, ctx, H, KV, D, page, 0)
-    q, K, V, table, cache, batch = _attend(case, 8)
+    q, K, V, table, cache, batch = _attend(case, 8, bounds=bounds)
     n, kv, block = cache.pages.shape
     gap = 700 * 1024 * 1024
     big = torch.empty((n - 1) * gap + kv * block, dtype=torch.uint8, device="cuda")
@@ -331,10 +349,11 @@ def test_attend_strides_alias_and_far_pages(q_lens):
     _close(R.f64(plain).reshape(-1, H, D), want, tol)
 
 
+@pytest.mark.parametrize("bounds", BOUNDS)
 @pytest.mark.parametrize("q_len", [1, 60])
-def test_attend_repeats_bit_for_bit_and_on_another_stream(q_len):
+def test_attend_repeats_bit_for_bit_and_on_another_stream(q_len, bounds):
     case = ([q_len] * 5, [3000, 60, 1, 800, 1999], 16, 4, 128, 64, 0)
-    q, K, V, table, cache, batch = _attend(case, 9)
+    q, K, V, table, cache, batch = _attend(case, 9, bounds=bounds)
     first = _run(q, cache, batch, 16, 0.1)
     ws = store.kv4_workspace(cache, 16, batch)
     st = torch.cuda.Stream()
@@ -368,11 +387,12 @@ def test_attend_graph_replay_with_refilled_tables():
         _close(R.f64(out).reshape(-1, H, D), want, tol)
 
 
+@pytest.mark.parametrize("bounds", BOUNDS)
 @pytest.mark.parametrize("q_len", [1, 4, 70])
-def test_attend_device_faults(q_len):
+def test_attend_device_faults(q_len, bounds):
     H, KV, D, page = 4, 2, 64, 16
     case = ([q_len, q_len, q_len], [200, 96, 130], H, KV, D, page, 0)
-    q, K, V, table, cache, batch = _attend(case, 11)
+    q, K, V, table, cache, batch = _attend(case, 11, bounds=bounds)
     ws, st = store.kv4_workspace(cache, H, batch), _status()
     clean = _run(q, cache, batch, H, 0.1)
     rows = [slice(i * q_len, (i + 1) * q_len) for i in range(3)]
@@ -409,10 +429,23 @@ def test_attend_device_faults(q_len):
     _close(R.f64(out).reshape(-1, H, D)[:2 * q_len], want[:2 * q_len], tol[:2 * q_len])
 
 
-def test_attend_nan_in_a_visible_place_stays_in_its_head():
-    case = ([1, 1], [50, 50], 4, 2, 64, 16, 0)
-    q, K, V, table, cache, batch = _attend(case, 12)
-    at = 16 * 64 + 3 * 4                                           # K params of position 3, kv head 1 of sequence 0
-    cache.pages[int(table[0, 0]), 1, at:at + 4] = torch.tensor([0, 0x7E, 0, 0x7E], dtype=torch.uint8)
-    out = _run(q, cache, batch, 4, 0.1).view(2, 4, 64)
-    assert out[0, 2:].isnan().all() and out[0, :2].isfinite().all() and out[1].isfinite().all()
+@pytest.mark.parametrize("bounds", BOUNDS)
+@pytest.mark.parametrize("part", ["k", "v"])
+@pytest.mark.parametrize("q_len", [1, 3, 40, 150])
+def test_attend_nan_reaches_the_rows_that_see_it(q_len, part, bounds):
+    """A NaN in one position's K or V of one kv head (of V, in one group of dims): rows that see the position get
+    NaN (in those dims), the others are as without it."""
+    D, page, n_kv = 128, 16, 2
+    case = ([q_len, 2], [q_len + 70, 90], 4, n_kv, D, page, 0)
+    q, K, V, table, cache, batch = _attend(case, 12, bounds=bounds)
+    clean = _run(q, cache, batch, 4, 0.1).view(-1, 4, D)
+    at = 70 + q_len // 2                                          # seen by the rows from q_len // 2 on
+    o = at % page
+    off = page * D + o * 8 + 4 if part == "k" else page * (D + 8) + (o // 2) * 16 + 8 + 2 * (o % 2)      # group 1 of K, of V
+    for low in (0, 2 if part == "k" else 4):
+        cache.pages[int(table[0, at // page]), 1, off + low:off + low + 2] = torch.tensor([0, 0x7E], dtype=torch.uint8)
+    out = _run(q, cache, batch, 4, 0.1).view(-1, 4, D)
+    sees = torch.zeros(q_len + 2, 4, D, dtype=torch.bool, device="cuda")
+    sees[q_len // 2:q_len, 2:, (64 if part == "v" else 0):] = True
+    assert torch.equal(out.isnan(), sees)
+    assert torch.equal(out[~sees], clean[~sees])
