@@ -33,8 +33,9 @@ def unpack(pages, page, D):
     for odd in (0, 1):
         for j in range(4):
             v[:, :, odd::2, j::4] = (vw >> np.uint32(16 * odd + 4 * j)) & 15
-    kp = raw[..., page * D:page * (D + 4 * G)].copy().view("<f2").reshape(n, kv, page, G, 2).astype(np.float64)
-    vp = raw[..., page * (D + 4 * G):].copy().view("<f2").reshape(n, kv, page // 2, G, 2, 2).astype(np.float64)
+    with np.errstate(invalid="ignore"):   # what a page holds past its positions may be anything
+        kp = raw[..., page * D:page * (D + 4 * G)].copy().view("<f2").reshape(n, kv, page, G, 2).astype(np.float64)
+        vp = raw[..., page * (D + 4 * G):].copy().view("<f2").reshape(n, kv, page // 2, G, 2, 2).astype(np.float64)
     vp = np.moveaxis(vp, -1, 3).reshape(n, kv, page, G, 2)
     at = np.arange(D) // GROUP
     with np.errstate(invalid="ignore", over="ignore"):
