@@ -152,46 +152,64 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     // ---- the ring
     const int pos0 = tile * kTile;
     const uint8_t* head_pages = a.cache.pages + static_cast<long long>(h) * block_bytes(ps, D);
-    const bool split = ps < kTile;   // a tile is two pages
-    unsigned has = 0;                // stages' halves that hold positions
+    unsigned has = 0;   // stages' halves that hold positions
     auto page_at = [&](int pos) -> int { return pos < q.ctx ? __ldg(table + (pos >> a.cache.page_shift)) : -1; };
-    int next0 = n_mine > 0 ? page_at(pos0) : -1, next1 = n_mine > 0 && split ? page_at(pos0 + kHalf) : -1;
+    // Bytes of a tile (or of half of one) in a block: codes at 16 lane, params at param_at.
+    const uint32_t ring_at = tc::smem_u32(ring) + 16 * lane;
+    const int codes_v = v_codes_off(ps, D);
+    int next = n_mine > 0 ? page_at(pos0) : -1;   // the next page to be read
+    const uint8_t *codes = nullptr, *params = nullptr;
+    int left = 0;                                 // tiles left in the page
     auto issue = [&](int i) {
         const int pos = pos0 + i * kTile, st = i % kStages;
-        const int page0 = next0, page1 = split ? next1 : page0;
-        if (i + 1 < n_mine) {
-            next0 = page_at(pos + kTile);
-            if (split) next1 = page_at(pos + kTile + kHalf);
-        }
+        const uint32_t dst = ring_at + st * S::kStage;
         has &= ~(3u << (2 * st));
-        if (i < n_mine) {
-            const bool ok0 = static_cast<unsigned>(page0) < static_cast<unsigned>(a.cache.n_pages);
-            const bool ok1 = static_cast<unsigned>(page1) < static_cast<unsigned>(a.cache.n_pages) && pos + kHalf < q.ctx;
-            has |= (ok0 ? 1u : 0u) << (2 * st) | (ok1 ? 2u : 0u) << (2 * st);
-            if (lane == 0 && ((!ok0 && pos < q.ctx) || (!ok1 && pos + kHalf < q.ctx))) flag(a.status, LORA_DEV_BAD_PAGE);
-            const int off0 = pos & (ps - 1), off1 = (pos + kHalf) & (ps - 1);
-            const uint8_t* b0 = head_pages + static_cast<long long>(page0) * a.cache.page_stride;
-            const uint8_t* b1 = head_pages + static_cast<long long>(page1) * a.cache.page_stride;
-            const uint32_t dst = tc::smem_u32(ring + st * S::kStage) + 16 * lane;
-            const uint8_t* s0 = b0 + off0 * (D / 2) + 16 * lane;
-            const uint8_t* s1 = b1 + off1 * (D / 2) + 16 * lane;
-#pragma unroll
-            for (int c = 0; c < S::kCodeBytes; c += 512) {
-                if (ok0) {
-                    copy16(dst + c, s0 + c);
-                    copy16(dst + S::kVAt + c, s0 + v_codes_off(ps, D) + c);
-                }
-                if (ok1) {
-                    copy16(dst + S::kCodeBytes + c, s1 + c);
-                    copy16(dst + S::kVAt + S::kCodeBytes + c, s1 + v_codes_off(ps, D) + c);
-                }
+        if (i < n_mine && ps >= kTile) {
+            if (left == 0) {
+                const int off = pos & (ps - 1);
+                const bool ok = static_cast<unsigned>(next) < static_cast<unsigned>(a.cache.n_pages);
+                if (!ok && pos < q.ctx && lane == 0) flag(a.status, LORA_DEV_BAD_PAGE);
+                const uint8_t* block = head_pages + static_cast<long long>(next) * a.cache.page_stride;
+                codes = ok ? block + off * (D / 2) + 16 * lane : nullptr;
+                params = block + (lane & 16 ? v_params_off(ps, D) : k_params_off(ps, D)) + off * 4 * kGroups + 16 * (lane & 15);
+                left = (ps - off) / kTile;
+                next = page_at(pos + left * kTile);
             }
-            // params: eight lanes to a half of K's, then of V's
-            const int pl = lane & 7, second = (lane >> 3) & 1;
-            if (pl < S::kParamBytes / 16 && (second ? ok1 : ok0)) {
-                const uint8_t* src = (second ? b1 + off1 * 4 * kGroups : b0 + off0 * 4 * kGroups) +
-                                     (lane & 16 ? v_params_off(ps, D) : k_params_off(ps, D)) + 16 * pl;
-                copy16(tc::smem_u32(ring + st * S::kStage) + S::kKpAt + (lane >> 3) * S::kParamBytes + 16 * pl, src);
+            if (codes) {
+                has |= (pos + kHalf < q.ctx ? 3u : 1u) << (2 * st);
+#pragma unroll
+                for (int c = 0; c < 2 * S::kCodeBytes; c += 512) {
+                    copy16(dst + c, codes + c);
+                    copy16(dst + S::kVAt + c, codes + codes_v + c);
+                }
+                // sixteen lanes K's params, sixteen V's
+                if ((lane & 15) < 2 * S::kParamBytes / 16)
+                    copy16(dst + S::kKpAt + (lane >> 4) * (2 * S::kParamBytes - 256), params);
+                codes += kTile * D / 2;
+                params += kTile * 4 * kGroups;
+            }
+            --left;
+        } else if (i < n_mine) {   // pages of half a tile
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int at = pos + kHalf * hf, page = next;
+                next = page_at(at + kHalf);
+                if (at >= q.ctx) continue;
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.cache.n_pages)) {
+                    if (lane == 0) flag(a.status, LORA_DEV_BAD_PAGE);
+                    continue;
+                }
+                has |= 1u << (2 * st + hf);
+                const uint8_t* block = head_pages + static_cast<long long>(page) * a.cache.page_stride;
+#pragma unroll
+                for (int c = 0; c < S::kCodeBytes; c += 512) {
+                    copy16(dst + hf * S::kCodeBytes + c, block + 16 * lane + c);
+                    copy16(dst + S::kVAt + hf * S::kCodeBytes + c, block + codes_v + 16 * lane + c);
+                }
+                const int pl = lane & 15;
+                if (pl < S::kParamBytes / 16)
+                    copy16(dst + S::kKpAt + hf * S::kParamBytes + (lane >> 4) * (2 * S::kParamBytes - 256),
+                           block + (lane & 16 ? v_params_off(ps, D) : k_params_off(ps, D)) + 16 * pl);
             }
         }
         asm volatile("cp.async.commit_group;\n" ::: "memory");
