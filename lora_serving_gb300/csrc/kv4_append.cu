@@ -85,7 +85,7 @@ __device__ __forceinline__ void rotate8(float* a, float* b, const float* cs, con
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 8) kv4_append_kernel(AppendArgs a, int per_row)
+__global__ void __launch_bounds__(kThreads, 6) kv4_append_kernel(AppendArgs a, int per_row)
 {
     constexpr int kLanes = D / 16, kGroups = D / kv4::kGroup;
     const int row = blockIdx.x * (kThreads / per_row) + threadIdx.x / per_row, of_row = threadIdx.x % per_row;
