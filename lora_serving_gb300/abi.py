@@ -179,21 +179,27 @@ def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
     return t.data_ptr()
 
 
+def _ptr(t, name: str, dtype) -> int:
+    """Pointer of a CUDA tensor of this element type."""
+    if not t.is_cuda or t.dtype is not dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
 def _mat(t, name: str, dtype, n_rows: int, cols: int):
     """(pointer, leading dimension) of a row-major kernel operand: a CUDA
     tensor of this element type with n_rows rows and cols columns at least
     and unit column stride.  None: (NULL, 0)."""
     if t is None:
         return 0, 0
-    if not t.is_cuda or t.dtype is not dtype:
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
+    ptr = _ptr(t, name, dtype)
     shape = t.shape
     if len(shape) != 2 or shape[0] < n_rows or shape[1] < cols:
         raise ValueError(f"{name} must be 2-D with {n_rows} rows and {cols} columns at least, got {tuple(shape)}")
     ld, unit = t.stride()
     if unit != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have unit column stride")
-    return t.data_ptr(), ld
+    return ptr, ld
 
 
 try:   # the current stream's handle without a Stream object around it (3 us of a call's 10)
@@ -320,6 +326,7 @@ def lora_merge_batch(Ws, As, Bs, sign, *, stream=None):
                                                        _stream(stream)))
 
 
+_Axes = ctypes.c_int * LORA_MAX_ROPE_AXES
 _BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
 
 
@@ -329,8 +336,8 @@ def lora_rms_norm(x, weight, eps, *, residual=None, residual_out=None, y=None, y
     -> y (bf16) and/or y8 (float8_e4m3fn) with fp32 scales [n_rows][groups], one
     per `group` (128) columns or, with group 0, per row."""
     n_rows, width = x.shape
-    if weight.numel() != width or not weight.is_contiguous():
-        raise ValueError(f"weight must hold {width} contiguous values")
+    if weight.shape != (width,) or weight.stride(0) != 1:
+        raise ValueError(f"weight must hold {width} adjacent values")
     y_p, ld_y = _mat(y, "y", _BF16, n_rows, width)
     y8_p, ld_y8 = _mat(y8, "y8", _E4M3, n_rows, width)
     s_p, ld_s = _mat(scales, "scales", _F32, n_rows, (width + group - 1) // group if group > 0 else 1)
@@ -338,7 +345,7 @@ def lora_rms_norm(x, weight, eps, *, residual=None, residual_out=None, y=None, y
     x_p, ld_x = _mat(x, "x", _BF16, n_rows, width)
     r_p, ld_r = _mat(residual, "residual", _BF16, n_rows, width)
     st = load().lora_rms_norm(y_p, ld_y, y8_p, ld_y8, s_p, ld_s, group, ro_p, ld_ro, x_p, ld_x, r_p, ld_r,
-                              _dev(weight, "weight", "bf16"), n_rows, width, eps, _stream(stream))
+                              _ptr(weight, "weight", _BF16), n_rows, width, eps, _stream(stream))
     if st:
         raise LoraError("lora_rms_norm", st)
 
@@ -355,19 +362,22 @@ def lora_kv4_append(q_out, x, cache, batch, *, n_heads, q_off, k_off, v_off, rop
     [n_rows][n_axes] or None; axis_pairs: pairs of each axis (default: all
     on one axis)."""
     n = batch.c.n_rows
-    q_p, ld_q = _mat(q_out, "q_out", _BF16, n, n_heads * cache.c.head_dim)
+    q_p, ld_q = _mat(q_out, "q_out", _BF16, n, n_heads * cache.head_dim)
     x_p, ld_x = _mat(x, "x", _BF16, n, 0)
-    rot = max_pos = n_axes = pos_p = ld_pos = 0
+    rot = max_pos = n_axes = pos_p = ld_pos = rope_p = 0
     axes = None
     if rope is not None:
-        if rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous():
+        shape = rope.shape
+        if len(shape) != 3 or shape[2] != 2 or not rope.is_contiguous():
             raise ValueError("rope must be contiguous [max_pos][pairs][2]")
-        max_pos, rot = rope.shape[0], 2 * rope.shape[1]
-        pairs = (rot // 2,) if axis_pairs is None else axis_pairs
+        rope_p, max_pos, rot = _ptr(rope, "rope", _F32), shape[0], 2 * shape[1]
+        pairs = (shape[1],) if axis_pairs is None else axis_pairs
         n_axes = len(pairs)
-        axes = (ctypes.c_int * max(1, n_axes))(*pairs)
+        if not 1 <= n_axes <= LORA_MAX_ROPE_AXES:
+            raise ValueError(f"axis_pairs must have 1 to {LORA_MAX_ROPE_AXES} entries")
+        axes = _Axes(*pairs)
         pos_p, ld_pos = _mat(positions, "positions", _I32, n, n_axes)
-    st = load().lora_kv4_append(q_p, ld_q, x_p, ld_x, n_heads, q_off, k_off, v_off, _dev(rope, "rope", "f32"), rot,
+    st = load().lora_kv4_append(q_p, ld_q, x_p, ld_x, n_heads, q_off, k_off, v_off, rope_p, rot,
                                 max_pos, pos_p, ld_pos, axes, n_axes, cache.ref, batch.ref,
                                 _dev(dev_status, "dev_status", "i32"), _stream(stream))
     if st:
@@ -376,9 +386,9 @@ def lora_kv4_append(q_out, x, cache, batch, *, n_heads, q_off, k_off, v_off, rop
 
 def lora_kv4_read(k, v, cache, batch, *, dev_status=None, stream=None):
     """k, v [n_rows][n_kv * head_dim] <- the cached values of the rows' places."""
-    width = cache.c.n_kv * cache.c.head_dim
-    k_p, ld_k = _mat(k, "k", _BF16, batch.c.n_rows, width)
-    v_p, ld_v = _mat(v, "v", _BF16, batch.c.n_rows, width)
+    n, width = batch.c.n_rows, cache.n_kv * cache.head_dim
+    k_p, ld_k = _mat(k, "k", _BF16, n, width)
+    v_p, ld_v = _mat(v, "v", _BF16, n, width)
     st = load().lora_kv4_read(k_p, ld_k, v_p, ld_v, cache.ref, batch.ref, _dev(dev_status, "dev_status", "i32"),
                               _stream(stream))
     if st:
@@ -388,9 +398,9 @@ def lora_kv4_read(k, v, cache, batch, *, dev_status=None, stream=None):
 def lora_kv4_attend(out, q, cache, batch, workspace, *, n_heads, scale, window=0, dev_status=None, stream=None):
     """out [n_rows][n_heads * head_dim] <- causal attention of q over the cache
     (the last `window` positions, 0: all)."""
-    width = n_heads * cache.c.head_dim
-    out_p, ld_out = _mat(out, "out", _BF16, batch.c.n_rows, width)
-    q_p, ld_q = _mat(q, "q", _BF16, batch.c.n_rows, width)
+    n, width = batch.c.n_rows, n_heads * cache.head_dim
+    out_p, ld_out = _mat(out, "out", _BF16, n, width)
+    q_p, ld_q = _mat(q, "q", _BF16, n, width)
     st = load().lora_kv4_attend(out_p, ld_out, q_p, ld_q, n_heads, scale, window, cache.ref, batch.ref,
                                 _dev(workspace, "workspace"), workspace.nbytes,
                                 _dev(dev_status, "dev_status", "i32"), _stream(stream))
