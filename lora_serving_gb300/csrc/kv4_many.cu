@@ -17,11 +17,27 @@
 // do the softmax, one row to a thread: no row needs another thread's numbers.
 // The issuing threads take turns: the tensor cores serve two threads in
 // alternation, which drew the tiles of rows into step, both waiting for their
-// products at the same time and then both at the softmax (4900 clocks a tile of 128 positions).
+// products at the same time and then both at the softmax.
 // The running maximum moves only when a score passes it by 2^8, so O is
 // seldom rescaled.  The dims of a K word come out of their nibbles in the
 // order 0 4 1 5 2 6 3 7; Q is laid out in the same order instead of undoing
 // it, a sum over dims not minding.
+//
+// From item to item.  The warps that unpack K copy the next item's Q as soon
+// as the last scores of this one are there, and its first scores are computed
+// while this one's result is written.
+//
+// What bounds it.  The two products take 2150 of an SM's clocks a tile, a
+// tile of rows' own chain (softmax 1500, products 1075 and the ways between
+// them) 3150 to 3300.  After that, the code's size: five roles share the
+// SM's instruction cache, so what is seldom run (masked tiles, results,
+// finding the pieces) is written small, as loops, and once: at 115 KB, a masked
+// tile took 5000 clocks against 2000 for the others, and 16 prompts 357 us
+// in place of 308.
+//
+// Measured: 1024 rows of 64 heads over 32768 positions 744 us (1.45 PFLOP/s,
+// 0.74 of the measured bf16 peak); 16 prompts of 149 to 2011 tokens, 32
+// heads, 308 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,7 +54,9 @@ constexpr int kRowsPerTile = 128, kRowsPerItem = 256;
 constexpr int kTok = 128;                  // positions of a tile
 constexpr int kStages = 2;                 // tiles of K, and of V, in shared memory
 constexpr int kSoftWarps = 8, kVWarp = 12, kMmaWarp = 16;
-constexpr int kWarps = 20, kThreads = 32 * kWarps;   // two MMA warps; their two neighbours only scan
+constexpr int kWalkWarp = 18;              // beside the two MMA warps
+constexpr int kWarps = 20, kThreads = 32 * kWarps;
+constexpr int kPieces = 4;                 // pieces that the walking warp is ahead
 constexpr int kNotes = 4;                  // tiles of which the softmax has notes (see Notes)
 // Registers: 96 a thread at launch; the softmax warps, which hold a row's
 // scores and weights, take what the others give up:
@@ -49,6 +67,7 @@ constexpr int kItemCost = 4;               // an item's start and end, in tiles
 constexpr int kMinRange = 6;               // a CTA's range, at least
 constexpr float kSlack = 8.f, kLift = 7.f; // as in the kernel for few rows
 constexpr uint32_t kTmemCols = 512;
+constexpr int kOutBytes = 32 * 64;         // a softmax warp's part of the result on its way out: 32 dims of 32 rows
 
 template <int D>
 struct Shape {
@@ -57,7 +76,7 @@ struct Shape {
     static constexpr int kQTile = kRowsPerTile * D * 2;   // bytes
     static constexpr int kKTile = kTok * D * 2;
     static constexpr int kVHalf = D * 64 * 2, kVTile = 2 * kVHalf;   // [64 positions each][dim][position]
-    static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + 1024;   // and alignment
+    static constexpr int kSmem = 2 * kQTile + kStages * (kKTile + kVTile) + kSoftWarps * kOutBytes + 1024;   // and alignment
     // tensor memory columns
     static constexpr uint32_t kS = 0, kO = 256;           // S (and P) of tile x at 128 x, O at 256 + D x
 };
@@ -129,12 +148,12 @@ __device__ __forceinline__ void after_wait(uint32_t (&r)[32])
 // Bounded waits, in line and timed by the SM's clock: a read of the global
 // timer, before the first poll, took longer than most waits here.
 constexpr long long kTimeoutClocks = 400000000;   // 0.2 s at 2 GHz
-__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity)
+__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, long long limit = kTimeoutClocks)
 {
     if (tc::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (!tc::mbar_try_wait(bar, parity))
-        if (clock64() - t0 > kTimeoutClocks) return false;
+        if (clock64() - t0 > limit) return false;
     return true;
 }
 // Polling, for the thread that feeds the tensor cores.
@@ -188,9 +207,11 @@ __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.
 
 struct Barriers {
     uint64_t k_full[kStages], k_free[kStages], v_full[kStages], v_free[kStages];
-    uint64_t s_full[2], p_full[2];   // of a tile of rows
+    uint64_t q_raw[2], q_full[2], q_free[2];   // of a tile of rows: Q as copied, as the products want it, done with
+    uint64_t s_full[2], p_full[2];
     uint64_t o_full[2];
     uint64_t turn[2];                // a tile of rows' products may be issued
+    uint64_t piece_full[kPieces], piece_free[kPieces];
 };
 
 // What the unpacking warps tell the softmax of a tile, a bit per position:
@@ -232,22 +253,28 @@ __device__ __forceinline__ Block block_at(const Seq& q, int i, int group, int wi
     return b;
 }
 
-// A range's part of an item.
+// A range's part of an item, in shared memory: one warp walks the range, the
+// others wait for what it finds (a walk in each role's code doubled the
+// kernel's instructions).
 struct Piece {
-    int s, h;
-    Seq q;
-    Block b;
-    int tile0, tiles;    // the piece's tiles
-    bool starts, ends;   // whether the item begins, ends with it
-    int u1;              // where the item ends on the line
+    int s, h, row0;      // sequence, kv head, the batch row of the sequence's first
+    int block, rows;     // the block's rows are [block, block + rows) of the sequence's
+    int pos0, p0, p1;    // positions of the sequence's first row, of the block's first and last
+    int tile0, tiles;    // the piece's tiles; 0: the range has ended
+    int base;            // tiles of the range before it
+    int starts, ends;    // whether the item begins, ends with it
+    int last;            // the last CTA with a part of an item that begins but does not end here
+};
+struct Held : Piece {    // a softmax warp's copy
+    int all0, all1;      // all of its tile of rows sees all of these tiles of the piece, [all0, all1)
 };
 
-// Walks the pieces of a CTA's range.  The line goes by blocks of rows in the
+// Finds the pieces of a CTA's range.  The line goes by blocks of rows in the
 // order of the sequences, the kv heads of a block one after another.
 struct Walk {
     const AttendArgs& a;
     const int* prefix;   // blocks before each sequence
-    int group, share, x, end, s, i, at;   // share: places of a range; x: place on the line; block i of sequence s begins at `at`
+    int group, share, x, end, s, i, at, base = 0;   // share: places of a range; x: place on the line; block i of sequence s begins at `at`
     Seq q;
     Block b;
 
@@ -277,7 +304,8 @@ struct Walk {
         }
         set_block();
     }
-    __device__ __forceinline__ bool next(Piece& p)
+    // The next piece; the place at which its item ends, 0 after the last.
+    __device__ __forceinline__ int next(Piece& p)
     {
         while (x < end) {
             const int len = b.tiles + kItemCost;
@@ -296,16 +324,22 @@ struct Walk {
             x = min(end, u0 + len);
             if (t0 == t1) continue;   // nothing of it, or only its start, lies in the range
             p.s = s;
-            p.q = q;
-            p.b = b;
+            p.row0 = q.row0;
+            p.block = b.row0;
+            p.rows = b.rows;
+            p.pos0 = q.ctx - q.n;
+            p.p0 = b.p0;
+            p.p1 = b.p1;
             p.tile0 = b.tile0 + t0;
             p.tiles = t1 - t0;
+            p.base = base;
             p.starts = t0 == 0;
             p.ends = t1 == b.tiles;
-            p.u1 = u0 + len;
-            return true;
+            base += p.tiles;
+            return u0 + len;
         }
-        return false;
+        p.tiles = 0;
+        return 0;
     }
 };
 __device__ __forceinline__ int range_count(int total, int ctas) { return min(ctas, max(1, total / kMinRange)); }
@@ -321,18 +355,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
 {
     using S = Shape<D>;
     constexpr int kGroups = S::kGroups, kWords = S::kWords;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ Barriers bar;
     __shared__ Notes<kGroups> notes;
+    __shared__ Piece pieces[kPieces];
+    __shared__ Held held[kSoftWarps][2];
+    constexpr int kPieceWords = sizeof(Piece) / 4;
+    static_assert(kPieceWords <= 32, "a lane to a word");
     __shared__ uint32_t tmem_base;
     __shared__ int sums[kWarps];
-    __shared__ int cost[kThreads + 1];
     __shared__ int failed;
     uint8_t* smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* q_s = smem;
     uint8_t* k_s = smem + 2 * S::kQTile;
     uint8_t* v_s = k_s + kStages * S::kKTile;
-    int* prefix = reinterpret_cast<int*>(v_s + kStages * S::kVTile);
+    uint8_t* out_s = v_s + kStages * S::kVTile;
+    int* cost = reinterpret_cast<int*>(out_s);   // until the ranges' places are known
+    static_assert(sizeof(int) * (kThreads + 1) <= kSoftWarps * kOutBytes, "shared memory");
+    int* prefix = reinterpret_cast<int*>(out_s + kSoftWarps * kOutBytes);
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0), lane = tid & 31;
 
     if (warp == kMmaWarp) tc::tmem_alloc(&tmem_base, kTmemCols);
@@ -344,10 +384,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             tc::mbar_init(&bar.v_free[i], 2);
         }
         for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&bar.q_raw[i], 128);   // the threads that unpack K
+            tc::mbar_init(&bar.q_full[i], 4);
+            tc::mbar_init(&bar.q_free[i], 1);
             tc::mbar_init(&bar.s_full[i], 1);
             tc::mbar_init(&bar.p_full[i], 4);
             tc::mbar_init(&bar.o_full[i], 1);
             tc::mbar_init(&bar.turn[i], 1);
+        }
+        for (int i = 0; i < kPieces; ++i) {
+            tc::mbar_init(&bar.piece_full[i], 1);
+            tc::mbar_init(&bar.piece_free[i], kWalkWarp);   // the other roles' warps
         }
         tc::mbar_init_fence();
         failed = 0;
@@ -355,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     if (tid < kNotes) notes.any_sick[tid] = 0;
     tc::grid_dep_wait();
     tc::grid_dep_launch();
+    if (tid == 0) left.records[blockIdx.x].rows = 0;
 
     // ---- this CTA's range: blocks before each sequence, then places before each thread's share of the blocks
     const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
@@ -378,16 +426,21 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     tc::tc_fence_before();
     __syncthreads();   // barriers, the tensor memory's address, the running sums
     tc::tc_fence_after();
-    const int total = cost[kThreads], n_ranges = range_count(total, gridDim.x);
-    const int begin = range_at(total, n_ranges, blockIdx.x), end = range_at(total, n_ranges, blockIdx.x + 1);
     const uint32_t tmem = tmem_base;
-    if (tid == 0) left.records[blockIdx.x].rows = 0;
-    if (begin < end) {
-        Walk walk(a, prefix, cost, per, total / n_ranges, begin, end);
-        Piece pc{};
-        // rows at positions lo..hi see all of the piece's tile j
-        auto inner = [&](int j, int lo, int hi) {
-            const int c = (pc.tile0 + j) * kTok;
+    {
+        // The n-th piece of the range, null after the last (or with ok false); a warp gives it back when it is done with it.
+        bool ok = true;
+        auto piece = [&](int n) -> const Piece* {
+            ok = ok && wait_for(&bar.piece_full[n % kPieces], (n / kPieces) & 1);
+            return ok && pieces[n % kPieces].tiles ? &pieces[n % kPieces] : nullptr;
+        };
+        auto give_back = [&](int n) {
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bar.piece_free[n % kPieces]);
+        };
+        // rows at positions lo..hi see all of tile t
+        auto inner = [&](int t, int lo, int hi) {
+            const int c = t * kTok;
             return c + kTok - 1 <= lo && (a.window == 0 || c > hi - a.window);
         };
 
@@ -397,243 +450,259 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // 32 lanes of tensor memory, << 16
             const uint32_t ts = tmem + lanes + S::kS + 128 * x, to = tmem + lanes + S::kO + D * x;
             const float inf = __int_as_float(0x7F800000);
-            // f(which, element of a matrix with this leading dimension, place in the swizzled tile) for every 16 bytes
-            // of the warp's 32 rows, a row to D / 8 neighbouring lanes
-            auto warp_rows = [&](const Piece& p, int ld, uint8_t* tile_s, auto f) {
-                constexpr int kLanes = D / 8, kStep = 32 / kLanes;
-                const int c = lane % kLanes;
-                int r = (x * 4 + (warp & 3)) * 32 + lane / kLanes;
-                const int t = (p.b.row0 + r) / group, dt = kStep / group, dh = kStep - dt * group;
-                int hh = p.b.row0 + r - t * group;
-                long long at = static_cast<long long>(p.q.row0 + t) * ld + (p.h * group + hh) * D + 8 * c;
-                const int on = dt * ld + dh * D, wrap = ld - group * D;   // to the next row, and where that is the next token's
-                uint8_t* place = tile_s + (c >> 3) * (kRowsPerTile * 128) + (r & 127) * 128;
-#pragma unroll
-                for (int i = 0; i < 32; i += kStep) {
-                    if (r < p.b.rows) f(i / kStep, at, place + (((c & 7) ^ (r & 7)) << 4));
-                    r += kStep;
-                    place += kStep * 128;
-                    hh += dh;
-                    at += on;
-                    if (hh >= group) {
-                        hh -= group;
-                        at += wrap;
+            const int rt = x * kRowsPerTile + (tid & 127);   // this thread's row of an item
+            uint8_t* const mine_s = out_s + warp * kOutBytes;
+            int n = 0;   // pieces so far
+            // The next piece with rows in this tile of rows, as the warp's own copy (it is still at the last one's result
+            // when it looks for it, and there may be any number to pass by).
+            auto next_piece = [&](int i) -> const Held* {
+                const Piece* p;
+                while ((p = piece(n))) {
+                    const bool has = x * kRowsPerTile < p->rows;
+                    Held& h = held[warp][i & 1];
+                    if (has) {
+                        if (lane < kPieceWords) reinterpret_cast<int*>(static_cast<Piece*>(&h))[lane] = reinterpret_cast<const int*>(p)[lane];
+                        const int lo = p->pos0 + (p->block + x * kRowsPerTile) / group;
+                        const int hi = p->pos0 + (p->block + min(p->rows, (x + 1) * kRowsPerTile) - 1) / group;
+                        if (lane == 0) h.all0 = max(1, a.window > 0 && hi >= a.window ? (hi - a.window) / kTok + 1 - p->tile0 : 0);   // the first sets the maximum
+                        if (lane == 0) h.all1 = (max(0, lo + 1)) / kTok - p->tile0;
                     }
+                    give_back(n++);
+                    if (has) return &h;
                 }
+                return nullptr;
             };
-            int tile = 0, mine = 0, items = 0;   // tiles so far; of this tile of rows; and its items
-            bool ok = true;
-            while (ok && walk.next(pc)) {
-                const int h = pc.h, n_tiles = pc.tiles, rows = pc.b.rows, p0 = pc.b.p0, p1 = pc.b.p1;
-                if (x * kRowsPerTile >= rows) {
-                    tile += n_tiles;
-                    continue;
+            // Q: one row to a thread, taken to fp16 with a power of two, in its place; the factor back to log2 scores
+            auto take_q = [&](bool live, int items, float& mult) {
+                if (!wait_for(&bar.q_raw[x], items & 1)) return false;
+                const int r = tid & 127;
+                uint8_t* dst = q_s + x * S::kQTile + r * 128;
+                auto at = [&](int c) { return reinterpret_cast<uint4*>(dst + (c >> 3) * (kRowsPerTile * 128) + (((c & 7) ^ (r & 7)) << 4)); };
+                __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
+#pragma unroll 4
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = *at(c);
+                    const uint32_t p[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t u = p[e] & 0x7FFF7FFFu;
+                        top2 = __hmax2(top2, *reinterpret_cast<const __nv_bfloat162*>(&u));
+                    }
                 }
-                const int r = x * kRowsPerTile + (tid & 127);   // row of the item
-                const int row = pc.b.row0 + r;
-                const bool live = r < rows;
-                const int pos = pc.q.ctx - pc.q.n + row / group;
-                // ---- Q: one row to a thread, taken to fp16 with a power of two, into the swizzled tile (the
-                // last item's products with it are done: its result has been read)
-                float mult;
-                {
-                    // the warp's rows come in whole lines (16 bytes of 32 rows to an instruction cost as many
-                    // lines as rows), then each thread takes its own
-                    warp_rows(pc, a.ld_q, q_s + x * S::kQTile, [&](int, long long e, uint8_t* at) {
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(tc::smem_u32(at)), "l"(a.q + e) : "memory");
-                    });
-                    asm volatile("cp.async.wait_all;\n" ::: "memory");
-                    __syncwarp();
-                    const int rt = tid & 127;
-                    uint8_t* dst = q_s + x * S::kQTile + rt * 128;
-                    auto at = [&](int c) { return reinterpret_cast<uint4*>(dst + (c >> 3) * (kRowsPerTile * 128) + (((c & 7) ^ (rt & 7)) << 4)); };
-                    uint4 raw[D / 8];
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) raw[c] = live ? *at(c) : make_uint4(0, 0, 0, 0);
-                    __nv_bfloat162 top2 = __float2bfloat162_rn(0.f);
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint32_t p[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t u = p[e] & 0x7FFF7FFFu;
-                            top2 = __hmax2(top2, *reinterpret_cast<const __nv_bfloat162*>(&u));
-                        }
-                    }
-                    const float top = fmaxf(__low2float(top2), __high2float(top2));
-                    const int fe = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
-                    float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : 1.f;
-                    const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
-                    mult = fabsf(a.scale) * 1.4426950408889634f * down;   // scores in log2, never a negative factor
-                    if (a.scale < 0.f) up = -up;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 v = raw[c];
-                        const float f[8] = {bf16_lo(v.x) * up, bf16_hi(v.x) * up, bf16_lo(v.y) * up, bf16_hi(v.y) * up,
-                                            bf16_lo(v.z) * up, bf16_hi(v.z) * up, bf16_lo(v.w) * up, bf16_hi(v.w) * up};
-                        *at(c) = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
-                    }
+                // (a row past the last holds what was there: its factor is 0, so that its scores are finite or NaN, and its own)
+                const float top = live ? fmaxf(__low2float(top2), __high2float(top2)) : 0.f;
+                const int fe = min(261 - static_cast<int>(__float_as_uint(top) >> 23), 253);
+                float up = top > 0.f ? __uint_as_float(static_cast<uint32_t>(fe) << 23) : live ? 1.f : 0.f;
+                const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - fe) << 23) : 1.f;
+                // scores in log2, never a negative factor; nor 0, which would make a masked score's -inf a NaN (1e-30 of
+                // the largest product is below 2^-50)
+                mult = fmaxf(fabsf(a.scale) * 1.4426950408889634f * down, 1e-30f);
+                if (a.scale < 0.f) up = -up;
+#pragma unroll 2
+                for (int c = 0; c < D / 8; ++c) {
+                    const uint4 v = *at(c);
+                    const float f[8] = {bf16_lo(v.x) * up, bf16_hi(v.x) * up, bf16_lo(v.y) * up, bf16_hi(v.y) * up,
+                                        bf16_lo(v.z) * up, bf16_hi(v.z) * up, bf16_lo(v.w) * up, bf16_hi(v.w) * up};
+                    *at(c) = make_uint4(pack_f16x2(f[0], f[4]), pack_f16x2(f[1], f[5]), pack_f16x2(f[2], f[6]), pack_f16x2(f[3], f[7]));
                 }
                 tc::fence_async_smem();
-                tc::named_barrier(1 + x, 128 + 32);   // Q is in place (the tile's MMA warp waits too)
-
-                // ---- softmax
-                const int x0 = pc.b.row0 + x * kRowsPerTile, x1 = pc.b.row0 + min(rows, (x + 1) * kRowsPerTile) - 1;
-                const int lo = pc.q.ctx - pc.q.n + x0 / group, hi = pc.q.ctx - pc.q.n + x1 / group;
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&bar.q_full[x]);
+                return true;
+            };
+            int mine = 0, items = 0;   // tiles and items of this tile of rows so far
+            float mult = 0.f;
+            const Held* pc = next_piece(0);
+            if (pc) ok = take_q(rt < pc->rows, 0, mult);
+            while (pc && ok) {
                 float top = -inf, sum = 0.f;
                 uint32_t sick = 0;   // groups of dims in which this row sees a value that is not finite
+                // Moves the running maximum where a score passes it by 2^8; `first`: there are no sums yet.  (The last
+                // product with V is done: the scores at hand were issued after it.)
+                auto raise = [&](float high, bool first) {
+                    if (__builtin_expect(!__any_sync(0xFFFFFFFFu, high > top + kSlack), 1)) return false;
+                    const float next = fmaxf(high, top);
+                    const float keep = next == -inf ? 1.f : ex2(top - next);
+                    top = next;
+                    sum *= keep;
+                    if (!first) {
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            uint32_t w[16];
+                            tmem_ld16_start(to + c, w);
+                            tmem_ld16_wait(w);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
+                            tmem_st16(to + c, w);
+                        }
+                    }
+                    return true;
+                };
+                const int n_tiles = pc->tiles, ja = pc->all0, jb = pc->all1;
                 for (int j = 0; j < n_tiles; ++j) {
+                    const int note = (pc->base + j) & (kNotes - 1);
+                    const bool in = j >= ja && j < jb;
                     if (!wait_for(&bar.s_full[x], (mine + j) & 1)) { ok = false; break; }
                     tc::tc_fence_after();
-                    const int note = (tile + j) & (kNotes - 1);
+                    uint32_t v[2][32];   // scores: one load ahead of the arithmetic
+                    tmem_ld32_start(ts, v[0]);
                     const uint4 hid4 = notes.hidden[note];
-                    const uint32_t hid[4] = {hid4.x, hid4.y, hid4.z, hid4.w};
-                    const bool all = inner(j, lo, hi) && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
-                    const int c0 = (pc.tile0 + j) * kTok;
-                    // this row sees columns [c_lo, c_hi) of the tile
-                    const int c_hi = pos + 1 - c0, c_lo = a.window > 0 ? pos + 1 - a.window - c0 : 0;
-                    auto highest = [&](const float (&m)[4]) {
-                        const float h = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * mult;
-                        return h != h ? -inf : h;   // 0 * -inf: nothing seen
+                    const bool all = in && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
+                    auto sees = [&](int c) {   // a bit for each of 32 columns that this row sees
+                        const int c_hi = pc->pos0 + (pc->block + rt) / group + 1 - (pc->tile0 + j) * kTok - 32 * c;
+                        return bits_in(a.window > 0 ? c_hi - a.window : 0, c_hi) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c];
                     };
-                    if (j == 0) {   // the first tile's maximum
-                        float m[4] = {-inf, -inf, -inf, -inf};
-#pragma unroll 1
-                        for (int c = 0; c < kTok / 32; ++c) {
-                            uint32_t w[32];
-                            tmem_ld32_start(ts + 32 * c, w);
-                            tmem_wait_ld();
-                            after_wait(w);
-                            const uint32_t see = bits_in(c_lo - 32 * c, c_hi - 32 * c) & ~(c == 0 ? hid[0] : c == 1 ? hid[1] : c == 2 ? hid[2] : hid[3]);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) m[e & 3] = fmaxf(m[e & 3], (see >> e) & 1u ? __uint_as_float(w[e]) : -inf);
-                        }
-                        top = highest(m);
-                    }
-                    // Weights against the running maximum as it stands; where a score passes it by 2^8 the
-                    // maximum moves, O is rescaled and they are taken again.
-                    uint32_t p[kTok / 2];
-                    float2 part[2];
-                    for (;;) {
-                        const float off = top == -inf ? 0.f : kLift - top;
-                        const float2 mult2 = make_float2(mult, mult), off2 = make_float2(off, off);
-                        float m[4] = {-inf, -inf, -inf, -inf};
-                        part[0] = part[1] = make_float2(0.f, 0.f);
-                        auto weigh = [&](auto masked) {
-                            constexpr bool kMasked = decltype(masked)::value;
-                            uint32_t v[2][32];   // one load ahead of the arithmetic
-                            tmem_ld32_start(ts, v[0]);
+                    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    if (__builtin_expect(all, 1)) {
+                        // Weights against the running maximum as it stands, taken again where it has to move.
+                        uint32_t p[kTok / 2];
+                        for (;;) {
+                            const float off = top == -inf ? 0.f : kLift - top;
+                            const float2 mult2 = make_float2(mult, mult), off2 = make_float2(off, off);
+                            float m[2] = {-inf, -inf};
+                            part[0] = part[1] = make_float2(0.f, 0.f);
 #pragma unroll
                             for (int c = 0; c < kTok / 32; ++c) {
                                 uint32_t(&w)[32] = v[c & 1];
                                 tmem_wait_ld();
                                 after_wait(w);
                                 if (c + 1 < kTok / 32) tmem_ld32_start(ts + 32 * (c + 1), v[(c + 1) & 1]);
-                                const uint32_t see = kMasked ? bits_in(c_lo - 32 * c, c_hi - 32 * c) & ~hid[c] : 0u;
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) {
-                                    float2 x2 = make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
-                                    if (kMasked) {
-                                        if (!((see >> e) & 1u)) x2.x = -inf;
-                                        if (!((see >> e) & 2u)) x2.y = -inf;
-                                    }
-                                    m[(e >> 1) & 3] = fmaxf(m[(e >> 1) & 3], fmaxf(x2.x, x2.y));
+                                    const float2 x2 = make_float2(__uint_as_float(w[e]), __uint_as_float(w[e + 1]));
+                                    m[(e >> 1) & 1] = fmaxf(m[(e >> 1) & 1], fmaxf(x2.x, x2.y));
                                     float2 y = fma2(x2, mult2, off2);
                                     y.x = ex2(y.x);
                                     y.y = ex2(y.y);
-                                    if (kMasked) {   // 0 * -inf with a scale of 0
-                                        if (!((see >> e) & 1u)) y.x = 0.f;
-                                        if (!((see >> e) & 2u)) y.y = 0.f;
-                                    }
                                     part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], y);
                                     p[16 * c + (e >> 1)] = pack_f16x2(y.x, y.y);
                                 }
                             }
-                        };
-                        if (all) weigh(std::false_type{}); else weigh(std::true_type{});
-                        const float high = highest(m);
-                        if (!__any_sync(0xFFFFFFFFu, high > top + kSlack)) break;
-                        const float next = fmaxf(high, top);
-                        const float keep = next == -inf ? 1.f : ex2(top - next);
-                        top = next;
-                        sum *= keep;
-                        {   // (the last product with V is done: this tile's scores were issued after it)
+                            if (!raise(fmaxf(m[0], m[1]) * mult, false)) break;
+                            tmem_ld32_start(ts, v[0]);
+                        }
 #pragma unroll
-                            for (int c = 0; c < D; c += 16) {
-                                uint32_t w[16];
-                                tmem_ld16_start(to + c, w);
-                                tmem_ld16_wait(w);
+                        for (int c = 0; c < kTok / 2; c += 16) tmem_st16(ts + c, p + c);
+                    } else {
+                        // An item's first tile, which sets the maximum, or a tile that not every row sees all of: the
+                        // maximum first, then the weights, 32 columns at a time (few instructions for what is seldom
+                        // run: they are read from memory when it is).
+                        float m[2] = {-inf, -inf};
+                        tmem_wait_ld();
+                        after_wait(v[0]);
+#pragma unroll 1
+                        for (int c = 0; c < kTok / 32; ++c) {
+                            const uint32_t see = sees(c);
+                            if (!__any_sync(0xFFFFFFFFu, see)) continue;
+                            uint32_t w[32];
+                            tmem_ld32_start(ts + 32 * c, w);
+                            tmem_wait_ld();
+                            after_wait(w);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * keep);
-                                tmem_st16(to + c, w);
+                            for (int e = 0; e < 32; ++e) m[e & 1] = fmaxf(m[e & 1], (see >> e) & 1u ? __uint_as_float(w[e]) : -inf);
+                        }
+                        raise(fmaxf(m[0], m[1]) * mult, j == 0);
+                        const float off = top == -inf ? 0.f : kLift - top;
+                        const float2 mult2 = make_float2(mult, mult), off2 = make_float2(off, off);
+#pragma unroll 1
+                        for (int c = 0; c < kTok / 32; ++c) {
+                            const uint32_t see = sees(c);
+                            uint32_t p[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) p[e] = 0;
+                            if (__any_sync(0xFFFFFFFFu, see)) {
+                                uint32_t w[32];
+                                tmem_ld32_start(ts + 32 * c, w);
+                                tmem_wait_ld();
+                                after_wait(w);
+#pragma unroll
+                                for (int e = 0; e < 32; e += 2) {
+                                    const float2 x2 = make_float2((see >> e) & 1u ? __uint_as_float(w[e]) : -inf, (see >> e) & 2u ? __uint_as_float(w[e + 1]) : -inf);
+                                    float2 y = fma2(x2, mult2, off2);
+                                    y.x = ex2(y.x);
+                                    y.y = ex2(y.y);
+                                    part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], y);
+                                    p[e >> 1] = pack_f16x2(y.x, y.y);
+                                }
                             }
+                            tmem_st16(ts + 16 * c, p);   // over scores that have been read
                         }
                     }
                     sum += (part[0].x + part[0].y) + (part[1].x + part[1].y);
-#pragma unroll
-                    for (int c = 0; c < kTok / 2; c += 16) tmem_st16(ts + c, p + c);
-                    if (notes.any_sick[note] && !inner(j, p0, p1)) {
-                        for (int g = 0; g < kGroups; ++g)
-                            for (int c = 0; c < kTok; c += 32)
-                                if (notes.sick[note][g][c >> 5] & bits_in(c_lo - c, c_hi - c) & ~hid[c >> 5]) sick |= 1u << g;
+                    if (__builtin_expect(notes.any_sick[note] && !inner(pc->tile0 + j, pc->p0, pc->p1), 0)) {
+#pragma unroll 1
+                        for (int c = 0; c < kTok / 32; ++c) {
+                            const uint32_t see = all ? 0xFFFFFFFFu : sees(c);
+                            for (int g = 0; g < kGroups; ++g)
+                                if (notes.sick[note][g][c] & see) sick |= 1u << g;
+                        }
                     }
                     tmem_wait_st();
                     tc::tc_fence_before();
                     __syncwarp();
                     if (lane == 0) tc::mbar_arrive(&bar.p_full[x]);
                 }
-                // ---- the result, or a partial one
+                // ---- the next item's Q, whose copy began when this one's last scores were there: its first scores are
+                // computed while this result is written
+                if (!ok) break;
+                const Held* const old = pc;
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                pc = next_piece(items + 1);
+                if (pc) ok = take_q(rt < pc->rows, items + 1, mult);
+                // ---- the result, or a partial one, 32 dims at a time
                 if (ok) ok = wait_for(&bar.o_full[x], items & 1);
                 if (!ok) break;
                 tc::tc_fence_after();
-                const bool whole = pc.starts && pc.ends;
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                if (whole) {   // through the place of Q, whose products are done, to whole lines
-                    const int rt = tid & 127;
-                    uint8_t* dst = q_s + x * S::kQTile + rt * 128;
-                    uint32_t v[2][32];   // one load ahead of the arithmetic
-                    tmem_ld32_start(to, v[0]);
+                if (old->starts && old->ends) {   // through shared memory, 64 bytes of a row to four lanes
+                    const int r0 = old->block + x * kRowsPerTile + (warp & 3) * 32 + (lane >> 2), r_end = old->block + old->rows;
+                    bf16_t* o[4];
 #pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t(&w)[32] = v[c & 1];
+                    for (int i = 0; i < 4; ++i) {
+                        const int t = (r0 + 8 * i) / group;
+                        o[i] = a.out + static_cast<long long>(old->row0 + t) * a.ld_out + (old->h * group + r0 + 8 * i - t * group) * D + 8 * (lane & 3);
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t w[32];
+                        tmem_ld32_start(to + c, w);
                         tmem_wait_ld();
                         after_wait(w);
-                        if (c + 1 < D / 32) tmem_ld32_start(to + 32 * (c + 1), v[(c + 1) & 1]);
-                        const float k = (sick >> (32 * c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
+                        const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : inv;
                         auto pair = [&](int e) { return pack_bf16x2(__uint_as_float(w[e]) * k, __uint_as_float(w[e + 1]) * k); };
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            const int ch = (32 * c + e) >> 3;
-                            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kRowsPerTile * 128) + (((ch & 7) ^ (rt & 7)) << 4)) =
-                                make_uint4(pair(e), pair(e + 2), pair(e + 4), pair(e + 6));
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4*>(mine_s + lane * 64 + (((e >> 3) ^ ((lane >> 1) & 3)) << 4)) = make_uint4(pair(e), pair(e + 2), pair(e + 4), pair(e + 6));
+                        __syncwarp();
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = (lane >> 2) + 8 * i;
+                            const uint4 q = *reinterpret_cast<const uint4*>(mine_s + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
+                            if (r0 + 8 * i < r_end) *reinterpret_cast<uint4*>(o[i] + c) = q;
                         }
+                        __syncwarp();
                     }
-                    __syncwarp();
-                    warp_rows(pc, a.ld_out, q_s + x * S::kQTile, [&](int, long long e, uint8_t* at) { *reinterpret_cast<uint4*>(a.out + e) = *reinterpret_cast<uint4*>(at); });
-                    __syncwarp();
                 } else {
-                    float* part_o = left.slot(blockIdx.x, pc.starts, D);
-                    part_o[kRowsPerItem * D + r] = top;
-                    part_o[kRowsPerItem * (D + 1) + r] = sum;
-#pragma unroll
+                    float* part_o = left.slot(blockIdx.x, old->starts, D);
+                    part_o[kRowsPerItem * D + rt] = top;
+                    part_o[kRowsPerItem * (D + 1) + rt] = sum;
+#pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
-                        float v[32];
-                        tc::tmem_ld32(to + c, v);
+                        uint32_t w[32];
+                        tmem_ld32_start(to + c, w);
+                        tmem_wait_ld();
+                        after_wait(w);
                         const float k = (sick >> (c / kGroup)) & 1u ? __int_as_float(0x7FC00000) : 1.f;
+                        auto f = [&](int e) { return __uint_as_float(w[e]) * k; };
+                        if (rt < old->rows) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            if (live) *reinterpret_cast<float4*>(part_o + r * D + c + e) = make_float4(v[e] * k, v[e + 1] * k, v[e + 2] * k, v[e + 3] * k);
+                            for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(part_o + rt * D + c + e) = make_float4(f(e), f(e + 1), f(e + 2), f(e + 3));
+                        }
                     }
                 }
                 // the loads above are done before the next item's first product with V: its weights come after
                 tc::tc_fence_before();
-                if (tid == 0 && pc.starts && !pc.ends) {
-                    Record rec{rows, pc.b.row0, pc.q.row0, h, static_cast<int>(blockIdx.x)};
-                    while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, rec.last + 1) < pc.u1) ++rec.last;
-                    left.records[blockIdx.x] = rec;
-                }
-                tile += n_tiles;
-                mine += n_tiles;
+                if (tid == 0 && old->starts && !old->ends) left.records[blockIdx.x] = Record{old->rows, old->block, old->row0, old->h, old->last};
+                mine += old->tiles;
                 ++items;
             }
             if (!ok) failed = 1;
@@ -653,16 +722,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 bool hidden;       // K: the position's page is bad
                 int page;          // of the tile to be loaded next
             };
-            int p0 = 0, p1 = 0, j_end = 0;
+            int p0 = 0, p1 = 0, j_end = 0, tile0 = 0, n_tiles = 0, head = 0;
             const int32_t* table = nullptr;
             auto page_at = [&](int j) -> int {   // -1: no row sees the place; -2: its page is bad
-                const int p = (pc.tile0 + j) * kTok + my_tok;
-                if (j >= pc.tiles || p >= j_end || idle) return -1;
+                const int p = (tile0 + j) * kTok + my_tok;
+                if (j >= n_tiles || p >= j_end || idle) return -1;
                 const int page = __ldg(table + (p >> a.cache.page_shift));
                 return static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages) ? page : -2;
             };
+            // A tile begins where a page does, or in the middle of one of 256: where this thread's bytes lie in its block
+            // is the same for every tile but for that half.
+            const int off = my_tok & (ps - 1);
+            const int codes_at = is_k ? off * (D / 2) : v_codes_off(ps, D) + (off >> 1) * D + 16 * quad;
+            const int params_at = is_k ? k_params_off(ps, D) + off * kGroups * 4 : v_params_off(ps, D) + ((off >> 1) * kGroups + quad * 16 / kGroup) * 8;
+            const long long head_bytes = block_bytes(ps, D);
             auto load = [&](Raw& r, int j) {
-                const int p = (pc.tile0 + j) * kTok + my_tok, off = p & (ps - 1), page = r.page;
+                const int page = r.page;
                 r.page = page_at(j + 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) r.w[i] = make_uint4(0, 0, 0, 0);
@@ -672,22 +747,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 r.hidden = page == -2;
                 if (page == -2) flag(a.status, LORA_DEV_BAD_PAGE);
                 if (page < 0) return;
-                const uint8_t* b = block_of(a.cache, page, pc.h);
+                const int second = ps > kTok && (tile0 + j) & 1 ? kTok : 0;
+                const uint8_t* b = a.cache.pages + page * a.cache.page_stride + head * head_bytes;
+                const uint8_t* c = b + codes_at + second * (D / 2);
+                const uint8_t* w = b + params_at + second * kGroups * 4;
                 if (is_k) {
 #pragma unroll
-                    for (int t = 0; t < D / 32; ++t) r.w[t] = __ldg(reinterpret_cast<const uint4*>(b + off * (D / 2)) + t);
+                    for (int t = 0; t < D / 32; ++t) r.w[t] = __ldg(reinterpret_cast<const uint4*>(c) + t);
 #pragma unroll
-                    for (int g = 0; g < kGroups; ++g) r.par[g] = __ldg(reinterpret_cast<const uint32_t*>(b + k_params_off(ps, D)) + off * kGroups + g);
-                    if (!inner(j, p0, p1)) {
-#pragma unroll
+                    for (int g = 0; g < kGroups; ++g) r.par[g] = __ldg(reinterpret_cast<const uint32_t*>(w) + g);
+                    if (__builtin_expect(!inner(tile0 + j, p0, p1), 0)) {
+                        const int at = off + second;
+#pragma unroll 1
                         for (int g = 0; g < kGroups; ++g) {
-                            const uint16_t* w = reinterpret_cast<const uint16_t*>(b + v_params_off(ps, D)) + ((off >> 1) * kGroups + g) * 4 + (off & 1);
-                            r.sick |= (not_finite(w[0]) || not_finite(w[2]) ? 1u : 0u) << g;
+                            const uint16_t* v = reinterpret_cast<const uint16_t*>(b + v_params_off(ps, D)) + ((at >> 1) * kGroups + g) * 4 + (at & 1);
+                            r.sick |= (not_finite(v[0]) || not_finite(v[2]) ? 1u : 0u) << g;
                         }
                     }
                 } else {
-                    const uint8_t* c = b + v_codes_off(ps, D) + (off >> 1) * D + 16 * quad;
-                    const uint8_t* w = b + v_params_off(ps, D) + ((off >> 1) * kGroups + quad * 16 / kGroup) * 8;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         r.w[i] = __ldg(reinterpret_cast<const uint4*>(c + i * D));
@@ -721,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 n &= kNotes - 1;
                 const uint32_t gone = __ballot_sync(0xFFFFFFFFu, r.hidden);
                 if (lane == 0) reinterpret_cast<uint32_t*>(&notes.hidden[n])[u >> 5] = gone;
-                if (!inner(j, p0, p1)) {
+                if (!inner(tile0 + j, p0, p1)) {
 #pragma unroll
                     for (int g = 0; g < kGroups; ++g) {
                         const uint32_t bits = __ballot_sync(0xFFFFFFFFu, (r.sick >> g) & 1u);
@@ -734,9 +811,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             };
             auto store_v = [&](Raw& r, int j, int n) {
                 if (idle) return;
-                if (!inner(j, p0, p1)) {
+                if (__builtin_expect(!inner(tile0 + j, p0, p1), 0)) {
                     // positions past the last row's, and values that are not finite, count as zeros
-                    const int p = (pc.tile0 + j) * kTok + my_tok;
+                    const int p = (tile0 + j) * kTok + my_tok;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = p + 2 * i;
@@ -767,33 +844,75 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             };
             uint64_t* full = is_k ? bar.k_full : bar.v_full;
             uint64_t* free = is_k ? bar.k_free : bar.v_free;
+            // Q's rows as they are into the swizzled tile, a row to D / 8 neighbouring lanes (16 bytes of 32 rows to an
+            // instruction would cost as many lines as rows)
+            uint32_t q_odd = 0, q_any = 0;   // a bit for each tile of rows: whether its items so far are odd, and any
+            auto copy_q = [&](const Piece* pc, int x) {
+                const int rows = min(kRowsPerTile, pc->rows - x * kRowsPerTile);
+                if (rows <= 0) return true;
+                if ((q_any >> x) & 1u && !wait_for(&bar.q_free[x], ((q_odd >> x) & 1u) ^ 1u)) return false;
+                q_any |= 1u << x;
+                q_odd ^= 1u << x;
+                constexpr int kLanes = D / 8, kStep = 128 / kLanes;
+                const int c = u % kLanes;
+                int r = u / kLanes, hh = pc->block + x * kRowsPerTile + r, t = hh / group;
+                hh -= t * group;
+                const bf16_t* src = a.q + static_cast<long long>(pc->row0 + t) * a.ld_q + (head * group + hh) * D + 8 * c;
+                const int dt = kStep / group, dh = kStep - dt * group;
+                const uint32_t dst = tc::smem_u32(q_s) + x * S::kQTile + (c >> 3) * (kRowsPerTile * 128);
+#pragma unroll 2
+                for (; r < rows; r += kStep) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "l"(src) : "memory");
+                    src += static_cast<long long>(dt) * a.ld_q + dh * D;
+                    hh += dh;
+                    if (hh >= group) {   // the next token's
+                        hh -= group;
+                        src += a.ld_q - group * D;
+                    }
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];\n" ::"r"(tc::smem_u32(&bar.q_raw[x])) : "memory");
+                return true;
+            };
             // a tile on its way, and the page of the one after it
-            int n = 0;
-            bool ok = true;
-            while (ok && walk.next(pc)) {
-                p0 = pc.b.p0;
-                p1 = pc.b.p1;
+            int n = 0;   // tiles so far
+            const Piece* pc;
+            for (int i = 0; (pc = piece(i)) && ok; ++i) {
+                p0 = pc->p0;
+                p1 = pc->p1;
+                tile0 = pc->tile0;
+                n_tiles = pc->tiles;
+                head = pc->h;
                 j_end = max(0, p1 + 1);
-                table = a.batch.block_table + static_cast<long long>(pc.s) * a.batch.ld_table;
+                table = a.batch.block_table + static_cast<long long>(pc->s) * a.batch.ld_table;
                 if (is_k) {   // these warps are ahead of the softmax: Q's lines are on their way when it comes for them
-                    for (int i = u; i < pc.b.rows * (D / 64); i += 128) {
-                        const int row = pc.b.row0 + i / (D / 64), t = row / group;
-                        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(a.q + static_cast<long long>(pc.q.row0 + t) * a.ld_q +
-                                                                       (pc.h * group + row - t * group) * D + 64 * (i % (D / 64))));
+#pragma unroll 1
+                    for (int i = u; i < pc->rows * (D / 64); i += 128) {
+                        const int row = pc->block + i / (D / 64), t = row / group;
+                        asm volatile("prefetch.global.L2 [%0];\n" ::"l"(a.q + static_cast<long long>(pc->row0 + t) * a.ld_q +
+                                                                       (head * group + row - t * group) * D + 64 * (i % (D / 64))));
                     }
                 }
                 Raw r;
                 r.page = page_at(0);
-                load(r, 0);
-                for (int j = 0; j < pc.tiles; ++j, ++n) {
-                    const int st = n & (kStages - 1);
-                    if (n >= kStages && !wait_for(&free[st], ((n / kStages) & 1) ^ 1)) { ok = false; break; }
-                    if (is_k) store_k(r, j, n); else store_v(r, j, n);
-                    tc::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&full[st]);
-                    if (j + 1 < pc.tiles) load(r, j + 1);
+                for (int j = -1; j < n_tiles; ++j) {
+                    if (j >= 0) {
+                        const int st = n & (kStages - 1);
+                        if (n >= kStages && !wait_for(&free[st], ((n / kStages) & 1) ^ 1)) { ok = false; break; }
+                        if (is_k) store_k(r, j, n); else store_v(r, j, n);
+                        tc::fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(&full[st]);
+                        ++n;
+                    }
+                    if (j + 1 < n_tiles) load(r, j + 1);
+                    // Q after the first tile: its place, and the next stage, are free when the last item's scores are done
+                    if (is_k && j == 0) {
+#pragma unroll 1
+                        for (int x = 0; x < 2; ++x) ok = ok && copy_q(pc, x);
+                        if (!ok) break;
+                    }
                 }
+                give_back(i);
             }
             if (!ok) failed = 1;
         } else {
@@ -809,11 +928,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 const uint64_t q_d = tc::sdesc_sw128(tc::smem_u32(q_s) + x * S::kQTile);
                 const uint64_t k_d = tc::sdesc_sw128(tc::smem_u32(k_s)), v_d = tc::sdesc_sw128(tc::smem_u32(v_s));
                 const bool lead = elect_one();
-                int n = 0, mine = 0, turns = 0;   // tiles so far; of this tile of rows; its turns
+                int n = 0, mine = 0, items = 0, turns = 0;   // tiles so far; of this tile of rows; its items and turns
                 bool both = false;
                 auto my_turn = [&]() { return !both || wait_polling(&bar.turn[x], turns++ & 1); };
                 auto your_turn = [&]() { if (both) tc::mbar_arrive(&bar.turn[x ^ 1]); };
-                auto scores = [&](int t) -> bool {   // t: the tile's place among all of the range
+                auto scores = [&](int t, bool last) -> bool {   // t: the tile's place among all of the range; the item's last
                     const int st = t & (kStages - 1);
                     if (!wait_polling(&bar.k_full[st], (t / kStages) & 1)) return false;
                     tc::tc_fence_after();
@@ -826,15 +945,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         }
                         tc::mma_commit(&bar.s_full[x]);
                         tc::mma_commit(&bar.k_free[st]);
+                        if (last) tc::mma_commit(&bar.q_free[x]);
                         your_turn();
                     }
                     __syncwarp();
                     return true;
                 };
-                bool ok = true, first = true;   // first: no turn has been taken
-                while (ok && walk.next(pc)) {
-                    const int n_tiles = pc.tiles;
-                    both = pc.b.rows > kRowsPerTile;
+                bool first = true;   // no turn has been taken
+                const Piece* pc;
+                for (int i = 0; (pc = piece(i)) && ok; give_back(i), ++i) {
+                    const int n_tiles = pc->tiles;
+                    both = pc->rows > kRowsPerTile;
                     if (x == 1 && !both) {
                         // the stages pass this tile of rows by, in step (a parity tells a phase only from its neighbours)
                         for (int j = 0; ok && j < n_tiles; ++j, ++n) {
@@ -846,31 +967,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         }
                         continue;
                     }
-                    tc::named_barrier(1 + x, 128 + 32);
-                    // the first tile of rows goes first; later items wait for the turn that the last one left over
-                    ok = ((x == 0 && first) || my_turn()) && scores(n);
-                    if (both) first = false;
-                    for (int j = 0; ok && j < n_tiles; ++j) {
-                        const int st = (n + j) & (kStages - 1);
-                        ok = wait_polling(&bar.v_full[st], ((n + j) / kStages) & 1) && my_turn() && wait_polling(&bar.p_full[x], (mine + j) & 1);
-                        if (!ok) break;
-                        tc::tc_fence_after();
-                        if (lead) {
-                            const uint64_t v_j = v_d + static_cast<uint64_t>(st * (S::kVTile >> 4));
+                    ok = wait_polling(&bar.q_full[x], items++ & 1);
+                    for (int j = 0; ok && j <= n_tiles; ++j) {
+                        if (j == 0) {
+                            // the first tile of rows goes first; later items wait for the turn that the last one left over
+                            ok = (x == 0 && first) || my_turn();
+                            if (both) first = false;
+                        } else {
+                            const int st = n & (kStages - 1);
+                            ok = wait_polling(&bar.v_full[st], (n / kStages) & 1) && my_turn() && wait_polling(&bar.p_full[x], mine & 1);
+                            if (!ok) break;
+                            tc::tc_fence_after();
+                            if (lead) {
+                                const uint64_t v_j = v_d + static_cast<uint64_t>(st * (S::kVTile >> 4));
 #pragma unroll
-                            for (int k = 0; k < kTok / 16; ++k)
-                                mma_ts(o_t, s_t + 8 * k, v_j + (((k >> 2) * S::kVHalf + (k & 3) * 32) >> 4), id_o, j > 0 || k > 0);
-                            tc::mma_commit(&bar.v_free[st]);
-                            if (j + 1 == n_tiles) {
-                                tc::mma_commit(&bar.o_full[x]);
-                                your_turn();
+                                for (int k = 0; k < kTok / 16; ++k)
+                                    mma_ts(o_t, s_t + 8 * k, v_j + (((k >> 2) * S::kVHalf + (k & 3) * 32) >> 4), id_o, j > 1 || k > 0);
+                                tc::mma_commit(&bar.v_free[st]);
+                                if (j == n_tiles) {
+                                    tc::mma_commit(&bar.o_full[x]);
+                                    your_turn();
+                                }
                             }
+                            __syncwarp();
+                            ++n;
+                            ++mine;
                         }
-                        __syncwarp();
-                        if (j + 1 < n_tiles) ok = scores(n + j + 1);
+                        if (ok && j < n_tiles) ok = scores(n, j + 1 == n_tiles);
                     }
-                    n += n_tiles;
-                    mine += n_tiles;
+                }
+                if (!ok) failed = 1;
+            } else if (warp == kWalkWarp) {
+                const int total = cost[kThreads], n_ranges = range_count(total, gridDim.x);
+                Walk walk(a, prefix, cost, per, total / n_ranges, range_at(total, n_ranges, blockIdx.x), range_at(total, n_ranges, blockIdx.x + 1));
+                int tiles[kPieces] = {};   // of the pieces not yet given back
+                for (int i = 0;; ++i) {
+                    Piece p;
+                    const int u1 = walk.next(p);
+                    p.last = blockIdx.x;
+                    if (p.tiles && p.starts && !p.ends)
+                        while (p.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, p.last + 1) < u1) ++p.last;
+                    // a piece may take as long as it has tiles
+                    long long limit = kTimeoutClocks;
+#pragma unroll
+                    for (int k = 0; k < kPieces; ++k) limit += 20000ll * tiles[k];
+                    if (i >= kPieces && !wait_for(&bar.piece_free[i % kPieces], (i / kPieces & 1) ^ 1, limit)) { ok = false; break; }
+                    if (lane == 0) pieces[i % kPieces] = p;
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&bar.piece_full[i % kPieces]);
+                    if (!p.tiles) break;
+#pragma unroll
+                    for (int k = kPieces - 1; k > 0; --k) tiles[k] = tiles[k - 1];
+                    tiles[0] = p.tiles;
                 }
                 if (!ok) failed = 1;
             }
@@ -887,8 +1035,7 @@ template <int D>
 cudaError_t run(const AttendArgs& a, int few_rows, void* ws, Partials* left, cudaStream_t stream)
 {
     using S = Shape<D>;
-    constexpr int kMaxSmem = 220 * 1024;
-    static_assert(S::kSmem + 4 * (kMaxSeqs + 1) <= kMaxSmem, "shared memory");
+    constexpr int kMaxSmem = S::kSmem + 4 * (kMaxSeqs + 1);
     static bool attr_set = false;
     if (!attr_set) {
         const cudaError_t e = cudaFuncSetAttribute(kv4_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
