@@ -538,8 +538,9 @@ lora_status_t lora_kv4_read(lora_bf16_t* k, int ld_k, lora_bf16_t* v, int ld_v, 
  * largest), cached values to fp16.
  * Errors (before anything is enqueued): as lora_kv4_append, plus
  * LORA_ERR_SHAPE (n_heads not a multiple of n_kv, more than 64 q heads to a
- * kv head, more than 4096 sequences, n_seqs * max_ctx_len * n_kv / 16 past
- * 31 bits), LORA_ERR_WORKSPACE, LORA_ERR_INVALID_ARG (scale not finite,
+ * kv head, more than 4096 sequences, more tiles in all than 31 bits
+ * count: of 32 positions for every 8 rows of a kv head, or of 128 for every
+ * 256), LORA_ERR_WORKSPACE, LORA_ERR_INVALID_ARG (scale not finite,
  * window < 0).
  */
 lora_status_t lora_kv4_attend(lora_bf16_t* out, int ld_out, const lora_bf16_t* q, int ld_q, int n_heads, float scale,

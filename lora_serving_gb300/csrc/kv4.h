@@ -95,6 +95,8 @@ struct AttendArgs {
     int32_t* status;
 };
 constexpr int kMaxSeqs = 4096;   // sequences of one attention call (their running sum lies in shared memory)
+// The longest line of tiles that a batch within these bounds lays out (the kernels count its places in 32 bits).
+long long kv4_attend_places(const AttendArgs& a);
 size_t kv4_attend_workspace(int n_heads, int n_kv, int head_dim, int max_q_len);
 cudaError_t launch_kv4_attend(const AttendArgs& a, cudaStream_t stream);
 

@@ -185,15 +185,13 @@ lora_status_t lora_kv4_attend(lora_bf16_t* out, int ld_out, const lora_bf16_t* q
     const int n_kv = a.cache.n_kv, D = a.cache.head_dim;
     if (n_heads % n_kv != 0 || n_heads / n_kv > kMaxGroupHeads) return LORA_ERR_SHAPE;
     if (batch->n_rows == 0) return LORA_OK;
-    // the kernels count the batch's tiles of 16 positions in 32 bits
-    if (batch->n_seqs > lora::kMaxSeqs ||
-        (batch->max_ctx_len / 16 + 2LL) * batch->n_seqs * n_kv > 0x7FFFFFFFLL)
-        return LORA_ERR_SHAPE;
+    a.n_heads = n_heads; a.window = window;
+    if (batch->n_seqs > lora::kMaxSeqs || lora::kv4_attend_places(a) > 0x7FFFFFFFLL) return LORA_ERR_SHAPE;
     LORA_TRY(check_matrix(q, ld_q, static_cast<long long>(n_heads) * D));
     LORA_TRY(check_matrix(out, ld_out, static_cast<long long>(n_heads) * D));
     if (!workspace || ws_bytes < lora_kv4_attend_workspace_bytes(n_heads, n_kv, D, batch->max_q_len)) return LORA_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return LORA_ERR_ALIGNMENT;
-    a.out = out; a.ld_out = ld_out; a.q = q; a.ld_q = ld_q; a.n_heads = n_heads; a.scale = scale; a.window = window;
+    a.out = out; a.ld_out = ld_out; a.q = q; a.ld_q = ld_q; a.scale = scale;
     a.ws = workspace; a.ws_bytes = ws_bytes; a.status = dev_status;
     return cuda_status(lora::launch_kv4_attend(a, reinterpret_cast<cudaStream_t>(stream)));
 }

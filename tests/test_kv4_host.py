@@ -136,6 +136,19 @@ def test_attend_refusals(_lib, change, want):
     assert _status(_lib.lora_kv4_attend(*v.values())) == "LORA_ERR_" + want
 
 
+@pytest.mark.parametrize("batch,want", [
+    (dict(n_rows=1 << 24, max_q_len=1 << 24, max_ctx_len=1 << 24, n_seqs=1), "SHAPE"),      # 2^17 blocks of 2^17 tiles
+    (dict(n_rows=4096, max_q_len=1, max_ctx_len=1 << 24, n_seqs=4096), "SHAPE"),            # 2^13 units of 2^19 tiles
+    (dict(n_rows=4096, max_q_len=1, max_ctx_len=1 << 22, n_seqs=4096), "WORKSPACE"),        # 2^30: counted in 32 bits
+])
+def test_attend_refuses_more_tiles_than_31_bits(_lib, batch, want):
+    c, b = _cache(), _batch(**batch, ld_table=1 << 20)
+    args = [P, 512, P, 512, 4, 0.1, 0, ctypes.byref(c), ctypes.byref(b), 0, 0, 0, 0]
+    assert _status(_lib.lora_kv4_attend(*args)) == "LORA_ERR_" + want
+    args[6] = 4096                                                                          # a window bounds the tiles
+    assert _status(_lib.lora_kv4_attend(*args)) == "LORA_ERR_WORKSPACE"
+
+
 def test_null_structs(_lib):
     c, b = _cache(), _batch()
     assert _status(_lib.lora_kv4_read(P, 256, P, 256, None, ctypes.byref(b), 0, 0)) == "LORA_ERR_INVALID_ARG"
