@@ -35,9 +35,9 @@
 // tile took 5000 clocks against 2000 for the others, and 16 prompts 357 us
 // in place of 308.
 //
-// Measured: 1024 rows of 64 heads over 32768 positions 744 us (1.45 PFLOP/s,
-// 0.74 of the measured bf16 peak); 16 prompts of 149 to 2011 tokens, 32
-// heads, 308 us.
+// Measured: 1024 rows of 64 heads over 32768 positions 735 us (1.47 PFLOP/s,
+// 0.75 of the measured bf16 peak); 16 prompts of 149 to 2011 tokens, 32
+// heads, 305 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -269,31 +269,31 @@ struct Held : Piece {    // a softmax warp's copy
     int all0, all1;      // all of its tile of rows sees all of these tiles of the piece, [all0, all1)
 };
 
-// Finds the pieces of a CTA's range.  The line goes by blocks of rows in the
-// order of the sequences, the kv heads of a block one after another.
-struct Walk {
-    const AttendArgs& a;
-    const int* prefix;   // blocks before each sequence
-    int group, share, x, end, s, i, at, base = 0;   // share: places of a range; x: place on the line; block i of sequence s begins at `at`
+__device__ __forceinline__ int range_count(int total, int ctas) { return min(ctas, max(1, total / kMinRange)); }
+// total * b / n without leaving 32 bits (n is a number of CTAs)
+__device__ __forceinline__ int range_at(int total, int n, int b)
+{
+    b = min(b, n);
+    return total / n * b + total % n * b / n;
+}
+
+// A place on the line: block i of sequence s, which begins at `at`.
+struct Place {
+    int s, i, at;
     Seq q;
     Block b;
+};
 
-    __device__ __forceinline__ void set_block()
+// Finds the pieces of a CTA's range.  The line goes by blocks of rows in the
+// order of the sequences, the kv heads of a block one after another.
+struct Walk : Place {
+    const AttendArgs& a;
+    const int* prefix;   // blocks before each sequence
+    int group, share, x, end, base = 0;   // share: places of a range; x: place on the line
+
+    __device__ __forceinline__ Walk(const AttendArgs& args, const int* pre, const Place& start, int share_, int begin, int end_)
+        : Place(start), a(args), prefix(pre), group(args.n_heads / args.cache.n_kv), share(share_), x(begin), end(end_)
     {
-        load_seq(a.batch, s, q, nullptr);
-        b = block_at(q, i, group, a.window);
-    }
-    // cost: places before each thread's blocks, `per` blocks to a thread
-    __device__ __forceinline__ Walk(const AttendArgs& args, const int* pre, const int* cost, int per, int share_, int begin, int end_)
-        : a(args), prefix(pre), group(args.n_heads / args.cache.n_kv), share(share_), x(begin), end(end_)
-    {
-        if (x >= end) return;
-        const int c = seq_at(cost, kThreads, x);
-        at = cost[c];
-        s = seq_at(prefix, a.batch.n_seqs, c * per);
-        i = c * per - prefix[s];
-        set_block();
-        while (x >= at + (b.tiles + kItemCost) * a.cache.n_kv) next_block();
     }
     __device__ __forceinline__ void next_block()
     {
@@ -302,7 +302,8 @@ struct Walk {
             i = 0;
             do ++s; while (prefix[s] == prefix[s + 1]);
         }
-        set_block();
+        load_seq(a.batch, s, q, nullptr);
+        b = block_at(q, i, group, a.window);
     }
     // The next piece; the place at which its item ends, 0 after the last.
     __device__ __forceinline__ int next(Piece& p)
@@ -342,12 +343,6 @@ struct Walk {
         return 0;
     }
 };
-__device__ __forceinline__ int range_count(int total, int ctas) { return min(ctas, max(1, total / kMinRange)); }
-__device__ __forceinline__ int range_at(int total, int n, int b)
-{
-    return static_cast<int>(static_cast<long long>(total) * min(b, n) / n);
-}
-
 constexpr int kMaxCtas = 160;   // CTAs that the workspace has room for
 
 template <int D>
@@ -358,6 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     extern __shared__ __align__(16) uint8_t smem_raw[];
     __shared__ Barriers bar;
     __shared__ Notes<kGroups> notes;
+    __shared__ Place first;
     __shared__ Piece pieces[kPieces];
     __shared__ Held held[kSoftWarps][2];
     constexpr int kPieceWords = sizeof(Piece) / 4;
@@ -404,25 +400,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     tc::grid_dep_launch();
     if (tid == 0) left.records[blockIdx.x].rows = 0;
 
-    // ---- this CTA's range: blocks before each sequence, then places before each thread's share of the blocks
+    // ---- this CTA's range: blocks before each sequence, then places before each thread's share of the blocks; the
+    // thread in whose share the range begins finds its first block
     const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
+    Seq* const seqs = reinterpret_cast<Seq*>(k_s);   // until K is there
+    static_assert(sizeof(Seq) * kMaxSeqs <= kStages * (S::kKTile + S::kVTile), "shared memory");
     scan_seqs<kWarps>(a.batch.n_seqs, prefix, sums, [&](int s) {
         Seq q;
         const bool ok = load_seq(a.batch, s, q, blockIdx.x == 0 ? a.status : nullptr);
+        seqs[s] = q;
         return ok && q.n * group > few_rows ? (q.n * group + kRowsPerItem - 1) / kRowsPerItem : 0;
     });
-    __syncthreads();
     const int blocks = prefix[a.batch.n_seqs], per = (blocks + kThreads - 1) / kThreads;
+    Place mine;
+    auto block = [&](int f) {
+        mine.s = seq_at(prefix, a.batch.n_seqs, f);
+        mine.i = f - prefix[mine.s];
+        mine.q = seqs[mine.s];
+        mine.b = block_at(mine.q, mine.i, group, a.window);
+        return (mine.b.tiles + kItemCost) * a.cache.n_kv;
+    };
     scan_seqs<kWarps>(kThreads, cost, sums, [&](int t) {
         int sum = 0;
-        for (int f = t * per; f < min(blocks, (t + 1) * per); ++f) {
-            const int s = seq_at(prefix, a.batch.n_seqs, f);
-            Seq q;
-            load_seq(a.batch, s, q, nullptr);
-            sum += (block_at(q, f - prefix[s], group, a.window).tiles + kItemCost) * a.cache.n_kv;
-        }
+#pragma unroll 1
+        for (int f = t * per; f < min(blocks, (t + 1) * per); ++f) sum += block(f);
         return sum;
     });
+    const int total = cost[kThreads], n_ranges = range_count(total, gridDim.x);
+    const int begin = range_at(total, n_ranges, blockIdx.x), end = range_at(total, n_ranges, blockIdx.x + 1);
+    if (begin < end && cost[tid] <= begin && begin < cost[tid + 1]) {
+        mine.at = cost[tid];
+        int len;
+#pragma unroll 1
+        for (int f = tid * per; begin >= mine.at + (len = block(f)); ++f) mine.at += len;
+        first = mine;
+    }
     tc::tc_fence_before();
     __syncthreads();   // barriers, the tensor memory's address, the running sums
     tc::tc_fence_after();
@@ -884,7 +896,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 head = pc->h;
                 j_end = max(0, p1 + 1);
                 table = a.batch.block_table + static_cast<long long>(pc->s) * a.batch.ld_table;
-                if (is_k) {   // these warps are ahead of the softmax: Q's lines are on their way when it comes for them
+                if (is_k && i > 0) {   // these warps are ahead: Q's lines are on their way when its place is free
 #pragma unroll 1
                     for (int i = u; i < pc->rows * (D / 64); i += 128) {
                         const int row = pc->block + i / (D / 64), t = row / group;
@@ -906,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     }
                     if (j + 1 < n_tiles) load(r, j + 1);
                     // Q after the first tile: its place, and the next stage, are free when the last item's scores are done
-                    if (is_k && j == 0) {
+                    if (is_k && j == (i > 0 ? 0 : -1)) {
 #pragma unroll 1
                         for (int x = 0; x < 2; ++x) ok = ok && copy_q(pc, x);
                         if (!ok) break;
@@ -998,8 +1010,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 }
                 if (!ok) failed = 1;
             } else if (warp == kWalkWarp) {
-                const int total = cost[kThreads], n_ranges = range_count(total, gridDim.x);
-                Walk walk(a, prefix, cost, per, total / n_ranges, range_at(total, n_ranges, blockIdx.x), range_at(total, n_ranges, blockIdx.x + 1));
+                Walk walk(a, prefix, first, total / n_ranges, begin, end);
                 int tiles[kPieces] = {};   // of the pieces not yet given back
                 for (int i = 0;; ++i) {
                     Piece p;

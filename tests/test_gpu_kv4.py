@@ -296,6 +296,21 @@ def test_attend(case, bounds):
             assert (got[t] == 0).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 20])
+def test_attend_many_short_sequences(D, window):
+    """More blocks of query rows than SMs, several to each, most of them with
+    nothing in the second tile of 128 rows, long runs of these between two
+    that have both; short ones for the kernel for few rows among them."""
+    q_lens = ([30] * 37 + [70] + [2] * 5 + [64, 33] + [31] * 40 + [90]) * 2
+    ctx = [n + 7 * (i % 5) for i, n in enumerate(q_lens)]
+    case = (q_lens, ctx, 32, 8, D, 32, window)
+    q, K, V, table, cache, batch = _attend(case, 5 + D, bounds="exact")
+    got = R.f64(_run(q, cache, batch, 32, 0.1, window)).reshape(-1, 32, D)
+    want, tol = R.attend(R.f64(q).reshape(-1, 32, D), K, V, q_lens, ctx, table, 32, 0.1, window)
+    _close(got, want, tol)
+
+
 @pytest.mark.parametrize("q_len", [1, 4, 40])
 @pytest.mark.parametrize("scale", [0.0, -0.1, 3.0])
 @pytest.mark.parametrize("bounds", BOUNDS)
