@@ -75,7 +75,8 @@ struct Shape {
 __device__ __forceinline__ int range_count(int total, int warps) { return min(warps, max(1, total)); }
 __device__ __forceinline__ int range_at(int total, int n, int w)
 {
-    return static_cast<int>(static_cast<long long>(total) * min(w, n) / n);
+    w = min(w, n);   // without leaving 32 bits: n is a number of warps
+    return total / n * w + total % n * w / n;
 }
 
 // First tile, and tiles, that a sequence's rows see.
@@ -149,6 +150,14 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     const int32_t* table = a.batch.block_table + static_cast<long long>(s) * a.batch.ld_table;
     const float inf = __int_as_float(0x7F800000);
 
+    // q's way begins before the tables'
+    uint4 raw[kWords];
+    {
+        const bf16_t* qp = a.q + static_cast<long long>(q.row0 + (row0 + g) / group) * a.ld_q + (h * group + (row0 + g) % group) * D + 8 * t;
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) raw[w] = g < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
+    }
+
     // ---- the ring
     const int pos0 = tile * kTile;
     const uint8_t* head_pages = a.cache.pages + static_cast<long long>(h) * block_bytes(ps, D);
@@ -221,12 +230,9 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     uint32_t qf[kWords][4];     // pairs (dims e, e + 4); odd pairs carry 1/16
     float mult[2], qsum[kGroups][2], qoff[kGroups][2];   // of rows 2t, 2t + 1
     {
-        uint4 raw[kWords];
         float top = 0.f;
-        const bf16_t* qp = a.q + static_cast<long long>(q.row0 + (row0 + g) / group) * a.ld_q + (h * group + (row0 + g) % group) * D + 8 * t;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
-            raw[w] = g < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
             const uint32_t part[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(part[e])), fabsf(bf16_hi(part[e]))));
