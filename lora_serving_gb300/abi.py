@@ -1,4 +1,5 @@
-"""Thin ctypes binding of ``liblora.so`` (the C ABI declared in include/lora.h).
+"""Thin binding of ``liblora.so`` (the C ABI declared in include/lora.h): ctypes, and
+csrc/pycalls.c for the calls between a decode step's projections.
 
 Argument marshalling only: every function here has the name of the C entry
 point it calls, takes torch tensors (device memory for kernel entry points,
@@ -9,6 +10,7 @@ fallback: if the CUDA library is missing the import fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import numpy as np
@@ -16,6 +18,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora.so")
+CALLS_PATH = os.path.join(_HERE, "_pycalls.so")
 
 LORA_MAX_RANK = 128
 LORA_BGMV_MAX_RANK = 32
@@ -137,6 +140,27 @@ def load(path: str | None = None):
     return lib
 
 
+_calls = None
+
+
+def _load_calls():
+    """The module csrc/pycalls.c, bound to the library: the calls between a
+    step's projections, whose kernels take less time than ctypes takes to
+    convert their arguments."""
+    global _calls
+    lib = load()
+    if not os.path.exists(CALLS_PATH):
+        raise RuntimeError(f"extension {CALLS_PATH} is missing: run lora_serving_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("lora_serving_gb300._pycalls", CALLS_PATH)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    fns = tuple(ctypes.cast(f, ctypes.c_void_p).value
+                for f in (lib.lora_rms_norm, lib.lora_kv4_append, lib.lora_kv4_read, lib.lora_kv4_attend))
+    mod.bind(fns, (torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn), _cur_device, _raw_stream)
+    _calls = mod
+    return mod
+
+
 def _check(fn: str, st: int):
     if st != 0:
         raise LoraError(fn, st)
@@ -179,37 +203,15 @@ def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
     return t.data_ptr()
 
 
-def _ptr(t, name: str, dtype) -> int:
-    """Pointer of a CUDA tensor of this element type."""
-    if not t.is_cuda or t.dtype is not dtype:
-        raise ValueError(f"{name} must be a CUDA tensor of {dtype}, got {t.dtype} on {t.device}")
-    return t.data_ptr()
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the stream's handle without a Stream object around it (3 us)
+    _cur_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+else:
+    _cur_device = lambda: torch.cuda.current_device()  # noqa: E731
+    _raw_stream = lambda dev: torch.cuda.current_stream(dev).cuda_stream  # noqa: E731
 
 
-def _mat(t, name: str, dtype, n_rows: int, cols: int):
-    """(pointer, leading dimension) of a row-major kernel operand: a CUDA
-    tensor of this element type with n_rows rows and cols columns at least
-    and unit column stride.  None: (NULL, 0)."""
-    if t is None:
-        return 0, 0
-    ptr = _ptr(t, name, dtype)
-    shape = t.shape
-    if len(shape) != 2 or shape[0] < n_rows or shape[1] < cols:
-        raise ValueError(f"{name} must be 2-D with {n_rows} rows and {cols} columns at least, got {tuple(shape)}")
-    ld, unit = t.stride()
-    if unit != 1 and shape[1] > 1:
-        raise ValueError(f"{name} must have unit column stride")
-    return ptr, ld
-
-
-try:   # the current stream's handle without a Stream object around it (3 us of a call's 10)
-    _raw_stream, _cur_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-
-    def _current_stream() -> int:
-        return _raw_stream(_cur_device()) if torch.cuda.is_initialized() else torch.cuda.current_stream().cuda_stream
-except AttributeError:
-    def _current_stream() -> int:
-        return torch.cuda.current_stream().cuda_stream
+def _current_stream() -> int:
+    return _raw_stream(_cur_device()) if torch.cuda.is_initialized() else torch.cuda.current_stream().cuda_stream
 
 
 def _stream(stream) -> int:
@@ -326,26 +328,12 @@ def lora_merge_batch(Ws, As, Bs, sign, *, stream=None):
                                                        _stream(stream)))
 
 
-_Axes = ctypes.c_int * LORA_MAX_ROPE_AXES
-_BF16, _F32, _I32, _E4M3 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn
-
-
 def lora_rms_norm(x, weight, eps, *, residual=None, residual_out=None, y=None, y8=None, scales=None, group=0,
                   stream=None):
     """h = bf16(x + residual) -> residual_out; n = h / sqrt(mean(h^2) + eps) * weight
     -> y (bf16) and/or y8 (float8_e4m3fn) with fp32 scales [n_rows][groups], one
     per `group` (128) columns or, with group 0, per row."""
-    n_rows, width = x.shape
-    if weight.shape != (width,) or weight.stride(0) != 1:
-        raise ValueError(f"weight must hold {width} adjacent values")
-    y_p, ld_y = _mat(y, "y", _BF16, n_rows, width)
-    y8_p, ld_y8 = _mat(y8, "y8", _E4M3, n_rows, width)
-    s_p, ld_s = _mat(scales, "scales", _F32, n_rows, (width + group - 1) // group if group > 0 else 1)
-    ro_p, ld_ro = _mat(residual_out, "residual_out", _BF16, n_rows, width)
-    x_p, ld_x = _mat(x, "x", _BF16, n_rows, width)
-    r_p, ld_r = _mat(residual, "residual", _BF16, n_rows, width)
-    st = load().lora_rms_norm(y_p, ld_y, y8_p, ld_y8, s_p, ld_s, group, ro_p, ld_ro, x_p, ld_x, r_p, ld_r,
-                              _ptr(weight, "weight", _BF16), n_rows, width, eps, _stream(stream))
+    st = (_calls or _load_calls()).rms_norm(x, weight, eps, residual, residual_out, y, y8, scales, group, stream)
     if st:
         raise LoraError("lora_rms_norm", st)
 
@@ -361,36 +349,15 @@ def lora_kv4_append(q_out, x, cache, batch, *, n_heads, q_off, k_off, v_off, rop
     rope: fp32 [max_pos][pairs][2] (cos, sin) or None; positions: int32
     [n_rows][n_axes] or None; axis_pairs: pairs of each axis (default: all
     on one axis)."""
-    n = batch.c.n_rows
-    q_p, ld_q = _mat(q_out, "q_out", _BF16, n, n_heads * cache.head_dim)
-    x_p, ld_x = _mat(x, "x", _BF16, n, 0)
-    rot = max_pos = n_axes = pos_p = ld_pos = rope_p = 0
-    axes = None
-    if rope is not None:
-        shape = rope.shape
-        if len(shape) != 3 or shape[2] != 2 or not rope.is_contiguous():
-            raise ValueError("rope must be contiguous [max_pos][pairs][2]")
-        rope_p, max_pos, rot = _ptr(rope, "rope", _F32), shape[0], 2 * shape[1]
-        pairs = (shape[1],) if axis_pairs is None else axis_pairs
-        n_axes = len(pairs)
-        if not 1 <= n_axes <= LORA_MAX_ROPE_AXES:
-            raise ValueError(f"axis_pairs must have 1 to {LORA_MAX_ROPE_AXES} entries")
-        axes = _Axes(*pairs)
-        pos_p, ld_pos = _mat(positions, "positions", _I32, n, n_axes)
-    st = load().lora_kv4_append(q_p, ld_q, x_p, ld_x, n_heads, q_off, k_off, v_off, rope_p, rot,
-                                max_pos, pos_p, ld_pos, axes, n_axes, cache.ref, batch.ref,
-                                _dev(dev_status, "dev_status", "i32"), _stream(stream))
+    st = (_calls or _load_calls()).kv4_append(q_out, x, cache.addr, batch.addr, n_heads, q_off, k_off, v_off, rope,
+                                              positions, axis_pairs, dev_status, stream)
     if st:
         raise LoraError("lora_kv4_append", st)
 
 
 def lora_kv4_read(k, v, cache, batch, *, dev_status=None, stream=None):
     """k, v [n_rows][n_kv * head_dim] <- the cached values of the rows' places."""
-    n, width = batch.c.n_rows, cache.n_kv * cache.head_dim
-    k_p, ld_k = _mat(k, "k", _BF16, n, width)
-    v_p, ld_v = _mat(v, "v", _BF16, n, width)
-    st = load().lora_kv4_read(k_p, ld_k, v_p, ld_v, cache.ref, batch.ref, _dev(dev_status, "dev_status", "i32"),
-                              _stream(stream))
+    st = (_calls or _load_calls()).kv4_read(k, v, cache.addr, batch.addr, dev_status, stream)
     if st:
         raise LoraError("lora_kv4_read", st)
 
@@ -398,12 +365,8 @@ def lora_kv4_read(k, v, cache, batch, *, dev_status=None, stream=None):
 def lora_kv4_attend(out, q, cache, batch, workspace, *, n_heads, scale, window=0, dev_status=None, stream=None):
     """out [n_rows][n_heads * head_dim] <- causal attention of q over the cache
     (the last `window` positions, 0: all)."""
-    n, width = batch.c.n_rows, n_heads * cache.head_dim
-    out_p, ld_out = _mat(out, "out", _BF16, n, width)
-    q_p, ld_q = _mat(q, "q", _BF16, n, width)
-    st = load().lora_kv4_attend(out_p, ld_out, q_p, ld_q, n_heads, scale, window, cache.ref, batch.ref,
-                                _dev(workspace, "workspace"), workspace.nbytes,
-                                _dev(dev_status, "dev_status", "i32"), _stream(stream))
+    st = (_calls or _load_calls()).kv4_attend(out, q, cache.addr, batch.addr, workspace, n_heads, scale, window,
+                                              dev_status, stream)
     if st:
         raise LoraError("lora_kv4_attend", st)
 

@@ -1,4 +1,5 @@
-"""Builds ``liblora.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_103a.
+"""Builds ``liblora.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_103a, and
+``_pycalls.so``, the Python side of some of its calls, with gcc.
 
 Each translation unit compiles in parallel into ``_build/``; the shared
 library lands next to this file.  No cmake, one ``-gencode``.
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblora.so")
+CALLS = os.path.join(HERE, "_pycalls.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -40,9 +43,9 @@ def _deps():
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
@@ -81,6 +84,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # the Python side of some calls: plain C against the interpreter's headers (abi.py hands it the library's functions)
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+           os.path.join(CSRC, "pycalls.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on pycalls.c:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
     return LIB
 
 

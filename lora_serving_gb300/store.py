@@ -157,7 +157,7 @@ class KV4Cache:
         self.n_pages, self.page_size, self.n_kv, self.head_dim = n_pages, page_size, n_kv, head_dim
         stride = pages.stride(0) if n_pages > 1 else n_kv * block
         self.c = abi.lora_kv4_cache_t(pages.data_ptr(), stride, n_pages, page_size, n_kv, head_dim)
-        self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self.c)
 
 
 class KV4Batch:
@@ -182,7 +182,7 @@ class KV4Batch:
         self.c = abi.lora_kv4_batch_t(abi._dev(q_starts, "q_starts", "i32"), abi._dev(ctx_lens, "ctx_lens", "i32"),
                                       abi._dev(block_table, "block_table", "i32", True), ld, n_seqs,
                                       int(n_rows), int(max_q_len), int(max_ctx_len))
-        self.ref = ctypes.byref(self.c)
+        self.addr = ctypes.addressof(self.c)
 
     @classmethod
     def from_lens(cls, q_lens, ctx_lens, block_table, device="cuda"):

@@ -464,3 +464,47 @@ def test_attend_nan_reaches_the_rows_that_see_it(q_len, part, bounds):
     sees[q_len // 2:q_len, 2:, (64 if part == "v" else 0):] = True
     assert torch.equal(out.isnan(), sees)
     assert torch.equal(out[~sees], clean[~sees])
+
+
+def test_python_calls_check_their_tensors():
+    """What would make a kernel read or write past a tensor, or another type,
+    is refused before anything is enqueued; raw status pointers pass."""
+    H, KV, D, page = 4, 2, 128, 32
+    cache = store.KV4Cache(4, page, KV, D)
+    batch = store.KV4Batch.from_lens([3, 1], [3, 40], [[0, 1], [2, 3]])
+    T, W = 4, (H + 2 * KV) * D
+    x, q = torch.zeros(T, W, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, H * D, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(T, KV * D, dtype=torch.bfloat16, device="cuda")
+    rope = store.rope_table(64, D // 2)
+    pos = torch.zeros(T, 3, dtype=torch.int32, device="cuda")
+    ws = store.kv4_workspace(cache, H, batch)
+    st = _status()
+    n0 = abi.lora_kernel_launch_count()
+
+    def append(**c):
+        v = dict(q=q, x=x, rope=rope, positions=pos, axis_pairs=(20, 20, 24), dev_status=st) | c
+        abi.lora_kv4_append(v.pop("q"), v.pop("x"), cache, batch, n_heads=H, q_off=0, k_off=H * D, v_off=(H + KV) * D, **v)
+
+    bad = [lambda: append(q=q[:3]), lambda: append(q=q[:, :-8]), lambda: append(q=q.float()), lambda: append(q=q.t()), lambda: append(q=q[0]),
+           lambda: append(x=x.half()), lambda: append(x=x[:2]), lambda: append(rope=rope.double()), lambda: append(rope=rope[:, ::2]),
+           lambda: append(rope=rope[..., 0]), lambda: append(positions=pos.long()), lambda: append(positions=pos[:, :2]),
+           lambda: append(axis_pairs=(16, 16, 16, 16)), lambda: append(axis_pairs=()), lambda: append(dev_status=st.float()),
+           lambda: abi.lora_kv4_read(k, k[:3], cache, batch), lambda: abi.lora_kv4_read(k[:, ::2], k, cache, batch),
+           lambda: abi.lora_kv4_attend(q, q[:, :-D], cache, batch, ws, n_heads=H, scale=0.1),
+           lambda: abi.lora_kv4_attend(q, q, cache, batch, ws.cpu(), n_heads=H, scale=0.1),
+           lambda: abi.lora_rms_norm(x, torch.ones(W, device="cuda"), 1e-5, y=x),
+           lambda: abi.lora_rms_norm(x, x[0].clone(), 1e-5, y=x[:3]),
+           lambda: abi.lora_rms_norm(x, x[0].clone(), 1e-5, y8=x.to(torch.float8_e4m3fn), scales=torch.ones(T, W // 128 - 1, device="cuda"), group=128)]
+    for f in bad:
+        with pytest.raises(ValueError):
+            f()
+    assert abi.lora_kernel_launch_count() == n0
+    append(dev_status=st.data_ptr())
+    append(rope=None, dev_status=None)
+    append(axis_pairs=[20, 20, 24], positions=pos[:, :])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    abi.lora_kv4_attend(q, q, cache, batch, ws, n_heads=H, scale=0.1, dev_status=st, stream=s)
+    abi.lora_kv4_attend(q, q, cache, batch, ws, n_heads=H, scale=0.1, dev_status=st, stream=s.cuda_stream)
+    s.synchronize()
+    assert abi.lora_read_device_status(st) == 0

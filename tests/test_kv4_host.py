@@ -1,6 +1,7 @@
 """Host-side checks of the norm's and the 4-bit cache's entry points: sizes,
 and refusals before anything is enqueued (no kernel launches here)."""
 import ctypes
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -163,3 +164,38 @@ def test_python_handles_refuse_host_memory_and_wrong_shapes():
     z = torch.zeros(3, dtype=torch.int32)
     with pytest.raises(ValueError):
         store.KV4Batch(z, z, z.view(3, 1), n_rows=1, max_q_len=1, max_ctx_len=1)
+
+
+@pytest.mark.parametrize("call", ["norm", "append", "read", "attend"])
+def test_python_calls_refuse_host_tensors(_lib, call):
+    """A host pointer handed to a kernel is an illegal address."""
+    c, b = _cache(), _batch()
+    cache, batch = SimpleNamespace(addr=ctypes.addressof(c)), SimpleNamespace(addr=ctypes.addressof(b))
+    x = torch.zeros(5, 1024, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="must be a CUDA tensor"):
+        if call == "norm":
+            abi.lora_rms_norm(x, torch.ones(1024, dtype=torch.bfloat16), 1e-5, y=x)
+        elif call == "append":
+            abi.lora_kv4_append(x, x, cache, batch, n_heads=4, q_off=0, k_off=512, v_off=768)
+        elif call == "read":
+            abi.lora_kv4_read(x, x, cache, batch)
+        else:
+            abi.lora_kv4_attend(x, x, cache, batch, x, n_heads=4, scale=0.1)
+
+
+def test_python_calls_refuse_what_is_no_tensor(_lib):
+    c, b = _cache(), _batch()
+    cache, batch = SimpleNamespace(addr=ctypes.addressof(c)), SimpleNamespace(addr=ctypes.addressof(b))
+    with pytest.raises(AttributeError):
+        abi.lora_kv4_read([1.0], [1.0], cache, batch)
+    with pytest.raises(ValueError, match="no cache"):
+        abi.lora_kv4_read(None, None, SimpleNamespace(addr=0), batch)
+    with pytest.raises(ValueError, match="out of range"):
+        abi.lora_kv4_attend(None, None, cache, batch, None, n_heads=1 << 40, scale=0.1)
+    with pytest.raises(TypeError):
+        abi.lora_kv4_attend(None, None, cache, batch, None, n_heads=4, scale="a")
+    for bad in (torch.ones(8), torch.ones(16)[::2], torch.ones(8, 2)):   # a weight that is not the row's
+        with pytest.raises(ValueError, match="adjacent"):
+            abi.lora_rms_norm(torch.zeros(2, 16), bad, 1e-5)
+    with pytest.raises(ValueError, match="2-D"):
+        abi.lora_rms_norm(torch.zeros(16), torch.ones(16), 1e-5)
