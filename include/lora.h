@@ -535,7 +535,11 @@ lora_status_t lora_kv4_read(lora_bf16_t* k, int ld_k, lora_bf16_t* v, int ld_v, 
  * Sums, maxima and products accumulate in fp32; the softmax weights are
  * rounded to fp16 for the product with V, q is taken to fp16 after scaling
  * each row by a power of two (exact but for elements 2^-22 below the row's
- * largest), cached values to fp16.
+ * largest), cached values to fp16.  A call repeats bit for bit; another batch
+ * around the same rows may cut their sums at other places, and with them the
+ * last bits.
+ * Device-detected faults as above; LORA_DEV_TIMEOUT: a wait inside the call
+ * ran out, and rows of the call are undefined.
  * Errors (before anything is enqueued): as lora_kv4_append, plus
  * LORA_ERR_SHAPE (n_heads not a multiple of n_kv, more than 64 q heads to a
  * kv head, more than 4096 sequences, more tiles in all than 31 bits

@@ -20,8 +20,8 @@ constexpr int kFewRows = 24;
 // the shorter time by that account and the launches' fixed times (9 and 22 us:
 // so small batches of longer rows go to it too), otherwise kFewRows.
 // Measured both ways (us, 8 kv heads of 128, few / many): one sequence of 1000
-// positions with 256 rows 20 / 34, of 16000 with 40 rows 32 / 36 and with 64
-// 42 / 37; 32 of 1000 with 40 rows 51 / 61, of 8000 303 / 201.
+// positions with 256 rows 20 / 35, of 16000 with 40 rows 31 / 34 and with 64
+// 40 / 35; 32 of 1000 with 40 rows 49 / 49, with 64 72 / 50, of 8000 287 / 196.
 int few_limit(const AttendArgs& a)
 {
     const int group = a.n_heads / a.cache.n_kv;
