@@ -41,7 +41,7 @@ long long kv4_attend_places(const AttendArgs& a)
     // positions that rows so many positions apart see
     auto span = [&](long long apart) { return a.window > 0 ? std::min(a.batch.max_ctx_len + 0LL, a.window + apart) : a.batch.max_ctx_len; };
     // units of 8 rows over tiles of 32 positions, items of 256 over 128: a tile cut at either end, and a start's cost
-    const long long few = a.batch.n_seqs * ((std::min<long long>(few_limit(a), rows) + 7) / 8) * (span(a.batch.max_q_len) / 32 + 4);
+    const long long few = a.batch.n_seqs * ((std::min<long long>(few_limit(a), rows) + 7) / 8) * (span(a.batch.max_q_len) / 32 + 5);
     const long long many = (a.batch.n_rows * group / 256 + a.batch.n_seqs) * (span(256) / 128 + 6);
     return std::max(few, rows > few_limit(a) ? many : 0) * a.cache.n_kv;
 }

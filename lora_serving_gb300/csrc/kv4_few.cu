@@ -53,7 +53,9 @@ constexpr int kRows = 8;
 constexpr int kCtas = 2, kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kTile = 32;          // positions per tile: two halves of 16, the products' M
 constexpr int kHalf = 16;
-constexpr int kUnitCost = 2;       // a unit's start (tables, q, the first copies), in tiles
+// A unit's start (tables, q, the first copies), in tiles: drafts 20.4 us, with 2
+// 21.5; 64 requests 25.3 with 2 and with 3, 28.7 with 1, 25.9 with 4.
+constexpr int kUnitCost = 3;
 constexpr float kNone = -3e38f;    // the running maximum before any score (finite, so that no difference is NaN)
 constexpr float kSlack = 8.f;      // log2 by which a score may pass the running maximum
 constexpr float kLift = 7.f;       // weights carry 2^7: at most 2^15, and fp16 holds them down to 2^-31 of the largest
