@@ -49,8 +49,11 @@ long long kv4_attend_places(const AttendArgs& a)
 namespace {
 
 // Joins the pieces behind each record, in order: kQuads 16-byte pieces of a
-// row's sums to a thread, as many CTAs to a record as its slot's rows need.
-constexpr int kJoinThreads = 256, kQuads = 1;
+// row's sums to a thread, as many CTAs to a record as its slot's rows need
+// (most records are empty, and a CTA costs its launch: 24 requests in a window
+// 65.1 us with one piece to a thread, 62.7 with 2, 63.1 with 4; 16 prompts
+// 306, 308, 301).
+constexpr int kJoinThreads = 256, kQuads = 4;
 __host__ __device__ constexpr int join_ctas(int rows, int D) { return (rows * (D / 4) + kJoinThreads * kQuads - 1) / (kJoinThreads * kQuads); }
 
 template <int D>
