@@ -533,7 +533,8 @@ lora_status_t lora_kv4_read(lora_bf16_t* k, int ld_k, lora_bf16_t* v, int ld_v, 
  * workspace [dev] at least lora_kv4_attend_workspace_bytes(...) bytes,
  *           256-byte aligned; scratch, calls that may overlap need their own
  * Sums, maxima and products accumulate in fp32; the softmax weights are
- * rounded to fp16 for the product with V, q is taken to fp16 after scaling
+ * rounded to fp16 for the product with V (one below 2^-31 of the row's
+ * largest vanishes), q is taken to fp16 after scaling
  * each row by a power of two (exact but for elements 2^-22 below the row's
  * largest), cached values to fp16.  A call repeats bit for bit; another batch
  * around the same rows may cut their sums at other places, and with them the
