@@ -1,6 +1,9 @@
 // kv4.h -- internal launchers of the norm and the 4-bit cache's operators.
 #pragma once
 
+#include <atomic>
+#include <cstdint>
+
 #include "kv4.cuh"
 #include "launch.h"
 
@@ -9,9 +12,23 @@ namespace lora {
 // Multiprocessors of the current device (GB300: 152).
 int device_sms();
 
+// Runs `set` (a kernel's attributes) once on each device.
+template <class F>
+cudaError_t once_on_device(std::atomic<uint64_t>& done, F set)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = 1ull << (dev & 63);
+    if (e != cudaSuccess || (done.load(std::memory_order_relaxed) & bit)) return e;
+    e = set();
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
+
 // Launch configuration under programmatic dependent launch: every kernel
 // here waits (griddepcontrol.wait) before its first read of memory, so only
-// its own start overlaps the kernel before it.
+// its own start overlaps the kernel before it (the second kernel of a call,
+// whose first has waited, waits at its end).
 struct PdlLaunch {
     cudaLaunchConfig_t cfg{};
     cudaLaunchAttribute attr[1];

@@ -672,14 +672,12 @@ template <int D>
 cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partials* left, cudaStream_t stream)
 {
     using S = Shape<D>;
-    static bool attr_set = false;
-    cudaError_t e = cudaSuccess;
-    if (!attr_set) {
-        e = cudaFuncSetAttribute(kv4_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kv4_unit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-        if (e != cudaSuccess) return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_on_device(done, [&] {
+        const cudaError_t f = cudaFuncSetAttribute(kv4_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
+        return f == cudaSuccess ? cudaFuncSetAttribute(kv4_unit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) : f;
+    });
+    if (e != cudaSuccess) return e;
     const int ctas = std::min(kMaxCtas, device_sms() * kCtas);
     // Units that all have a cluster on the GPU at once, with at most kUnitTiles tiles to a warp: a cluster each.
     // Measured both ways (us, heads of 128 in groups of 4, cluster / ranges): one sequence of 1000, 8000, 32000
@@ -688,7 +686,7 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partial
     // which every SM takes part in.
     const long long units = static_cast<long long>(a.batch.n_seqs) * a.cache.n_kv * ((few_rows + kRows - 1) / kRows);
     if (a.batch.max_ctx_len <= kTile * kUnitTiles * kCluster * kWarps) {
-        static int room = -1;   // clusters on the GPU at once
+        static std::atomic<int> room{-1};   // clusters on the GPU at once
         PdlLaunch l(dim3(static_cast<unsigned>(units * kCluster)), kThreads, S::kSmem, stream);
         cudaLaunchAttribute attr[2];
         attr[0] = l.attr[0];

@@ -1047,16 +1047,13 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, Partials* left, cud
 {
     using S = Shape<D>;
     constexpr int kMaxSmem = S::kSmem + 4 * (kMaxSeqs + 1);
-    static bool attr_set = false;
-    if (!attr_set) {
-        const cudaError_t e = cudaFuncSetAttribute(kv4_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-        if (e != cudaSuccess) return e;
-        attr_set = true;
-    }
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = once_on_device(done, [&] { return cudaFuncSetAttribute(kv4_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem); });
+    if (e != cudaSuccess) return e;
     const int ctas = std::min(kMaxCtas, device_sms());
     PdlLaunch l(dim3(ctas), kThreads, S::kSmem + 4 * (a.batch.n_seqs + 1), stream);
     *left = partials_at(ws, ctas, kRowsPerItem);
-    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D>, a, few_rows, *left);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D>, a, few_rows, *left);
     note_launch();
     return e;
 }
