@@ -103,6 +103,8 @@ struct AttendArgs {
     const bf16_t* q;
     int ld_q;
     int n_heads;
+    int group;              // heads to a kv head
+    uint32_t group_magic;   // n / group is the upper half of n times this (0 where group is 1)
     float scale;
     int window;
     kv4::Cache cache;

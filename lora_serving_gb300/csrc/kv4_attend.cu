@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv
     const int n0 = p0.ctas * join_ctas(p0.rows, D);
     const bool second = static_cast<int>(blockIdx.x) >= n0;
     const kv4::Partials& p = second ? p1 : p0;
-    const int per = join_ctas(p.rows, D), x = blockIdx.x - (second ? n0 : 0), b = x / per, group = a.n_heads / a.cache.n_kv;
+    const int per = join_ctas(p.rows, D), x = blockIdx.x - (second ? n0 : 0), b = x / per, group = a.group;
     const kv4::Record u = p.records[b];
     const float inf = __int_as_float(0x7F800000);
     for (int e = (x - b * per) * kJoinThreads + threadIdx.x; e < u.rows * (D / 4); e += per * kJoinThreads) {
@@ -85,8 +85,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv
             l = fmaf(s[p.rows * (D + 1) + r], w, l);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int row = u.block_row0 + r;
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.seq_row0 + row / group) * a.ld_out + (u.h * group + row % group) * D + d) =
+        const int row = u.block_row0 + r, tok = row / group;
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.seq_row0 + tok) * a.ld_out + (u.h * group + row - tok * group) * D + d) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
 }

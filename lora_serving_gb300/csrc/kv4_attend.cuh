@@ -121,6 +121,13 @@ __device__ __forceinline__ void scan_seqs(int n_seqs, int* prefix, int* sums, F 
         __syncthreads();
     }
 }
+// A row (position x head) of a sequence to its position, without a division:
+// exact for 2^26 rows, to which n times the magic number's error (group, at
+// most 64) stays below 2^32; the kernel for few rows has far fewer.
+__device__ __forceinline__ int by_group(const AttendArgs& a, int n)
+{
+    return a.group_magic ? static_cast<int>(__umulhi(static_cast<uint32_t>(n), a.group_magic)) : n;
+}
 // The last s with prefix[s] <= x.
 __device__ __forceinline__ int seq_at(const int* prefix, int n_seqs, int x)
 {

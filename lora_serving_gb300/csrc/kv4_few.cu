@@ -112,13 +112,13 @@ __device__ __forceinline__ Unit unit_at(const AttendArgs& a, const int* prefix, 
     Unit u;
     u.s = lo;
     load_seq(a.batch, lo, u.q, nullptr);
-    const int group = a.n_heads / a.cache.n_kv, slices = slices_of(u.q, group);
-    u.len = (prefix[lo + 1] - prefix[lo]) / (a.cache.n_kv * slices);
+    const int slices = slices_of(u.q, a.group);
+    u.len = tiles_of(u.q, a.window) + kUnitCost;
     const int v = (x - prefix[lo]) / u.len;
     u.u0 = prefix[lo] + v * u.len;
-    u.h = v / slices;
+    u.h = slices == 1 ? v : v / slices;
     u.row0 = (v - u.h * slices) * kRows;
-    u.rows = min(kRows, u.q.n * group - u.row0);
+    u.rows = min(kRows, u.q.n * a.group - u.row0);
     return u;
 }
 
@@ -153,7 +153,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     using S = Shape<D>;
     constexpr int kGroups = S::kGroups, kWords = S::kWords, kStages = S::kStages;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
+    const int group = a.group, ps = a.cache.page_size;
     const int p0 = q.ctx - q.n;   // position of the first row
     const int32_t* table = a.batch.block_table + static_cast<long long>(s) * a.batch.ld_table;
     const float inf = __int_as_float(0x7F800000);
@@ -161,7 +161,8 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     // q's way begins before the tables'
     uint4 raw[kWords];
     {
-        const bf16_t* qp = a.q + static_cast<long long>(q.row0 + (row0 + g) / group) * a.ld_q + (h * group + (row0 + g) % group) * D + 8 * t;
+        const int tok = by_group(a, row0 + g);
+        const bf16_t* qp = a.q + static_cast<long long>(q.row0 + tok) * a.ld_q + (h * group + row0 + g - tok * group) * D + 8 * t;
 #pragma unroll
         for (int w = 0; w < kWords; ++w) raw[w] = g < rows ? *reinterpret_cast<const uint4*>(qp + 32 * w) : make_uint4(0, 0, 0, 0);
     }
@@ -289,7 +290,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     }
     int last[2];   // position of rows 2t, 2t + 1: the last one they see
 #pragma unroll
-    for (int c = 0; c < 2; ++c) last[c] = p0 + (row0 + 2 * t + c) / group;
+    for (int c = 0; c < 2; ++c) last[c] = p0 + by_group(a, row0 + 2 * t + c);
 
     float (&acc)[D / 16][4] = out.acc;
     float (&top)[2] = out.top, (&sum)[2] = out.sum;
@@ -452,7 +453,7 @@ __device__ __forceinline__ void put(const AttendArgs& a, int h, const Seq& q, in
 {
     using S = Shape<D>;
     constexpr int kWords = S::kWords;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, group = a.n_heads / a.cache.n_kv;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, group = a.group;
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         float l = o.sum[c];
@@ -463,7 +464,8 @@ __device__ __forceinline__ void put(const AttendArgs& a, int h, const Seq& q, in
         if (r >= rows) continue;
         if (!slot) {
             const float k = l == 0.f ? 0.f : 1.f / l;
-            bf16_t* d = a.out + static_cast<long long>(q.row0 + (row0 + r) / group) * a.ld_out + (h * group + (row0 + r) % group) * D + g * (D / 8);
+            const int tok = by_group(a, row0 + r);
+            bf16_t* d = a.out + static_cast<long long>(q.row0 + tok) * a.ld_out + (h * group + row0 + r - tok * group) * D + g * (D / 8);
 #pragma unroll
             for (int w = 0; w < kWords; w += 2)
                 *reinterpret_cast<uint4*>(d + 4 * w) =
@@ -498,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, 
 
     if (!after) tc::grid_dep_wait();
     tc::grid_dep_launch();
-    const int group = a.n_heads / a.cache.n_kv;
+    const int group = a.group;
     scan_seqs<kWarps>(a.batch.n_seqs, prefix, warp_sums, [&](int s) {
         Seq q;
         const bool ok = load_seq(a.batch, s, q, blockIdx.x == 0 ? a.status : nullptr);
@@ -558,7 +560,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, 
             if (starts && ends) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const int row = first.row0 + r;
-                *reinterpret_cast<uint2*>(a.out + static_cast<long long>(first.seq_row0 + row / group) * a.ld_out + (first.h * group + row % group) * D + d) =
+                const int tok = by_group(a, row);
+                *reinterpret_cast<uint2*>(a.out + static_cast<long long>(first.seq_row0 + tok) * a.ld_out + (first.h * group + row - tok * group) * D + d) =
                     make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
             } else {
                 *reinterpret_cast<float4*>(to + r * D + d) = o;
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_unit_kernel(AttendArgs a,
     const int tid = threadIdx.x, warp = tid >> 5, rank = static_cast<int>(cluster_rank());
     uint8_t* ring = smem + warp * S::kRing;
     float* mine = reinterpret_cast<float*>(smem + kWarps * S::kRing);   // the CTA's partial result: sums, then (maximum, sum of weights)
-    const int group = a.n_heads / a.cache.n_kv, slices = (few_rows + kRows - 1) / kRows, per_seq = a.cache.n_kv * slices;
+    const int group = a.group, slices = (few_rows + kRows - 1) / kRows, per_seq = a.cache.n_kv * slices;
     const int unit = blockIdx.x / kCluster, s = unit / per_seq, h = (unit - s * per_seq) / slices, row0 = (unit - s * per_seq - h * slices) * kRows;
     const float inf = __int_as_float(0x7F800000);
 
@@ -657,7 +660,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_unit_kernel(AttendArgs a,
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         const int row = row0 + r;
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(q.row0 + row / group) * a.ld_out + (h * group + row % group) * D + d) =
+        const int tok = by_group(a, row);
+        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(q.row0 + tok) * a.ld_out + (h * group + row - tok * group) * D + d) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
     cluster_arrive();
