@@ -527,7 +527,10 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, 
     }
     __syncthreads();
 
-    // ---- join the CTA's partial results, unit by unit
+    // ---- join the CTA's partial results, unit by unit.  Units of heads of 64, which leave warps without work, begin
+    // at the warp where the one before ended (drafts 19.7 -> 19.0 us; with heads of 128 the main loop lost more to
+    // registers than that: 8 x 131072 positions 231 -> 234).
+    int begin_warp = 0;
     auto slot_of = [&](int w, int k) {
         return k == 0 ? first_slot + w * S::kPartial : reinterpret_cast<const float*>(smem + w * S::kRing);
     };
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, 
         const int last = 31 - __clz(set), ends = pieces[last >> 1][last & 1].ends;
         const bool starts = i0 & 1;
         float* to = left.slot(b, starts, D);
-        for (int e = tid; e < first.rows * (D / 4); e += kThreads) {
+        for (int e = D == 64 ? ((warp - begin_warp) & (kWarps - 1)) * 32 + lane : tid; e < first.rows * (D / 4); e += kThreads) {
             const int r = e / (D / 4), d = e % (D / 4) * 4;
             float m = -inf, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -571,6 +574,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, 
                 }
             }
         }
+        if (D == 64) begin_warp += (first.rows * (D / 4) + 31) / 32;
         if (starts && !ends) {
             rec = Record{first.rows, first.row0, first.seq_row0, first.h, b};
             while (rec.last + 1 < static_cast<int>(gridDim.x) && range_at(total, n_ranges, (rec.last + 1) * kWarps) < first.u1) ++rec.last;
