@@ -29,15 +29,17 @@
 //
 // What bounds it.  The two products take 2150 of an SM's clocks a tile, a
 // tile of rows' own chain (softmax 1500, products 1075 and the ways between
-// them) 3150 to 3300.  After that, the code's size: five roles share the
-// SM's instruction cache, so what is seldom run (masked tiles, results,
-// finding the pieces) is written small, as loops, and once: at 115 KB, a masked
-// tile took 5000 clocks against 2000 for the others, and 16 prompts 357 us
-// in place of 308.
+// them) 3150 to 3300.  After that, an item's masked tile, Q and result, and the
+// code's size: five roles share the SM's instruction cache, so what is seldom
+// run (masked tiles, results, finding the pieces) is written small, as loops,
+// and once: 115 KB instead of 80 took 16 prompts 357 us instead of 305.  A
+// first tile that all rows see begins with its first columns' maximum: in the
+// masked tiles' code it took the prompts 302 us, a chunk, where another test
+// stands in every tile, 735.
 //
-// Measured: 1024 rows of 64 heads over 32768 positions 735 us (1.47 PFLOP/s,
-// 0.75 of the measured bf16 peak); 16 prompts of 149 to 2011 tokens, 32
-// heads, 301 us.
+// Measured: 1024 rows of 64 heads over 32768 positions 750 us (1.44 PFLOP/s,
+// 0.73 of the measured bf16 peak); 16 prompts of 149 to 2011 tokens, 32
+// heads, 291 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -476,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         if (lane < kPieceWords) reinterpret_cast<int*>(static_cast<Piece*>(&h))[lane] = reinterpret_cast<const int*>(p)[lane];
                         const int lo = p->pos0 + (p->block + x * kRowsPerTile) / group;
                         const int hi = p->pos0 + (p->block + min(p->rows, (x + 1) * kRowsPerTile) - 1) / group;
-                        if (lane == 0) h.all0 = max(1, a.window > 0 && hi >= a.window ? (hi - a.window) / kTok + 1 - p->tile0 : 0);   // the first sets the maximum
+                        if (lane == 0) h.all0 = a.window > 0 && hi >= a.window ? (hi - a.window) / kTok + 1 - p->tile0 : 0;
                         if (lane == 0) h.all1 = (max(0, lo + 1)) / kTok - p->tile0;
                     }
                     give_back(n++);
@@ -566,7 +568,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     };
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     if (__builtin_expect(all, 1)) {
-                        // Weights against the running maximum as it stands, taken again where it has to move.
+                        // Weights against the running maximum as it stands, taken again where it has to move; in an
+                        // item's first tile it begins as that of the first columns (and what O holds then does not matter).
+                        if (__builtin_expect(j == 0, 0)) {
+                            tmem_wait_ld();
+                            after_wait(v[0]);
+                            float m[2] = {-inf, -inf};
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) m[e & 1] = fmaxf(m[e & 1], __uint_as_float(v[0][e]));
+                            top = fmaxf(m[0], m[1]) * mult;
+                        }
                         uint32_t p[kTok / 2];
                         for (;;) {
                             const float off = top == -inf ? 0.f : kLift - top;
@@ -596,9 +607,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
 #pragma unroll
                         for (int c = 0; c < kTok / 2; c += 16) tmem_st16(ts + c, p + c);
                     } else {
-                        // An item's first tile, which sets the maximum, or a tile that not every row sees all of: the
-                        // maximum first, then the weights, 32 columns at a time (few instructions for what is seldom
-                        // run: they are read from memory when it is).
+                        // A tile that not every row sees all of: the maximum first, then the weights, 32 columns at a
+                        // time (few instructions for what is seldom run: they are read from memory when it is).
                         float m[2] = {-inf, -inf};
                         tmem_wait_ld();
                         after_wait(v[0]);
