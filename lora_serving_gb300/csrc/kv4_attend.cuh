@@ -87,6 +87,10 @@ __device__ __forceinline__ void values(uint32_t w, __half2 step, __half2 low, ui
     v[3] = as_u32(__hfma2(__hfma2(as_h2(pick(y, 0x00F000F0u)), s, k16), step, low));
 }
 
+// The first position that a row at p sees (with p before the first position, as it may be, 0: the row has nothing to
+// see).  No window and no p take this out of 32 bits: p - window + 1 alone would leave them.
+__device__ __forceinline__ int seen_from(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
+
 // Whether an fp16 pair holds an infinity or a NaN.
 __device__ __forceinline__ bool not_finite(uint32_t h2)
 {

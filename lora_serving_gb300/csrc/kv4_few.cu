@@ -90,7 +90,7 @@ __device__ __forceinline__ int range_at(int total, int n, int w)
 // First tile, and tiles, that a sequence's rows see.
 __device__ __forceinline__ int first_tile(const Seq& q, int window)
 {
-    return window > 0 ? max(0, q.ctx - q.n - window + 1) / kTile : 0;
+    return seen_from(q.ctx - q.n, window) / kTile;
 }
 __device__ __forceinline__ int tiles_of(const Seq& q, int window)
 {
@@ -395,7 +395,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
             if (!inner) {
                 // positions that no row sees count as zeros whatever they hold, and a value that is
                 // not finite is taken out here and put back below for the rows that see it
-                const int j_end = there ? q.ctx : 0, j_begin = a.window > 0 ? p0 - a.window + 1 : 0;
+                const int j_end = there ? q.ctx : 0, j_begin = seen_from(p0, a.window);
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int j = j0 + kHalf * hf + 2 * t + 8 * r;

@@ -249,8 +249,7 @@ __device__ __forceinline__ Block block_at(const Seq& q, int i, int group, int wi
     b.rows = min(kRowsPerItem, q.n * group - b.row0);
     b.p0 = q.ctx - q.n + b.row0 / group;
     b.p1 = q.ctx - q.n + (b.row0 + b.rows - 1) / group;
-    const int begin = window > 0 ? max(0, b.p0 - window + 1) : 0;
-    b.tile0 = begin / kTok;
+    b.tile0 = seen_from(b.p0, window) / kTok;
     b.tiles = max(1, (max(0, b.p1 + 1) + kTok - 1) / kTok - b.tile0);   // at least one: its rows get their zeros
     return b;
 }
@@ -564,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     const bool all = in && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
                     auto sees = [&](int c) {   // a bit for each of 32 columns that this row sees
                         const int c_hi = pc->pos0 + (pc->block + rt) / group + 1 - (pc->tile0 + j) * kTok - 32 * c;
-                        return bits_in(a.window > 0 ? c_hi - a.window : 0, c_hi) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c];
+                        return bits_in(a.window > 0 && c_hi > a.window ? c_hi - a.window : 0, c_hi) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c];
                     };
                     float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     if (__builtin_expect(all, 1)) {
