@@ -526,7 +526,10 @@ lora_status_t lora_kv4_read(lora_bf16_t* k, int ld_k, lora_bf16_t* v, int ld_v, 
  *   out = sum_j softmax_j(scale * q . k_j) v_j
  * over the cached values (code * step + low); a row that sees nothing gets
  * zeros.  Masked positions, and the rest of a partly filled page, do not
- * reach the result whatever their bytes hold.
+ * reach the result whatever their bytes hold.  A position of a group of V in
+ * which low or 15 step + low is no finite fp16 number (an append stores a NaN
+ * as one, and no other) makes that group's dims NaN or infinite for the rows
+ * that see it.
  * out, q    [dev] bf16 [n_rows][ld_out], [n_rows][ld_q], n_heads * head_dim
  *           columns; out may be q itself
  * scale     finite, usually 1 / sqrt(head_dim)

@@ -91,10 +91,12 @@ __device__ __forceinline__ void values(uint32_t w, __half2 step, __half2 low, ui
 // see).  No window and no p take this out of 32 bits: p - window + 1 alone would leave them.
 __device__ __forceinline__ int seen_from(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
 
-// Whether an fp16 pair holds an infinity or a NaN.
-__device__ __forceinline__ bool not_finite(uint32_t h2)
+// Which halves of a (steps, lows) pair have codes whose value is no finite fp16 number: with step and low finite a value
+// can still leave fp16, and code 15's does if any does (low itself is code 0's).  An append leaves none.
+__device__ __forceinline__ uint32_t not_finite(uint32_t step, uint32_t low)
 {
-    return (h2 & 0x7C00u) == 0x7C00u || (h2 & 0x7C000000u) == 0x7C000000u;
+    const uint32_t end = as_u32(__hfma2(__float2half2_rn(15.f), as_h2(step), as_h2(low)));
+    return ((end & 0x7C00u) == 0x7C00u ? 0xFFFFu : 0u) | ((end & 0x7C000000u) == 0x7C000000u ? 0xFFFF0000u : 0u);
 }
 
 // Running sum over the sequences of count(s), in shared memory (prefix: one

@@ -402,9 +402,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                     const uint32_t keep = (j >= j_begin && j < j_end ? 0xFFFFu : 0u) | (j + 1 >= j_begin && j + 1 < j_end ? 0xFFFF0000u : 0u);
                     step[r] &= keep;
                     low[r] &= keep;
-                    uint32_t bad = 0;
-                    if (not_finite(step[r] & 0xFFFFu) || not_finite(low[r] & 0xFFFFu)) bad |= 0xFFFFu;
-                    if (not_finite(step[r] & 0xFFFF0000u) || not_finite(low[r] & 0xFFFF0000u)) bad |= 0xFFFF0000u;
+                    const uint32_t bad = not_finite(step[r], low[r]);
                     step[r] &= ~bad;
                     low[r] &= ~bad;
                     poison |= bad != 0;
@@ -428,7 +426,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                 const int j = j0 + k;
                 const __half* p = reinterpret_cast<const __half*>(src + S::kVpAt + (k / kHalf) * S::kParamBytes) +
                                   (((k % kHalf) >> 1) * kGroups + vg) * 4 + (k & 1);
-                const float nan = __half2float(p[0]) * 0.f + __half2float(p[2]) * 0.f;   // 0 where both are finite
+                const float nan = __half2float(__hfma(__float2half_rn(15.f), p[0], p[2])) * 0.f;   // 0 where every value is finite
                 if (nan == 0.f || j >= q.ctx) continue;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {

@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
 #pragma unroll 1
                         for (int g = 0; g < kGroups; ++g) {
                             const uint16_t* v = reinterpret_cast<const uint16_t*>(b + v_params_off(ps, D)) + ((at >> 1) * kGroups + g) * 4 + (at & 1);
-                            r.sick |= (not_finite(v[0]) || not_finite(v[2]) ? 1u : 0u) << g;
+                            r.sick |= (not_finite(v[0], v[2]) ? 1u : 0u) << g;
                         }
                     }
                 } else {
@@ -833,16 +833,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
             auto store_v = [&](Raw& r, int j, int n) {
                 if (idle) return;
                 if (__builtin_expect(!inner(tile0 + j, p0, p1), 0)) {
-                    // positions past the last row's, and values that are not finite, count as zeros
-                    const int p = (tile0 + j) * kTok + my_tok;
+                    // positions that no row sees, and values that are not finite, count as zeros
+                    const int p = (tile0 + j) * kTok + my_tok, begin = seen_from(p0, a.window);
+                    auto seen = [&](int at) { return at >= begin && at < j_end; };
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = p + 2 * i;
                         uint32_t& step = r.par[2 * i];
                         uint32_t& low = r.par[2 * i + 1];
-                        uint32_t keep = (at < j_end ? 0xFFFFu : 0u) | (at + 1 < j_end ? 0xFFFF0000u : 0u);
-                        if (not_finite(step & 0xFFFFu) || not_finite(low & 0xFFFFu)) keep &= 0xFFFF0000u;
-                        if (not_finite(step & 0xFFFF0000u) || not_finite(low & 0xFFFF0000u)) keep &= 0xFFFFu;
+                        const uint32_t keep = ((seen(at) ? 0xFFFFu : 0u) | (seen(at + 1) ? 0xFFFF0000u : 0u)) & ~not_finite(step, low);
                         step &= keep;
                         low &= keep;
                     }

@@ -1,6 +1,8 @@
-"""lora_kv4_attend and what its rows do not see: windows wider than any context."""
+"""lora_kv4_attend and what its rows do not see: positions behind a window and
+ahead of a row, whatever their bytes, windows wider than any context."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -16,6 +18,76 @@ def _built():
     build()
     abi.load()
     assert torch.cuda.is_available()
+
+
+def _poison_v(pages, page, D, n, o, step, low):
+    """The parameters of V at offset o of page n, every head and group."""
+    for g in range(D // 64):
+        at = page * (D + 4 * (D // 64)) + ((o // 2) * (D // 64) + g) * 8 + 2 * (o % 2)
+        pages[n, :, at:at + 2] = np.array([step], "<f2").view(np.uint8)
+        pages[n, :, at + 4:at + 6] = np.array([low], "<f2").view(np.uint8)
+
+
+def _poison_k(pages, page, D, n, o, step, low):
+    at = page * D + o * 4 * (D // 64)
+    pages[n, :, at:at + 4 * (D // 64)] = np.tile(np.array([step, low], "<f2").view(np.uint8), D // 64)
+
+
+# (step, low): not finite, and finite ones whose values leave fp16
+BYTES = [(np.nan, np.inf), (60000.0, 0.0), (-65504.0, 65504.0), (4400.0, 30000.0), (0.0, -np.inf)]
+WINDOWED = [  # q_lens, ctx_lens, heads, kv, D, page, window
+    ([1], [5000], 8, 2, 128, 64, 1000),
+    ([1, 1, 2], [300, 90, 700], 8, 2, 128, 16, 40),
+    ([3, 1], [601, 333], 12, 4, 64, 32, 77),
+    ([40, 33], [400, 999], 8, 2, 128, 16, 100),
+    ([70, 130], [500, 1300], 8, 8, 64, 256, 333),
+    ([150], [1150], 16, 2, 128, 128, 517),
+]
+
+
+def _first_seen(n, c, window):
+    return max(0, c - n - window + 1)
+
+
+@pytest.mark.parametrize("bounds", BOUNDS)
+@pytest.mark.parametrize("case", WINDOWED, ids=range(len(WINDOWED)))
+def test_bytes_behind_the_window(case, bounds):
+    q_lens, ctx, H, KV, D, page, window = case
+    q, K, V, table, cache, batch = _attend(case, 40 + H + D, bounds=bounds)
+    scale = 1 / math.sqrt(D)
+    clean = _run(q, cache, batch, H, scale, window)
+    want, tol = R.attend(R.f64(q).reshape(-1, H, D), K, V, q_lens, ctx, table, page, scale, window)
+    _close(R.f64(clean).reshape(-1, H, D), want, tol)
+    keep = cache.pages.cpu().numpy()
+    for step, low in BYTES:
+        pages = keep.copy()
+        for s, (n, c) in enumerate(zip(q_lens, ctx)):
+            for p in range(_first_seen(n, c, window)):
+                _poison_k(pages, page, D, table[s][p // page], p % page, step, low)
+                _poison_v(pages, page, D, table[s][p // page], p % page, step, low)
+        cache.pages.copy_(torch.from_numpy(pages))
+        assert torch.equal(_run(q, cache, batch, H, scale, window), clean), (step, low)
+
+
+@pytest.mark.parametrize("bounds", BOUNDS)
+@pytest.mark.parametrize("q_len", [2, 5, 40, 200])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bytes_ahead_of_a_row(q_len, D, bounds):
+    """V of the last positions, which only the last rows see: the others are as they were."""
+    H, KV, page = 4, 2, 16
+    case = ([q_len, q_len], [q_len + 170, q_len], H, KV, D, page, 0)
+    q, K, V, table, cache, batch = _attend(case, 60 + q_len, bounds=bounds)
+    clean = _run(q, cache, batch, H, 0.1).view(2, q_len, -1)
+    keep = cache.pages.cpu().numpy()
+    last = max(1, q_len // 3)
+    for step, low in BYTES:
+        pages = keep.copy()
+        for s, c in enumerate(case[1]):
+            for p in range(c - last, c):
+                _poison_v(pages, page, D, table[s][p // page], p % page, step, low)
+        cache.pages.copy_(torch.from_numpy(pages))
+        got = _run(q, cache, batch, H, 0.1).view(2, q_len, -1)
+        assert torch.equal(got[:, :q_len - last], clean[:, :q_len - last]), (step, low)
 
 
 @pytest.mark.parametrize("bounds", BOUNDS)
