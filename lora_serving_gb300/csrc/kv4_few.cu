@@ -171,11 +171,13 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     const int pos0 = tile * kTile;
     const uint8_t* head_pages = a.cache.pages + static_cast<long long>(h) * block_bytes(ps, D);
     unsigned has = 0;   // stages' halves that hold positions
-    auto page_at = [&](int pos) -> int { return pos < q.ctx ? __ldg(table + (pos >> a.cache.page_shift)) : -1; };
+    auto page_at = [&](int pos) -> int { return pos < q.ctx ? max(-1, __ldg(table + (pos >> a.cache.page_shift))) : -1; };
     // Bytes of a tile (or of half of one) in a block: codes at 16 lane, params at param_at.
     const uint32_t ring_at = tc::smem_u32(ring) + 16 * lane;
     const int codes_v = v_codes_off(ps, D);
-    int next = n_mine > 0 ? page_at(pos0) : -1;   // the next page to be read
+    // the next page to be read; a page of half a tile, the first, may lie behind the window of every row
+    constexpr int kUnseen = -2;
+    int next = n_mine <= 0 ? -1 : ps < kTile && pos0 + kHalf <= seen_from(p0, a.window) ? kUnseen : page_at(pos0);
     const uint8_t *codes = nullptr, *params = nullptr;
     int left = 0;                                 // tiles left in the page
     auto issue = [&](int i) {
@@ -212,7 +214,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
             for (int hf = 0; hf < 2; ++hf) {
                 const int at = pos + kHalf * hf, page = next;
                 next = page_at(at + kHalf);
-                if (at >= q.ctx) continue;
+                if (at >= q.ctx || page == kUnseen) continue;
                 if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.cache.n_pages)) {
                     if (lane == 0) flag(a.status, LORA_DEV_BAD_PAGE);
                     continue;

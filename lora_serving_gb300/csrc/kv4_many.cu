@@ -743,11 +743,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 bool hidden;       // K: the position's page is bad
                 int page;          // of the tile to be loaded next
             };
-            int p0 = 0, p1 = 0, j_end = 0, tile0 = 0, n_tiles = 0, head = 0;
+            int p0 = 0, p1 = 0, j_begin = 0, j_end = 0, tile0 = 0, n_tiles = 0, head = 0;   // rows see [j_begin, j_end)
+            const int reach = is_k ? 1 : 8;                     // positions of this thread
             const int32_t* table = nullptr;
             auto page_at = [&](int j) -> int {   // -1: no row sees the place; -2: its page is bad
                 const int p = (tile0 + j) * kTok + my_tok;
-                if (j >= n_tiles || p >= j_end || idle) return -1;
+                if (j >= n_tiles || p >= j_end || p + reach <= j_begin || idle) return -1;
                 const int page = __ldg(table + (p >> a.cache.page_shift));
                 return static_cast<unsigned>(page) < static_cast<unsigned>(a.cache.n_pages) ? page : -2;
             };
@@ -834,8 +835,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 if (idle) return;
                 if (__builtin_expect(!inner(tile0 + j, p0, p1), 0)) {
                     // positions that no row sees, and values that are not finite, count as zeros
-                    const int p = (tile0 + j) * kTok + my_tok, begin = seen_from(p0, a.window);
-                    auto seen = [&](int at) { return at >= begin && at < j_end; };
+                    const int p = (tile0 + j) * kTok + my_tok;
+                    auto seen = [&](int at) { return at >= j_begin && at < j_end; };
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = p + 2 * i;
@@ -902,6 +903,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 tile0 = pc->tile0;
                 n_tiles = pc->tiles;
                 head = pc->h;
+                j_begin = seen_from(p0, a.window);
                 j_end = max(0, p1 + 1);
                 table = a.batch.block_table + static_cast<long long>(pc->s) * a.batch.ld_table;
                 if (is_k && i > 0) {   // these warps are ahead: Q's lines are on their way when its place is free

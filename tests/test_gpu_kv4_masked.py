@@ -1,5 +1,6 @@
 """lora_kv4_attend and what its rows do not see: positions behind a window and
-ahead of a row, whatever their bytes, windows wider than any context."""
+ahead of a row, whatever their bytes, pages that were given back, windows
+wider than any context."""
 import math
 
 import numpy as np
@@ -88,6 +89,22 @@ def test_bytes_ahead_of_a_row(q_len, D, bounds):
         cache.pages.copy_(torch.from_numpy(pages))
         got = _run(q, cache, batch, H, 0.1).view(2, q_len, -1)
         assert torch.equal(got[:, :q_len - last], clean[:, :q_len - last]), (step, low)
+
+
+@pytest.mark.parametrize("bounds", BOUNDS)
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("q_lens", [[1, 1, 1], [2, 1, 4], [60, 1, 33]])
+def test_pages_given_back_behind_the_window(q_lens, page, bounds):
+    """A table may name any page, or none, where no row sees a position."""
+    H, KV, D = 8, 2, 128
+    for ctx, window in (([1000, 600, 300], 100), ([733, 1290, 65], 17), ([2000, 90, 1111], 512), ([999, 1001, 1003], 1)):
+        case = (q_lens, ctx, H, KV, D, page, window)
+        q, K, V, table, cache, batch = _attend(case, page + window, bounds=bounds)
+        clean = _run(q, cache, batch, H, 0.1, window)
+        for none in (-1, 10 ** 6):
+            for s, (n, c) in enumerate(zip(q_lens, ctx)):
+                batch.block_table[s, :_first_seen(n, c, window) // page] = none
+            assert torch.equal(_run(q, cache, batch, H, 0.1, window), clean)        # (and no status)
 
 
 @pytest.mark.parametrize("bounds", BOUNDS)
