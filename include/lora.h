@@ -549,7 +549,8 @@ lora_status_t lora_kv4_read(lora_bf16_t* k, int ld_k, lora_bf16_t* v, int ld_v, 
  * ran out, and rows of the call are undefined.
  * Errors (before anything is enqueued): as lora_kv4_append, plus
  * LORA_ERR_SHAPE (n_heads not a multiple of n_kv, more than 64 q heads to a
- * kv head, more than 4096 sequences, more tiles in all than 31 bits
+ * kv head, more than 4096 sequences, max_ctx_len above 2^30, more than 2^30
+ * rows times heads of a kv head, more tiles in all than 31 bits
  * count: of 32 positions for every 8 rows of a kv head, or of 128 for every
  * 256), LORA_ERR_WORKSPACE, LORA_ERR_INVALID_ARG (scale not finite,
  * window < 0).

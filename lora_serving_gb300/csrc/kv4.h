@@ -114,6 +114,11 @@ struct AttendArgs {
     int32_t* status;
 };
 constexpr int kMaxSeqs = 4096;   // sequences of one attention call (their running sum lies in shared memory)
+// Positions of a sequence, and rows x heads of a kv head, of one attention
+// call: the kernels count both in 32 bits, past the end of what they hold by
+// a page, a tile or a block, and from a row before the first position back by
+// a window (which the host cuts to the positions).
+constexpr int kMaxPositions = 1 << 30;
 // The longest line of tiles that a batch within these bounds lays out (the kernels count its places in 32 bits).
 long long kv4_attend_places(const AttendArgs& a);
 size_t kv4_attend_workspace(int n_heads, int n_kv, int head_dim, int max_q_len);

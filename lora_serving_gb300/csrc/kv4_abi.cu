@@ -185,7 +185,9 @@ lora_status_t lora_kv4_attend(lora_bf16_t* out, int ld_out, const lora_bf16_t* q
     const int n_kv = a.cache.n_kv, D = a.cache.head_dim;
     if (n_heads % n_kv != 0 || n_heads / n_kv > kMaxGroupHeads) return LORA_ERR_SHAPE;
     if (batch->n_rows == 0) return LORA_OK;
-    a.n_heads = n_heads; a.window = window; a.group = n_heads / n_kv;
+    a.n_heads = n_heads; a.group = n_heads / n_kv;
+    if (batch->max_ctx_len > lora::kMaxPositions || static_cast<long long>(batch->n_rows) * a.group > lora::kMaxPositions) return LORA_ERR_SHAPE;
+    a.window = window < batch->max_ctx_len ? window : 0;   // one as wide as the longest context hides nothing
     a.group_magic = a.group > 1 ? static_cast<uint32_t>((1ULL << 32) / a.group + 1) : 0;
     if (batch->n_seqs > lora::kMaxSeqs || lora::kv4_attend_places(a) > 0x7FFFFFFFLL) return LORA_ERR_SHAPE;
     LORA_TRY(check_matrix(q, ld_q, static_cast<long long>(n_heads) * D));
