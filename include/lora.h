@@ -398,8 +398,11 @@ lora_status_t lora_merge_batch(int n, lora_bf16_t* const* W, const int* ld_w, co
  * scales          [dev] fp32 [n_rows][ld_scales], 4-byte aligned (with y8)
  * group           columns per scale: 128 (the last group may be shorter),
  *                 or 0 for one scale per row
- * A group of zeros has scale 0 and codes 0.  A NaN in a row makes the whole
- * row NaN.  Apart from the aliases named above, outputs overlap no input.
+ * A group whose scale is 0 in fp32 (zeros, and values up to 3.1e-43) has codes
+ * 0.  A NaN in a row makes the whole row NaN.  All of it is fp32 arithmetic: a
+ * row whose sum of squares passes fp32's range (|h| of 2^63 or so) gives zeros,
+ * and with eps 0 one whose sum is 0 (zeros, |h| below 2^-75) gives NaN or
+ * infinities.  Apart from the aliases named above, outputs overlap no input.
  * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL x or
  * weight, neither y nor y8, y8 without scales, residual without
  * residual_out or the reverse, n_rows < 0, width <= 0, eps negative or not finite),

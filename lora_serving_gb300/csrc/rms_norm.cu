@@ -44,6 +44,9 @@ __device__ __forceinline__ uint2 to_e4m3x8(const float* n, float inv)
     return make_uint2(r[0], r[1]);
 }
 
+// Groups whose largest value is below kSmall (448 / g is finite down to 1.3e-36) are scaled up first.
+constexpr float kSmall = 0x1p-64f, kUp = 0x1p64f;
+
 // Chunk j of a thread: columns 8 * (j * blockDim.x + threadIdx.x).  Sixteen
 // neighbouring lanes then hold the 128 columns of a scale.
 template <int NCH>
@@ -141,7 +144,12 @@ __global__ void __launch_bounds__(1024) rms_norm_kernel(NormArgs a)
                 for (int o = 8; o > 0; o >>= 1) g = max_abs(g, __shfl_xor_sync(0xFFFFFFFFu, g, o));
                 if (live && (c & 15) == 0) a.scales[row * a.ld_scales + (c >> 4)] = g / 448.f;
             }
-            // a NaN stays NaN through the product, so g == 0 is the only special case
+            if (g < kSmall) {   // 448 / g might be no fp32 number: both taken up by a power of two, unless the scale is 0
+                g = g / 448.f == 0.f ? 0.f : g * kUp;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) n[i] *= kUp;
+            }
+            // a NaN stays NaN through the product, so g == 0 is the only special case left
             const float inv = g == 0.f ? 0.f : 448.f / g;
             if (live) *reinterpret_cast<uint2*>(a.y8 + row * a.ld_y8 + 8 * c) = to_e4m3x8(n, inv);
         }
