@@ -203,10 +203,12 @@ static PyObject* kv4_append(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *q, *x, *rope = NULL, *pos = NULL, *status_word, *stream;
     int ld_q, ld_x, ld_pos = 0, heads, q_off, k_off, v_off, rot = 0, max_pos = 0, axes = 0, pairs[LORA_MAX_ROPE_AXES];
     if (count(n, 13) || structs(a[2], a[3], &cache, &batch) || as_int(a[4], "n_heads", &heads) || as_int(a[5], "q_off", &q_off) ||
-        as_int(a[6], "k_off", &k_off) || as_int(a[7], "v_off", &v_off) ||
-        matrix(a[0], "q_out", bf16, batch->n_rows, (long)heads * cache->head_dim, &q, &ld_q) ||
-        matrix(a[1], "x", bf16, batch->n_rows, 0, &x, &ld_x))
+        as_int(a[6], "k_off", &k_off) || as_int(a[7], "v_off", &v_off))
         return NULL;
+    /* the columns that the slices end at, of x itself: the library knows the row stride of the buffer that x may be a part of */
+    const long nq = (long)heads * cache->head_dim, nk = (long)cache->n_kv * cache->head_dim;
+    const long kv_end = (k_off > v_off ? k_off : v_off) + nk, end = q_off + nq > kv_end ? q_off + nq : kv_end;
+    if (matrix(a[0], "q_out", bf16, batch->n_rows, nq, &q, &ld_q) || matrix(a[1], "x", bf16, batch->n_rows, end, &x, &ld_x)) return NULL;
     if (a[8] != Py_None) {
         long s[3];
         const int dims = sizes(a[8], s);
