@@ -455,11 +455,14 @@ typedef struct {
  * Device-detected faults: a sequence whose table entries are inconsistent
  * (q_starts decreasing or past n_rows, more rows than max_q_len, ctx_lens
  * negative or above max_ctx_len) is skipped and sets LORA_DEV_BAD_SEGMENT
- * (lora_kv4_attend does not write its rows); a page id outside [0, n_pages)
- * sets LORA_DEV_BAD_PAGE, and its positions count as masked.  Entries of pages
- * without a position that the call needs may hold anything: those past
- * ctx_lens, and in lora_kv4_attend those that lie behind the window of all of
- * the sequence's rows (a page given back, say).
+ * (lora_kv4_attend does not write its rows; where q_starts decreases it may
+ * leave out other sequences too, and rows that two sequences claim are
+ * undefined; lora_kv4_append and lora_kv4_read look at the sequences that
+ * their rows lie in).  A page id outside [0, n_pages) sets LORA_DEV_BAD_PAGE,
+ * and its positions count as masked.  Entries of pages without a position
+ * that the call needs may hold anything: those past ctx_lens, and in
+ * lora_kv4_attend those that lie behind the window of all of the sequence's
+ * rows (a page given back, say).
  */
 typedef struct {
     const int32_t* q_starts;    /* [dev] [n_seqs+1]; q_starts[0] == 0, q_starts[n_seqs] == n_rows */

@@ -406,13 +406,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     const int group = a.n_heads / a.cache.n_kv, ps = a.cache.page_size;
     Seq* const seqs = reinterpret_cast<Seq*>(k_s);   // until K is there
     static_assert(sizeof(Seq) * kMaxSeqs <= kStages * (S::kKTile + S::kVTile), "shared memory");
+    bool falls = false;   // q_starts decreases: the sequences together may have more rows than the batch, and more tiles than are counted in 31 bits
     scan_seqs<kWarps>(a.batch.n_seqs, prefix, sums, [&](int s) {
         Seq q;
         const bool ok = load_seq(a.batch, s, q, blockIdx.x == 0 ? a.status : nullptr);
         seqs[s] = q;
+        falls |= !ok && __ldg(a.batch.q_starts + s + 1) < __ldg(a.batch.q_starts + s);
         return ok && q.n * group > few_rows ? (q.n * group + kRowsPerItem - 1) / kRowsPerItem : 0;
     });
-    const int blocks = prefix[a.batch.n_seqs], per = (blocks + kThreads - 1) / kThreads;
+    const int blocks = __syncthreads_or(falls) ? 0 : prefix[a.batch.n_seqs], per = (blocks + kThreads - 1) / kThreads;
     Place mine;
     auto block = [&](int f) {
         mine.s = seq_at(prefix, a.batch.n_seqs, f);

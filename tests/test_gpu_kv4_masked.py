@@ -8,8 +8,8 @@ import pytest
 import torch
 
 import kv4_ref as R
-from lora_serving_gb300 import abi, build
-from test_gpu_kv4 import BOUNDS, _attend, _close, _run
+from lora_serving_gb300 import abi, build, store
+from test_gpu_kv4 import BOUNDS, _attend, _close, _run, _status
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,15 @@ def test_windows_wider_than_any_context(case, window, bounds):
     assert torch.equal(got, _run(q, cache, batch, H, scale, 0))
     want, tol = R.attend(R.f64(q).reshape(-1, H, D), K, V, q_lens, ctx, table, page, scale)
     _close(R.f64(got).reshape(-1, H, D), want, tol)
+
+
+def test_tables_that_decrease():
+    """The kernel for many rows leaves its sequences out of a batch whose q_starts decrease: together they could have more
+    rows than the batch, and more tiles than its bounds allow."""
+    H, KV, D, page = 8, 2, 128, 32
+    q, K, V, table, cache, batch = _attend(([60, 50, 90], [100, 300, 200], H, KV, D, page, 0), 90, bounds="loose")
+    batch.q_starts.copy_(torch.tensor([0, 60, 20, 110], dtype=torch.int32))
+    out, st = torch.full_like(q, 5.0), _status()
+    abi.lora_kv4_attend(out, q, cache, batch, store.kv4_workspace(cache, H, batch), n_heads=H, scale=0.1, dev_status=st)
+    assert abi.lora_read_device_status(st) == abi.LORA_DEV_BAD_SEGMENT
+    assert (out == 5).all()
