@@ -150,7 +150,7 @@ def _load_calls():
     global _calls
     lib = load()
     if not os.path.exists(CALLS_PATH):
-        raise RuntimeError(f"extension {CALLS_PATH} is missing: run lora_serving_gb300.build.build()")
+        raise RuntimeError(f"extension {CALLS_PATH} is missing: run lora_serving_gb300.build() with a C compiler and Python's headers")
     spec = importlib.util.spec_from_file_location("lora_serving_gb300._pycalls", CALLS_PATH)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)

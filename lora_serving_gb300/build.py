@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -38,21 +39,31 @@ def _sources():
     return sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
-def _deps():
-    return [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "lora.h")]
-
-
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
+def _stale(out, names) -> bool:
+    """Whether `out` is missing or older than one of these files of csrc/, or the header."""
+    if not os.path.exists(out):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    deps = [os.path.join(CSRC, f) for f in names] + [os.path.join(INCLUDE, "lora.h")]
+    return any(os.path.getmtime(p) > os.path.getmtime(out) for p in deps)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every source under csrc/ and link liblora.so; returns its path."""
-    if not force and not _stale():
-        return LIB
+    """Compile every source under csrc/ and link liblora.so; returns its path.
+    Then _pycalls.so, without which the calls that need it raise: on a machine
+    that lacks a C compiler or Python's headers there is a warning here."""
+    if force or _stale(LIB, [f for f in os.listdir(CSRC) if f != "pycalls.c"]):
+        _build_lib(verbose, extra_flags)
+    if force or _stale(CALLS, ["pycalls.c"]):
+        try:
+            _build_calls()
+        except (OSError, RuntimeError) as e:
+            if os.path.exists(CALLS):   # of another version of the library
+                os.remove(CALLS)
+            warnings.warn(f"no {os.path.basename(CALLS)}: lora_rms_norm and lora_kv4_* cannot be called from Python ({e})")
+    return LIB
+
+
+def _build_lib(verbose, extra_flags):
     cuda = _cuda_home()
     nvcc = os.path.join(cuda, "bin", "nvcc")
     os.makedirs(BUILD, exist_ok=True)
@@ -84,7 +95,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    # the Python side of some calls: plain C against the interpreter's headers (abi.py hands it the library's functions)
+
+
+def _build_calls():
+    """The Python side of some calls: plain C against the interpreter's headers (abi.py hands it the library's functions)."""
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CC", "gcc"), "-O2", "-Wall", "-fPIC", "-shared", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
            os.path.join(CSRC, "pycalls.c"), "-o", tmp]
@@ -92,7 +106,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"gcc failed on pycalls.c:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, CALLS)
-    return LIB
 
 
 if __name__ == "__main__":
