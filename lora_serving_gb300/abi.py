@@ -14,7 +14,11 @@ import importlib.util
 import os
 
 import numpy as np
-import torch
+
+try:
+    import torch
+except ImportError:   # the host helpers (metadata, adapter preparation) do without it
+    torch = None
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "liblora.so")
@@ -149,6 +153,8 @@ def _load_calls():
     convert their arguments."""
     global _calls
     lib = load()
+    if torch is None:
+        raise RuntimeError("lora_rms_norm and lora_kv4_* take torch tensors, and torch cannot be imported")
     if not os.path.exists(CALLS_PATH):
         raise RuntimeError(f"extension {CALLS_PATH} is missing: run lora_serving_gb300.build() with a C compiler and Python's headers")
     spec = importlib.util.spec_from_file_location("lora_serving_gb300._pycalls", CALLS_PATH)
@@ -181,8 +187,8 @@ def _ld(t) -> int:
     return int(t.stride(0))
 
 
-_DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
-           "e4m3": torch.float8_e4m3fn}
+_DTYPES = torch and {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
+                     "e4m3": torch.float8_e4m3fn}
 
 
 def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
@@ -203,7 +209,7 @@ def _dev(t, name: str, dtype: str | None = None, mat: bool = False) -> int:
     return t.data_ptr()
 
 
-if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the stream's handle without a Stream object around it (3 us)
+if torch and hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the stream's handle without a Stream object around it (3 us)
     _cur_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 else:
     _cur_device = lambda: torch.cuda.current_device()  # noqa: E731
