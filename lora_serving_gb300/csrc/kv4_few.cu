@@ -681,7 +681,12 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partial
 {
     using S = Shape<D>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = once_on_device(done, [&] {
+    static std::atomic<int> clusters[64];   // that each device has room for at once; 0: not asked yet
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::atomic<int>& room = clusters[dev & 63];
+    e = once_on_device(done, [&] {
         const cudaError_t f = cudaFuncSetAttribute(kv4_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
         return f == cudaSuccess ? cudaFuncSetAttribute(kv4_unit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) : f;
     });
@@ -694,7 +699,6 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partial
     // which every SM takes part in.
     const long long units = static_cast<long long>(a.batch.n_seqs) * a.cache.n_kv * ((few_rows + kRows - 1) / kRows);
     if (a.batch.max_ctx_len <= kTile * kUnitTiles * kCluster * kWarps) {
-        static std::atomic<int> room{-1};   // clusters on the GPU at once
         PdlLaunch l(dim3(static_cast<unsigned>(units * kCluster)), kThreads, S::kSmem, stream);
         cudaLaunchAttribute attr[2];
         attr[0] = l.attr[0];
@@ -703,7 +707,7 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partial
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         l.cfg.attrs = attr;
         l.cfg.numAttrs = 2;
-        if (room < 0) {
+        if (room == 0) {
             int n = 0;
             cudaLaunchConfig_t one = l.cfg;   // the query does without the other attribute
             one.gridDim = dim3(kCluster);
