@@ -1,16 +1,17 @@
 // kv4_append.cu -- rotary embedding of q and k with up to three position
 // axes, 4-bit quantisation of k and v into their pages, and the way back.
 //
-// A row is one CTA.  A team of head_dim / 16 lanes holds a head, sixteen dims
+// A row is one CTA or, from kWarpRows rows on, one warp.  A team of head_dim / 16 lanes holds a head, sixteen dims
 // a lane, as two chunks of eight; in the rotated part the chunks are the two
 // halves of eight pairs, so a rotation needs no exchange.  The team's lanes
 // hold the same pairs for every head they take, so a lane reads its (cos,
 // sin) once per row.  A group's minimum and maximum cross the team by
 // shuffles.  Bound: HBM (the row in, q and a quarter of k and v out), and with
 // many rows instructions: products are rounded one by one, so that the cached
-// bytes are the formula's whatever the compiler.  Measured: 17 k rows of 24 + 2 * 8
-// heads 72 us (4.3 TB/s, 0.64 of a copy's rate; an issue slot in two taken), their reading back
-// 14; 256 rows 7.3 both, two kernels' latency.
+// bytes are the formula's whatever the compiler.  Measured, in a graph: 15,797
+// rows of 32 + 2 * 8 heads 67 us (350 MB in and out, 5.2 TB/s, 0.77 of a copy's
+// rate; an issue slot in two taken), their reading back 15 (cold and alone 72
+// and 20); 256 rows 4.3 and 2.6, latency.
 #include <algorithm>
 
 #include "kv4.h"

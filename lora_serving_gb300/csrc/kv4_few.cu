@@ -28,7 +28,7 @@
 // meets no other warp until its range ends.
 //
 // What bounds it.  HBM by its bytes, but the unpacking takes longer: 8 requests of
-// 131072 positions, 64 heads in groups of 8, 232 us, 5.2 TB/s, 0.77 of a copy's
+// 131072 positions, 64 heads in groups of 8, 231 us, 5.2 TB/s, 0.78 of a copy's
 // rate, an issue slot in 0.63; without V's unpacking 197 us, without K's 220.
 // Small batches are starts and ends: 64 requests of up to 8192 positions 25 us
 // for 61 MB (start 4, about five tiles a warp 12, the second kernel 4), one of
@@ -48,6 +48,9 @@ using namespace kv4;
 // which unpack once for more rows, were slower for their registers: one CTA on
 // an SM (us, 32 requests of up to 1000 positions, rows of a kv head 16 / 32, by
 // slices of 8, 16, 32: heads of 128 16 / 21, 16 / 22, 29 / 33; of 64 13 / 17, 12 / 15, 15 / 17).
+// Those are starts and ends; wider slices were not timed on long contexts,
+// where each slice unpacks its kv head's bytes again: 8 requests, 4 kv heads,
+// 8 / 16 / 24 rows of each, 32000 positions 40 / 68 / 94 us, 131072 126 / 234 / 344.
 constexpr int kRows = 8;
 // Two CTAs of eight warps on an SM: 128 registers a thread.
 constexpr int kCtas = 2, kWarps = 8, kThreads = 32 * kWarps;

@@ -37,9 +37,9 @@
 // masked tiles' code it took the prompts 302 us, a chunk, where another test
 // stands in every tile, 735.
 //
-// Measured: 1024 rows of 64 heads over 32768 positions 750 us (1.44 PFLOP/s,
-// 0.73 of the measured bf16 peak); 16 prompts of 149 to 2011 tokens, 32
-// heads, 291 us.
+// Measured: 1024 rows of 64 heads over 32768 positions 745 to 755 us (1.44
+// PFLOP/s, 0.73 of the measured bf16 peak); 16 prompts of 149 to 2011 tokens,
+// 32 heads, 290 us.
 #include <algorithm>
 #include <type_traits>
 
