@@ -79,7 +79,10 @@ typedef enum {
                                           group outgrew meta->max_gseg_len; rows skipped */
 #define LORA_DEV_BAD_PAGE 0x8          /* a block table named a page outside [0, n_pages): nothing is
                                           read from or written to it (see lora_kv4_*) */
-#define LORA_DEV_BAD_POSITION 0x10     /* a rotary position outside [0, max_pos); row skipped */
+#define LORA_DEV_BAD_POSITION 0x10     /* a rotary position outside [0, max_pos), an accepted path that
+                                          does not rise inside its rows; row or sequence skipped */
+#define LORA_DEV_NO_PAGES 0x20         /* lora_kv4_plan: a sequence's new pages are not there; it has no
+                                          place in the batch */
 #define LORA_DEV_TIMEOUT 0x4           /* an asynchronous copy did not land within 0.2 s (never
                                           expected): the kernel that waited stops; rows of y it
                                           had not finished keep their previous values (a shrink
@@ -568,6 +571,190 @@ lora_status_t lora_kv4_attend(lora_bf16_t* out, int ld_out, const lora_bf16_t* q
 /* Workspace bytes of lora_kv4_attend for these heads and batches of at most
  * max_q_len rows to a sequence; 0 for counts it rejects. */
 size_t lora_kv4_attend_workspace_bytes(int n_heads, int n_kv, int head_dim, int max_q_len);
+
+/* ------------------------------------------------------------------ *
+ *  Drafted decoding over the 4-bit cache: a step's tables and pages, the
+ *  attention of drafted trees, the logits' rules, and the accepted rows.
+ *  A step is lora_kv4_plan, then per layer lora_kv4_append and
+ *  lora_kv4_attend_tree, lora_logits_adjust, and, once the accepted path of
+ *  each tree is known, lora_kv4_keep over all layers' caches.  None of them
+ *  needs a value on the host, so a step can be captured and replayed.
+ *  Ordering as for the entry points above.
+ * ------------------------------------------------------------------ */
+
+/*
+ * Pages of a cache (the same ids in every layer's): the free ones on a
+ * stack, and how many each sequence's row of the block table holds.  The
+ * counters go out to arrays of their own or to the same: with others a plan
+ * can be made again or dropped, since what it writes beside the counters
+ * lies past what they count.
+ */
+typedef struct {
+    int32_t* free_pages;   /* [dev] [n_pages]; entries [0, *n_free) are free, the last one is the next */
+    const int32_t* n_free; /* [dev] */
+    const int32_t* held;   /* [dev] [n_seqs] pages in each row of block_table */
+    int32_t* n_free_out;   /* [dev] may be n_free */
+    int32_t* held_out;     /* [dev] [n_seqs] may be held */
+    int32_t* block_table;  /* [dev] [n_seqs][ld_table] */
+    int ld_table;          /* at least ceil(max_ctx_len / page_size) */
+    int n_pages;
+    int page_size;         /* as lora_kv4_cache_t */
+} lora_kv4_pool_t;
+
+/*
+ * A step's tables from the rows that its sequences bring.  Sequence s has
+ * lens[s] cached positions and brings q_lens[s] rows; -1 (or less): it has
+ * ended.
+ *   1. The pages that ended sequences hold go onto the stack, in the order of
+ *      the sequences and of their tables.
+ *   2. q_starts = running sum of the rows; ctx_lens[s] = lens[s] + q_lens[s]
+ *      (0 for an ended one).
+ *   3. A sequence with rows whose ctx_lens[s] positions need more pages than
+ *      it holds takes the missing ones from the top of the stack, in the order
+ *      of the sequences, and they follow the others in its row of block_table.
+ *      Where the running sum of what is asked for passes the stack, the
+ *      sequence gets none and has no place in the batch
+ *      (LORA_DEV_NO_PAGES): its ctx_lens is 0, and its rows, which stay
+ *      counted in q_starts, are skipped by lora_kv4_append and get zeros from
+ *      the attention (which count a row before the first position so).
+ *   4. Of every row: its sequence, its position lens[s] + depth for the rotary
+ *      embedding (depth: depths[row], its depth in a drafted tree, or, with
+ *      depths NULL, its number in the sequence), and its slot, page * page_size
+ *      + place in the page (-1 where the table names no page); -1 in each for
+ *      rows of sequences without a place and for rows past the last.  A depth outside [0, max_ctx_len) gives the
+ *      position -1.
+ * q_starts, ctx_lens and block_table are those of a lora_kv4_batch_t with
+ * n_rows = max_rows; the counts may change from call to call, and replay to
+ * replay, within the bounds.
+ * q_starts  [dev] int32 [n_seqs + 1]     ctx_lens [dev] int32 [n_seqs]
+ * row_seq, positions  [dev] int32 [max_rows] or NULL;  slots [dev] int64 [max_rows] or NULL
+ * q_lens, lens  [dev] int32 [n_seqs];  depths [dev] int32 [max_rows] or NULL
+ * ctx_lens is not lens itself; apart from the aliases that the pool names,
+ * outputs overlap no input and no other output.
+ * Device-detected faults: LORA_DEV_BAD_SEGMENT for a sequence with more than
+ * max_q_len rows, with lens negative or ctx_lens above max_ctx_len, with held
+ * outside [0, ld_table], or with rows past max_rows: it has no place, as in 3
+ * (the row starts are cut to max_rows); one that has ended with such a held
+ * gives nothing back.  LORA_DEV_BAD_PAGE: n_free outside [0, n_pages] counts
+ * as 0, and pages given back past n_pages in all are dropped.
+ * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL pointers,
+ * negative counts, no pages, ctx_lens the same as lens), LORA_ERR_SHAPE
+ * (page_size, ld_table, more than 4096 sequences, max_ctx_len, max_rows or
+ * n_pages above 2^30), LORA_ERR_ALIGNMENT (4 bytes; slots 8), LORA_ERR_CUDA.
+ */
+lora_status_t lora_kv4_plan(int32_t* q_starts, int32_t* ctx_lens, int32_t* row_seq, int32_t* positions, int64_t* slots,
+                            const int32_t* q_lens, const int32_t* lens, const int32_t* depths, int n_seqs, int max_rows,
+                            int max_q_len, int max_ctx_len, const lora_kv4_pool_t* pool, int32_t* dev_status,
+                            lora_stream_t stream);
+
+/*
+ * lora_kv4_attend for rows that are trees of drafted tokens: the rows of a
+ * sequence, at the positions base .. base + n - 1 with base = ctx_lens[s] - n,
+ * see one another as their bits say, and all see the positions before base.
+ * Row i of its sequence sees
+ *   base + j  where bit j of tree[row i] is set, j < n,
+ *   j < base  all of them, with window > 0 only j > base + depth - window,
+ * where depth is the number of its set bits below n less one (0 where it has
+ * none).  Bits name ancestors and the row itself; any set is taken, the
+ * window is not applied to it, and bits from n on are not looked at.  With
+ * bits 0..i in row i (and a window of n at least) this is lora_kv4_attend.
+ * tree  [dev] uint32 [n_rows][ld_tree], bit j % 32 of word j / 32;
+ *       ld_tree >= ceil(max_q_len / 32)
+ * All else, arguments, workspace, rounding, rows that see nothing or have no
+ * place, bytes that no row sees, faults and errors, as lora_kv4_attend;
+ * LORA_ERR_INVALID_ARG also for tree NULL, LORA_ERR_SHAPE for ld_tree,
+ * LORA_ERR_ALIGNMENT for tree (4 bytes).
+ */
+lora_status_t lora_kv4_attend_tree(lora_bf16_t* out, int ld_out, const lora_bf16_t* q, int ld_q, int n_heads, float scale,
+                                   int window, const uint32_t* tree, int ld_tree, const lora_kv4_cache_t* cache,
+                                   const lora_kv4_batch_t* batch, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                   lora_stream_t stream);
+
+/* Caches that one launch of lora_kv4_keep takes (more are several launches). */
+#define LORA_KEEP_LAYERS 64
+
+/*
+ * Keeps the accepted rows of each sequence's tree: with base = ctx_lens[s] - n
+ * (n rows), the cached position base + path[s][i] becomes position base + i
+ * for i < n_keep[s], in each of the caches (one per layer, all with the
+ * batch's block table), bit for bit.  path[s] rises strictly within [0, n).
+ * lens[s] = base + n_keep[s]: the sequence's cached positions from now on
+ * (those behind hold what they held).
+ * caches  [host] n_caches structs of the same page size, heads and dimension
+ * n_keep  [dev] int32 [n_seqs];  path [dev] int32 [n_seqs][ld_path]
+ * lens    [dev] int32 [n_seqs] or NULL; not the batch's ctx_lens
+ * A sequence with more rows than positions (one without a place) is left as
+ * it is, and so is its lens; so is, flagged, one with inconsistent tables or
+ * n_keep outside [0, min(n, ld_path)] (LORA_DEV_BAD_SEGMENT) or with a path
+ * that does not rise inside its rows (LORA_DEV_BAD_POSITION).  Where a position
+ * that moves lies or would come to lie in a page that a cache does not have
+ * (LORA_DEV_BAD_PAGE), nothing moves in that cache.
+ * Two sequences that share a page which a row moves in race.
+ * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL pointers,
+ * n_caches < 0, the same pages twice, lens the same as ctx_lens), LORA_ERR_SHAPE (caches that
+ * differ, ld_path < 0, a block table too small), LORA_ERR_METADATA and
+ * LORA_ERR_ALIGNMENT as lora_kv4_append, LORA_ERR_CUDA.
+ */
+lora_status_t lora_kv4_keep(const lora_kv4_cache_t* caches, int n_caches, const lora_kv4_batch_t* batch,
+                            const int32_t* n_keep, const int32_t* path, int ld_path, int32_t* lens,
+                            int32_t* dev_status, lora_stream_t stream);
+
+/* Element types of lora_logits_adjust. */
+typedef enum { LORA_BF16 = 0, LORA_F32 = 1 } lora_dtype_t;
+
+/* What a request's sampling asks of its logits; arrays of n_seqs entries,
+ * [dev].  repetition, frequency and presence may be NULL (1, 0 and 0). */
+typedef struct {
+    const int32_t* tokens;      /* [n_seqs][ld_tokens]: the request's tokens, the prompt's first */
+    const int32_t* prompt_lens; /* of these, the prompt's */
+    const int32_t* token_lens;  /* all of them */
+    const float *repetition, *frequency, *presence;
+    const int32_t* bias_ids;    /* [n_seqs][ld_bias] tokens with a bias, or NULL */
+    const float* bias;          /* [n_seqs][ld_bias] */
+    const int32_t* n_bias;      /* entries of each row */
+    int ld_tokens, ld_bias, n_seqs;
+} lora_logits_rules_t;
+
+/*
+ * The rules of each row's request applied to its logits: with x = logits[t][v],
+ * c the times that v occurs among the request's tokens behind the prompt and
+ * on the row's path, and v seen if it occurs anywhere among them or the prompt,
+ *   x <- x > 0 ? x / repetition : x * repetition     if v is seen
+ *   x <- x - frequency * c - presence * [c > 0]
+ *   x <- x + bias(v)
+ *   x <- -infinity                                   if v is not allowed
+ * in fp32, rounded once to out's type.
+ * out        [dev] bf16 or fp32 [n_rows][ld_out]; may be logits itself where the types are the same
+ * logits     [dev] bf16 or fp32 [n_rows][ld]; both 16-byte aligned, ld and ld_out multiples of 8;
+ *            columns from vocab on are neither read nor written (any vocab)
+ * rules      [host] struct, or NULL: no penalties and biases
+ * row_seq    [dev] int32 [n_rows] request of each row, -1: the row is not written; NULL: row t is request t's
+ * drafts     [dev] int32 [n_rows] with tree and q_starts, or NULL: the token of each row of drafted trees;
+ *            the path of a row is the rows of its request, [q_starts[s], q_starts[s + 1]), whose bits it has
+ * tree       [dev] uint32 [n_rows][ld_tree], as lora_kv4_attend_tree; bits from 32 ld_tree on are none
+ * q_starts   [dev] int32 [n_seqs + 1]
+ * allowed    [dev] uint32 [n_allowed][ld_allowed] or NULL: bit v % 32 of word v / 32 allows token v
+ * allowed_rows [dev] int32 [n_rows] set of each row, -1: none; NULL: row t has set t (n_allowed >= n_rows)
+ * Tokens outside [0, vocab), in tokens, drafts or bias_ids, count for nothing.
+ * Of a token's entries in bias_ids the last one counts.
+ * Device-detected faults, each of which leaves the row unwritten: row_seq
+ * outside [-1, n_seqs), token_lens outside [0, ld_tokens], prompt_lens outside
+ * [0, token_lens], n_bias outside [0, ld_bias], with drafts a row outside its
+ * request's rows (LORA_DEV_BAD_SEGMENT); allowed_rows outside [-1, n_allowed)
+ * (LORA_DEV_SLOT_OUT_OF_RANGE).
+ * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL pointers,
+ * a negative count, an unknown type, drafts without rules, tree or q_starts,
+ * n_rows above n_seqs without row_seq, n_rows above n_allowed without
+ * allowed_rows, out the same as logits with another type or leading dimension),
+ * LORA_ERR_SHAPE (a leading dimension too small, vocab above 2^30, ld_tokens
+ * + 32 ld_tree above 2^20 - 1 or ld_bias above 2047, which the counters hold),
+ * LORA_ERR_ALIGNMENT, LORA_ERR_CUDA.
+ */
+lora_status_t lora_logits_adjust(void* out, lora_dtype_t out_type, int ld_out, const void* logits, lora_dtype_t type, int ld,
+                                 int n_rows, int vocab, const lora_logits_rules_t* rules, const int32_t* row_seq,
+                                 const int32_t* drafts, const uint32_t* tree, int ld_tree, const int32_t* q_starts,
+                                 const uint32_t* allowed, int ld_allowed, int n_allowed, const int32_t* allowed_rows,
+                                 int32_t* dev_status, lora_stream_t stream);
 
 /* ------------------------------------------------------------------ *
  *  Adapter slots: GPU slots fed from a host cache of prepared adapters

@@ -35,7 +35,10 @@ LORA_APPLY_Y_READY = 0x4
 LORA_DEV_TIMEOUT = 0x4
 LORA_DEV_BAD_PAGE = 0x8
 LORA_DEV_BAD_POSITION = 0x10
+LORA_DEV_NO_PAGES = 0x20
 LORA_MAX_ROPE_AXES = 3
+LORA_KEEP_LAYERS = 64
+LORA_BF16, LORA_F32 = 0, 1
 
 STATUS = {
     0: "LORA_OK", 1: "LORA_ERR_INVALID_ARG", 2: "LORA_ERR_SHAPE",
@@ -52,7 +55,7 @@ EXPORTS = (
     "lora_slots_create", "lora_slots_destroy", "lora_slots_register", "lora_slots_acquire",
     "lora_slots_slot_of", "lora_slots_stats",
     "lora_rms_norm", "lora_kv4_block_bytes", "lora_kv4_append", "lora_kv4_read", "lora_kv4_attend",
-    "lora_kv4_attend_workspace_bytes",
+    "lora_kv4_attend_workspace_bytes", "lora_kv4_plan", "lora_kv4_attend_tree", "lora_kv4_keep", "lora_logits_adjust",
 )
 LORA_NOALLOC_SCRATCH_BYTES = 16 << 20
 
@@ -86,6 +89,27 @@ class lora_kv4_batch_t(ctypes.Structure):
     _fields_ = [("q_starts", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("ld_table", ctypes.c_int), ("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int),
                 ("max_q_len", ctypes.c_int), ("max_ctx_len", ctypes.c_int)]
+
+
+class lora_kv4_pool_t(ctypes.Structure):
+    _fields_ = [("free_pages", ctypes.c_void_p), ("n_free", ctypes.c_void_p), ("held", ctypes.c_void_p),
+                ("n_free_out", ctypes.c_void_p), ("held_out", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("ld_table", ctypes.c_int), ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int)]
+
+
+class plan_args_t(ctypes.Structure):
+    """plan_t of csrc/pycalls.c: what a store.KV4Plan keeps of lora_kv4_plan's arguments."""
+    _fields_ = [("q_starts", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("row_seq", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("n_seqs", ctypes.c_int32),
+                ("max_rows", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("max_ctx_len", ctypes.c_int32),
+                ("pool", lora_kv4_pool_t)]
+
+
+class lora_logits_rules_t(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p), ("token_lens", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_ids", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("n_bias", ctypes.c_void_p),
+                ("ld_tokens", ctypes.c_int), ("ld_bias", ctypes.c_int), ("n_seqs", ctypes.c_int)]
 
 
 _lib = None
@@ -128,6 +152,10 @@ def load(path: str | None = None):
         "lora_kv4_read": [P, i32, P, i32, P, P, P, P],
         "lora_kv4_attend": [P, i32, P, i32, i32, ctypes.c_float, i32, P, P, P, sz, P, P],
         "lora_kv4_attend_workspace_bytes": [i32, i32, i32, i32],
+        "lora_kv4_plan": [P, P, P, P, P, P, P, P, i32, i32, i32, i32, P, P, P],
+        "lora_kv4_attend_tree": [P, i32, P, i32, i32, ctypes.c_float, i32, P, i32, P, P, P, sz, P, P],
+        "lora_kv4_keep": [P, i32, P, P, P, i32, P, P, P],
+        "lora_logits_adjust": [P, i32, i32, P, i32, i32, i32, i32, P, P, P, P, i32, P, P, i32, i32, P, P, P],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -154,14 +182,15 @@ def _load_calls():
     global _calls
     lib = load()
     if torch is None:
-        raise RuntimeError("lora_rms_norm and lora_kv4_* take torch tensors, and torch cannot be imported")
+        raise RuntimeError("lora_rms_norm, lora_kv4_* and lora_logits_adjust take torch tensors, and torch cannot be imported")
     if not os.path.exists(CALLS_PATH):
         raise RuntimeError(f"extension {CALLS_PATH} is missing: run lora_serving_gb300.build() with a C compiler and Python's headers")
     spec = importlib.util.spec_from_file_location("lora_serving_gb300._pycalls", CALLS_PATH)
     mod = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(mod)
     fns = tuple(ctypes.cast(f, ctypes.c_void_p).value
-                for f in (lib.lora_rms_norm, lib.lora_kv4_append, lib.lora_kv4_read, lib.lora_kv4_attend))
+                for f in (lib.lora_rms_norm, lib.lora_kv4_append, lib.lora_kv4_read, lib.lora_kv4_attend, lib.lora_kv4_plan,
+                          lib.lora_kv4_attend_tree, lib.lora_kv4_keep, lib.lora_logits_adjust))
     mod.bind(fns, (torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn), _cur_device, _raw_stream)
     _calls = mod
     return mod
@@ -187,7 +216,7 @@ def _ld(t) -> int:
     return int(t.stride(0))
 
 
-_DTYPES = torch and {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
+_DTYPES = torch and {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "i64": torch.int64, "u8": torch.uint8,
                      "e4m3": torch.float8_e4m3fn}
 
 
@@ -379,6 +408,52 @@ def lora_kv4_attend(out, q, cache, batch, workspace, *, n_heads, scale, window=0
 
 def lora_kv4_attend_workspace_bytes(n_heads, n_kv, head_dim, max_q_len) -> int:
     return int(load().lora_kv4_attend_workspace_bytes(n_heads, n_kv, head_dim, max_q_len))
+
+
+def lora_kv4_plan(plan, q_lens, lens, *, depths=None, dev_status=None, stream=None):
+    """A step's tables and pages: `plan` (store.KV4Plan) gets the row starts,
+    lengths, pages, and each row's sequence, position and slot, from int32
+    q_lens (rows that each sequence brings; -1: it has ended) and lens (cached
+    positions); depths: int32 [max_rows], the rows' depths in drafted trees."""
+    st = (_calls or _load_calls()).kv4_plan(plan.addr, q_lens, lens, depths, dev_status, stream)
+    if st:
+        raise LoraError("lora_kv4_plan", st)
+
+
+def lora_kv4_attend_tree(out, q, cache, batch, tree, workspace, *, n_heads, scale, window=0, dev_status=None, stream=None):
+    """out [n_rows][n_heads * head_dim] <- attention of drafted trees' rows over
+    the cache: the positions before the sequence's first row (the last `window`
+    of them by the row's depth, 0: all), and of its rows those whose bits are
+    set in the row's int32 words of `tree` [n_rows][words]."""
+    st = (_calls or _load_calls()).kv4_attend_tree(out, q, cache.addr, batch.addr, tree, workspace, n_heads, scale, window,
+                                                   dev_status, stream)
+    if st:
+        raise LoraError("lora_kv4_attend_tree", st)
+
+
+def lora_kv4_keep(layers, batch, n_keep, path, *, lens=None, dev_status=None, stream=None):
+    """In every cache of `layers` (store.KV4Layers) the rows path[s][:n_keep[s]]
+    of sequence s of `batch` move up to follow its context; lens <- the
+    sequences' cached positions from now on.  int32 n_keep [n_seqs], path
+    [n_seqs][columns], lens [n_seqs]."""
+    st = (_calls or _load_calls()).kv4_keep(layers.addr, layers.n, batch.addr, n_keep, path, lens, dev_status, stream)
+    if st:
+        raise LoraError("lora_kv4_keep", st)
+
+
+def lora_logits_adjust(out, logits, rules=None, *, row_seq=None, drafts=None, tree=None, q_starts=None, allowed=None,
+                       allowed_rows=None, dev_status=None, stream=None):
+    """out <- logits [n_rows][vocab] (bf16 or fp32 each) under the penalties and
+    biases of `rules` (store.LogitsRules) for each row's request (row_seq: int32
+    [n_rows], -1: not written; default: row t is request t's), with the drafted
+    tokens on the row's path (drafts [n_rows], tree [n_rows][words], q_starts)
+    counted in, and -infinity where the row's set of `allowed` (int32
+    [sets][words], a bit per token; allowed_rows: set of each row, -1: none)
+    lacks the token."""
+    st = (_calls or _load_calls()).logits_adjust(out, logits, rules.addr if rules is not None else 0, row_seq, drafts, tree,
+                                                 q_starts, allowed, allowed_rows, dev_status, stream)
+    if st:
+        raise LoraError("lora_logits_adjust", st)
 
 
 class lora_slot_stats_t(ctypes.Structure):

@@ -112,6 +112,8 @@ struct AttendArgs {
     void* ws;
     size_t ws_bytes;
     int32_t* status;
+    const uint32_t* tree;   // bits of drafted trees' rows, [n_rows][ld_tree]; NULL: rows see what lies before them
+    int ld_tree;
 };
 constexpr int kMaxSeqs = 4096;   // sequences of one attention call (their running sum lies in shared memory)
 // Positions of a sequence, and rows x heads of a kv head, of one attention
@@ -123,5 +125,62 @@ constexpr int kMaxPositions = 1 << 30;
 long long kv4_attend_places(const AttendArgs& a);
 size_t kv4_attend_workspace(int n_heads, int n_kv, int head_dim, int max_q_len);
 cudaError_t launch_kv4_attend(const AttendArgs& a, cudaStream_t stream);
+
+struct PlanArgs {
+    int32_t* q_starts;
+    int32_t* ctx_lens;
+    int32_t* row_seq;
+    int32_t* positions;
+    int64_t* slots;
+    const int32_t* q_lens;
+    const int32_t* lens;
+    const int32_t* depths;
+    int n_seqs;
+    int max_rows;
+    int max_q_len;
+    int max_ctx_len;
+    lora_kv4_pool_t pool;
+    int page_shift;
+    int32_t* status;
+};
+cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream);
+
+struct KeepArgs {
+    struct Pages {
+        uint8_t* pages;
+        long long page_stride;
+        int n_pages;
+    };
+    Pages layers[LORA_KEEP_LAYERS];
+    kv4::Cache cache;   // what the layers have in common
+    kv4::Batch batch;
+    const int32_t* n_keep;
+    const int32_t* path;
+    int ld_path;
+    int32_t* lens;      // NULL in all launches but a call's first
+    int32_t* status;
+};
+cudaError_t launch_kv4_keep(const KeepArgs& a, int n_layers, cudaStream_t stream);
+
+struct LogitsArgs {
+    void* out;
+    int ld_out;
+    const void* logits;
+    int ld;
+    int n_rows;
+    int vocab;
+    lora_logits_rules_t rules;   // tokens NULL: none
+    const int32_t* row_seq;
+    const int32_t* drafts;
+    const uint32_t* tree;
+    int ld_tree;
+    const int32_t* q_starts;
+    const uint32_t* allowed;
+    int ld_allowed;
+    int n_allowed;
+    const int32_t* allowed_rows;
+    int32_t* status;
+};
+cudaError_t launch_logits_adjust(const LogitsArgs& a, bool in_f32, bool out_f32, cudaStream_t stream);
 
 }  // namespace lora

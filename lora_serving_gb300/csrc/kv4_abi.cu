@@ -1,7 +1,8 @@
-// kv4_abi.cu -- C ABI entry points of the norm and the 4-bit cache's
-// operators: host-side validation before anything is enqueued.
+// kv4_abi.cu -- C ABI entry points of the norm, the 4-bit cache's operators
+// and drafted decoding's: host-side validation before anything is enqueued.
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "kv4.h"
 
@@ -73,6 +74,31 @@ lora_status_t check_batch(const lora_kv4_batch_t* b, const lora::kv4::Cache& c, 
 }
 
 bool overlap(long long a0, long long an, long long b0, long long bn) { return a0 < b0 + bn && b0 < a0 + an; }
+
+// The checks of an attention call and its launch; `a` holds what only a tree's call sets.
+lora_status_t attend(lora::AttendArgs& a, lora_bf16_t* out, int ld_out, const lora_bf16_t* q, int ld_q, int n_heads, float scale,
+                     int window, const lora_kv4_cache_t* cache, const lora_kv4_batch_t* batch, void* workspace, size_t ws_bytes,
+                     int32_t* dev_status, lora_stream_t stream)
+{
+    LORA_TRY(check_cache(cache, a.cache));
+    LORA_TRY(check_batch(batch, a.cache, a.batch));
+    if (n_heads <= 0 || window < 0 || !std::isfinite(scale)) return LORA_ERR_INVALID_ARG;
+    const int n_kv = a.cache.n_kv, D = a.cache.head_dim;
+    if (n_heads % n_kv != 0 || n_heads / n_kv > kMaxGroupHeads) return LORA_ERR_SHAPE;
+    if (batch->n_rows == 0) return LORA_OK;
+    a.n_heads = n_heads; a.group = n_heads / n_kv;
+    if (batch->max_ctx_len > lora::kMaxPositions || static_cast<long long>(batch->n_rows) * a.group > lora::kMaxPositions) return LORA_ERR_SHAPE;
+    a.window = window < batch->max_ctx_len ? window : 0;   // one as wide as the longest context hides nothing
+    a.group_magic = a.group > 1 ? static_cast<uint32_t>((1ULL << 32) / a.group + 1) : 0;
+    if (batch->n_seqs > lora::kMaxSeqs || lora::kv4_attend_places(a) > 0x7FFFFFFFLL) return LORA_ERR_SHAPE;
+    LORA_TRY(check_matrix(q, ld_q, static_cast<long long>(n_heads) * D));
+    LORA_TRY(check_matrix(out, ld_out, static_cast<long long>(n_heads) * D));
+    if (!workspace || ws_bytes < lora_kv4_attend_workspace_bytes(n_heads, n_kv, D, batch->max_q_len)) return LORA_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return LORA_ERR_ALIGNMENT;
+    a.out = out; a.ld_out = ld_out; a.q = q; a.ld_q = ld_q; a.scale = scale;
+    a.ws = workspace; a.ws_bytes = ws_bytes; a.status = dev_status;
+    return cuda_status(lora::launch_kv4_attend(a, reinterpret_cast<cudaStream_t>(stream)));
+}
 
 }  // namespace
 
@@ -179,24 +205,129 @@ lora_status_t lora_kv4_attend(lora_bf16_t* out, int ld_out, const lora_bf16_t* q
                               void* workspace, size_t ws_bytes, int32_t* dev_status, lora_stream_t stream)
 {
     lora::AttendArgs a{};
-    LORA_TRY(check_cache(cache, a.cache));
-    LORA_TRY(check_batch(batch, a.cache, a.batch));
-    if (n_heads <= 0 || window < 0 || !std::isfinite(scale)) return LORA_ERR_INVALID_ARG;
-    const int n_kv = a.cache.n_kv, D = a.cache.head_dim;
-    if (n_heads % n_kv != 0 || n_heads / n_kv > kMaxGroupHeads) return LORA_ERR_SHAPE;
-    if (batch->n_rows == 0) return LORA_OK;
-    a.n_heads = n_heads; a.group = n_heads / n_kv;
-    if (batch->max_ctx_len > lora::kMaxPositions || static_cast<long long>(batch->n_rows) * a.group > lora::kMaxPositions) return LORA_ERR_SHAPE;
-    a.window = window < batch->max_ctx_len ? window : 0;   // one as wide as the longest context hides nothing
-    a.group_magic = a.group > 1 ? static_cast<uint32_t>((1ULL << 32) / a.group + 1) : 0;
-    if (batch->n_seqs > lora::kMaxSeqs || lora::kv4_attend_places(a) > 0x7FFFFFFFLL) return LORA_ERR_SHAPE;
-    LORA_TRY(check_matrix(q, ld_q, static_cast<long long>(n_heads) * D));
-    LORA_TRY(check_matrix(out, ld_out, static_cast<long long>(n_heads) * D));
-    if (!workspace || ws_bytes < lora_kv4_attend_workspace_bytes(n_heads, n_kv, D, batch->max_q_len)) return LORA_ERR_WORKSPACE;
-    if (!aligned(workspace, 256)) return LORA_ERR_ALIGNMENT;
-    a.out = out; a.ld_out = ld_out; a.q = q; a.ld_q = ld_q; a.scale = scale;
-    a.ws = workspace; a.ws_bytes = ws_bytes; a.status = dev_status;
-    return cuda_status(lora::launch_kv4_attend(a, reinterpret_cast<cudaStream_t>(stream)));
+    return attend(a, out, ld_out, q, ld_q, n_heads, scale, window, cache, batch, workspace, ws_bytes, dev_status, stream);
+}
+
+lora_status_t lora_kv4_attend_tree(lora_bf16_t* out, int ld_out, const lora_bf16_t* q, int ld_q, int n_heads, float scale,
+                                   int window, const uint32_t* tree, int ld_tree, const lora_kv4_cache_t* cache,
+                                   const lora_kv4_batch_t* batch, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                   lora_stream_t stream)
+{
+    lora::AttendArgs a{};
+    if (batch && batch->n_rows > 0) {
+        if (!tree) return LORA_ERR_INVALID_ARG;
+        if (ld_tree < (batch->max_q_len + 31LL) / 32) return LORA_ERR_SHAPE;
+        if (!aligned(tree, 4)) return LORA_ERR_ALIGNMENT;
+    }
+    a.tree = tree;
+    a.ld_tree = ld_tree;
+    return attend(a, out, ld_out, q, ld_q, n_heads, scale, window, cache, batch, workspace, ws_bytes, dev_status, stream);
+}
+
+lora_status_t lora_kv4_plan(int32_t* q_starts, int32_t* ctx_lens, int32_t* row_seq, int32_t* positions, int64_t* slots,
+                            const int32_t* q_lens, const int32_t* lens, const int32_t* depths, int n_seqs, int max_rows,
+                            int max_q_len, int max_ctx_len, const lora_kv4_pool_t* pool, int32_t* dev_status,
+                            lora_stream_t stream)
+{
+    if (!pool || n_seqs < 0 || max_rows < 0 || max_q_len < 0 || max_ctx_len < 0 || pool->n_pages <= 0) return LORA_ERR_INVALID_ARG;
+    if (!page_size_ok(pool->page_size) || n_seqs > lora::kMaxSeqs || max_ctx_len > lora::kMaxPositions ||
+        max_rows > lora::kMaxPositions || pool->n_pages > lora::kMaxPositions)
+        return LORA_ERR_SHAPE;
+    if (pool->ld_table < (max_ctx_len + pool->page_size - 1) / pool->page_size) return LORA_ERR_SHAPE;
+    if (!q_starts || !pool->free_pages || !pool->n_free || !pool->n_free_out) return LORA_ERR_INVALID_ARG;
+    if (n_seqs > 0 && (!ctx_lens || !q_lens || !lens || !pool->held || !pool->held_out || !pool->block_table || ctx_lens == lens))
+        return LORA_ERR_INVALID_ARG;
+    for (const void* p : {static_cast<const void*>(q_starts), static_cast<const void*>(ctx_lens), static_cast<const void*>(row_seq),
+                          static_cast<const void*>(positions), static_cast<const void*>(q_lens), static_cast<const void*>(lens),
+                          static_cast<const void*>(depths), static_cast<const void*>(pool->free_pages), static_cast<const void*>(pool->n_free),
+                          static_cast<const void*>(pool->held), static_cast<const void*>(pool->n_free_out),
+                          static_cast<const void*>(pool->held_out), static_cast<const void*>(pool->block_table)})
+        if (!aligned(p, 4)) return LORA_ERR_ALIGNMENT;
+    if (!aligned(slots, 8)) return LORA_ERR_ALIGNMENT;
+    lora::PlanArgs a{q_starts, ctx_lens, row_seq, positions, slots, q_lens, lens, depths, n_seqs, max_rows, max_q_len, max_ctx_len, *pool, 0, dev_status};
+    while ((1 << a.page_shift) < pool->page_size) ++a.page_shift;
+    return cuda_status(lora::launch_kv4_plan(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+lora_status_t lora_kv4_keep(const lora_kv4_cache_t* caches, int n_caches, const lora_kv4_batch_t* batch,
+                            const int32_t* n_keep, const int32_t* path, int ld_path, int32_t* lens,
+                            int32_t* dev_status, lora_stream_t stream)
+{
+    if (n_caches < 0 || (n_caches > 0 && !caches)) return LORA_ERR_INVALID_ARG;
+    lora::KeepArgs a{};
+    for (int i = 0; i < n_caches; ++i) {
+        lora::kv4::Cache c{};
+        LORA_TRY(check_cache(caches + i, c));
+        if (i == 0) {
+            a.cache = c;
+            LORA_TRY(check_batch(batch, c, a.batch));
+        }
+        for (int k = 0; k < i; ++k)
+            if (caches[k].pages == c.pages) return LORA_ERR_INVALID_ARG;   // two launches' worth of moves in one place
+        if (c.page_size != a.cache.page_size || c.n_kv != a.cache.n_kv || c.head_dim != a.cache.head_dim) return LORA_ERR_SHAPE;
+    }
+    if (n_caches == 0 || batch->n_seqs == 0) return LORA_OK;
+    if (!batch->q_starts || !batch->ctx_lens || !batch->block_table || !n_keep || !path || lens == batch->ctx_lens) return LORA_ERR_INVALID_ARG;
+    if (ld_path < 0 || batch->ld_table < (static_cast<long long>(batch->max_ctx_len) + a.cache.page_size - 1) / a.cache.page_size)
+        return LORA_ERR_SHAPE;
+    for (const void* p : {static_cast<const void*>(batch->q_starts), static_cast<const void*>(batch->ctx_lens),
+                          static_cast<const void*>(batch->block_table), static_cast<const void*>(n_keep), static_cast<const void*>(path),
+                          static_cast<const void*>(lens)})
+        if (!aligned(p, 4)) return LORA_ERR_ALIGNMENT;
+    a.n_keep = n_keep; a.path = path; a.ld_path = ld_path; a.status = dev_status;
+    for (int at = 0; at < n_caches; at += LORA_KEEP_LAYERS) {
+        const int n = n_caches - at < LORA_KEEP_LAYERS ? n_caches - at : LORA_KEEP_LAYERS;
+        for (int i = 0; i < n; ++i)
+            a.layers[i] = lora::KeepArgs::Pages{caches[at + i].pages, static_cast<long long>(caches[at + i].page_stride), caches[at + i].n_pages};
+        a.lens = at == 0 ? lens : nullptr;
+        LORA_TRY(cuda_status(lora::launch_kv4_keep(a, n, reinterpret_cast<cudaStream_t>(stream))));
+    }
+    return LORA_OK;
+}
+
+lora_status_t lora_logits_adjust(void* out, lora_dtype_t out_type, int ld_out, const void* logits, lora_dtype_t type, int ld,
+                                 int n_rows, int vocab, const lora_logits_rules_t* rules, const int32_t* row_seq,
+                                 const int32_t* drafts, const uint32_t* tree, int ld_tree, const int32_t* q_starts,
+                                 const uint32_t* allowed, int ld_allowed, int n_allowed, const int32_t* allowed_rows,
+                                 int32_t* dev_status, lora_stream_t stream)
+{
+    constexpr int kCounts = (1 << 20) - 1, kBiases = 2047;   // what a token's counter holds (logits.cu)
+    if (n_rows < 0 || vocab <= 0 || (type != LORA_BF16 && type != LORA_F32) || (out_type != LORA_BF16 && out_type != LORA_F32))
+        return LORA_ERR_INVALID_ARG;
+    if (vocab > lora::kMaxPositions) return LORA_ERR_SHAPE;
+    if (n_rows == 0) return LORA_OK;
+    LORA_TRY(check_matrix(logits, ld, vocab));
+    LORA_TRY(check_matrix(out, ld_out, vocab));
+    if (out == logits && (type != out_type || ld != ld_out)) return LORA_ERR_INVALID_ARG;
+    lora::LogitsArgs a{};
+    if (rules) {
+        const lora_logits_rules_t& r = *rules;
+        if (r.n_seqs <= 0 || r.ld_tokens < 0 || r.ld_bias < 0 || !r.tokens || !r.prompt_lens || !r.token_lens) return LORA_ERR_INVALID_ARG;
+        if (r.bias_ids && (!r.bias || !r.n_bias)) return LORA_ERR_INVALID_ARG;
+        if (!row_seq && n_rows > r.n_seqs) return LORA_ERR_INVALID_ARG;
+        if ((r.bias_ids && r.ld_bias > kBiases) || r.ld_tokens + (drafts ? 32LL * ld_tree : 0LL) > kCounts) return LORA_ERR_SHAPE;
+        for (const void* p : {static_cast<const void*>(r.tokens), static_cast<const void*>(r.prompt_lens), static_cast<const void*>(r.token_lens),
+                              static_cast<const void*>(r.repetition), static_cast<const void*>(r.frequency), static_cast<const void*>(r.presence),
+                              static_cast<const void*>(r.bias_ids), static_cast<const void*>(r.bias), static_cast<const void*>(r.n_bias)})
+            if (!aligned(p, 4)) return LORA_ERR_ALIGNMENT;
+        a.rules = r;
+    }
+    if (drafts) {
+        if (!rules || !tree || !q_starts) return LORA_ERR_INVALID_ARG;
+        if (ld_tree <= 0) return LORA_ERR_SHAPE;
+    }
+    if (allowed) {
+        if (n_allowed <= 0 || (!allowed_rows && n_rows > n_allowed)) return LORA_ERR_INVALID_ARG;
+        if (ld_allowed < (vocab + 31) / 32) return LORA_ERR_SHAPE;
+    }
+    for (const void* p : {static_cast<const void*>(row_seq), static_cast<const void*>(drafts), static_cast<const void*>(tree),
+                          static_cast<const void*>(q_starts), static_cast<const void*>(allowed), static_cast<const void*>(allowed_rows)})
+        if (!aligned(p, 4)) return LORA_ERR_ALIGNMENT;
+    a.out = out; a.ld_out = ld_out; a.logits = logits; a.ld = ld; a.n_rows = n_rows; a.vocab = vocab;
+    a.row_seq = row_seq; a.drafts = drafts; a.tree = tree; a.ld_tree = ld_tree; a.q_starts = q_starts;
+    a.allowed = allowed; a.ld_allowed = ld_allowed; a.n_allowed = n_allowed; a.allowed_rows = allowed_rows;
+    a.status = dev_status;
+    return cuda_status(lora::launch_logits_adjust(a, type == LORA_F32, out_type == LORA_F32, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -91,6 +91,29 @@ __device__ __forceinline__ void values(uint32_t w, __half2 step, __half2 low, ui
 // see).  No window and no p take this out of 32 bits: p - window + 1 alone would leave them.
 __device__ __forceinline__ int seen_from(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
 
+// ---- rows of drafted trees: they see the positions before their sequence's first row (`base`), and of its rows those
+// that their bits name
+__device__ __forceinline__ const uint32_t* tree_bits(const AttendArgs& a, const Seq& q, int i)
+{
+    return a.tree + static_cast<long long>(q.row0 + i) * a.ld_tree;
+}
+// A row's depth: its bits below n less one.
+__device__ __forceinline__ int tree_depth(const uint32_t* bits, int n)
+{
+    int set = 0;
+    for (int w = 0; 32 * w < n; ++w) set += __popc(__ldg(bits + w) & (n - 32 * w >= 32 ? 0xFFFFFFFFu : (1u << (n - 32 * w)) - 1u));
+    return max(set, 1) - 1;
+}
+// Whether row i of sequence q sees position j.  A row that lies before the first position sees nothing.
+__device__ __forceinline__ bool tree_sees(const AttendArgs& a, const Seq& q, int i, int j)
+{
+    const int base = q.ctx - q.n;
+    if (base + i < 0 || j >= q.ctx) return false;
+    const uint32_t* bits = tree_bits(a, q, i);
+    if (j >= base) return __ldg(bits + ((j - base) >> 5)) >> ((j - base) & 31) & 1u;
+    return a.window == 0 || j > base + tree_depth(bits, q.n) - a.window;
+}
+
 // Which halves of a (steps, lows) pair have codes whose value is no finite fp16 number: with step and low finite a value
 // can still leave fp16, and code 15's does if any does (low itself is code 0's).  An append leaves none.
 __device__ __forceinline__ uint32_t not_finite(uint32_t step, uint32_t low)

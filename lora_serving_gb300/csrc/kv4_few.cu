@@ -149,7 +149,7 @@ struct Sums {
 
 // One warp: `n_mine` tiles from tile `tile` of sequence s, kv head h, for the
 // rows [row0, row0 + rows).
-template <int D>
+template <int D, bool kTree>
 __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring, int s, int h, const Seq& q, int row0, int rows, int tile, int n_mine,
                                              Sums<D>& out)
 {
@@ -296,6 +296,8 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     int last[2];   // position of rows 2t, 2t + 1: the last one they see
 #pragma unroll
     for (int c = 0; c < 2; ++c) last[c] = p0 + by_group(a, row0 + 2 * t + c);
+    // in a tree, whether position j is hidden from row 2t + c
+    auto not_seen = [&](int c, int j) { return 2 * t + c >= rows || !tree_sees(a, q, last[c] - p0, j); };
 
     float (&acc)[D / 16][4] = out.acc;
     float (&top)[2] = out.top, (&sum)[2] = out.sum;
@@ -316,7 +318,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
         if (!live) continue;
         const int j0 = pos0 + i * kTile;   // the tile's first position
         // every row sees every position?
-        const bool inner = live == 3u && j0 + kTile - 1 <= p0 && (a.window == 0 || j0 > p0 + q.n - 1 - a.window);
+        const bool inner = live == 3u && j0 + kTile - 1 <= p0 - (kTree ? 1 : 0) && (a.window == 0 || j0 > p0 + q.n - 1 - a.window);
 
         const int vg = g * (D / 8) / kGroup;
         bool poison = false;
@@ -357,7 +359,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                 sc[c] *= mult[c & 1];
                 if (!inner) {
                     const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[c & 1];
-                    if (j > p || (a.window > 0 && j <= p - a.window) || !there) sc[c] = -inf;
+                    if ((kTree ? not_seen(c & 1, j) : j > p || (a.window > 0 && j <= p - a.window)) || !there) sc[c] = -inf;
                 }
                 up |= sc[c] > top[c & 1] + kSlack;
             }
@@ -435,7 +437,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                 if (nan == 0.f || j >= q.ctx) continue;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    if (j > last[c] || (a.window > 0 && j <= last[c] - a.window)) continue;
+                    if (kTree ? not_seen(c, j) : j > last[c] || (a.window > 0 && j <= last[c] - a.window)) continue;
 #pragma unroll
                     for (int m = 0; m < D / 16; ++m) {
                         acc[m][c] += nan;
@@ -489,7 +491,7 @@ __device__ __forceinline__ void put(const AttendArgs& a, int h, const Seq& q, in
     }
 }
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, int few_rows, Partials left, bool after)
 {
     using S = Shape<D>;
@@ -521,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, 
         x = min(end, u.u0 + u.len);
         if (t0 == t1) continue;   // only the unit's start lies in the range
         Sums<D> o;
-        attend_tiles<D>(a, ring, u.s, u.h, u.q, u.row0, u.rows, first_tile(u.q, a.window) + t0, t1 - t0, o);
+        attend_tiles<D, kTree>(a, ring, u.s, u.h, u.q, u.row0, u.rows, first_tile(u.q, a.window) + t0, t1 - t0, o);
         const bool whole = t0 == 0 && t1 == u.len - kUnitCost;
         float* slot = t0 > 0 ? first_slot + warp * S::kPartial : reinterpret_cast<float*>(ring);
         if (!whole && lane == 0)
@@ -592,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_few_kernel(AttendArgs a, 
 // launch, and no tables of the batch's work to build first.
 constexpr int kCluster = 8;
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, kCtas) kv4_unit_kernel(AttendArgs a, int few_rows, bool after)
 {
     using S = Shape<D>;
@@ -616,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) kv4_unit_kernel(AttendArgs a,
     const int t0 = share(rank * kWarps + warp), t1 = share(rank * kWarps + warp + 1);
     if (t0 < t1) {
         Sums<D> o;
-        attend_tiles<D>(a, ring, s, h, q, row0, rows, first_tile(q, a.window) + t0, t1 - t0, o);
+        attend_tiles<D, kTree>(a, ring, s, h, q, row0, rows, first_tile(q, a.window) + t0, t1 - t0, o);
         put<D>(a, h, q, row0, rows, o, reinterpret_cast<float*>(ring));
     }
     __syncthreads();
@@ -679,7 +681,7 @@ constexpr int kUnitTiles = 16;
 constexpr int kMaxSmem = 227 * 1024;
 static_assert(Shape<128>::kSmem + 4 * kMaxSeqs <= kMaxSmem, "shared memory");
 
-template <int D>
+template <int D, bool kTree>
 cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partials* left, cudaStream_t stream)
 {
     using S = Shape<D>;
@@ -690,8 +692,8 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partial
     if (e != cudaSuccess) return e;
     std::atomic<int>& room = clusters[dev & 63];
     e = once_on_device(done, [&] {
-        const cudaError_t f = cudaFuncSetAttribute(kv4_few_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
-        return f == cudaSuccess ? cudaFuncSetAttribute(kv4_unit_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) : f;
+        const cudaError_t f = cudaFuncSetAttribute(kv4_few_kernel<D, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem - 1024);
+        return f == cudaSuccess ? cudaFuncSetAttribute(kv4_unit_kernel<D, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) : f;
     });
     if (e != cudaSuccess) return e;
     const int ctas = std::min(kMaxCtas, device_sms() * kCtas);
@@ -716,20 +718,20 @@ cudaError_t run(const AttendArgs& a, int few_rows, void* ws, bool after, Partial
             one.gridDim = dim3(kCluster);
             one.attrs = attr + 1;
             one.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, kv4_unit_kernel<D>, &one);
+            e = cudaOccupancyMaxActiveClusters(&n, kv4_unit_kernel<D, kTree>, &one);
             if (e != cudaSuccess) return e;
             room = n;
         }
         if (units <= room) {
             left->ctas = 0;
-            e = cudaLaunchKernelEx(&l.cfg, kv4_unit_kernel<D>, a, few_rows, after);
+            e = cudaLaunchKernelEx(&l.cfg, kv4_unit_kernel<D, kTree>, a, few_rows, after);
             note_launch();
             return e;
         }
     }
     PdlLaunch l(dim3(ctas), kThreads, S::kSmem + 4 * a.batch.n_seqs, stream);
     *left = partials_at(ws, ctas, kRows);
-    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D>, a, few_rows, *left, after);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_few_kernel<D, kTree>, a, few_rows, *left, after);
     note_launch();
     return e;
 }
@@ -740,7 +742,8 @@ size_t kv4_few_workspace(int head_dim) { return partials_bytes(kMaxCtas, kRows, 
 
 cudaError_t launch_kv4_few(const AttendArgs& a, int few_rows, void* ws, bool after, Partials* left, cudaStream_t stream)
 {
-    return a.cache.head_dim == 64 ? run<64>(a, few_rows, ws, after, left, stream) : run<128>(a, few_rows, ws, after, left, stream);
+    if (a.tree) return a.cache.head_dim == 64 ? run<64, true>(a, few_rows, ws, after, left, stream) : run<128, true>(a, few_rows, ws, after, left, stream);
+    return a.cache.head_dim == 64 ? run<64, false>(a, few_rows, ws, after, left, stream) : run<128, false>(a, few_rows, ws, after, left, stream);
 }
 
 }  // namespace lora

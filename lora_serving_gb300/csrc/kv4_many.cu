@@ -239,16 +239,19 @@ __device__ __forceinline__ uint32_t bits_in(int lo, int hi)
 
 // 256 query rows of a sequence: its rows [row0, row0 + rows) of positions x
 // heads, the positions of the first and the last, and the tiles they see.
+// (Of a drafted tree's, whose rows may see any of one another: the positions
+// of the sequence's first row and of its last.)
 struct Block {
     int row0, rows, p0, p1, tile0, tiles;
 };
+template <bool kTree>
 __device__ __forceinline__ Block block_at(const Seq& q, int i, int group, int window)
 {
     Block b;
     b.row0 = i * kRowsPerItem;
     b.rows = min(kRowsPerItem, q.n * group - b.row0);
-    b.p0 = q.ctx - q.n + b.row0 / group;
-    b.p1 = q.ctx - q.n + (b.row0 + b.rows - 1) / group;
+    b.p0 = q.ctx - q.n + (kTree ? 0 : b.row0 / group);
+    b.p1 = kTree ? q.ctx - 1 : q.ctx - q.n + (b.row0 + b.rows - 1) / group;
     b.tile0 = seen_from(b.p0, window) / kTok;
     b.tiles = max(1, (max(0, b.p1 + 1) + kTok - 1) / kTok - b.tile0);   // at least one: its rows get their zeros
     return b;
@@ -270,6 +273,21 @@ struct Held : Piece {    // a softmax warp's copy
     int all0, all1;      // all of its tile of rows sees all of these tiles of the piece, [all0, all1)
 };
 
+// A drafted tree's row r of a piece: a bit for each of the 32 positions from j on that it sees.
+__device__ __forceinline__ uint32_t tree_columns(const AttendArgs& a, const Piece& p, int r, int j)
+{
+    const int i = (p.block + r) / (a.n_heads / a.cache.n_kv), n = p.p1 + 1 - p.pos0, at = j - p.pos0;
+    if (p.pos0 + i < 0) return 0;
+    const uint32_t* bits = tree_bits(a, Seq{p.row0, n, p.p1 + 1}, i);
+    uint32_t see = 0;
+    if (at > -32 && at < n) {   // its bits from `at` on: parts of two words
+        auto word = [&](int w) { return w >= 0 && 32 * w < n ? __ldg(bits + w) : 0u; };
+        see = __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31) & bits_in(0, n - at);
+    }
+    if (at < 0) see |= bits_in(a.window > 0 ? tree_depth(bits, n) - a.window + 1 - at : 0, -at);
+    return see;
+}
+
 __device__ __forceinline__ int range_count(int total, int ctas) { return min(ctas, max(1, total / kMinRange)); }
 // total * b / n without leaving 32 bits (n is a number of CTAs)
 __device__ __forceinline__ int range_at(int total, int n, int b)
@@ -287,6 +305,7 @@ struct Place {
 
 // Finds the pieces of a CTA's range.  The line goes by blocks of rows in the
 // order of the sequences, the kv heads of a block one after another.
+template <bool kTree>
 struct Walk : Place {
     const AttendArgs& a;
     const int* prefix;   // blocks before each sequence
@@ -304,7 +323,7 @@ struct Walk : Place {
             do ++s; while (prefix[s] == prefix[s + 1]);
         }
         load_seq(a.batch, s, q, nullptr);
-        b = block_at(q, i, group, a.window);
+        b = block_at<kTree>(q, i, group, a.window);
     }
     // The next piece; the place at which its item ends, 0 after the last.
     __device__ __forceinline__ int next(Piece& p)
@@ -346,7 +365,7 @@ struct Walk : Place {
 };
 constexpr int kMaxCtas = 160;   // CTAs that the workspace has room for
 
-template <int D>
+template <int D, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int few_rows, Partials left)
 {
     using S = Shape<D>;
@@ -420,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
         mine.s = seq_at(prefix, a.batch.n_seqs, f);
         mine.i = f - prefix[mine.s];
         mine.q = seqs[mine.s];
-        mine.b = block_at(mine.q, mine.i, group, a.window);
+        mine.b = block_at<kTree>(mine.q, mine.i, group, a.window);
         return (mine.b.tiles + kItemCost) * a.cache.n_kv;
     };
     scan_seqs<kWarps>(kThreads, cost, sums, [&](int t) {
@@ -456,7 +475,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
         // rows at positions lo..hi see all of tile t
         auto inner = [&](int t, int lo, int hi) {
             const int c = t * kTok;
-            return c + kTok - 1 <= lo && (a.window == 0 || c > hi - a.window);
+            return c + kTok - 1 <= lo - (kTree ? 1 : 0) && (a.window == 0 || c > hi - a.window);
         };
 
         if (warp < kSoftWarps) {
@@ -477,8 +496,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     Held& h = held[warp][i & 1];
                     if (has) {
                         if (lane < kPieceWords) reinterpret_cast<int*>(static_cast<Piece*>(&h))[lane] = reinterpret_cast<const int*>(p)[lane];
-                        const int lo = p->pos0 + (p->block + x * kRowsPerTile) / group;
-                        const int hi = p->pos0 + (p->block + min(p->rows, (x + 1) * kRowsPerTile) - 1) / group;
+                        const int lo = kTree ? p->p0 - 1 : p->pos0 + (p->block + x * kRowsPerTile) / group;
+                        const int hi = kTree ? p->p1 : p->pos0 + (p->block + min(p->rows, (x + 1) * kRowsPerTile) - 1) / group;
                         if (lane == 0) h.all0 = a.window > 0 && hi >= a.window ? (hi - a.window) / kTok + 1 - p->tile0 : 0;
                         if (lane == 0) h.all1 = (max(0, lo + 1)) / kTok - p->tile0;
                     }
@@ -563,7 +582,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     tmem_ld32_start(ts, v[0]);
                     const uint4 hid4 = notes.hidden[note];
                     const bool all = in && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
-                    auto sees = [&](int c) {   // a bit for each of 32 columns that this row sees
+                    auto sees = [&](int c) -> uint32_t {   // a bit for each of 32 columns that this row sees
+                        if (kTree) return rt < pc->rows ? tree_columns(a, *pc, rt, (pc->tile0 + j) * kTok + 32 * c) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c] : 0u;
                         const int c_hi = pc->pos0 + (pc->block + rt) / group + 1 - (pc->tile0 + j) * kTok - 32 * c;
                         return bits_in(a.window > 0 && c_hi > a.window ? c_hi - a.window : 0, c_hi) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c];
                     };
@@ -1022,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                 }
                 if (!ok) failed = 1;
             } else if (warp == kWalkWarp) {
-                Walk walk(a, prefix, first, total / n_ranges, begin, end);
+                Walk<kTree> walk(a, prefix, first, total / n_ranges, begin, end);
                 int tiles[kPieces] = {};   // of the pieces not yet given back
                 for (int i = 0;; ++i) {
                     Piece p;
@@ -1054,18 +1074,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
     if (tid == 0 && failed) flag(a.status, LORA_DEV_TIMEOUT);
 }
 
-template <int D>
+template <int D, bool kTree>
 cudaError_t run(const AttendArgs& a, int few_rows, void* ws, Partials* left, cudaStream_t stream)
 {
     using S = Shape<D>;
     constexpr int kMaxSmem = S::kSmem + 4 * (kMaxSeqs + 1);
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = once_on_device(done, [&] { return cudaFuncSetAttribute(kv4_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem); });
+    cudaError_t e = once_on_device(done, [&] { return cudaFuncSetAttribute(kv4_many_kernel<D, kTree>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem); });
     if (e != cudaSuccess) return e;
     const int ctas = std::min(kMaxCtas, device_sms());
     PdlLaunch l(dim3(ctas), kThreads, S::kSmem + 4 * (a.batch.n_seqs + 1), stream);
     *left = partials_at(ws, ctas, kRowsPerItem);
-    e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D>, a, few_rows, *left);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_many_kernel<D, kTree>, a, few_rows, *left);
     note_launch();
     return e;
 }
@@ -1076,7 +1096,8 @@ size_t kv4_many_workspace(int head_dim) { return partials_bytes(kMaxCtas, kRowsP
 
 cudaError_t launch_kv4_many(const AttendArgs& a, int few_rows, void* ws, Partials* left, cudaStream_t stream)
 {
-    return a.cache.head_dim == 64 ? run<64>(a, few_rows, ws, left, stream) : run<128>(a, few_rows, ws, left, stream);
+    if (a.tree) return a.cache.head_dim == 64 ? run<64, true>(a, few_rows, ws, left, stream) : run<128, true>(a, few_rows, ws, left, stream);
+    return a.cache.head_dim == 64 ? run<64, false>(a, few_rows, ws, left, stream) : run<128, false>(a, few_rows, ws, left, stream);
 }
 
 }  // namespace lora

@@ -1,5 +1,7 @@
 /* pycalls.c -- the Python side of the calls between a decode step's
- * projections: lora_rms_norm, lora_kv4_append, lora_kv4_read, lora_kv4_attend.
+ * projections: lora_rms_norm, lora_kv4_append, lora_kv4_read, lora_kv4_attend,
+ * and of drafted decoding: lora_kv4_plan, lora_kv4_attend_tree, lora_kv4_keep,
+ * lora_logits_adjust.
  *
  * A kernel of 3 us is launched from Python by a call of up to nineteen
  * arguments.  Read and converted by the interpreter one at a time they took
@@ -22,6 +24,10 @@ static __typeof__(&lora_rms_norm) norm_fn;
 static __typeof__(&lora_kv4_append) append_fn;
 static __typeof__(&lora_kv4_read) read_fn;
 static __typeof__(&lora_kv4_attend) attend_fn;
+static __typeof__(&lora_kv4_plan) plan_fn;
+static __typeof__(&lora_kv4_attend_tree) tree_fn;
+static __typeof__(&lora_kv4_keep) keep_fn;
+static __typeof__(&lora_logits_adjust) logits_fn;
 
 static PyObject* call0(PyObject* o, PyObject* method)
 {
@@ -279,13 +285,137 @@ static PyObject* kv4_attend(PyObject* self, PyObject* const* a, Py_ssize_t n)
     CALL(status, attend_fn(out, ld_out, q, ld_q, heads, scale, window, cache, batch, ws, bytes, status_word, stream));
 }
 
-/* ((addresses of lora_rms_norm, lora_kv4_append, lora_kv4_read, lora_kv4_attend), (bf16, fp32, int32, e4m3),
- * current_device, raw_stream) */
+/* A vector of so many adjacent entries of 32 bits at least; None: NULL. */
+static int vector(PyObject* t, const char* name, PyObject* dtype, long count, void** out)
+{
+    long n[3], st;
+    *out = NULL;
+    if (t == Py_None) return 0;
+    if (pointer(t, name, dtype, out)) return -1;
+    const int dims = sizes(t, n);
+    if (dims < 0 || (dims == 1 && strides(t, 1, &st))) return -1;
+    if (dims != 1 || n[0] < count || (st != 1 && n[0] > 1)) {
+        PyErr_Format(PyExc_ValueError, "%s must hold %ld adjacent entries at least", name, count);
+        return -1;
+    }
+    return 0;
+}
+
+/* What store.KV4Plan hands over: the call's arguments but for the lengths. */
+typedef struct {
+    int32_t *q_starts, *ctx_lens, *row_seq, *positions;
+    int64_t* slots;
+    int32_t n_seqs, max_rows, max_q_len, max_ctx_len;
+    lora_kv4_pool_t pool;
+} plan_t;
+
+/* (plan, q_lens, lens, depths, dev_status, stream) */
+static PyObject* kv4_plan(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    void *q, *lens, *depths, *status_word, *stream;
+    if (count(n, 6)) return NULL;
+    const plan_t* p = PyLong_AsVoidPtr(a[0]);
+    if (PyErr_Occurred()) return NULL;
+    if (!p) return PyErr_Format(PyExc_ValueError, "no plan");
+    if (vector(a[1], "q_lens", i32, p->n_seqs, &q) || vector(a[2], "lens", i32, p->n_seqs, &lens) || vector(a[3], "depths", i32, p->max_rows, &depths) ||
+        device(a[4], "dev_status", i32, &status_word) || stream_of(a[5], &stream))
+        return NULL;
+    CALL(status, plan_fn(p->q_starts, p->ctx_lens, p->row_seq, p->positions, p->slots, q, lens, depths, p->n_seqs, p->max_rows, p->max_q_len,
+                         p->max_ctx_len, &p->pool, status_word, stream));
+}
+
+/* (out, q, cache, batch, tree, workspace, n_heads, scale, window, dev_status, stream) */
+static PyObject* kv4_attend_tree(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    const lora_kv4_cache_t* cache;
+    const lora_kv4_batch_t* batch;
+    void *out, *q, *tree, *ws, *status_word, *stream;
+    int ld_out, ld_q, ld_tree, heads, window;
+    if (count(n, 11) || structs(a[2], a[3], &cache, &batch) || as_int(a[6], "n_heads", &heads) || as_int(a[8], "window", &window)) return NULL;
+    const float scale = (float)PyFloat_AsDouble(a[7]);
+    if (PyErr_Occurred()) return NULL;
+    const long width = (long)heads * cache->head_dim;
+    if (matrix(a[0], "out", bf16, batch->n_rows, width, &out, &ld_out) || matrix(a[1], "q", bf16, batch->n_rows, width, &q, &ld_q) ||
+        matrix(a[4], "tree", i32, batch->n_rows, (batch->max_q_len + 31L) / 32, &tree, &ld_tree) || pointer(a[5], "workspace", NULL, &ws))
+        return NULL;
+    if (batch->n_rows == 1 && ld_tree < (batch->max_q_len + 31L) / 32) ld_tree = (int)((batch->max_q_len + 31L) / 32);   /* one row: any stride */
+    PyObject* nb = PyObject_GetAttr(a[5], s_nbytes);
+    if (!nb) return NULL;
+    const size_t bytes = PyLong_AsSize_t(nb);
+    Py_DECREF(nb);
+    if (PyErr_Occurred() || device(a[9], "dev_status", i32, &status_word) || stream_of(a[10], &stream)) return NULL;
+    CALL(status, tree_fn(out, ld_out, q, ld_q, heads, scale, window, tree, ld_tree, cache, batch, ws, bytes, status_word, stream));
+}
+
+/* (caches, n_caches, batch, n_keep, path, lens, dev_status, stream) */
+static PyObject* kv4_keep(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    const lora_kv4_cache_t* caches;
+    const lora_kv4_batch_t* batch;
+    void *keep, *path, *lens, *status_word, *stream;
+    int n_caches, ld_path;
+    if (count(n, 8) || structs(a[0], a[2], &caches, &batch) || as_int(a[1], "n_caches", &n_caches)) return NULL;
+    if (vector(a[3], "n_keep", i32, batch->n_seqs, &keep) || matrix(a[4], "path", i32, batch->n_seqs, 0, &path, &ld_path) ||
+        vector(a[5], "lens", i32, batch->n_seqs, &lens) || device(a[6], "dev_status", i32, &status_word) || stream_of(a[7], &stream))
+        return NULL;
+    /* the entries of a row are its columns, whatever the stride */
+    long s[3];
+    if (sizes(a[4], s) < 0) return NULL;
+    if (batch->n_seqs > 1 && s[1] != ld_path) return PyErr_Format(PyExc_ValueError, "path must be contiguous");
+    CALL(status, keep_fn(caches, n_caches, batch, keep, path, (int)s[1], lens, status_word, stream));
+}
+
+/* Type and sizes of a matrix of logits. */
+static int logits_of(PyObject* t, const char* name, lora_dtype_t* type, void** out, int* ld, long shape[3])
+{
+    PyObject* dtype = PyObject_GetAttr(t, s_dtype);
+    if (!dtype) return -1;
+    *type = dtype == f32 ? LORA_F32 : LORA_BF16;   /* another type is refused as one that is no bf16 */
+    Py_DECREF(dtype);
+    if (sizes(t, shape) < 0) return -1;
+    return matrix(t, name, *type == LORA_F32 ? f32 : bf16, 0, 0, out, ld);
+}
+
+/* (out, logits, rules, row_seq, drafts, tree, q_starts, allowed, allowed_rows, dev_status, stream) */
+static PyObject* logits_adjust(PyObject* self, PyObject* const* a, Py_ssize_t n)
+{
+    void *out, *in, *row_seq, *drafts, *tree, *starts, *allowed, *allowed_rows, *status_word, *stream;
+    int ld_out, ld, ld_tree, ld_allowed, n_allowed = 0;
+    long so[3], si[3], sa[3], st[3];
+    lora_dtype_t type_out, type;
+    if (count(n, 11)) return NULL;
+    const lora_logits_rules_t* rules = PyLong_AsVoidPtr(a[2]);
+    if (PyErr_Occurred()) return NULL;
+    if (logits_of(a[0], "out", &type_out, &out, &ld_out, so) || logits_of(a[1], "logits", &type, &in, &ld, si)) return NULL;
+    if (so[0] != si[0] || so[1] != si[1] || si[0] > INT_MAX || si[1] > INT_MAX)
+        return PyErr_Format(PyExc_ValueError, "out must have the shape of logits, its sizes below 2^31");
+    const long rows = si[0], words = (si[1] + 31) / 32;
+    if (vector(a[3], "row_seq", i32, rows, &row_seq) || vector(a[4], "drafts", i32, rows, &drafts) || matrix(a[5], "tree", i32, rows, 1, &tree, &ld_tree) ||
+        vector(a[6], "q_starts", i32, rules ? rules->n_seqs + 1L : 0, &starts) || matrix(a[7], "allowed", i32, 1, words, &allowed, &ld_allowed) ||
+        vector(a[8], "allowed_rows", i32, rows, &allowed_rows) || device(a[9], "dev_status", i32, &status_word) || stream_of(a[10], &stream))
+        return NULL;
+    if (allowed) {
+        if (sizes(a[7], sa) < 0) return NULL;
+        if (sa[0] > INT_MAX) return PyErr_Format(PyExc_ValueError, "allowed must have less than 2^31 rows");
+        n_allowed = (int)sa[0];
+        if (n_allowed == 1 && ld_allowed < words) ld_allowed = (int)words;   /* one row: any stride */
+    }
+    if (tree) {   /* a row's words are its columns: what lies between rows of a wider buffer is not looked at */
+        if (sizes(a[5], st) < 0) return NULL;
+        if (rows > 1 && st[1] != ld_tree) return PyErr_Format(PyExc_ValueError, "tree must be contiguous");
+        ld_tree = (int)st[1];
+    }
+    CALL(status, logits_fn(out, type_out, ld_out, in, type, ld, (int)rows, (int)si[1], rules, row_seq, drafts, tree, ld_tree, starts, allowed,
+                           ld_allowed, n_allowed, allowed_rows, status_word, stream));
+}
+
+/* ((addresses of lora_rms_norm, lora_kv4_append, lora_kv4_read, lora_kv4_attend, lora_kv4_plan, lora_kv4_attend_tree, lora_kv4_keep,
+ * lora_logits_adjust), (bf16, fp32, int32, e4m3), current_device, raw_stream) */
 static PyObject* bind(PyObject* self, PyObject* args)
 {
-    unsigned long long fn[4];
+    unsigned long long fn[8];
     PyObject* o[6];
-    if (!PyArg_ParseTuple(args, "(KKKK)(OOOO)OO", &fn[0], &fn[1], &fn[2], &fn[3], &o[0], &o[1], &o[2], &o[3], &o[4], &o[5])) return NULL;
+    if (!PyArg_ParseTuple(args, "(KKKKKKKK)(OOOO)OO", &fn[0], &fn[1], &fn[2], &fn[3], &fn[4], &fn[5], &fn[6], &fn[7], &o[0], &o[1], &o[2], &o[3], &o[4], &o[5])) return NULL;
     PyObject** to[6] = {&bf16, &f32, &i32, &e4m3, &current_device, &raw_stream};
     for (int i = 0; i < 6; ++i) {
         Py_INCREF(o[i]);
@@ -295,6 +425,10 @@ static PyObject* bind(PyObject* self, PyObject* args)
     append_fn = (__typeof__(append_fn))(uintptr_t)fn[1];
     read_fn = (__typeof__(read_fn))(uintptr_t)fn[2];
     attend_fn = (__typeof__(attend_fn))(uintptr_t)fn[3];
+    plan_fn = (__typeof__(plan_fn))(uintptr_t)fn[4];
+    tree_fn = (__typeof__(tree_fn))(uintptr_t)fn[5];
+    keep_fn = (__typeof__(keep_fn))(uintptr_t)fn[6];
+    logits_fn = (__typeof__(logits_fn))(uintptr_t)fn[7];
     Py_RETURN_NONE;
 }
 
@@ -304,6 +438,10 @@ static PyMethodDef methods[] = {
     {"kv4_append", (PyCFunction)(void (*)(void))kv4_append, METH_FASTCALL, NULL},
     {"kv4_read", (PyCFunction)(void (*)(void))kv4_read, METH_FASTCALL, NULL},
     {"kv4_attend", (PyCFunction)(void (*)(void))kv4_attend, METH_FASTCALL, NULL},
+    {"kv4_plan", (PyCFunction)(void (*)(void))kv4_plan, METH_FASTCALL, NULL},
+    {"kv4_attend_tree", (PyCFunction)(void (*)(void))kv4_attend_tree, METH_FASTCALL, NULL},
+    {"kv4_keep", (PyCFunction)(void (*)(void))kv4_keep, METH_FASTCALL, NULL},
+    {"logits_adjust", (PyCFunction)(void (*)(void))logits_adjust, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL},
 };
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycalls", NULL, -1, methods, NULL, NULL, NULL, NULL};

@@ -200,6 +200,96 @@ def kv4_workspace(cache: KV4Cache, n_heads: int, batch: KV4Batch, device="cuda")
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+def _vector(t, name: str, dtype: str, n: int) -> int:
+    """Pointer of a device tensor of n adjacent entries at least; 0 for None."""
+    p = abi._dev(t, name, dtype)
+    if t is not None and (t.dim() != 1 or t.numel() < n or (t.numel() > 1 and t.stride(0) != 1)):
+        raise ValueError(f"{name} must hold {n} adjacent entries at least")
+    return p
+
+
+class KV4Plan:
+    """The tables of a server's steps and the pages behind them, for
+    abi.lora_kv4_plan.  Device int32 free_pages [n_pages] (a stack: the first
+    n_free [1] entries), held [n_seqs] and block_table [n_seqs][columns] are the
+    server's own; the counters' results go to them in place, or to n_free_out
+    and held_out, with which a plan can be made again or dropped.  The call
+    fills q_starts, ctx_lens, row_seq, positions [max_rows][1] (what
+    lora_kv4_append takes) and slots, and `batch` is the store.KV4Batch of the
+    step: rows from 0 to max_rows, of which those past the last are skipped."""
+
+    def __init__(self, free_pages, n_free, held, block_table, *, page_size: int, max_rows: int, max_q_len: int,
+                 max_ctx_len: int, n_free_out=None, held_out=None):
+        n_seqs = int(held.numel())
+        dev = held.device
+        self.free_pages, self.n_free, self.held, self.block_table = free_pages, n_free, held, block_table
+        self.n_free_out = n_free if n_free_out is None else n_free_out
+        self.held_out = held if held_out is None else held_out
+        if block_table.dim() != 2 or block_table.shape[0] != n_seqs:
+            raise ValueError(f"block_table must have {n_seqs} rows")
+        new = lambda n, dtype=torch.int32: torch.full((n,), -1, dtype=dtype, device=dev)  # noqa: E731
+        self.q_starts, self.ctx_lens = torch.zeros(n_seqs + 1, dtype=torch.int32, device=dev), torch.zeros(n_seqs, dtype=torch.int32, device=dev)
+        self.row_seq, self.positions, self.slots = new(max_rows), new(max_rows).view(-1, 1), new(max_rows, torch.int64)
+        self.batch = KV4Batch(self.q_starts, self.ctx_lens, block_table, n_rows=max_rows, max_q_len=max_q_len, max_ctx_len=max_ctx_len)
+        pool = abi.lora_kv4_pool_t(_vector(free_pages, "free_pages", "i32", 1), _vector(n_free, "n_free", "i32", 1),
+                                   _vector(held, "held", "i32", n_seqs), _vector(self.n_free_out, "n_free_out", "i32", 1),
+                                   _vector(self.held_out, "held_out", "i32", n_seqs), self.batch.c.block_table,
+                                   self.batch.c.ld_table, int(free_pages.numel()), int(page_size))
+        self.c = abi.plan_args_t(self.q_starts.data_ptr(), self.ctx_lens.data_ptr(), self.row_seq.data_ptr(),
+                                 self.positions.data_ptr(), self.slots.data_ptr(), n_seqs, int(max_rows), int(max_q_len),
+                                 int(max_ctx_len), pool)
+        self.addr = ctypes.addressof(self.c)
+
+    @classmethod
+    def empty(cls, n_seqs: int, n_pages: int, page_size: int, *, max_rows: int, max_q_len: int, max_ctx_len: int, device="cuda"):
+        """Of a cache whose pages are all free and will be taken in their order."""
+        i32 = lambda *a: torch.zeros(*a, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(torch.arange(n_pages - 1, -1, -1, dtype=torch.int32, device=device), i32(1) + n_pages, i32(n_seqs),
+                   i32(n_seqs, -(-max_ctx_len // page_size)) - 1, page_size=page_size, max_rows=max_rows, max_q_len=max_q_len,
+                   max_ctx_len=max_ctx_len)
+
+
+class KV4Layers:
+    """The caches of a model's layers, which one block table serves (abi.lora_kv4_keep)."""
+
+    def __init__(self, caches):
+        self.caches, self.n = list(caches), len(caches)
+        self.c = (abi.lora_kv4_cache_t * max(self.n, 1))(*[c.c for c in self.caches])
+        self.addr = ctypes.addressof(self.c)
+
+
+class LogitsRules:
+    """What requests ask of their logits (abi.lora_logits_adjust): int32 tokens
+    [n_seqs][columns] with prompt_lens and token_lens [n_seqs]; fp32
+    repetition, frequency and presence [n_seqs] or None; int32 bias_ids and fp32
+    bias [n_seqs][columns] with n_bias [n_seqs], or None.  The tensors may be
+    refilled between calls and replays."""
+
+    def __init__(self, tokens, prompt_lens, token_lens, *, repetition=None, frequency=None, presence=None, bias_ids=None,
+                 bias=None, n_bias=None):
+        n = int(token_lens.numel())
+        rows = lambda t, name, dtype: 0 if t is None else self._rows(t, name, dtype, n)  # noqa: E731
+        if (bias_ids is None) != (bias is None) or (bias_ids is None) != (n_bias is None):
+            raise ValueError("bias_ids, bias and n_bias come together")
+        if bias is not None and tuple(bias.shape) != tuple(bias_ids.shape):
+            raise ValueError("bias must have the shape of bias_ids")
+        v = lambda t, name, dtype: _vector(t, name, dtype, n)  # noqa: E731
+        self.keep = (tokens, prompt_lens, token_lens, repetition, frequency, presence, bias_ids, bias, n_bias)
+        self.c = abi.lora_logits_rules_t(rows(tokens, "tokens", "i32"), v(prompt_lens, "prompt_lens", "i32"),
+                                         v(token_lens, "token_lens", "i32"), v(repetition, "repetition", "f32"),
+                                         v(frequency, "frequency", "f32"), v(presence, "presence", "f32"),
+                                         rows(bias_ids, "bias_ids", "i32"), rows(bias, "bias", "f32"), v(n_bias, "n_bias", "i32"),
+                                         int(tokens.shape[1]), 0 if bias is None else int(bias.shape[1]), n)
+        self.addr = ctypes.addressof(self.c)
+
+    @staticmethod
+    def _rows(t, name, dtype, n):
+        p = abi._dev(t, name, dtype, True)
+        if t.shape[0] != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous, with {n} rows")
+        return p
+
+
 def rope_table(max_pos: int, pairs: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """fp32 [max_pos][pairs][2]: (cos, sin) of pos * base^(-i / pairs), angles in fp64."""
     f = base ** (-torch.arange(pairs, dtype=torch.float64) / pairs)
