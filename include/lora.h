@@ -746,7 +746,7 @@ typedef struct {
  * a negative count, an unknown type, drafts without rules, tree or q_starts,
  * n_rows above n_seqs without row_seq, n_rows above n_allowed without
  * allowed_rows, out the same as logits with another type or leading dimension),
- * LORA_ERR_SHAPE (a leading dimension too small, vocab above 2^30, ld_tokens
+ * LORA_ERR_SHAPE (a leading dimension too small, vocab above 2^25, ld_tokens
  * + 32 ld_tree above 2^20 - 1 or ld_bias above 2047, which the counters hold),
  * LORA_ERR_ALIGNMENT, LORA_ERR_CUDA.
  */

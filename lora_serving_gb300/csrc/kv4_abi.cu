@@ -244,7 +244,8 @@ lora_status_t lora_kv4_plan(int32_t* q_starts, int32_t* ctx_lens, int32_t* row_s
                           static_cast<const void*>(pool->held_out), static_cast<const void*>(pool->block_table)})
         if (!aligned(p, 4)) return LORA_ERR_ALIGNMENT;
     if (!aligned(slots, 8)) return LORA_ERR_ALIGNMENT;
-    lora::PlanArgs a{q_starts, ctx_lens, row_seq, positions, slots, q_lens, lens, depths, n_seqs, max_rows, max_q_len, max_ctx_len, *pool, 0, dev_status};
+    lora::PlanArgs a{q_starts, ctx_lens, row_seq, positions, slots, q_lens, lens, depths, n_seqs, max_rows, max_q_len, max_ctx_len, *pool, 0,
+                     aligned(row_seq, 16) && aligned(positions, 16) && aligned(slots, 16), dev_status};
     while ((1 << a.page_shift) < pool->page_size) ++a.page_shift;
     return cuda_status(lora::launch_kv4_plan(a, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -294,7 +295,7 @@ lora_status_t lora_logits_adjust(void* out, lora_dtype_t out_type, int ld_out, c
     constexpr int kCounts = (1 << 20) - 1, kBiases = 2047;   // what a token's counter holds (logits.cu)
     if (n_rows < 0 || vocab <= 0 || (type != LORA_BF16 && type != LORA_F32) || (out_type != LORA_BF16 && out_type != LORA_F32))
         return LORA_ERR_INVALID_ARG;
-    if (vocab > lora::kMaxPositions) return LORA_ERR_SHAPE;
+    if (vocab > 1 << 25) return LORA_ERR_SHAPE;
     if (n_rows == 0) return LORA_OK;
     LORA_TRY(check_matrix(logits, ld, vocab));
     LORA_TRY(check_matrix(out, ld_out, vocab));

@@ -3,13 +3,16 @@
 //
 // Three running sums over the sequences (rows, pages asked for, pages given
 // back) place everything: sequence s takes the stack's entries behind what the
-// sequences before it asked for.  Every CTA of the one cluster computes them
-// for itself, from all lengths, and writes a share of the results; the one
-// barrier between them stands behind the pages given back, since the next are
-// taken from the same stack, and behind the last read of counters that the
-// results may go to in place.  A sequence that asks for more than there is
-// gets nothing, and with it none after it gets any: the sums stay sums, no
-// sequence waiting for another's answer.
+// sequences before it asked for.  Every CTA computes them
+// for itself, from all lengths; rows, pages taken and pages given back are then
+// jobs for any thread, which finds its sequence by a search in a running sum.
+// No job waits for another: a page that was given back and is taken again in
+// the same call is read where it came from.  Where the counters' results go to
+// the place that other CTAs read them from, the CTAs are one cluster, whose one
+// barrier, begun before the sums, stands before these results alone.  A sequence
+// that asks for more than there is gets nothing, and with it none after it gets
+// any: the sums stay sums, no sequence waiting for another's answer.
+// Bound: latency, of a chain of loads, sums over the CTA, a search, and loads.
 #include <algorithm>
 
 #include "kv4.h"
@@ -19,14 +22,15 @@ namespace lora {
 
 namespace {
 
-constexpr int kMaxThreads = 1024, kOwn = kMaxSeqs / kMaxThreads;   // sequences of a thread
+constexpr int kMaxThreads = 1024, kFewThreads = 256, kOwn = 4;     // threads of a CTA; sequences of a thread
+static_assert(kMaxThreads * kOwn >= kMaxSeqs, "every sequence has a thread");
 constexpr int kRun = 4;                                            // neighbouring rows of a thread
 constexpr uint32_t kNoPlace = 0xFFFFFFFFu;
 
 // Sums that stop at their limit: what passes it is refused whatever its size.
 __device__ __forceinline__ uint32_t add_to(uint32_t a, uint32_t b, uint32_t limit) { return min(a + b, limit); }
 
-__global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, int ranks)
+__global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, int ranks, int workers, bool in_place)
 {
     extern __shared__ uint32_t smem[];
     __shared__ uint32_t sums[3][32];
@@ -34,10 +38,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     const int n = a.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int rank = static_cast<int>(blockIdx.x);
     uint32_t* const row_at = smem;               // [n + 1] a sequence's first row
-    uint32_t* const need_at = smem + n + 1;      // [n] pages asked for before it; kNoPlace: it has none
-    uint32_t* const held_s = need_at + n;        // [n]
+    uint32_t* const need_at = row_at + n + 1;    // [n] pages asked for before it
+    uint32_t* const back_at = need_at + n;       // [n] pages given back before it
+    uint32_t* const held_s = back_at + n;        // [n] pages that it held; kNoPlace: it has no place
     int32_t* const stack = a.pool.free_pages;
-    const int per = (n + blockDim.x - 1) / blockDim.x;
+    const int per = (n + blockDim.x - 1) / blockDim.x;   // at most kOwn
     tc::grid_dep_wait();
     tc::grid_dep_launch();
 
@@ -52,6 +57,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
         faults |= LORA_DEV_BAD_PAGE;
         n_free = 0;
     }
+    int q_of[kOwn], len_of[kOwn], held_of[kOwn];   // every load on its way before the first is looked at
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int s = tid * per + i;
+        const bool mine = i < per && s < n;
+        q_of[i] = mine ? __ldg(a.q_lens + s) : 0;
+        len_of[i] = mine ? __ldg(a.lens + s) : 0;
+        held_of[i] = mine ? __ldg(a.pool.held + s) : 0;
+    }
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
         const int s = tid * per + i;
@@ -59,7 +73,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
         ctx[i] = -1;
         held[i] = 0;
         if (i >= per || s >= n) continue;
-        const int q = __ldg(a.q_lens + s), len = __ldg(a.lens + s), h = __ldg(a.pool.held + s);
+        const int q = q_of[i], len = len_of[i], h = held_of[i];
         const bool counts = h >= 0 && h <= a.pool.ld_table;
         held[i] = h;
         if (!counts) faults |= LORA_DEV_BAD_SEGMENT;
@@ -80,6 +94,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
 #pragma unroll
         for (int k = 0; k < 3; ++k) sum[k] = add_to(sum[k], v[i][k], limit[k]);
     }
+    if (in_place) cluster_arrive();   // (waited for at the end)
     // ---- what lies before them
     uint32_t before[3], total[3];
 #pragma unroll
@@ -111,9 +126,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     const uint32_t there = min(static_cast<uint32_t>(n_free) + total[2], static_cast<uint32_t>(a.pool.n_pages));
     if (static_cast<uint32_t>(n_free) + total[2] > there) faults |= LORA_DEV_BAD_PAGE;
 
-    // ---- who gets what; pages given back, a warp to a sequence's
+    // ---- who gets what
     uint32_t at[kOwn][3];
     bool got[kOwn];
+    uint32_t mine_taken = 0;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
         const int s = tid * per + i;
@@ -133,79 +149,113 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
             got[i] = false;
         }
         if (!got[i]) v[i][1] = 0;
-        if (v[i][1] > 0) atomicMax(&taken, before[1]);
+        if (v[i][1] > 0) mine_taken = before[1];
         if (mine) {
             row_at[s] = at[i][0];
-            need_at[s] = got[i] ? at[i][1] : kNoPlace;
-            held_s[s] = held[i];
-        }
-        for (unsigned todo = __ballot_sync(0xFFFFFFFFu, v[i][2] > 0); todo; todo &= todo - 1) {
-            const int who = __ffs(todo) - 1, from = __shfl_sync(0xFFFFFFFFu, s, who);
-            const uint32_t count = __shfl_sync(0xFFFFFFFFu, v[i][2], who), to = n_free + __shfl_sync(0xFFFFFFFFu, at[i][2], who);
-            const int32_t* row = a.pool.block_table + static_cast<long long>(from) * a.pool.ld_table;
-            for (uint32_t j = lane + 32 * ((rank + from) % ranks); j < count; j += 32 * ranks)
-                if (to + j < static_cast<uint32_t>(a.pool.n_pages)) stack[to + j] = row[j];
+            need_at[s] = at[i][1];
+            back_at[s] = at[i][2];
+            held_s[s] = got[i] ? held[i] : kNoPlace;
         }
     }
+    mine_taken = __reduce_max_sync(0xFFFFFFFFu, mine_taken);
+    if (lane == 0 && mine_taken) atomicMax(&taken, mine_taken);
     if (tid == 0) row_at[n] = total[0];
     if (rank == 0 && faults) flag(a.status, faults);
-    cluster_arrive();
-    cluster_wait();
+    __syncthreads();
+    // the last sequence whose running sum is x or less: the one that x falls into, for x below the total
+    auto seq_at = [&](const uint32_t* sum, uint32_t x) {
+        int lo = 0, hi = n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (sum[mid] <= x) lo = mid; else hi = mid - 1;
+        }
+        return lo;
+    };
+    // The f-th page taken: from the stack's top, which is what has been given back, where it still lies.
+    auto page_taken = [&](uint32_t f) -> int {
+        const uint32_t from = there - 1 - f;
+        if (from < static_cast<uint32_t>(n_free)) return __ldg(stack + from);
+        const int s = seq_at(back_at, from - n_free);
+        return __ldg(a.pool.block_table + static_cast<long long>(s) * a.pool.ld_table + (from - n_free - back_at[s]));
+    };
+    const uint32_t n_back = there - n_free, n_taken = taken, runs = a.row_seq || a.positions || a.slots ? (a.max_rows + kRun - 1) / kRun : 0;
+    for (uint32_t job = tid < workers ? rank * workers + tid : 0xFFFFFFFFu; job < runs + n_taken + n_back; job += ranks * workers) {
+        if (job >= runs + n_taken) {   // a page given back: onto the stack
+            const uint32_t f = job - runs - n_taken;
+            const int s = seq_at(back_at, f);
+            stack[n_free + f] = __ldg(a.pool.block_table + static_cast<long long>(s) * a.pool.ld_table + (f - back_at[s]));
+            continue;
+        }
+        if (job >= runs) {   // a page taken: into the table, behind those that the sequence holds
+            const uint32_t f = job - runs;
+            const int s = seq_at(need_at, f);
+            a.pool.block_table[static_cast<long long>(s) * a.pool.ld_table + held_s[s] + (f - need_at[s])] = page_taken(f);
+            continue;
+        }
+        // ---- a run of neighbouring rows: one search for their first
+        const int t0 = kRun * static_cast<int>(job);
+        int lo = seq_at(row_at, t0), seq[kRun], pos[kRun], len[kRun], depth[kRun], page[kRun];
+        long long slot[kRun];
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            const int t = t0 + k;
+            const bool live = t < a.max_rows && static_cast<uint32_t>(t) < total[0];
+            while (live && row_at[lo + 1] <= static_cast<uint32_t>(t)) ++lo;
+            seq[k] = live && held_s[lo] != kNoPlace ? lo : -1;
+            len[k] = seq[k] >= 0 ? __ldg(a.lens + lo) : 0;
+            depth[k] = seq[k] >= 0 && a.depths ? __ldg(a.depths + t) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            page[k] = -1;
+            if (seq[k] < 0) continue;
+            const uint32_t at_page = (len[k] + t0 + k - static_cast<int>(row_at[seq[k]])) >> a.page_shift, h = held_s[seq[k]];
+            if (at_page < h) page[k] = __ldg(a.pool.block_table + static_cast<long long>(seq[k]) * a.pool.ld_table + at_page);
+            else page[k] = page_taken(need_at[seq[k]] + at_page - h);
+        }
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            const int i = t0 + k - (seq[k] >= 0 ? static_cast<int>(row_at[seq[k]]) : 0), d = a.depths ? depth[k] : i;
+            pos[k] = seq[k] >= 0 && d >= 0 && d < a.max_ctx_len ? len[k] + d : -1;
+            slot[k] = static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(a.pool.n_pages)
+                          ? (static_cast<long long>(page[k]) << a.page_shift) + ((len[k] + i) & (a.pool.page_size - 1)) : -1;
+        }
+        if (a.wide && t0 + kRun <= a.max_rows) {
+            if (a.row_seq) *reinterpret_cast<int4*>(a.row_seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
+            if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+            if (a.slots) {
+                *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
+                *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
+                if (t0 + k >= a.max_rows) break;
+                if (a.row_seq) a.row_seq[t0 + k] = seq[k];
+                if (a.positions) a.positions[t0 + k] = pos[k];
+                if (a.slots) a.slots[t0 + k] = slot[k];
+            }
+        }
+    }
 
-    // ---- lengths, and the new pages' table entries
-    const uint32_t rows_cut = static_cast<uint32_t>(a.max_rows);
+    // ---- the sequences' own
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
         const int s = tid * per + i;
         if (i < per && s < n && s % ranks == rank) {
-            a.q_starts[s] = static_cast<int32_t>(min(at[i][0], rows_cut));
+            a.q_starts[s] = static_cast<int32_t>(min(at[i][0], static_cast<uint32_t>(a.max_rows)));
             a.ctx_lens[s] = got[i] ? ctx[i] : 0;
-            a.pool.held_out[s] = held[i] + static_cast<int>(v[i][1]);
         }
-        for (unsigned todo = __ballot_sync(0xFFFFFFFFu, v[i][1] > 0); todo; todo &= todo - 1) {
-            const int who = __ffs(todo) - 1, to = __shfl_sync(0xFFFFFFFFu, s, who), h = __shfl_sync(0xFFFFFFFFu, held[i], who);
-            const uint32_t count = __shfl_sync(0xFFFFFFFFu, v[i][1], who), from = there - 1 - __shfl_sync(0xFFFFFFFFu, at[i][1], who);
-            int32_t* row = a.pool.block_table + static_cast<long long>(to) * a.pool.ld_table + h;
-            for (uint32_t j = lane + 32 * ((rank + to) % ranks); j < count; j += 32 * ranks) row[j] = __ldcg(stack + from - j);
-        }
+    }
+    if (in_place) cluster_wait();   // the other CTAs have read the counters, too, which these are in the place of
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+        const int s = tid * per + i;
+        if (i < per && s < n && s % ranks == rank) a.pool.held_out[s] = held[i] + static_cast<int>(v[i][1]);
     }
     if (rank == 0 && tid == 0) {
-        a.q_starts[n] = static_cast<int32_t>(min(total[0], rows_cut));
-        *a.pool.n_free_out = static_cast<int32_t>(there - taken);
-    }
-
-    // ---- the rows, a run of neighbours to a thread: one search for their first
-    if (!a.row_seq && !a.positions && !a.slots) return;
-    for (int t0 = kRun * (rank * blockDim.x + tid); t0 < a.max_rows; t0 += kRun * ranks * blockDim.x) {
-        int lo = 0, hi = n - 1;   // the last sequence that begins at t0 or before
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (row_at[mid] <= static_cast<uint32_t>(t0)) lo = mid; else hi = mid - 1;
-        }
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            const int t = t0 + k;
-            if (t >= a.max_rows) break;
-            int seq = -1, pos = -1;
-            int64_t slot = -1;
-            if (static_cast<uint32_t>(t) < total[0]) {
-                while (row_at[lo + 1] <= static_cast<uint32_t>(t)) ++lo;
-                if (need_at[lo] != kNoPlace) {
-                    seq = lo;
-                    const int len = __ldg(a.lens + lo), i = t - static_cast<int>(row_at[lo]), p = len + i;
-                    const int depth = a.depths ? __ldg(a.depths + t) : i;
-                    if (depth >= 0 && depth < a.max_ctx_len) pos = len + depth;
-                    const int at_page = p >> a.page_shift, h = static_cast<int>(held_s[lo]);
-                    const int page = at_page < h ? a.pool.block_table[static_cast<long long>(lo) * a.pool.ld_table + at_page]
-                                                 : __ldcg(stack + (there - 1 - need_at[lo] - (at_page - h)));
-                    if (static_cast<uint32_t>(page) < static_cast<uint32_t>(a.pool.n_pages))
-                        slot = (static_cast<int64_t>(page) << a.page_shift) + (p & (a.pool.page_size - 1));
-                }
-            }
-            if (a.row_seq) a.row_seq[t] = seq;
-            if (a.positions) a.positions[t] = pos;
-            if (a.slots) a.slots[t] = slot;
-        }
+        a.q_starts[n] = static_cast<int32_t>(min(total[0], static_cast<uint32_t>(a.max_rows)));
+        *a.pool.n_free_out = static_cast<int32_t>(there - n_taken);
     }
 }
 
@@ -213,21 +263,24 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
 
 cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream)
 {
-    const int smem = 4 * (3 * a.n_seqs + 1);
+    const int smem = 4 * (4 * a.n_seqs + 1);
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (3 * kMaxSeqs + 1)); });
+    cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (4 * kMaxSeqs + 1)); });
     if (e != cudaSuccess) return e;
-    const int threads = a.n_seqs <= 256 && a.max_rows <= 1024 ? 256 : kMaxThreads;
-    const int ranks = a.max_rows > 4096 ? 8 : 1;
+    const int threads = a.n_seqs <= kFewThreads * kOwn ? kFewThreads : kMaxThreads;
+    const bool in_place = a.pool.n_free_out == a.pool.n_free || a.pool.held_out == a.pool.held;
+    const long long jobs = (a.max_rows + kRun - 1ll) / kRun + a.n_seqs;
+    const int workers = in_place ? threads : kFewThreads;   // threads of a CTA that take jobs
+    const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? 8ll : 64ll)));
     PdlLaunch l(dim3(ranks), threads, smem, stream);
     cudaLaunchAttribute attr[2];
     attr[0] = l.attr[0];
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.x = in_place ? ranks : 1;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     l.cfg.attrs = attr;
     l.cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&l.cfg, kv4_plan_kernel, a, ranks);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_plan_kernel, a, ranks, workers, in_place);
     note_launch();
     return e;
 }

@@ -230,3 +230,34 @@ def test_replay_with_refilled_rules():
         g.replay()
         torch.cuda.synchronize()
         _check(out, *_want(d), F32)
+
+
+def test_trees_past_a_thread_block_and_rows_between_others():
+    """Paths of more rows than a block has threads; requests whose rows are not next to each other, some without rules."""
+    V = 3000
+    c = _case(12, [300, 1, 5], V, [200, 10, 50], 4, True, True)
+    c["bits"][0] = [(1 << (i + 1)) - 1 for i in range(300)]        # a chain
+    c["rep"][2], c["freq"][2], c["pres"][2] = 1, 0, 0
+    c["n_bias"][2] = 0                                             # nothing to do for this one
+    rules, kw = _args(c)
+    out = torch.full((306, V), 9.0, dtype=F32, device="cuda")
+    abi.lora_logits_adjust(out, c["x"][:, :V], rules, **kw)
+    _check(out, *_want(c), F32)
+    gaps = torch.full_like(out, 9.0)
+    seq = np.repeat(np.arange(3), c["q"])
+    seq[::2] = -1
+    seq[100:200:3] = -1
+    abi.lora_logits_adjust(gaps, c["x"][:, :V], rules, **{**kw, "row_seq": _i32(seq)})
+    keep = torch.from_numpy(seq >= 0).cuda()
+    assert torch.equal(gaps[keep], out[keep]) and (gaps[~keep] == 9).all()
+    # rows of two requests in turn: each row's own, whatever went before in its block
+    mix = np.arange(16) % 2
+    d = _case(13, [1] * 2, V, [300, 40], 6, False, False)
+    d["x"] = torch.from_numpy(np.random.default_rng(1).standard_normal((16, V)).astype(np.float32)).to(BF).cuda()
+    rules, _ = _args(d)
+    both = torch.empty(16, V, dtype=BF, device="cuda")
+    abi.lora_logits_adjust(both, d["x"], rules, row_seq=_i32(mix))
+    for t in range(16):
+        one = torch.empty(1, V, dtype=BF, device="cuda")
+        abi.lora_logits_adjust(one, d["x"][t:t + 1], rules, row_seq=_i32([mix[t]]))
+        assert torch.equal(one[0], both[t])
