@@ -91,6 +91,14 @@ __device__ __forceinline__ void values(uint32_t w, __half2 step, __half2 low, ui
 // see).  No window and no p take this out of 32 bits: p - window + 1 alone would leave them.
 __device__ __forceinline__ int seen_from(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
 
+// Bits [lo, hi) of 32, whatever the bounds.
+__device__ __forceinline__ uint32_t bits_in(int lo, int hi)
+{
+    const uint32_t below_hi = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+    const uint32_t below_lo = lo >= 32 ? 0xFFFFFFFFu : lo <= 0 ? 0u : (1u << lo) - 1u;
+    return below_hi & ~below_lo;
+}
+
 // ---- rows of drafted trees: they see the positions before their sequence's first row (`base`), and of its rows those
 // that their bits name
 __device__ __forceinline__ const uint32_t* tree_bits(const AttendArgs& a, const Seq& q, int i)
@@ -104,14 +112,20 @@ __device__ __forceinline__ int tree_depth(const uint32_t* bits, int n)
     for (int w = 0; 32 * w < n; ++w) set += __popc(__ldg(bits + w) & (n - 32 * w >= 32 ? 0xFFFFFFFFu : (1u << (n - 32 * w)) - 1u));
     return max(set, 1) - 1;
 }
-// Whether row i of sequence q sees position j.  A row that lies before the first position sees nothing.
-__device__ __forceinline__ bool tree_sees(const AttendArgs& a, const Seq& q, int i, int j)
+// A bit for each of the 32 positions from j on that row i of sequence q sees.  A row that lies before the first position
+// sees nothing.
+__device__ __forceinline__ uint32_t tree_sees32(const AttendArgs& a, const Seq& q, int i, int j)
 {
-    const int base = q.ctx - q.n;
-    if (base + i < 0 || j >= q.ctx) return false;
+    const int n = q.n, base = q.ctx - n, at = j - base;
+    if (base + i < 0) return 0;
     const uint32_t* bits = tree_bits(a, q, i);
-    if (j >= base) return __ldg(bits + ((j - base) >> 5)) >> ((j - base) & 31) & 1u;
-    return a.window == 0 || j > base + tree_depth(bits, q.n) - a.window;
+    uint32_t see = 0;
+    if (at > -32 && at < n) {   // its bits from `at` on: parts of two words
+        auto word = [&](int w) { return w >= 0 && 32 * w < n ? __ldg(bits + w) : 0u; };
+        see = __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31) & bits_in(0, n - at);
+    }
+    if (at < 0) see |= bits_in(a.window > 0 ? tree_depth(bits, n) - a.window + 1 - at : 0, -at);
+    return see;
 }
 
 // Which halves of a (steps, lows) pair have codes whose value is no finite fp16 number: with step and low finite a value

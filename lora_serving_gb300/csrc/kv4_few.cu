@@ -296,8 +296,6 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
     int last[2];   // position of rows 2t, 2t + 1: the last one they see
 #pragma unroll
     for (int c = 0; c < 2; ++c) last[c] = p0 + by_group(a, row0 + 2 * t + c);
-    // in a tree, whether position j is hidden from row 2t + c
-    auto not_seen = [&](int c, int j) { return 2 * t + c >= rows || !tree_sees(a, q, last[c] - p0, j); };
 
     float (&acc)[D / 16][4] = out.acc;
     float (&top)[2] = out.top, (&sum)[2] = out.sum;
@@ -322,6 +320,11 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
 
         const int vg = g * (D / 8) / kGroup;
         bool poison = false;
+        uint32_t see[2];   // of a tree's rows 2t, 2t + 1: the tile's positions that they see
+        if (kTree && !inner) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) see[c] = 2 * t + c < rows ? tree_sees32(a, q, last[c] - p0, j0) : 0u;
+        }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
             // ---- scores
@@ -359,7 +362,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                 sc[c] *= mult[c & 1];
                 if (!inner) {
                     const int j = j0 + kHalf * hf + g + 8 * (c >> 1), p = last[c & 1];
-                    if ((kTree ? not_seen(c & 1, j) : j > p || (a.window > 0 && j <= p - a.window)) || !there) sc[c] = -inf;
+                    if ((kTree ? !(see[c & 1] >> (j - j0) & 1u) : j > p || (a.window > 0 && j <= p - a.window)) || !there) sc[c] = -inf;
                 }
                 up |= sc[c] > top[c & 1] + kSlack;
             }
@@ -437,7 +440,7 @@ __device__ __forceinline__ void attend_tiles(const AttendArgs& a, uint8_t* ring,
                 if (nan == 0.f || j >= q.ctx) continue;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    if (kTree ? not_seen(c, j) : j > last[c] || (a.window > 0 && j <= last[c] - a.window)) continue;
+                    if (kTree ? !(see[c] >> k & 1u) : j > last[c] || (a.window > 0 && j <= last[c] - a.window)) continue;
 #pragma unroll
                     for (int m = 0; m < D / 16; ++m) {
                         acc[m][c] += nan;

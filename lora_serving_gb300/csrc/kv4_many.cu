@@ -229,14 +229,6 @@ struct Notes {
     uint32_t sick[kNotes][kGroups][kTok / 32];
 };
 
-// Bits [lo, hi) of 32, whatever the bounds.
-__device__ __forceinline__ uint32_t bits_in(int lo, int hi)
-{
-    const uint32_t below_hi = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
-    const uint32_t below_lo = lo >= 32 ? 0xFFFFFFFFu : lo <= 0 ? 0u : (1u << lo) - 1u;
-    return below_hi & ~below_lo;
-}
-
 // 256 query rows of a sequence: its rows [row0, row0 + rows) of positions x
 // heads, the positions of the first and the last, and the tiles they see.
 // (Of a drafted tree's, whose rows may see any of one another: the positions
@@ -272,21 +264,6 @@ struct Piece {
 struct Held : Piece {    // a softmax warp's copy
     int all0, all1;      // all of its tile of rows sees all of these tiles of the piece, [all0, all1)
 };
-
-// A drafted tree's row r of a piece: a bit for each of the 32 positions from j on that it sees.
-__device__ __forceinline__ uint32_t tree_columns(const AttendArgs& a, const Piece& p, int r, int j)
-{
-    const int i = (p.block + r) / (a.n_heads / a.cache.n_kv), n = p.p1 + 1 - p.pos0, at = j - p.pos0;
-    if (p.pos0 + i < 0) return 0;
-    const uint32_t* bits = tree_bits(a, Seq{p.row0, n, p.p1 + 1}, i);
-    uint32_t see = 0;
-    if (at > -32 && at < n) {   // its bits from `at` on: parts of two words
-        auto word = [&](int w) { return w >= 0 && 32 * w < n ? __ldg(bits + w) : 0u; };
-        see = __funnelshift_r(word(at >> 5), word((at >> 5) + 1), at & 31) & bits_in(0, n - at);
-    }
-    if (at < 0) see |= bits_in(a.window > 0 ? tree_depth(bits, n) - a.window + 1 - at : 0, -at);
-    return see;
-}
 
 __device__ __forceinline__ int range_count(int total, int ctas) { return min(ctas, max(1, total / kMinRange)); }
 // total * b / n without leaving 32 bits (n is a number of CTAs)
@@ -582,8 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                     tmem_ld32_start(ts, v[0]);
                     const uint4 hid4 = notes.hidden[note];
                     const bool all = in && (hid4.x | hid4.y | hid4.z | hid4.w) == 0;
+                    uint32_t* const see4 = reinterpret_cast<uint32_t*>(mine_s) + 4 * lane;   // a tree's row and masked tile: its bits, where the result will be
                     auto sees = [&](int c) -> uint32_t {   // a bit for each of 32 columns that this row sees
-                        if (kTree) return rt < pc->rows ? tree_columns(a, *pc, rt, (pc->tile0 + j) * kTok + 32 * c) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c] : 0u;
+                        if (kTree) return see4[c];
                         const int c_hi = pc->pos0 + (pc->block + rt) / group + 1 - (pc->tile0 + j) * kTok - 32 * c;
                         return bits_in(a.window > 0 && c_hi > a.window ? c_hi - a.window : 0, c_hi) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c];
                     };
@@ -631,6 +609,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_many_kernel(AttendArgs a, int
                         // A tile that not every row sees all of: the maximum first, then the weights, 32 columns at a
                         // time (few instructions for what is seldom run: they are read from memory when it is).
                         float m[2] = {-inf, -inf};
+                        if (kTree) {
+                            const Seq seq{pc->row0, pc->p1 + 1 - pc->pos0, pc->p1 + 1};
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c)
+                                see4[c] = rt < pc->rows ? tree_sees32(a, seq, (pc->block + rt) / group, (pc->tile0 + j) * kTok + 32 * c) & ~reinterpret_cast<const uint32_t*>(&notes.hidden[note])[c] : 0u;
+                        }
                         tmem_wait_ld();
                         after_wait(v[0]);
 #pragma unroll 1

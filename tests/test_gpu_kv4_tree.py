@@ -69,6 +69,10 @@ CASES = [  # rows of each sequence, positions with them, heads, kv, D, page, win
     ([9, 30], [700, 45], 4, 4, 64, 16, 3),                          # narrower than the trees' depth
     ([64, 50], [1500, 100], 32, 8, 128, 64, 200),
     ([64, 64], [5000, 300], 16, 2, 64, 128, 1),
+    ([16] * 12, [2000 + 37 * i for i in range(12)], 16, 2, 128, 64, 0),   # 128 rows of a kv head: both halves of the SM's tensor memory
+    ([9, 16, 13, 32, 5, 16, 30], [1500, 257, 400, 3000, 129, 128, 140], 32, 4, 128, 64, 0),   # with items of 256 between them
+    ([14] * 9, [700 + 61 * i for i in range(9)], 16, 2, 64, 16, 300),
+    ([12], [9000], 8, 1, 128, 128, 0),                              # one item over many SMs
     ([6], [3], 4, 2, 128, 16, 0),                                   # rows before the first position
     ([60, 70], [30, 0], 8, 1, 128, 16, 20),
 ]
