@@ -17,7 +17,7 @@
 
 #include "lora.h"
 
-static PyObject *s_is_cuda, *s_dtype, *s_device, *s_shape, *s_stride, *s_data_ptr, *s_nbytes, *s_is_contiguous, *s_cuda_stream;
+static PyObject *s_is_cuda, *s_dtype, *s_device, *s_shape, *s_stride, *s_data_ptr, *s_nbytes, *s_is_contiguous, *s_cuda_stream, *s_numel;
 static PyObject *bf16, *f32, *i32, *e4m3;      /* torch's dtype objects */
 static PyObject *current_device, *raw_stream;  /* () -> device index; (device index) -> stream handle */
 static __typeof__(&lora_rms_norm) norm_fn;
@@ -285,20 +285,20 @@ static PyObject* kv4_attend(PyObject* self, PyObject* const* a, Py_ssize_t n)
     CALL(status, attend_fn(out, ld_out, q, ld_q, heads, scale, window, cache, batch, ws, bytes, status_word, stream));
 }
 
-/* A vector of so many adjacent entries of 32 bits at least; None: NULL. */
+/* So many adjacent entries at least, of a contiguous tensor of this element type; None: NULL.  (Two attributes that are
+ * cheaper than sizes and strides: a call may have six such tensors.) */
 static int vector(PyObject* t, const char* name, PyObject* dtype, long count, void** out)
 {
-    long n[3], st;
     *out = NULL;
     if (t == Py_None) return 0;
     if (pointer(t, name, dtype, out)) return -1;
-    const int dims = sizes(t, n);
-    if (dims < 0 || (dims == 1 && strides(t, 1, &st))) return -1;
-    if (dims != 1 || n[0] < count || (st != 1 && n[0] > 1)) {
-        PyErr_Format(PyExc_ValueError, "%s must hold %ld adjacent entries at least", name, count);
-        return -1;
-    }
-    return 0;
+    PyObject *n = call0(t, s_numel), *c = n ? call0(t, s_is_contiguous) : NULL;
+    const long has = c ? PyLong_AsLong(n) : 0;
+    const int ok = c && !PyErr_Occurred() && c == Py_True && has >= count;
+    Py_XDECREF(n);
+    Py_XDECREF(c);
+    if (!ok && !PyErr_Occurred()) PyErr_Format(PyExc_ValueError, "%s must hold %ld adjacent entries at least", name, count);
+    return ok ? 0 : -1;
 }
 
 /* What store.KV4Plan hands over: the call's arguments but for the lengths. */
@@ -448,9 +448,9 @@ static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycalls", NULL, -1,
 
 PyMODINIT_FUNC PyInit__pycalls(void)
 {
-    PyObject** names[] = {&s_is_cuda, &s_dtype, &s_device, &s_shape, &s_stride, &s_data_ptr, &s_nbytes, &s_is_contiguous, &s_cuda_stream};
-    const char* text[] = {"is_cuda", "dtype", "device", "shape", "stride", "data_ptr", "nbytes", "is_contiguous", "cuda_stream"};
-    for (int i = 0; i < 9; ++i)
+    PyObject** names[] = {&s_is_cuda, &s_dtype, &s_device, &s_shape, &s_stride, &s_data_ptr, &s_nbytes, &s_is_contiguous, &s_cuda_stream, &s_numel};
+    const char* text[] = {"is_cuda", "dtype", "device", "shape", "stride", "data_ptr", "nbytes", "is_contiguous", "cuda_stream", "numel"};
+    for (int i = 0; i < 10; ++i)
         if (!*names[i] && !(*names[i] = PyUnicode_InternFromString(text[i]))) return NULL;
     return PyModule_Create(&module);
 }
