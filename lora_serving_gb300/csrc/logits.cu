@@ -18,7 +18,8 @@
 // warp without rules) and the start of a CTA's first row: tables, tokens,
 // counts, 4 us, which few CTAs are there to hide.  Measured: 512 rows of 128256
 // tokens in trees of 32, bf16, masks and penalties 60 us (263 MB, 0.66 of a
-// copy's rate; with masks alone 48), 64 rows to fp32 16.7 (50 MB; 12.2).
+// copy's rate; with masks alone 44), 64 rows to fp32 15.3 (50 MB; 12.1), one row
+// of 32000 tokens 1.7, start to start.
 #include <algorithm>
 
 #include "kv4.h"
@@ -34,10 +35,12 @@ constexpr int kBiasShift = 21;
 constexpr int kBlock = 256;  // neighbouring tokens of a chunk: a warp's vectors
 constexpr int kAtOnce = 8;   // of a request's tokens, that a thread has on their way
 constexpr int kRows = 4;     // of a CTA, at most
-// CTAs with one vector to a thread, per SM, up to which a call is small: 4 rows of 128256 tokens 3.6 us (4.4 in larger
-// chunks), 8 rows 5.6 (6.3), but 16 rows 9.2 (7.9).
+// CTAs with one vector to a thread, per SM, up to which a call is small: 4 rows of 128256 tokens 3.3 us (4.4 in larger
+// chunks), 8 rows 4.8 (6.3), but 16 rows 9.2 (7.2).
 constexpr int kSmall = 4;
-constexpr int kCtas = 3;     // on an SM: 80 registers a thread, for the vectors on their way
+// On an SM: 80 registers a thread, for the vectors on their way.  Measured (us, 64 / 256 rows of 128256 tokens, no drafts; CTAs
+// and vectors): 3 and 5 15.2 / 45.3, 4 and 5 16.3 / 45.6, 4 and 4 16.2 / 48.0, 5 and 3 17.0 / 54.2.
+constexpr int kCtas = 3;
 constexpr int kVecs16 = 5;   // vectors of a thread and row; of fp32 logits, which are twice as long, 2
 
 template <bool F32>
@@ -182,7 +185,8 @@ struct Shape {
     static constexpr int kSmem = kChunk * 4 + kChunk / 8;       // words, and a bit to each
 };
 
-template <bool IN32, bool OUT32, int kVecs>
+// kDrafts: rows of drafted trees, which share a request's counts; without them a CTA has one row.
+template <bool IN32, bool OUT32, int kVecs, bool kDrafts>
 __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsArgs a, int rows_each, int chunks, uint32_t magic)
 {
     using S = Shape<kVecs>;
@@ -192,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
     const int tid = threadIdx.x, lane = tid & 31;
     const int group = blockIdx.x / chunks, x = blockIdx.x - group * chunks;
     const int place = ((tid >> 5) + x) % kWarps;        // the warp's blocks: the dense first ones go to another scheduler in every CTA
-    const int t_begin = group * rows_each, t_end = min(a.n_rows, t_begin + rows_each);
+    const int t_begin = group * rows_each, t_end = kDrafts ? min(a.n_rows, t_begin + rows_each) : t_begin + 1;
     const bool rules = a.rules.tokens != nullptr;
     auto clear = [&] {
         for (int i = tid; i < S::kSmem / 16; i += kThreads) reinterpret_cast<uint4*>(words)[i] = make_uint4(0, 0, 0, 0);
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
         next.seq = a.row_seq ? __ldg(a.row_seq + t) : t;
         next.set = !a.allowed ? -1 : a.allowed_rows ? __ldg(a.allowed_rows + t) : t;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) next.bits[i] = a.drafts && i < a.ld_tree ? __ldg(a.tree + static_cast<long long>(t) * a.ld_tree + i) : 0;
+        for (int i = 0; i < 2; ++i) next.bits[i] = kDrafts && i < a.ld_tree ? __ldg(a.tree + static_cast<long long>(t) * a.ld_tree + i) : 0;
     };
     fetch_row(t_begin);
     {
@@ -245,18 +249,27 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
         for (int k = 0; k < kVecs; ++k) fetch(k, in_row(t_begin), mask);
     }
     int counted = -1;              // the request whose words these are
-    Request r = request_of(a, next.seq);
+    Request r{};
     int mine[2] = {-1, -1};        // words of the lane's drafted tokens (of the first 64) that are in the warp's blocks
     for (int t = t_begin; t < t_end; ++t) {
         const Row row = next;
         const int s = row.seq;
         if (t + 1 < t_end) fetch_row(t + 1);
         if (s != counted) {
-            if (t > t_begin) r = request_of(a, s);
             counted = s;
+            // its first tokens and biases on their way with its lengths, which say later how many of them count
+            const int32_t* const tokens = a.rules.tokens + static_cast<long long>(s) * a.rules.ld_tokens;
+            const int32_t* const ids = a.rules.bias_ids + static_cast<long long>(s) * a.rules.ld_bias;
+            // (registers that rows which follow need for their vectors: 512 rows in trees 60 us, 64 with this)
+            const bool known = !kDrafts && rules && s >= 0 && s < a.rules.n_seqs;
+            int early[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) early[k] = known && tid + k * kThreads < a.rules.ld_tokens ? __ldg(tokens + tid + k * kThreads) : -1;
+            const int early_id = known && a.rules.bias_ids && tid < a.rules.ld_bias ? __ldg(ids + tid) : -1;
+            r = request_of(a, s);
             mine[0] = mine[1] = -1;
             if (!r.plain) {
-                if (a.drafts) {
+                if (kDrafts) {
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         if (lane + 32 * i < r.end - r.first) mine[i] = own_word(__ldg(a.drafts + r.first + lane + 32 * i));
@@ -268,19 +281,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
                 }
                 clean = false;
                 if (r.biases) {
-                    const int32_t* ids = a.rules.bias_ids + static_cast<long long>(s) * a.rules.ld_bias;
                     for (int i = tid; i < r.biases; i += kThreads) {
-                        const int w = word_of(__ldg(ids + i));
+                        const int w = word_of(!kDrafts && i < kThreads ? early_id : __ldg(ids + i));
                         if (w >= 0 && atomicMax(words + w, static_cast<uint32_t>(i + 1) << kBiasShift) == 0) note(w);
                     }
                     __syncthreads();   // counts go on top of the largest
                 }
                 if (r.counts) {
-                    const int32_t* tokens = a.rules.tokens + static_cast<long long>(s) * a.rules.ld_tokens;
                     for (int i0 = tid; i0 < r.len; i0 += kAtOnce * kThreads) {
                         int id[kAtOnce];
 #pragma unroll
-                        for (int k = 0; k < kAtOnce; ++k) id[k] = i0 + k * kThreads < r.len ? __ldg(tokens + i0 + k * kThreads) : -1;
+                        for (int k = 0; k < kAtOnce; ++k) id[k] = i0 + k * kThreads >= r.len ? -1 : !kDrafts && i0 < kAtOnce * kThreads ? early[k] : __ldg(tokens + i0 + k * kThreads);
 #pragma unroll
                         for (int k = 0; k < kAtOnce; ++k) {
                             const int w = word_of(id[k]);
@@ -297,12 +308,12 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
             flag(status, LORA_DEV_SLOT_OUT_OF_RANGE);
             live = false;
         }
-        if (live && (!r.ok || (a.drafts && (t < r.first || t >= r.end)))) {
+        if (live && (!r.ok || (kDrafts && (t < r.first || t >= r.end)))) {
             flag(status, LORA_DEV_BAD_SEGMENT);
             live = false;
         }
         // ---- the row's path, every warp those of its tokens that are in its blocks (no other looks at them)
-        const int n_path = !live || r.plain || !a.drafts ? 0 : min(r.end - r.first, 32 * a.ld_tree);
+        const int n_path = !kDrafts || !live || r.plain ? 0 : min(r.end - r.first, 32 * a.ld_tree);
         auto path = [&](auto each) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -352,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
     }
 }
 
-template <bool IN32, bool OUT32, int kVecs>
+template <bool IN32, bool OUT32, int kVecs, bool kDrafts>
 cudaError_t run(const LogitsArgs& a, cudaStream_t stream)
 {
     using S = Shape<kVecs>;
@@ -360,11 +371,11 @@ cudaError_t run(const LogitsArgs& a, cudaStream_t stream)
     // Rows of a drafted tree to a CTA, that share its counts, as long as the CTAs fill the SMs.  Measured (us, 16 trees of
     // 32 rows, 128256 tokens; 3 waves of CTAs with 4 rows): 1 row 95, 4 rows 59.7, 8 rows 68.
     int rows_each = 1;
-    while (a.drafts && rows_each < kRows && static_cast<long long>(chunks) * ((a.n_rows + 2 * rows_each - 1) / (2 * rows_each)) >= kCtas * device_sms()) rows_each *= 2;
+    while (kDrafts && rows_each < kRows && static_cast<long long>(chunks) * ((a.n_rows + 2 * rows_each - 1) / (2 * rows_each)) >= kCtas * device_sms()) rows_each *= 2;
     const long long ctas = static_cast<long long>(chunks) * ((a.n_rows + rows_each - 1) / rows_each);
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     PdlLaunch l(dim3(static_cast<unsigned>(ctas)), kThreads, a.rules.tokens ? S::kSmem : 0, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, logits_adjust_kernel<IN32, OUT32, kVecs>, a, rows_each, chunks, chunks > 1 ? static_cast<uint32_t>((1ull << 32) / chunks + 1) : 0);
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, logits_adjust_kernel<IN32, OUT32, kVecs, kDrafts>, a, rows_each, chunks, chunks > 1 ? static_cast<uint32_t>((1ull << 32) / chunks + 1) : 0);
     note_launch();
     return e;
 }
@@ -374,7 +385,9 @@ cudaError_t pick(const LogitsArgs& a, cudaStream_t stream)
 {
     // Small calls want their chunks on as many SMs as there are.
     const long long ctas = static_cast<long long>(a.n_rows) * ((a.vocab + 8 * kThreads - 1) / (8 * kThreads));
-    return ctas < kSmall * device_sms() ? run<IN32, OUT32, 1>(a, stream) : run<IN32, OUT32, IN32 ? kVecs16 / 2 : kVecs16>(a, stream);
+    constexpr int kVecs = IN32 ? kVecs16 / 2 : kVecs16;
+    if (ctas < kSmall * device_sms()) return a.drafts ? run<IN32, OUT32, 1, true>(a, stream) : run<IN32, OUT32, 1, false>(a, stream);
+    return a.drafts ? run<IN32, OUT32, kVecs, true>(a, stream) : run<IN32, OUT32, kVecs, false>(a, stream);
 }
 
 }  // namespace
