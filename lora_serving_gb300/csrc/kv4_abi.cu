@@ -256,6 +256,7 @@ lora_status_t lora_kv4_keep(const lora_kv4_cache_t* caches, int n_caches, const 
 {
     if (n_caches < 0 || (n_caches > 0 && !caches)) return LORA_ERR_INVALID_ARG;
     lora::KeepArgs a{};
+    uint64_t seen[4] = {};
     for (int i = 0; i < n_caches; ++i) {
         lora::kv4::Cache c{};
         LORA_TRY(check_cache(caches + i, c));
@@ -263,8 +264,12 @@ lora_status_t lora_kv4_keep(const lora_kv4_cache_t* caches, int n_caches, const 
             a.cache = c;
             LORA_TRY(check_batch(batch, c, a.batch));
         }
-        for (int k = 0; k < i; ++k)
-            if (caches[k].pages == c.pages) return LORA_ERR_INVALID_ARG;   // two launches' worth of moves in one place
+        // the same pages twice would be moved twice: a bit for each of 256 classes of pointers, and a look at the others where it is set
+        const unsigned bit = static_cast<unsigned>((reinterpret_cast<uintptr_t>(c.pages) >> 8) * 0x9E3779B97F4A7C15ull >> 56);
+        if (seen[bit >> 6] >> (bit & 63) & 1u)
+            for (int k = 0; k < i; ++k)
+                if (caches[k].pages == c.pages) return LORA_ERR_INVALID_ARG;
+        seen[bit >> 6] |= 1ull << (bit & 63);
         if (c.page_size != a.cache.page_size || c.n_kv != a.cache.n_kv || c.head_dim != a.cache.head_dim) return LORA_ERR_SHAPE;
     }
     if (n_caches == 0 || batch->n_seqs == 0) return LORA_OK;

@@ -46,15 +46,16 @@ static int as_int(PyObject* o, const char* name, int* out)
     return 0;
 }
 
-/* Pointer of a CUDA tensor of this element type (NULL: any). */
-static int pointer(PyObject* t, const char* name, PyObject* want, void** out)
+/* Pointer of a CUDA tensor of one of two element types (want NULL: any); which of them in `second` where there are two. */
+static int pointer_of(PyObject* t, const char* name, PyObject* want, PyObject* other, int* second, void** out)
 {
     PyObject *cuda = PyObject_GetAttr(t, s_is_cuda), *dtype = NULL, *p;
     if (!cuda) return -1;
     const int is_cuda = cuda == Py_True;
     Py_DECREF(cuda);
     if (!(dtype = PyObject_GetAttr(t, s_dtype))) return -1;
-    if (!is_cuda || (want && dtype != want)) {
+    if (second) *second = dtype == other;
+    if (!is_cuda || (want && dtype != want && dtype != other)) {
         PyObject* device = PyObject_GetAttr(t, s_device);
         if (device && want) PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor of %S, got %S on %S", name, want, dtype, device);
         else if (device) PyErr_Format(PyExc_ValueError, "%s must be a CUDA tensor, got one on %S", name, device);
@@ -68,6 +69,9 @@ static int pointer(PyObject* t, const char* name, PyObject* want, void** out)
     Py_DECREF(p);
     return PyErr_Occurred() ? -1 : 0;
 }
+
+/* ... of this one. */
+static int pointer(PyObject* t, const char* name, PyObject* want, void** out) { return pointer_of(t, name, want, want, NULL, out); }
 
 /* A tensor's sizes: how many dimensions, the first three of them in `out`; -1 with an error. */
 static int sizes(PyObject* t, long out[3])
@@ -100,16 +104,17 @@ static int strides(PyObject* t, int n, long* out)
     return PyErr_Occurred() ? -1 : 0;
 }
 
-/* Pointer and leading dimension of a row-major operand: a CUDA tensor of this
- * element type with so many rows and columns at least and unit column
- * stride; its sizes in `shape` where asked for.  None: (NULL, 0). */
-static int matrix(PyObject* t, const char* name, PyObject* dtype, long rows, long cols, void** out, int* ld)
+/* Pointer and leading dimension of a row-major operand: a CUDA tensor of
+ * one of two element types (which of them in `second`) with so many rows and
+ * columns at least and unit column stride; its sizes in `n`. */
+static int matrix_of(PyObject* t, const char* name, PyObject* dtype, PyObject* other, int* second, long rows, long cols, void** out, int* ld, long n[3])
 {
-    long n[3], st[2];
+    long st[2];
     *out = NULL;
     *ld = 0;
+    n[0] = n[1] = 0;
     if (t == Py_None) return 0;
-    if (pointer(t, name, dtype, out)) return -1;
+    if (pointer_of(t, name, dtype, other, second, out)) return -1;
     const int dims = sizes(t, n);
     if (dims < 0) return -1;
     if (dims != 2 || n[0] < rows || n[1] < cols) {
@@ -123,6 +128,13 @@ static int matrix(PyObject* t, const char* name, PyObject* dtype, long rows, lon
     }
     *ld = (int)st[0];
     return 0;
+}
+
+/* ... of this one.  None: (NULL, 0). */
+static int matrix(PyObject* t, const char* name, PyObject* dtype, long rows, long cols, void** out, int* ld)
+{
+    long n[3];
+    return matrix_of(t, name, dtype, dtype, NULL, rows, cols, out, ld, n);
 }
 
 /* A tensor, a raw pointer as an integer, or None. */
@@ -354,26 +366,13 @@ static PyObject* kv4_keep(PyObject* self, PyObject* const* a, Py_ssize_t n)
     const lora_kv4_batch_t* batch;
     void *keep, *path, *lens, *status_word, *stream;
     int n_caches, ld_path;
+    long s[3];
     if (count(n, 8) || structs(a[0], a[2], &caches, &batch) || as_int(a[1], "n_caches", &n_caches)) return NULL;
-    if (vector(a[3], "n_keep", i32, batch->n_seqs, &keep) || matrix(a[4], "path", i32, batch->n_seqs, 0, &path, &ld_path) ||
+    if (vector(a[3], "n_keep", i32, batch->n_seqs, &keep) || matrix_of(a[4], "path", i32, i32, NULL, batch->n_seqs, 0, &path, &ld_path, s) ||
         vector(a[5], "lens", i32, batch->n_seqs, &lens) || device(a[6], "dev_status", i32, &status_word) || stream_of(a[7], &stream))
         return NULL;
-    /* the entries of a row are its columns, whatever the stride */
-    long s[3];
-    if (sizes(a[4], s) < 0) return NULL;
-    if (batch->n_seqs > 1 && s[1] != ld_path) return PyErr_Format(PyExc_ValueError, "path must be contiguous");
+    if (batch->n_seqs > 1 && s[1] != ld_path) return PyErr_Format(PyExc_ValueError, "path must be contiguous");   /* a row's entries are its columns */
     CALL(status, keep_fn(caches, n_caches, batch, keep, path, (int)s[1], lens, status_word, stream));
-}
-
-/* Type and sizes of a matrix of logits. */
-static int logits_of(PyObject* t, const char* name, lora_dtype_t* type, void** out, int* ld, long shape[3])
-{
-    PyObject* dtype = PyObject_GetAttr(t, s_dtype);
-    if (!dtype) return -1;
-    *type = dtype == f32 ? LORA_F32 : LORA_BF16;   /* another type is refused as one that is no bf16 */
-    Py_DECREF(dtype);
-    if (sizes(t, shape) < 0) return -1;
-    return matrix(t, name, *type == LORA_F32 ? f32 : bf16, 0, 0, out, ld);
 }
 
 /* (out, logits, rules, row_seq, drafts, tree, q_starts, allowed, allowed_rows, dev_status, stream) */
@@ -382,30 +381,30 @@ static PyObject* logits_adjust(PyObject* self, PyObject* const* a, Py_ssize_t n)
     void *out, *in, *row_seq, *drafts, *tree, *starts, *allowed, *allowed_rows, *status_word, *stream;
     int ld_out, ld, ld_tree, ld_allowed, n_allowed = 0;
     long so[3], si[3], sa[3], st[3];
-    lora_dtype_t type_out, type;
+    int out_f32 = 0, in_f32 = 0;
     if (count(n, 11)) return NULL;
     const lora_logits_rules_t* rules = PyLong_AsVoidPtr(a[2]);
     if (PyErr_Occurred()) return NULL;
-    if (logits_of(a[0], "out", &type_out, &out, &ld_out, so) || logits_of(a[1], "logits", &type, &in, &ld, si)) return NULL;
+    if (matrix_of(a[0], "out", bf16, f32, &out_f32, 0, 0, &out, &ld_out, so) || matrix_of(a[1], "logits", bf16, f32, &in_f32, 0, 0, &in, &ld, si)) return NULL;
     if (so[0] != si[0] || so[1] != si[1] || si[0] > INT_MAX || si[1] > INT_MAX)
         return PyErr_Format(PyExc_ValueError, "out must have the shape of logits, its sizes below 2^31");
     const long rows = si[0], words = (si[1] + 31) / 32;
-    if (vector(a[3], "row_seq", i32, rows, &row_seq) || vector(a[4], "drafts", i32, rows, &drafts) || matrix(a[5], "tree", i32, rows, 1, &tree, &ld_tree) ||
-        vector(a[6], "q_starts", i32, rules ? rules->n_seqs + 1L : 0, &starts) || matrix(a[7], "allowed", i32, 1, words, &allowed, &ld_allowed) ||
+    if (vector(a[3], "row_seq", i32, rows, &row_seq) || vector(a[4], "drafts", i32, rows, &drafts) ||
+        matrix_of(a[5], "tree", i32, i32, NULL, rows, 1, &tree, &ld_tree, st) ||
+        vector(a[6], "q_starts", i32, rules ? rules->n_seqs + 1L : 0, &starts) ||
+        matrix_of(a[7], "allowed", i32, i32, NULL, 1, words, &allowed, &ld_allowed, sa) ||
         vector(a[8], "allowed_rows", i32, rows, &allowed_rows) || device(a[9], "dev_status", i32, &status_word) || stream_of(a[10], &stream))
         return NULL;
     if (allowed) {
-        if (sizes(a[7], sa) < 0) return NULL;
         if (sa[0] > INT_MAX) return PyErr_Format(PyExc_ValueError, "allowed must have less than 2^31 rows");
         n_allowed = (int)sa[0];
         if (n_allowed == 1 && ld_allowed < words) ld_allowed = (int)words;   /* one row: any stride */
     }
     if (tree) {   /* a row's words are its columns: what lies between rows of a wider buffer is not looked at */
-        if (sizes(a[5], st) < 0) return NULL;
         if (rows > 1 && st[1] != ld_tree) return PyErr_Format(PyExc_ValueError, "tree must be contiguous");
         ld_tree = (int)st[1];
     }
-    CALL(status, logits_fn(out, type_out, ld_out, in, type, ld, (int)rows, (int)si[1], rules, row_seq, drafts, tree, ld_tree, starts, allowed,
+    CALL(status, logits_fn(out, out_f32 ? LORA_F32 : LORA_BF16, ld_out, in, in_f32 ? LORA_F32 : LORA_BF16, ld, (int)rows, (int)si[1], rules, row_seq, drafts, tree, ld_tree, starts, allowed,
                            ld_allowed, n_allowed, allowed_rows, status_word, stream));
 }
 
