@@ -27,6 +27,9 @@
 // A warp copies its own tiles ahead with cp.async into a ring of its own and
 // meets no other warp until its range ends.
 //
+// Drafted trees (kTree) differ in tiles that reach past the sequence's first
+// row: a row's 32 bits of such a tile come from its words at once.
+//
 // What bounds it.  HBM by its bytes, but the unpacking takes longer: 8 requests of
 // 131072 positions, 64 heads in groups of 8, 231 us, 5.2 TB/s, 0.78 of a copy's
 // rate, an issue slot in 0.63; without V's unpacking 197 us, without K's 220.

@@ -12,7 +12,8 @@
 // path[i] > i on.
 // Bound: latency, of the tables (path, pages) and then of the positions
 // themselves, 144 bytes in four places; beyond that the half words of V, which
-// DRAM fetches and writes by sectors.
+// DRAM fetches and writes by sectors.  Measured, start to start: 64 requests in
+// 32 layers (14 MB) 9.8 us, a fifth of a copy's rate; one request in 28 layers 2.7.
 #include <algorithm>
 
 #include "kv4.h"

@@ -3,16 +3,20 @@
 //
 // Three running sums over the sequences (rows, pages asked for, pages given
 // back) place everything: sequence s takes the stack's entries behind what the
-// sequences before it asked for.  Every CTA computes them
-// for itself, from all lengths; rows, pages taken and pages given back are then
-// jobs for any thread, which finds its sequence by a search in a running sum.
-// No job waits for another: a page that was given back and is taken again in
-// the same call is read where it came from.  Where the counters' results go to
+// sequences before it asked for.  Every CTA computes them for itself, from all
+// lengths; rows, pages taken and pages given back are then jobs for any thread,
+// which finds its sequence by a search in a running sum.  (A warp that went
+// through its sequences one after another took 20 us for 4096 of them.)  No job
+// waits for another: a page that was given back and is taken again in the same
+// call is read where it came from.  Where the counters' results go to
 // the place that other CTAs read them from, the CTAs are one cluster, whose one
 // barrier, begun before the sums, stands before these results alone.  A sequence
 // that asks for more than there is gets nothing, and with it none after it gets
 // any: the sums stay sums, no sequence waiting for another's answer.
-// Bound: latency, of a chain of loads, sums over the CTA, a search, and loads.
+// Bound: latency, of a chain of loads, sums over the CTA, a search, and loads;
+// with thousands of sequences the sums' instructions, which every CTA repeats.
+// Measured, start to start: 64 requests of a token 4.4 us, 256 with 16 prompts
+// among them (17 k rows) 6.2 (7.3 with the counters in place), 4096 trees 11.8.
 #include <algorithm>
 
 #include "kv4.h"
@@ -270,7 +274,9 @@ cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream)
     const int threads = a.n_seqs <= kFewThreads * kOwn ? kFewThreads : kMaxThreads;
     const bool in_place = a.pool.n_free_out == a.pool.n_free || a.pool.held_out == a.pool.held;
     const long long jobs = (a.max_rows + kRun - 1ll) / kRun + a.n_seqs;
-    const int workers = in_place ? threads : kFewThreads;   // threads of a CTA that take jobs
+    // Threads of a CTA that take jobs: 256 of each where there may be any number of CTAs (us, 4096 sequences: 11.8 with 64 to 512,
+    // 12.9 with 1024), all in a cluster.
+    const int workers = in_place ? threads : kFewThreads;
     const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? 8ll : 64ll)));
     PdlLaunch l(dim3(ranks), threads, smem, stream);
     cudaLaunchAttribute attr[2];
