@@ -15,8 +15,8 @@
 // any: the sums stay sums, no sequence waiting for another's answer.
 // Bound: latency, of a chain of loads, sums over the CTA, a search, and loads;
 // with thousands of sequences the sums' instructions, which every CTA repeats.
-// Measured, start to start: 64 requests of a token 4.4 us, 256 with 16 prompts
-// among them (17 k rows) 6.2 (7.3 with the counters in place), 4096 trees 11.8.
+// Measured, start to start: 64 requests of a token 2.8 us, 256 with 16 prompts
+// among them (17 k rows) 3.9 (6.4 with the counters in place), 4096 trees 10.5.
 #include <algorithm>
 
 #include "kv4.h"
@@ -26,14 +26,16 @@ namespace lora {
 
 namespace {
 
-constexpr int kMaxThreads = 1024, kFewThreads = 256, kOwn = 4;     // threads of a CTA; sequences of a thread
-static_assert(kMaxThreads * kOwn >= kMaxSeqs, "every sequence has a thread");
-constexpr int kRun = 4;                                            // neighbouring rows of a thread
+constexpr int kMaxThreads = 1024, kFewThreads = 256, kMostOwn = 4;   // threads of a CTA; sequences of a thread
+static_assert(kMaxThreads * kMostOwn >= kMaxSeqs, "every sequence has a thread");
+constexpr int kRanks = 8;                                            // CTAs of a cluster, at most
 constexpr uint32_t kNoPlace = 0xFFFFFFFFu;
 
 // Sums that stop at their limit: what passes it is refused whatever its size.
 __device__ __forceinline__ uint32_t add_to(uint32_t a, uint32_t b, uint32_t limit) { return min(a + b, limit); }
 
+// kOwn: sequences of a thread; kRun: neighbouring rows of a job.
+template <int kOwn, int kRun>
 __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, int ranks, int workers, bool in_place)
 {
     extern __shared__ uint32_t smem[];
@@ -224,12 +226,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
             slot[k] = static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(a.pool.n_pages)
                           ? (static_cast<long long>(page[k]) << a.page_shift) + ((len[k] + i) & (a.pool.page_size - 1)) : -1;
         }
-        if (a.wide && t0 + kRun <= a.max_rows) {
-            if (a.row_seq) *reinterpret_cast<int4*>(a.row_seq + t0) = make_int4(seq[0], seq[1], seq[2], seq[3]);
-            if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        if (kRun == 4 && a.wide && t0 + kRun <= a.max_rows) {
+            if (a.row_seq) *reinterpret_cast<int4*>(a.row_seq + t0) = make_int4(seq[0], seq[1 % kRun], seq[2 % kRun], seq[3 % kRun]);
+            if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1 % kRun], pos[2 % kRun], pos[3 % kRun]);
             if (a.slots) {
-                *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1]);
-                *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2], slot[3]);
+                *reinterpret_cast<longlong2*>(a.slots + t0) = make_longlong2(slot[0], slot[1 % kRun]);
+                *reinterpret_cast<longlong2*>(a.slots + t0 + 2) = make_longlong2(slot[2 % kRun], slot[3 % kRun]);
             }
         } else {
 #pragma unroll
@@ -263,32 +265,42 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     }
 }
 
-}  // namespace
-
-cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream)
+template <int kOwn, int kRun>
+cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stream)
 {
     const int smem = 4 * (4 * a.n_seqs + 1);
     static std::atomic<uint64_t> done{0};
-    cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(kv4_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (4 * kMaxSeqs + 1)); });
+    cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(kv4_plan_kernel<kOwn, kRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (4 * kMaxSeqs + 1)); });
     if (e != cudaSuccess) return e;
-    const int threads = a.n_seqs <= kFewThreads * kOwn ? kFewThreads : kMaxThreads;
-    const bool in_place = a.pool.n_free_out == a.pool.n_free || a.pool.held_out == a.pool.held;
     const long long jobs = (a.max_rows + kRun - 1ll) / kRun + a.n_seqs;
-    // Threads of a CTA that take jobs: 256 of each where there may be any number of CTAs (us, 4096 sequences: 11.8 with 64 to 512,
-    // 12.9 with 1024), all in a cluster.
+    // Threads of a CTA that take jobs: 256 of each where there may be any number of CTAs, all in a cluster.
     const int workers = in_place ? threads : kFewThreads;
-    const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? 8ll : 64ll)));
+    const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? kRanks + 0ll : 64ll)));
     PdlLaunch l(dim3(ranks), threads, smem, stream);
     cudaLaunchAttribute attr[2];
     attr[0] = l.attr[0];
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = in_place ? ranks : 1;
+    attr[1].val.clusterDim.x = ranks;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     l.cfg.attrs = attr;
-    l.cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&l.cfg, kv4_plan_kernel, a, ranks, workers, in_place);
+    l.cfg.numAttrs = in_place ? 2 : 1;
+    e = cudaLaunchKernelEx(&l.cfg, kv4_plan_kernel<kOwn, kRun>, a, ranks, workers, in_place);
     note_launch();
     return e;
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream)
+{
+    // A kernel that runs once is bound by the reading of its code, too: one sequence to a thread and one row to a job where that
+    // does (us: 64 requests 2.8, in code for four of each 4.4; 17 k rows 3.9 and 6.2).  Runs of four rows only where a cluster's CTAs
+    // would go through more than two rounds (in place, 256 requests: 15547 rows 6.4 and, one by one, 9.8; 3992 rows 4.2 and 4.3).
+    const bool in_place = a.pool.n_free_out == a.pool.n_free || a.pool.held_out == a.pool.held;
+    const int threads = a.n_seqs <= kFewThreads ? kFewThreads : kMaxThreads;
+    const bool runs = in_place && a.max_rows > 2 * kRanks * threads;
+    if (a.n_seqs <= kMaxThreads) return runs ? run<1, 4>(a, threads, in_place, stream) : run<1, 1>(a, threads, in_place, stream);
+    return runs ? run<kMostOwn, 4>(a, threads, in_place, stream) : run<kMostOwn, 1>(a, threads, in_place, stream);
 }
 
 }  // namespace lora
