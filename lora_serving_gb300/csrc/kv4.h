@@ -141,7 +141,7 @@ struct PlanArgs {
     int max_ctx_len;
     lora_kv4_pool_t pool;
     int page_shift;
-    bool wide;   // row_seq, positions and slots on 16 bytes
+    bool wide_in, wide_out;   // q_lens, lens and held on 16 bytes; row_seq, positions and slots
     int32_t* status;
 };
 cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream);

@@ -245,6 +245,7 @@ lora_status_t lora_kv4_plan(int32_t* q_starts, int32_t* ctx_lens, int32_t* row_s
         if (!aligned(p, 4)) return LORA_ERR_ALIGNMENT;
     if (!aligned(slots, 8)) return LORA_ERR_ALIGNMENT;
     lora::PlanArgs a{q_starts, ctx_lens, row_seq, positions, slots, q_lens, lens, depths, n_seqs, max_rows, max_q_len, max_ctx_len, *pool, 0,
+                     aligned(q_lens, 16) && aligned(lens, 16) && aligned(pool->held, 16),
                      aligned(row_seq, 16) && aligned(positions, 16) && aligned(slots, 16), dev_status};
     while ((1 << a.page_shift) < pool->page_size) ++a.page_shift;
     return cuda_status(lora::launch_kv4_plan(a, reinterpret_cast<cudaStream_t>(stream)));

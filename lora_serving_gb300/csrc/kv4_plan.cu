@@ -16,7 +16,7 @@
 // Bound: latency, of a chain of loads, sums over the CTA, a search, and loads;
 // with thousands of sequences the sums' instructions, which every CTA repeats.
 // Measured, start to start: 64 requests of a token 2.8 us, 256 with 16 prompts
-// among them (17 k rows) 3.9 (6.4 with the counters in place), 4096 trees 10.5.
+// among them (17 k rows) 3.9 (5.3 with the counters in place), 4096 trees 7.7 (9.6).
 #include <algorithm>
 
 #include "kv4.h"
@@ -38,17 +38,17 @@ __device__ __forceinline__ uint32_t add_to(uint32_t a, uint32_t b, uint32_t limi
 template <int kOwn, int kRun>
 __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, int ranks, int workers, bool in_place)
 {
-    extern __shared__ uint32_t smem[];
+    extern __shared__ __align__(16) uint32_t smem[];
     __shared__ uint32_t sums[3][32];
     __shared__ uint32_t taken;
     const int n = a.n_seqs, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int rank = static_cast<int>(blockIdx.x);
-    uint32_t* const row_at = smem;               // [n + 1] a sequence's first row
-    uint32_t* const need_at = row_at + n + 1;    // [n] pages asked for before it
-    uint32_t* const back_at = need_at + n;       // [n] pages given back before it
-    uint32_t* const held_s = back_at + n;        // [n] pages that it held; kNoPlace: it has no place
+    const int n4 = (n + 3) & ~3;
+    uint32_t* const need_at = smem;              // [n4] pages asked for before a sequence
+    uint32_t* const back_at = need_at + n4;      // [n4] pages given back before it
+    uint32_t* const held_s = back_at + n4;       // [n4] pages that it held; kNoPlace: it has no place
+    uint32_t* const row_at = held_s + n4;        // [n4 + 1] its first row
     int32_t* const stack = a.pool.free_pages;
-    const int per = (n + blockDim.x - 1) / blockDim.x;   // at most kOwn
     tc::grid_dep_wait();
     tc::grid_dep_launch();
 
@@ -64,21 +64,25 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
         n_free = 0;
     }
     int q_of[kOwn], len_of[kOwn], held_of[kOwn];   // every load on its way before the first is looked at
+    auto load = [&](const int32_t* from, int (&to)[kOwn]) {
+        if (kOwn == 4 && a.wide_in && tid * 4 + 3 < n) {
+            const int4 x = __ldg(reinterpret_cast<const int4*>(from) + tid);
+            to[0] = x.x; to[1 % kOwn] = x.y; to[2 % kOwn] = x.z; to[3 % kOwn] = x.w;
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kOwn; ++i) to[i] = tid * kOwn + i < n ? __ldg(from + tid * kOwn + i) : 0;
+    };
+    load(a.q_lens, q_of);
+    load(a.lens, len_of);
+    load(a.pool.held, held_of);
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-        const int s = tid * per + i;
-        const bool mine = i < per && s < n;
-        q_of[i] = mine ? __ldg(a.q_lens + s) : 0;
-        len_of[i] = mine ? __ldg(a.lens + s) : 0;
-        held_of[i] = mine ? __ldg(a.pool.held + s) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kOwn; ++i) {
-        const int s = tid * per + i;
+        const int s = tid * kOwn + i;
         v[i][0] = v[i][1] = v[i][2] = 0;
         ctx[i] = -1;
         held[i] = 0;
-        if (i >= per || s >= n) continue;
+        if (s >= n) continue;
         const int q = q_of[i], len = len_of[i], h = held_of[i];
         const bool counts = h >= 0 && h <= a.pool.ld_table;
         held[i] = h;
@@ -138,8 +142,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     uint32_t mine_taken = 0;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-        const int s = tid * per + i;
-        const bool mine = i < per && s < n;
+        const int s = tid * kOwn + i;
+        const bool mine = s < n;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
             at[i][k] = before[k];
@@ -156,12 +160,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
         }
         if (!got[i]) v[i][1] = 0;
         if (v[i][1] > 0) mine_taken = before[1];
-        if (mine) {
+        if (kOwn == 1 && mine) {
             row_at[s] = at[i][0];
             need_at[s] = at[i][1];
             back_at[s] = at[i][2];
             held_s[s] = got[i] ? held[i] : kNoPlace;
         }
+    }
+    if (kOwn == 4 && tid * 4 < n) {
+        auto four = [&](uint32_t* to, uint32_t x, uint32_t y, uint32_t z, uint32_t w) { *reinterpret_cast<uint4*>(to + 4 * tid) = make_uint4(x, y, z, w); };
+        four(row_at, at[0][0], at[1 % kOwn][0], at[2 % kOwn][0], at[3 % kOwn][0]);
+        four(need_at, at[0][1], at[1 % kOwn][1], at[2 % kOwn][1], at[3 % kOwn][1]);
+        four(back_at, at[0][2], at[1 % kOwn][2], at[2 % kOwn][2], at[3 % kOwn][2]);
+        four(held_s, got[0] ? held[0] : kNoPlace, got[1 % kOwn] ? held[1 % kOwn] : kNoPlace, got[2 % kOwn] ? held[2 % kOwn] : kNoPlace, got[3 % kOwn] ? held[3 % kOwn] : kNoPlace);
     }
     mine_taken = __reduce_max_sync(0xFFFFFFFFu, mine_taken);
     if (lane == 0 && mine_taken) atomicMax(&taken, mine_taken);
@@ -226,7 +237,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
             slot[k] = static_cast<uint32_t>(page[k]) < static_cast<uint32_t>(a.pool.n_pages)
                           ? (static_cast<long long>(page[k]) << a.page_shift) + ((len[k] + i) & (a.pool.page_size - 1)) : -1;
         }
-        if (kRun == 4 && a.wide && t0 + kRun <= a.max_rows) {
+        if (kRun == 4 && a.wide_out && t0 + kRun <= a.max_rows) {
             if (a.row_seq) *reinterpret_cast<int4*>(a.row_seq + t0) = make_int4(seq[0], seq[1 % kRun], seq[2 % kRun], seq[3 % kRun]);
             if (a.positions) *reinterpret_cast<int4*>(a.positions + t0) = make_int4(pos[0], pos[1 % kRun], pos[2 % kRun], pos[3 % kRun]);
             if (a.slots) {
@@ -247,8 +258,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     // ---- the sequences' own
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-        const int s = tid * per + i;
-        if (i < per && s < n && s % ranks == rank) {
+        const int s = tid * kOwn + i;
+        if (s < n && s % ranks == rank) {
             a.q_starts[s] = static_cast<int32_t>(min(at[i][0], static_cast<uint32_t>(a.max_rows)));
             a.ctx_lens[s] = got[i] ? ctx[i] : 0;
         }
@@ -256,8 +267,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     if (in_place) cluster_wait();   // the other CTAs have read the counters, too, which these are in the place of
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
-        const int s = tid * per + i;
-        if (i < per && s < n && s % ranks == rank) a.pool.held_out[s] = held[i] + static_cast<int>(v[i][1]);
+        const int s = tid * kOwn + i;
+        if (s < n && s % ranks == rank) a.pool.held_out[s] = held[i] + static_cast<int>(v[i][1]);
     }
     if (rank == 0 && tid == 0) {
         a.q_starts[n] = static_cast<int32_t>(min(total[0], static_cast<uint32_t>(a.max_rows)));
@@ -268,14 +279,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
 template <int kOwn, int kRun>
 cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stream)
 {
-    const int smem = 4 * (4 * a.n_seqs + 1);
+    const int smem = 4 * (4 * ((a.n_seqs + 3) & ~3) + 1);
     static std::atomic<uint64_t> done{0};
     cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(kv4_plan_kernel<kOwn, kRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (4 * kMaxSeqs + 1)); });
     if (e != cudaSuccess) return e;
     const long long jobs = (a.max_rows + kRun - 1ll) / kRun + a.n_seqs;
-    // Threads of a CTA that take jobs: 256 of each where there may be any number of CTAs, all in a cluster.
-    const int workers = in_place ? threads : kFewThreads;
-    const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? kRanks + 0ll : 64ll)));
+    // Threads of a CTA that take jobs: 256 where the CTAs are enough for that (4096 trees, 32 k rows: 7.7 us, 9.4 in 64 CTAs
+    // with two rounds; 262 k rows 11.5, with all threads 7.9).
+    const int workers = in_place || jobs > static_cast<long long>(device_sms()) * kFewThreads ? threads : kFewThreads;
+    const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? kRanks + 0ll : device_sms() + 0ll)));
     PdlLaunch l(dim3(ranks), threads, smem, stream);
     cudaLaunchAttribute attr[2];
     attr[0] = l.attr[0];
@@ -293,11 +305,13 @@ cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stre
 
 cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream)
 {
-    // A kernel that runs once is bound by the reading of its code, too: one sequence to a thread and one row to a job where that
-    // does (us: 64 requests 2.8, in code for four of each 4.4; 17 k rows 3.9 and 6.2).  Runs of four rows only where a cluster's CTAs
-    // would go through more than two rounds (in place, 256 requests: 15547 rows 6.4 and, one by one, 9.8; 3992 rows 4.2 and 4.3).
+    // Measured (us): a kernel that runs once is bound by the reading of its code, too: one sequence to a thread and one row to a
+    // job where that does (64 requests 2.8, in code for four of each 4.4; 17 k rows 3.9 and 6.2).  256 threads a CTA for up to 256
+    // sequences, as long as that many CTAs hold the rows (256 requests, 128 k rows: 6.8, with 1024 threads 5.0; in place,
+    // 15.5 k rows: 6.4 and 5.3, 4 k rows 4.2 both).  Runs of four rows only where a cluster's threads would go through more than
+    // two rounds (in place, 4096 requests: 31.6 k rows 9.6 and, one by one, 12.2; 16 k rows 9.9 and 8.8).
     const bool in_place = a.pool.n_free_out == a.pool.n_free || a.pool.held_out == a.pool.held;
-    const int threads = a.n_seqs <= kFewThreads ? kFewThreads : kMaxThreads;
+    const int threads = a.n_seqs <= kFewThreads && a.max_rows <= kFewThreads * (in_place ? 2 * kRanks : device_sms()) ? kFewThreads : kMaxThreads;
     const bool runs = in_place && a.max_rows > 2 * kRanks * threads;
     if (a.n_seqs <= kMaxThreads) return runs ? run<1, 4>(a, threads, in_place, stream) : run<1, 1>(a, threads, in_place, stream);
     return runs ? run<kMostOwn, 4>(a, threads, in_place, stream) : run<kMostOwn, 1>(a, threads, in_place, stream);

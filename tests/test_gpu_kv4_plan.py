@@ -84,6 +84,23 @@ def test_plan(case, in_place):
         _check(p, word, want, faults)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n,q_max", [(3, 9), (256, 90), (257, 5), (700, 60), (1024, 3), (1027, 4), (1100, 50), (4095, 5)])
+def test_arrays_off_16_bytes(n, q_max, in_place):
+    """Lengths and tables that start four bytes behind a 16-byte boundary, at each count of sequences and rows to a thread."""
+    rng = np.random.default_rng(n)
+    st = _state(rng, n, 32, 300, 3 * n, q_max=q_max)
+    rows = int(np.maximum(st["q"], 0).sum()) + n % 5
+    want, faults = R.plan(st["q"], st["lens"], st["held"], st["table"], st["free"], st["n_free"], page=32, max_rows=rows, max_q=q_max, max_ctx=300)
+    off = lambda a: _i32(np.concatenate([[-9], a]))[1:]
+    more = {} if in_place else dict(n_free_out=off([-5]), held_out=off(np.full(n, -5)))
+    p = store.KV4Plan(off(st["free"]), off([st["n_free"]]), off(st["held"]), _i32(st["table"]), page_size=32, max_rows=rows, max_q_len=q_max,
+                      max_ctx_len=300, **more)
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    abi.lora_kv4_plan(p, off(st["q"]), off(st["lens"]), dev_status=word)
+    _check(p, word, want, faults)
+
+
 @pytest.mark.parametrize("n,spare", [(8, 0), (8, 3), (300, 20), (4096, 100)])
 def test_too_few_pages(n, spare):
     rng = np.random.default_rng(spare + n)
