@@ -587,7 +587,8 @@ size_t lora_kv4_attend_workspace_bytes(int n_heads, int n_kv, int head_dim, int 
  * stack, and how many each sequence's row of the block table holds.  The
  * counters go out to arrays of their own or to the same: with others a plan
  * can be made again or dropped, since what it writes beside the counters
- * lies past what they count.
+ * lies past what they count.  A page is one sequence's or on the stack: one
+ * that two rows of the table hold would be given back by each.
  */
 typedef struct {
     int32_t* free_pages;   /* [dev] [n_pages]; entries [0, *n_free) are free, the last one is the next */
@@ -747,7 +748,8 @@ typedef struct {
  * n_rows above n_seqs without row_seq, n_rows above n_allowed without
  * allowed_rows, out the same as logits with another type or leading dimension),
  * LORA_ERR_SHAPE (a leading dimension too small, vocab above 2^25, ld_tokens
- * + 32 ld_tree above 2^20 - 1 or ld_bias above 2047, which the counters hold),
+ * + 32 ld_tree above 2^20 - 1 or ld_bias above 2047, which the counters hold,
+ * n_rows ceil(vocab / 2048) above 2^30),
  * LORA_ERR_ALIGNMENT, LORA_ERR_CUDA.
  */
 lora_status_t lora_logits_adjust(void* out, lora_dtype_t out_type, int ld_out, const void* logits, lora_dtype_t type, int ld,

@@ -301,7 +301,7 @@ lora_status_t lora_logits_adjust(void* out, lora_dtype_t out_type, int ld_out, c
     constexpr int kCounts = (1 << 20) - 1, kBiases = 2047;   // what a token's counter holds (logits.cu)
     if (n_rows < 0 || vocab <= 0 || (type != LORA_BF16 && type != LORA_F32) || (out_type != LORA_BF16 && out_type != LORA_F32))
         return LORA_ERR_INVALID_ARG;
-    if (vocab > 1 << 25) return LORA_ERR_SHAPE;
+    if (vocab > 1 << 25 || static_cast<long long>(n_rows) * ((vocab + 2047) / 2048) > 1 << 30) return LORA_ERR_SHAPE;
     if (n_rows == 0) return LORA_OK;
     LORA_TRY(check_matrix(logits, ld, vocab));
     LORA_TRY(check_matrix(out, ld_out, vocab));

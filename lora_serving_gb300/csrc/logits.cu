@@ -372,8 +372,7 @@ cudaError_t run(const LogitsArgs& a, cudaStream_t stream)
     // 32 rows, 128256 tokens; 3 waves of CTAs with 4 rows): 1 row 95, 4 rows 59.7, 8 rows 68.
     int rows_each = 1;
     while (kDrafts && rows_each < kRows && static_cast<long long>(chunks) * ((a.n_rows + 2 * rows_each - 1) / (2 * rows_each)) >= kCtas * device_sms()) rows_each *= 2;
-    const long long ctas = static_cast<long long>(chunks) * ((a.n_rows + rows_each - 1) / rows_each);
-    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const long long ctas = static_cast<long long>(chunks) * ((a.n_rows + rows_each - 1) / rows_each);   // (the entry point bounds it)
     PdlLaunch l(dim3(static_cast<unsigned>(ctas)), kThreads, a.rules.tokens ? S::kSmem : 0, stream);
     const cudaError_t e = cudaLaunchKernelEx(&l.cfg, logits_adjust_kernel<IN32, OUT32, kVecs, kDrafts>, a, rows_each, chunks, chunks > 1 ? static_cast<uint32_t>((1ull << 32) / chunks + 1) : 0);
     note_launch();

@@ -119,6 +119,7 @@ LOGITS = dict(out=P, out_type=0, ld_out=104, x=P << 1, type=0, ld=104, n=5, voca
     (dict(ld=96), "SHAPE"), (dict(ld_out=96), "SHAPE"), (dict(vocab=(1 << 25) + 1), "SHAPE"), (dict(allowed=P, ld_allowed=3, n_allowed=5), "SHAPE"),
     (dict(rules=dict(ld_tokens=1 << 20)), "SHAPE"), (dict(rules=dict(ld_tokens=(1 << 20) - 40), drafts=P, tree=P, ld_tree=2, q_starts=P), "SHAPE"),
     (dict(rules=dict(ids=P, bias=P, n_bias=P, ld_bias=2048)), "SHAPE"), (dict(drafts=P, tree=P, ld_tree=0, q_starts=P), "SHAPE"),
+    (dict(n=(1 << 30) + 1, rules=None), "SHAPE"), (dict(n=1 << 20, vocab=1 << 25, ld=1 << 25, ld_out=1 << 25, rules=None), "SHAPE"),
     (dict(ld=108), "ALIGNMENT"), (dict(x=P + 8), "ALIGNMENT"), (dict(out=P + 4), "ALIGNMENT"), (dict(row_seq=P + 2), "ALIGNMENT"),
     (dict(rules=dict(rep=P + 1)), "ALIGNMENT"), (dict(allowed=P + 2, ld_allowed=4, n_allowed=5), "ALIGNMENT"),
 ])
