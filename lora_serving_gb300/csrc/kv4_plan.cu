@@ -15,8 +15,8 @@
 // any: the sums stay sums, no sequence waiting for another's answer.
 // Bound: latency, of a chain of loads, sums over the CTA, a search, and loads;
 // with thousands of sequences the sums' instructions, which every CTA repeats.
-// Measured, start to start: 64 requests of a token 2.8 us, 256 with 16 prompts
-// among them (17 k rows) 3.9 (5.3 with the counters in place), 4096 trees 7.7 (9.6).
+// Measured, start to start: 64 requests of a token 2.5 us, 256 with 16 prompts
+// among them (17 k rows) 3.5 (4.9 with the counters in place), 4096 trees 6.4 (8.4).
 #include <algorithm>
 
 #include "kv4.h"
@@ -32,11 +32,11 @@ constexpr int kRanks = 8;                                            // CTAs of 
 constexpr uint32_t kNoPlace = 0xFFFFFFFFu;
 
 // Sums that stop at their limit: what passes it is refused whatever its size.
-__device__ __forceinline__ uint32_t add_to(uint32_t a, uint32_t b, uint32_t limit) { return min(a + b, limit); }
+__device__ __forceinline__ uint32_t add_to(uint32_t a, uint32_t b, uint32_t limit) { return __viaddmin_u32(a, b, limit); }
 
 // kOwn: sequences of a thread; kRun: neighbouring rows of a job.
 template <int kOwn, int kRun>
-__global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, int ranks, int workers, bool in_place)
+__global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, int ranks, int workers, int each, bool in_place)
 {
     extern __shared__ __align__(16) uint32_t smem[];
     __shared__ uint32_t sums[3][32];
@@ -255,11 +255,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
         }
     }
 
-    // ---- the sequences' own
+    // ---- the sequences' own: one CTA writes a thread's (taken in turn, by a remainder for each, they cost 4096 trees 1.1 us)
+    const bool writes = tid >= rank * each && tid < rank * each + each;
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
         const int s = tid * kOwn + i;
-        if (s < n && s % ranks == rank) {
+        if (s < n && writes) {
             a.q_starts[s] = static_cast<int32_t>(min(at[i][0], static_cast<uint32_t>(a.max_rows)));
             a.ctx_lens[s] = got[i] ? ctx[i] : 0;
         }
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
         const int s = tid * kOwn + i;
-        if (s < n && s % ranks == rank) a.pool.held_out[s] = held[i] + static_cast<int>(v[i][1]);
+        if (s < n && writes) a.pool.held_out[s] = held[i] + static_cast<int>(v[i][1]);
     }
     if (rank == 0 && tid == 0) {
         a.q_starts[n] = static_cast<int32_t>(min(total[0], static_cast<uint32_t>(a.max_rows)));
@@ -284,8 +285,8 @@ cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stre
     cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(kv4_plan_kernel<kOwn, kRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (4 * kMaxSeqs + 1)); });
     if (e != cudaSuccess) return e;
     const long long jobs = (a.max_rows + kRun - 1ll) / kRun + a.n_seqs;
-    // Threads of a CTA that take jobs: 256 where the CTAs are enough for that (4096 trees, 32 k rows: 7.7 us, 9.4 in 64 CTAs
-    // with two rounds; 262 k rows 11.5, with all threads 7.9).
+    // Threads of a CTA that take jobs: 256 where the CTAs are enough for that (4096 trees, 32 k rows: 7.7 us, 9.4 in 64
+    // CTAs with two rounds; 262 k rows 11.5, with all threads 7.9).
     const int workers = in_place || jobs > static_cast<long long>(device_sms()) * kFewThreads ? threads : kFewThreads;
     const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? kRanks + 0ll : device_sms() + 0ll)));
     PdlLaunch l(dim3(ranks), threads, smem, stream);
@@ -296,7 +297,7 @@ cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stre
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     l.cfg.attrs = attr;
     l.cfg.numAttrs = in_place ? 2 : 1;
-    e = cudaLaunchKernelEx(&l.cfg, kv4_plan_kernel<kOwn, kRun>, a, ranks, workers, in_place);
+    e = cudaLaunchKernelEx(&l.cfg, kv4_plan_kernel<kOwn, kRun>, a, ranks, workers, (threads + ranks - 1) / ranks, in_place);
     note_launch();
     return e;
 }
@@ -306,12 +307,14 @@ cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stre
 cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream)
 {
     // Measured (us): a kernel that runs once is bound by the reading of its code, too: one sequence to a thread and one row to a
-    // job where that does (64 requests 2.8, in code for four of each 4.4; 17 k rows 3.9 and 6.2).  256 threads a CTA for up to 256
-    // sequences, as long as that many CTAs hold the rows (256 requests, 128 k rows: 6.8, with 1024 threads 5.0; in place,
-    // 15.5 k rows: 6.4 and 5.3, 4 k rows 4.2 both).  Runs of four rows only where a cluster's threads would go through more than
-    // two rounds (in place, 4096 requests: 31.6 k rows 9.6 and, one by one, 12.2; 16 k rows 9.9 and 8.8).
+    // job where that does (64 requests 2.8, in code for four of each 4.4; 17 k rows 3.9 and 6.2).  As many threads as that needs
+    // (300 requests 4.2, with 1024 threads 4.6), 256 at least, as long as the CTAs hold the rows (256 requests, 128 k rows: 6.8,
+    // with 1024 threads 5.0; in place, 15.5 k rows: 6.4 and 5.3, 4 k rows 4.2 both).  Runs of four rows only where a cluster's
+    // threads would go through more than two rounds (in place, 4096 requests: 31.6 k rows 9.6 and, one by one, 12.2; 16 k rows
+    // 9.9 and 8.8).
     const bool in_place = a.pool.n_free_out == a.pool.n_free || a.pool.held_out == a.pool.held;
-    const int threads = a.n_seqs <= kFewThreads && a.max_rows <= kFewThreads * (in_place ? 2 * kRanks : device_sms()) ? kFewThreads : kMaxThreads;
+    const int fewest = std::min(std::max((a.n_seqs + 255) / 256 * 256, kFewThreads), kMaxThreads);
+    const int threads = a.max_rows <= fewest * (in_place ? 2 * kRanks : device_sms()) ? fewest : kMaxThreads;
     const bool runs = in_place && a.max_rows > 2 * kRanks * threads;
     if (a.n_seqs <= kMaxThreads) return runs ? run<1, 4>(a, threads, in_place, stream) : run<1, 1>(a, threads, in_place, stream);
     return runs ? run<kMostOwn, 4>(a, threads, in_place, stream) : run<kMostOwn, 1>(a, threads, in_place, stream);
