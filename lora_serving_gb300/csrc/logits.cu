@@ -17,7 +17,7 @@
 // What bounds it.  HBM by its bytes, then instructions (some 45 a vector of a
 // warp without rules) and the start of a CTA's first row: tables, tokens,
 // counts, 4 us, which few CTAs are there to hide.  Measured: 512 rows of 128256
-// tokens in trees of 32, bf16, masks and penalties 60 us (263 MB, 0.66 of a
+// tokens in trees of 32, bf16, masks and penalties 57 us (263 MB, 0.69 of a
 // copy's rate; with masks alone 44), 64 rows to fp32 15.3 (50 MB; 12.1), one row
 // of 32000 tokens 1.7, start to start.
 #include <algorithm>
@@ -95,10 +95,6 @@ __device__ __forceinline__ void put8(char* to, const Raw<IN32>& r, uint32_t keep
 {
     const uint4 v = r.u[0], w = r.u[IN32 ? 1 : 0];
     if (!IN32 && !OUT32) {
-        if (keep == 0xFFu && some == 0) {
-            *reinterpret_cast<uint4*>(to) = v;
-            return;
-        }
         uint32_t h[4] = {v.x, v.y, v.z, v.w};
         for (; some; some &= some - 1) {   // one after the other: few have any, and eight tests in a row cost every warp eight branches
             const int i = __ffs(some) - 1;
@@ -251,6 +247,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
     int counted = -1;              // the request whose words these are
     Request r{};
     int mine[2] = {-1, -1};        // words of the lane's drafted tokens (of the first 64) that are in the warp's blocks
+    bool paths = false;            // whether the warp has any: most have none (512 rows in trees of 32 57.4 us, 58.0 without the test)
     for (int t = t_begin; t < t_end; ++t) {
         const Row row = next;
         const int s = row.seq;
@@ -273,6 +270,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         if (lane + 32 * i < r.end - r.first) mine[i] = own_word(__ldg(a.drafts + r.first + lane + 32 * i));
+                    paths = r.end - r.first > 64 || __any_sync(0xFFFFFFFFu, mine[0] >= 0 || mine[1] >= 0);
                 }
                 __syncthreads();   // the words are cleared, or the last request's have been read
                 if (!clean) {
@@ -313,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
             live = false;
         }
         // ---- the row's path, every warp those of its tokens that are in its blocks (no other looks at them)
-        const int n_path = !kDrafts || !live || r.plain ? 0 : min(r.end - r.first, 32 * a.ld_tree);
+        const int n_path = !kDrafts || !live || r.plain || !paths ? 0 : min(r.end - r.first, 32 * a.ld_tree);
         auto path = [&](auto each) {
 #pragma unroll
             for (int i = 0; i < 2; ++i)
