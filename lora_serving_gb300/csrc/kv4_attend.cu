@@ -54,11 +54,14 @@ long long kv4_attend_places(const AttendArgs& a)
 namespace {
 
 // Joins the pieces behind each record, in order: kQuads 16-byte pieces of a
-// row's sums to a thread, as many CTAs to a record as its slot's rows need
-// (most records are empty, and a CTA costs its launch: 24 requests in a window
-// 65.1 us with one piece to a thread, 62.7 with 2, 63.1 with 4; 16 prompts
-// 306, 308, 301).
-constexpr int kJoinThreads = 256, kQuads = 4;
+// row's sums to a thread, a row to neighbouring threads, as many CTAs to a
+// record as its slot's rows need.  A chain of latencies: the first two pieces,
+// most often all there are, come as one, and with short slots before the
+// record says whether they count.  Measured (us, the call; 16 trees of 16 to 64
+// rows in a window of 4096 / 32 of 2 to 6): maxima, then sums, a row after the
+// other 48.9 / 16.2; together, with 1, 2 and 4 to a thread 45.7, 44.1, 44.2 /
+// 16.2; before the record 50.4 (what does not count is read, too) / 15.8.
+constexpr int kJoinThreads = 256, kQuads = 2, kEarlyRows = 32;
 __host__ __device__ constexpr int join_ctas(int rows, int D) { return (rows * (D / 4) + kJoinThreads * kQuads - 1) / (kJoinThreads * kQuads); }
 
 template <int D>
@@ -72,28 +75,54 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv
     const int per = join_ctas(p.rows, D), x = blockIdx.x - (second ? n0 : 0), b = x / per, group = a.group;
     const kv4::Record u = p.records[b];
     const float inf = __int_as_float(0x7F800000);
-    for (int e = (x - b * per) * kJoinThreads + threadIdx.x; e < u.rows * (D / 4); e += per * kJoinThreads) {
-        const int r = e / (D / 4), d = e % (D / 4) * 4;
-        float m = -inf, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int k = b; k <= u.last; ++k) m = fmaxf(m, p.slot(k, k == b, D)[p.rows * D + r]);
-#pragma unroll 4
-        for (int k = b; k <= u.last; ++k) {
-            const float* s = p.slot(k, k == b, D);
-            const float w = m == -inf ? 0.f : kv4::ex2(s[p.rows * D + r] - m);
-            const float4 v = *reinterpret_cast<const float4*>(s + r * D + d);
-            o.x = fmaf(v.x, w, o.x);
-            o.y = fmaf(v.y, w, o.y);
-            o.z = fmaf(v.z, w, o.z);
-            o.w = fmaf(v.w, w, o.w);
-            l = fmaf(s[p.rows * (D + 1) + r], w, l);
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const int row = u.block_row0 + r, tok = row / group;
-        *reinterpret_cast<uint2*>(a.out + static_cast<long long>(u.seq_row0 + tok) * a.ld_out + (u.h * group + row - tok * group) * D + d) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+    constexpr int kPer = D / (4 * kQuads), kRows = kJoinThreads / kPer;   // threads of a row, rows of a CTA
+    const int r = (x - b * per) * kRows + threadIdx.x / kPer, d = 4 * (threadIdx.x % kPer);
+    const bool early = p.rows <= kEarlyRows;
+    if (early ? r >= p.rows : r >= u.rows) return;
+    // The first two pieces, most often all, are on their way together.
+    float m = -inf, l = 0.f, top[2], sum[2];
+    float4 o[kQuads], v[2][kQuads];
+    auto load = [&](int k, float& at_top, float& at_sum, float4 (&to)[kQuads]) {
+        const float* s = p.slot(k, k == b, D);
+        at_top = s[p.rows * D + r];
+        at_sum = s[p.rows * (D + 1) + r];
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) to[i] = *reinterpret_cast<const float4*>(s + r * D + d + 4 * kPer * i);
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (early ? b + k < p.ctas : b + k <= u.last) load(b + k, top[k], sum[k], v[k]);
     }
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r >= u.rows) return;
+    if (b >= u.last) top[1] = -inf;
+    m = fmaxf(top[0], top[1]);
+    for (int k = b + 2; k <= u.last; ++k) m = fmaxf(m, p.slot(k, false, D)[p.rows * D + r]);
+    auto add = [&](float at_top, float at_sum, const float4 (&from)[kQuads]) {
+        const float w = m == -inf ? 0.f : kv4::ex2(at_top - m);
+#pragma unroll
+        for (int i = 0; i < kQuads; ++i) {
+            o[i].x = fmaf(from[i].x, w, o[i].x);
+            o[i].y = fmaf(from[i].y, w, o[i].y);
+            o[i].z = fmaf(from[i].z, w, o[i].z);
+            o[i].w = fmaf(from[i].w, w, o[i].w);
+        }
+        l = fmaf(at_sum, w, l);
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (b + k <= u.last) add(top[k], sum[k], v[k]);
+    for (int k = b + 2; k <= u.last; ++k) {
+        load(k, top[0], sum[0], v[0]);
+        add(top[0], sum[0], v[0]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int row = u.block_row0 + r, tok = row / group;
+    bf16_t* const out = a.out + static_cast<long long>(u.seq_row0 + tok) * a.ld_out + (u.h * group + row - tok * group) * D + d;
+#pragma unroll
+    for (int i = 0; i < kQuads; ++i)
+        *reinterpret_cast<uint2*>(out + 4 * kPer * i) = make_uint2(pack_bf16x2(o[i].x * inv, o[i].y * inv), pack_bf16x2(o[i].z * inv, o[i].w * inv));
 }
 
 }  // namespace
