@@ -57,18 +57,21 @@ namespace {
 // row's sums to a thread, a row to neighbouring threads, as many CTAs to a
 // record as its slot's rows need.  A chain of latencies: the first two pieces,
 // most often all there are, come as one, and with short slots before the
-// record says whether they count.  Measured (us, the call; 16 trees of 16 to 64
-// rows in a window of 4096 / 32 of 2 to 6): maxima, then sums, a row after the
-// other 48.9 / 16.2; together, with 1, 2 and 4 to a thread 45.7, 44.1, 44.2 /
-// 16.2; before the record 50.4 (what does not count is read, too) / 15.8.
-constexpr int kJoinThreads = 256, kQuads = 2, kEarlyRows = 32;
+// record says whether they count (with long ones what does not count costs more
+// than it saves).  Measured (us, the call; 16 trees of 16 to 64 rows in a window
+// of 4096 / 32 of 2 to 6): maxima, then sums, one row after another 49.0 / 16.2;
+// together, with 1, 2, 4 and 8 pieces to a thread 45.7, 44.1, 44.2, 47.0 / 16.2;
+// before the record 50.4 / 15.8.
+constexpr int kJoinThreads = 256, kQuads = 4, kEarlyRows = 32;
 __host__ __device__ constexpr int join_ctas(int rows, int D) { return (rows * (D / 4) + kJoinThreads * kQuads - 1) / (kJoinThreads * kQuads); }
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv4::Partials p0, kv4::Partials p1)
 {
     tc::grid_dep_wait();
-    tc::grid_dep_launch();
+    // When the next launch may begin decides which SMs the next call's CTAs come to, and with that what they share on the way from
+    // memory: at once, here, 8 trees of 64 rows over 32768 positions take 415 us and 16 prompts 297; at the end 425 and 290.
+    if (a.tree) tc::grid_dep_launch();
     const int n0 = p0.ctas * join_ctas(p0.rows, D);
     const bool second = static_cast<int>(blockIdx.x) >= n0;
     const kv4::Partials& p = second ? p1 : p0;
@@ -117,6 +120,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv
         load(k, top[0], sum[0], v[0]);
         add(top[0], sum[0], v[0]);
     }
+    if (!a.tree) tc::grid_dep_launch();
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int row = u.block_row0 + r, tok = row / group;
     bf16_t* const out = a.out + static_cast<long long>(u.seq_row0 + tok) * a.ld_out + (u.h * group + row - tok * group) * D + d;
