@@ -46,8 +46,7 @@ long long kv4_attend_places(const AttendArgs& a)
     // units of 8 rows over tiles of 32 positions, items of 256 over 128: a tile cut at either end, and a start's cost
     const long long few = a.batch.n_seqs * ((std::min<long long>(few_limit(a), rows) + 7) / 8) * (span(a.batch.max_q_len) / 32 + 5);
     // (every row of a tree may see all of the tree's, whichever block of 256 it is in)
-    // and a tile of 256 rows is two places
-    const long long many = (a.batch.n_rows * group / 256 + a.batch.n_seqs) * (span(a.tree ? a.batch.max_q_len : 256) / 128 + 6) * (a.tree ? 2 : 1);
+    const long long many = (a.batch.n_rows * group / 256 + a.batch.n_seqs) * (span(a.tree ? a.batch.max_q_len : 256) / 128 + 6);
     return std::max(few, rows > few_limit(a) ? many : 0) * a.cache.n_kv;
 }
 
