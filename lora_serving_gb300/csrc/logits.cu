@@ -380,10 +380,11 @@ cudaError_t run(const LogitsArgs& a, cudaStream_t stream)
 template <bool IN32, bool OUT32>
 cudaError_t pick(const LogitsArgs& a, cudaStream_t stream)
 {
-    // Small calls want their chunks on as many SMs as there are.
+    // Small calls want their chunks on as many SMs as there are, and a vocabulary that fits in the short chunk has no use for the
+    // long one's words (16384 rows of 2048 tokens 108 us, in long chunks 145; of 4096 tokens 196 and 162).
     const long long ctas = static_cast<long long>(a.n_rows) * ((a.vocab + 8 * kThreads - 1) / (8 * kThreads));
     constexpr int kVecs = IN32 ? kVecs16 / 2 : kVecs16;
-    if (ctas < kSmall * device_sms()) return a.drafts ? run<IN32, OUT32, 1, true>(a, stream) : run<IN32, OUT32, 1, false>(a, stream);
+    if (a.vocab <= 8 * kThreads || ctas < kSmall * device_sms()) return a.drafts ? run<IN32, OUT32, 1, true>(a, stream) : run<IN32, OUT32, 1, false>(a, stream);
     return a.drafts ? run<IN32, OUT32, kVecs, true>(a, stream) : run<IN32, OUT32, kVecs, false>(a, stream);
 }
 

@@ -111,6 +111,20 @@ CASES = [  # rows of each request, vocabulary, tokens of each, biases, drafts, m
 ]
 
 
+@pytest.mark.parametrize("kinds", [(BF, BF), (F32, F32)], ids=["bb", "ff"])
+@pytest.mark.parametrize("q,V", [([40] * 50, 300), ([40] * 50, 2048), ([130, 70, 1], 4099), ([200, 65], 150)], ids=lambda v: str(v) if isinstance(v, int) else f"{len(v)}x{max(v)}")
+def test_rows_of_large_trees(q, V, kinds):
+    """Rows that share a CTA in a vocabulary of one short chunk, and paths of more than two words."""
+    c = _case(V, q, V, [30] * len(q), 4, True, True, kinds)
+    rules, kw = _args(c)
+    out = torch.full((sum(q), c["wide"]), 9.0, dtype=kinds[1], device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    abi.lora_logits_adjust(out[:, :V], c["x"][:, :V], rules, dev_status=st, **kw)
+    assert abi.lora_read_device_status(st) == 0
+    _check(out[:, :V], *_want(c), kinds[1])
+    assert (out[:, V:] == 9).all()
+
+
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"{len(c[0])}x{max(c[0])}-{c[1]}")
 @pytest.mark.parametrize("kinds", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)], ids=["bb", "bf", "ff", "fb"])
 def test_adjust(case, kinds):
