@@ -18,7 +18,7 @@
 // warp without rules) and the start of a CTA's first row: tables, tokens,
 // counts, 4 us, which few CTAs are there to hide.  Measured: 512 rows of 128256
 // tokens in trees of 32, bf16, masks and penalties 57 us (263 MB, 0.69 of a
-// copy's rate; with masks alone 44), 64 rows to fp32 15.3 (50 MB; 12.1), one row
+// copy's rate; with masks alone 44), 64 rows to fp32 14.1 (50 MB; 12.1), one row
 // of 32000 tokens 1.7, start to start.
 #include <algorithm>
 
@@ -175,17 +175,18 @@ struct Row {
     uint32_t bits[2];   // of its path, the first 64
 };
 
-template <int kVecs>
+// kVecs: vectors of a thread on their way; kTurns: so often, of a row.
+template <int kVecs, int kTurns>
 struct Shape {
-    static constexpr int kChunk = 8 * kThreads * kVecs;         // tokens of a CTA
+    static constexpr int kChunk = 8 * kThreads * kVecs * kTurns;   // tokens of a CTA
     static constexpr int kSmem = kChunk * 4 + kChunk / 8;       // words, and a bit to each
 };
 
 // kDrafts: rows of drafted trees, which share a request's counts; without them a CTA has one row.
-template <bool IN32, bool OUT32, int kVecs, bool kDrafts>
+template <bool IN32, bool OUT32, int kVecs, int kTurns, bool kDrafts>
 __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsArgs a, int rows_each, int chunks, uint32_t magic)
 {
-    using S = Shape<kVecs>;
+    using S = Shape<kVecs, kTurns>;
     constexpr int kIn = IN32 ? 4 : 2, kOut = OUT32 ? 4 : 2;
     extern __shared__ __align__(16) uint32_t words[];   // [kChunk]
     uint32_t* const some = words + S::kChunk;           // [kChunk / 32] the tokens that have a word (or had one on a path)
@@ -225,8 +226,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
         return reinterpret_cast<const uint8_t*>(set >= 0 && set < a.n_allowed ? a.allowed + static_cast<long long>(set) * a.ld_allowed : nullptr);
     };
     auto in_row = [&](int t) { return static_cast<const char*>(a.logits) + static_cast<long long>(t) * a.ld * kIn; };
-    auto fetch = [&](int k, const char* row, const uint8_t* mask) {
-        const uint32_t c = c0 + k * c_step;
+    auto fetch = [&](int k, int turn, const char* row, const uint8_t* mask) {
+        const uint32_t c = c0 + (turn * kVecs + k) * c_step;
         if (c < full) {
             load8<IN32>(row, c, raw[k]);
             keep[k] = mask ? __ldg(mask + (c >> 3)) : 0xFFu;
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
     {
         const uint8_t* mask = mask_of(next.set);
 #pragma unroll
-        for (int k = 0; k < kVecs; ++k) fetch(k, in_row(t_begin), mask);
+        for (int k = 0; k < kVecs; ++k) fetch(k, 0, in_row(t_begin), mask);
     }
     int counted = -1;              // the request whose words these are
     Request r{};
@@ -332,15 +333,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
         const uint8_t* const next_mask = mask_of(next.set);
         if (live) {
             char* const out = static_cast<char*>(a.out) + static_cast<long long>(t) * a.ld_out * kOut;
+#pragma unroll 1
+            for (int turn = 0; turn < kTurns; ++turn) {
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) {
-                const uint32_t c = c0 + k * c_step;
-                const int at = (k * kWarps + place) * kBlock + 8 * lane;
-                if (c < full)
-                    put8<IN32, OUT32>(out + c * kOut, raw[k], keep[k], r.plain ? 0 : reinterpret_cast<const uint8_t*>(some)[at >> 3], words + at, r.rule);
-                if (more) fetch(k, next_in, next_mask);
+                for (int k = 0; k < kVecs; ++k) {
+                    const uint32_t c = c0 + (turn * kVecs + k) * c_step;
+                    const int at = ((turn * kVecs + k) * kWarps + place) * kBlock + 8 * lane;
+                    if (c < full)
+                        put8<IN32, OUT32>(out + c * kOut, raw[k], keep[k], r.plain ? 0 : reinterpret_cast<const uint8_t*>(some)[at >> 3], words + at, r.rule);
+                    if (kTurns > 1 && turn + 1 < kTurns) fetch(k, turn + 1, in_row(t), mask_of(row.set));
+                    else if (more) fetch(k, 0, next_in, next_mask);
+                }
             }
-            if (tail >= 0 && tail < kVecs) {
+            if (tail >= 0 && tail < kVecs * kTurns) {
                 const char* const in = in_row(t);
                 const uint8_t* const mask = mask_of(row.set);
                 for (int c = full; c < a.vocab; ++c) {
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
             }
         } else if (more) {
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) fetch(k, next_in, next_mask);
+            for (int k = 0; k < kVecs; ++k) fetch(k, 0, next_in, next_mask);
         }
         if (n_path) {   // the path off again
             __syncwarp();
@@ -361,10 +366,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) logits_adjust_kernel(LogitsAr
     }
 }
 
-template <bool IN32, bool OUT32, int kVecs, bool kDrafts>
+template <bool IN32, bool OUT32, int kVecs, int kTurns, bool kDrafts>
 cudaError_t run(const LogitsArgs& a, cudaStream_t stream)
 {
-    using S = Shape<kVecs>;
+    using S = Shape<kVecs, kTurns>;
+    static std::atomic<uint64_t> done{0};
+    if (S::kSmem > 48 * 1024) {
+        const cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(logits_adjust_kernel<IN32, OUT32, kVecs, kTurns, kDrafts>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem); });
+        if (e != cudaSuccess) return e;
+    }
     const int chunks = (a.vocab + S::kChunk - 1) / S::kChunk;
     // Rows of a drafted tree to a CTA, that share its counts, as long as the CTAs fill the SMs.  Measured (us, 16 trees of
     // 32 rows, 128256 tokens; 3 waves of CTAs with 4 rows): 1 row 95, 4 rows 59.7, 8 rows 68.
@@ -372,7 +382,7 @@ cudaError_t run(const LogitsArgs& a, cudaStream_t stream)
     while (kDrafts && rows_each < kRows && static_cast<long long>(chunks) * ((a.n_rows + 2 * rows_each - 1) / (2 * rows_each)) >= kCtas * device_sms()) rows_each *= 2;
     const long long ctas = static_cast<long long>(chunks) * ((a.n_rows + rows_each - 1) / rows_each);   // (the entry point bounds it)
     PdlLaunch l(dim3(static_cast<unsigned>(ctas)), kThreads, a.rules.tokens ? S::kSmem : 0, stream);
-    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, logits_adjust_kernel<IN32, OUT32, kVecs, kDrafts>, a, rows_each, chunks, chunks > 1 ? static_cast<uint32_t>((1ull << 32) / chunks + 1) : 0);
+    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, logits_adjust_kernel<IN32, OUT32, kVecs, kTurns, kDrafts>, a, rows_each, chunks, chunks > 1 ? static_cast<uint32_t>((1ull << 32) / chunks + 1) : 0);
     note_launch();
     return e;
 }
@@ -384,8 +394,16 @@ cudaError_t pick(const LogitsArgs& a, cudaStream_t stream)
     // long one's words (16384 rows of 2048 tokens 108 us, in long chunks 145; of 4096 tokens 196 and 162).
     const long long ctas = static_cast<long long>(a.n_rows) * ((a.vocab + 8 * kThreads - 1) / (8 * kThreads));
     constexpr int kVecs = IN32 ? kVecs16 / 2 : kVecs16;
-    if (a.vocab <= 8 * kThreads || ctas < kSmall * device_sms()) return a.drafts ? run<IN32, OUT32, 1, true>(a, stream) : run<IN32, OUT32, 1, false>(a, stream);
-    return a.drafts ? run<IN32, OUT32, kVecs, true>(a, stream) : run<IN32, OUT32, kVecs, false>(a, stream);
+    if (a.vocab <= 8 * kThreads || ctas < kSmall * device_sms()) return a.drafts ? run<IN32, OUT32, 1, 1, true>(a, stream) : run<IN32, OUT32, 1, 1, false>(a, stream);
+    if (a.drafts) return run<IN32, OUT32, kVecs, 1, true>(a, stream);
+    // Longer chunks, read in turns: fewer starts, but each takes longer.  Measured (us, rows of 128256 tokens): bf16 to fp32, where
+    // they make one wave of two, 48 rows 12.7 in chunks of five vectors and 11.3 in three turns of three, 64 rows 14.1 and 12.7;
+    // where they do not, 32 rows 8.8 and 10.1, 96 rows 23.1 and 23.3, 200 rows of 50257 18.8 and 21.8.  fp32, past two waves, in
+    // chunks of two vectors and two turns of three 32 rows 10.4 and 9.9, 256 rows 69.5 and 51.1; before, 16 rows 6.4 and 7.9.
+    const long long slots = kCtas * device_sms();
+    auto takes = [&](int vecs) { return static_cast<long long>(a.n_rows) * ((a.vocab + 8 * kThreads * vecs - 1) / (8 * kThreads * vecs)); };
+    if (IN32 ? takes(kVecs) > 2 * slots : takes(kVecs) > slots && takes(9) <= slots) return run<IN32, OUT32, 3, IN32 ? 2 : 3, false>(a, stream);
+    return run<IN32, OUT32, kVecs, 1, false>(a, stream);
 }
 
 }  // namespace

@@ -111,6 +111,23 @@ CASES = [  # rows of each request, vocabulary, tokens of each, biases, drafts, m
 ]
 
 
+@pytest.mark.parametrize("kinds", [(BF, BF), (BF, F32), (F32, F32), (F32, BF)], ids=["bb", "bf", "ff", "fb"])
+@pytest.mark.parametrize("rows,V", [(56, 100003), (66, 65537), (100, 50257), (16, 131071)])
+def test_chunks_in_turns(rows, V, kinds):
+    """Decode batches on either side of where the chunks change their length."""
+    rng = np.random.default_rng(V)
+    c = _case(V, [1] * rows, V, rng.integers(0, 400, rows).tolist(), 6, False, True, kinds)
+    rules, kw = _args(c)
+    out = torch.full((rows, c["wide"]), 9.0, dtype=kinds[1], device="cuda")
+    abi.lora_logits_adjust(out[:, :V], c["x"][:, :V], rules, **kw)
+    _check(out[:, :V], *_want(c), kinds[1])
+    assert (out[:, V:] == 9).all()
+    if kinds[0] == kinds[1]:     # in place
+        x = c["x"][:, :V]
+        abi.lora_logits_adjust(x, x, rules, **kw)
+        assert torch.equal(x, out[:, :V])
+
+
 @pytest.mark.parametrize("kinds", [(BF, BF), (F32, F32)], ids=["bb", "ff"])
 @pytest.mark.parametrize("q,V", [([40] * 50, 300), ([40] * 50, 2048), ([130, 70, 1], 4099), ([200, 65], 150)], ids=lambda v: str(v) if isinstance(v, int) else f"{len(v)}x{max(v)}")
 def test_rows_of_large_trees(q, V, kinds):
