@@ -13,7 +13,7 @@
 // Bound: latency, of the tables (path, pages) and then of the positions
 // themselves, 144 bytes in four places; beyond that the half words of V, which
 // DRAM fetches and writes by sectors.  Measured, start to start: 64 requests in
-// 32 layers (14 MB) 9.8 us, a fifth of a copy's rate; one request in 28 layers 2.7.
+// 32 layers (14 MB) 9.2 us, a quarter of a copy's rate; one request in 28 layers 2.6.
 #include <algorithm>
 
 #include "kv4.h"
@@ -25,8 +25,10 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMoves = 4;      // of a warp: eight lanes to each
-constexpr int kTogether = 2;   // units on their way (us, 64 requests, 32 layers: 9.8; with 1 11.3, with 4 10.8, which has fewer warps)
-constexpr int kUnits = 16;     // of a CTA, as long as the CTAs fill the SMs
+// Units on their way, with the registers for four CTAs on an SM, and units of a CTA, fewer where the CTAs would not be three to
+// an SM.  Measured (us, 16 / 64 / 256 requests, 32 layers of 8 heads): 3 and 24 4.7 / 9.2 / 32.6, 2 and 16 4.4 / 9.7 / 35.5, 4 and
+// 32 5.4 / 11.2 / 33.2; 2 and 16 in five CTAs 5.1 / 9.8 / 33.4, in six 6.5 / 10.1 / 32.6.  32 requests 6.6, with CTAs for two to an SM 8.0.
+constexpr int kTogether = 3, kUnits = 24;
 
 // kBytes adjacent bytes, 4 to 16, in words.
 template <int kBytes>
@@ -44,7 +46,7 @@ __device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t (&w)[4])
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 6) kv4_keep_kernel(const __grid_constant__ KeepArgs a, int n_layers, int layers_each)
+__global__ void __launch_bounds__(kThreads, 4) kv4_keep_kernel(const __grid_constant__ KeepArgs a, int n_layers, int layers_each)
 {
     constexpr int kGroups = D / kv4::kGroup;
     const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 6) kv4_keep_kernel(const __grid_cons
 cudaError_t launch_kv4_keep(const KeepArgs& a, int n_layers, cudaStream_t stream)
 {
     int each = std::max(1, std::min(n_layers, kUnits / a.cache.n_kv));
-    while (each > 1 && static_cast<long long>(a.batch.n_seqs) * ((n_layers + each - 1) / each) < 2 * device_sms()) each /= 2;
+    while (each > 1 && static_cast<long long>(a.batch.n_seqs) * ((n_layers + each - 1) / each) < 3 * device_sms()) --each;
     PdlLaunch l(dim3(a.batch.n_seqs, (n_layers + each - 1) / each), kThreads, 0, stream);
     const cudaError_t e = a.cache.head_dim == 64 ? cudaLaunchKernelEx(&l.cfg, kv4_keep_kernel<64>, a, n_layers, each) : cudaLaunchKernelEx(&l.cfg, kv4_keep_kernel<128>, a, n_layers, each);
     note_launch();
