@@ -25,13 +25,20 @@ constexpr int kFewRows = 24;
 // The account takes the whole context, a window or not: 64 rows in 32000
 // positions with a window of 1024 go to the kernel for many and take 25 us,
 // where the same rows in 1088 positions take 14 in the other.
+// Drafted trees have an account of their own, from 70 batches of even lengths
+// timed both ways (1 to 64 requests, up to 512 rows of a kv head, 100 to 8000
+// positions): 1.2 % on the mean above the faster kernel, 3.5 % by the other
+// account; 16 trees of 18 rows, 64 heads, over 164 positions 28 / 20, 13 of 9
+// over 854 35 / 28, one of 26 over 6812 29 / 32.  It takes the window's positions.
 int few_limit(const AttendArgs& a)
 {
     const int group = a.n_heads / a.cache.n_kv;
     const long long rows = static_cast<long long>(group) * a.batch.max_q_len;
-    const double units = static_cast<double>(a.batch.n_seqs) * a.cache.n_kv, ctx = a.batch.max_ctx_len;
-    const double few = 9e-6 + units * std::ceil(rows / 8.) * (ctx / 32 + 2) * 0.9e-9;
-    const double many = 22e-6 + units * std::ceil(rows / 256.) * (ctx / 128 + 4) * 11.5e-9;
+    const double units = static_cast<double>(a.batch.n_seqs) * a.cache.n_kv;
+    const double ctx = a.tree && a.window > 0 ? std::min(a.batch.max_ctx_len + 0LL, a.window + 0LL + a.batch.max_q_len) : a.batch.max_ctx_len;
+    const double slices = units * std::ceil(rows / 8.) * (ctx / 32 + 2), items = units * std::ceil(rows / 256.);
+    const double few = a.tree ? 10e-6 + slices * (a.cache.head_dim == 64 ? 0.62e-9 : 0.9e-9) : 9e-6 + slices * 0.9e-9;
+    const double many = 22e-6 + (a.tree ? items * (ctx / 128) * 12.5e-9 : items * (ctx / 128 + 4) * 11.5e-9);
     if (rows <= kFewRows || few <= many) return static_cast<int>(std::min<long long>(rows, 1 << 30));
     return group <= kFewRows ? kFewRows : 0;
 }
