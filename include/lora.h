@@ -476,6 +476,8 @@ typedef struct {
     int n_rows;
     int max_q_len;              /* host values; upper bounds, which pick the kernel form */
     int max_ctx_len;            /* and size the grids */
+    const int32_t* held;        /* [dev] [n_seqs] or NULL: of a lora_kv4_plan's batch its held_out, which
+                                   lora_kv4_keep alone looks at */
 } lora_kv4_batch_t;
 
 /* Bytes of one page's block of one kv head; 0 for a page size or head
@@ -624,9 +626,9 @@ typedef struct {
  *      + place in the page (-1 where the table names no page); -1 in each for
  *      rows of sequences without a place and for rows past the last.  A depth outside [0, max_ctx_len) gives the
  *      position -1.
- * q_starts, ctx_lens and block_table are those of a lora_kv4_batch_t with
- * n_rows = max_rows; the counts may change from call to call, and replay to
- * replay, within the bounds.
+ * q_starts, ctx_lens, block_table and, as held, held_out are those of a
+ * lora_kv4_batch_t with n_rows = max_rows; the counts may change from call to
+ * call, and replay to replay, within the bounds.
  * q_starts  [dev] int32 [n_seqs + 1]     ctx_lens [dev] int32 [n_seqs]
  * row_seq, positions  [dev] int32 [max_rows] or NULL;  slots [dev] int64 [max_rows] or NULL
  * q_lens, lens  [dev] int32 [n_seqs];  depths [dev] int32 [max_rows] or NULL
@@ -684,8 +686,12 @@ lora_status_t lora_kv4_attend_tree(lora_bf16_t* out, int ld_out, const lora_bf16
  * caches  [host] n_caches structs of the same page size, heads and dimension
  * n_keep  [dev] int32 [n_seqs];  path [dev] int32 [n_seqs][ld_path]
  * lens    [dev] int32 [n_seqs] or NULL; not the batch's ctx_lens
- * A sequence with more rows than positions (one without a place) is left as
- * it is, and so is its lens; so is, flagged, one with inconsistent tables or
+ * A sequence without a place is left as it is, and so is its lens: one with
+ * more rows than positions, or, where the batch names held, one without rows
+ * and positions that holds pages (an ended one holds none, and its lens
+ * becomes 0).  Without held a sequence that a plan refused and that has no
+ * rows in the batch (it was idle, or max_rows cut them all) looks like an ended
+ * one.  So is left, flagged, one with inconsistent tables or
  * n_keep outside [0, min(n, ld_path)] (LORA_DEV_BAD_SEGMENT) or with a path
  * that does not rise inside its rows (LORA_DEV_BAD_POSITION).  Where a position
  * that moves lies or would come to lie in a page that a cache does not have
@@ -694,7 +700,7 @@ lora_status_t lora_kv4_attend_tree(lora_bf16_t* out, int ld_out, const lora_bf16
  * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL pointers,
  * n_caches < 0, the same pages twice, lens the same as ctx_lens), LORA_ERR_SHAPE (caches that
  * differ, ld_path < 0, a block table too small), LORA_ERR_METADATA and
- * LORA_ERR_ALIGNMENT as lora_kv4_append, LORA_ERR_CUDA.
+ * LORA_ERR_ALIGNMENT as lora_kv4_append (held too), LORA_ERR_CUDA.
  */
 lora_status_t lora_kv4_keep(const lora_kv4_cache_t* caches, int n_caches, const lora_kv4_batch_t* batch,
                             const int32_t* n_keep, const int32_t* path, int ld_path, int32_t* lens,

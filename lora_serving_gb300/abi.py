@@ -88,7 +88,7 @@ class lora_kv4_cache_t(ctypes.Structure):
 class lora_kv4_batch_t(ctypes.Structure):
     _fields_ = [("q_starts", ctypes.c_void_p), ("ctx_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("ld_table", ctypes.c_int), ("n_seqs", ctypes.c_int), ("n_rows", ctypes.c_int),
-                ("max_q_len", ctypes.c_int), ("max_ctx_len", ctypes.c_int)]
+                ("max_q_len", ctypes.c_int), ("max_ctx_len", ctypes.c_int), ("held", ctypes.c_void_p)]
 
 
 class lora_kv4_pool_t(ctypes.Structure):

@@ -155,6 +155,7 @@ struct KeepArgs {
     Pages layers[LORA_KEEP_LAYERS];
     kv4::Cache cache;   // what the layers have in common
     kv4::Batch batch;
+    const int32_t* held;   // pages of each sequence, or NULL
     const int32_t* n_keep;
     const int32_t* path;
     int ld_path;

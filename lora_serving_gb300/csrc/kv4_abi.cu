@@ -278,10 +278,10 @@ lora_status_t lora_kv4_keep(const lora_kv4_cache_t* caches, int n_caches, const 
     if (ld_path < 0 || batch->ld_table < (static_cast<long long>(batch->max_ctx_len) + a.cache.page_size - 1) / a.cache.page_size)
         return LORA_ERR_SHAPE;
     for (const void* p : {static_cast<const void*>(batch->q_starts), static_cast<const void*>(batch->ctx_lens),
-                          static_cast<const void*>(batch->block_table), static_cast<const void*>(n_keep), static_cast<const void*>(path),
-                          static_cast<const void*>(lens)})
+                          static_cast<const void*>(batch->block_table), static_cast<const void*>(batch->held), static_cast<const void*>(n_keep),
+                          static_cast<const void*>(path), static_cast<const void*>(lens)})
         if (!aligned(p, 4)) return LORA_ERR_ALIGNMENT;
-    a.n_keep = n_keep; a.path = path; a.ld_path = ld_path; a.status = dev_status;
+    a.held = batch->held; a.n_keep = n_keep; a.path = path; a.ld_path = ld_path; a.status = dev_status;
     for (int at = 0; at < n_caches; at += LORA_KEEP_LAYERS) {
         const int n = n_caches - at < LORA_KEEP_LAYERS ? n_caches - at : LORA_KEEP_LAYERS;
         for (int i = 0; i < n; ++i)

@@ -58,11 +58,12 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_keep_kernel(const __grid_cons
     const int32_t* path = a.path + static_cast<long long>(s) * a.ld_path;
     const int32_t* table = a.batch.block_table + static_cast<long long>(s) * a.batch.ld_table;
     const int keep = __ldg(a.n_keep + s);
+    const int held = a.held ? __ldg(a.held + s) : 0;
     const int early = lane < a.ld_path ? __ldg(path + lane) : 0;
     kv4::Seq q;
     if (!kv4::load_seq(a.batch, s, q, status)) return;
     const int base = q.ctx - q.n;
-    if (base < 0) return;   // a sequence without a place
+    if (base < 0 || (q.ctx == 0 && held != 0)) return;   // a sequence without a place; with rows or, holding pages, without
     if (keep < 0 || keep > q.n || keep > a.ld_path) {
         flag(status, LORA_DEV_BAD_SEGMENT);
         return;

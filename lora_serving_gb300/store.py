@@ -164,16 +164,17 @@ class KV4Batch:
     """Where a batch's rows stand in a cache: device int32 q_starts [n_seqs+1],
     ctx_lens [n_seqs] and block_table [n_seqs][pages], with the host's upper
     bounds.  The tensors may be refilled between calls (and replays of a
-    captured graph) as long as the bounds hold."""
+    captured graph) as long as the bounds hold.  held: device int32 [n_seqs],
+    the pages of each sequence of a lora_kv4_plan's batch (its held_out)."""
 
-    def __init__(self, q_starts, ctx_lens, block_table, *, n_rows: int, max_q_len: int, max_ctx_len: int):
+    def __init__(self, q_starts, ctx_lens, block_table, *, n_rows: int, max_q_len: int, max_ctx_len: int, held=None):
         n_seqs = int(ctx_lens.numel())
         for name, t, n in (("q_starts", q_starts, n_seqs + 1), ("ctx_lens", ctx_lens, n_seqs)):
             if t.dim() != 1 or t.numel() != n or (n > 1 and t.stride(0) != 1):
                 raise ValueError(f"{name} must hold {n} adjacent entries")
         if block_table.shape[0] != n_seqs:
             raise ValueError(f"block_table must have {n_seqs} rows")
-        self.q_starts, self.ctx_lens, self.block_table = q_starts, ctx_lens, block_table
+        self.q_starts, self.ctx_lens, self.block_table, self.held = q_starts, ctx_lens, block_table, held
         # the C side checks ld_table against max_ctx_len: with a stride wider
         # than the row it would pass a table that is too narrow
         ld = int(block_table.shape[1])
@@ -181,7 +182,7 @@ class KV4Batch:
             raise ValueError("block_table must be contiguous")
         self.c = abi.lora_kv4_batch_t(abi._dev(q_starts, "q_starts", "i32"), abi._dev(ctx_lens, "ctx_lens", "i32"),
                                       abi._dev(block_table, "block_table", "i32", True), ld, n_seqs,
-                                      int(n_rows), int(max_q_len), int(max_ctx_len))
+                                      int(n_rows), int(max_q_len), int(max_ctx_len), _vector(held, "held", "i32", n_seqs))
         self.addr = ctypes.addressof(self.c)
 
     @classmethod
@@ -230,7 +231,8 @@ class KV4Plan:
         new = lambda n, dtype=torch.int32: torch.full((n,), -1, dtype=dtype, device=dev)  # noqa: E731
         self.q_starts, self.ctx_lens = torch.zeros(n_seqs + 1, dtype=torch.int32, device=dev), torch.zeros(n_seqs, dtype=torch.int32, device=dev)
         self.row_seq, self.positions, self.slots = new(max_rows), new(max_rows).view(-1, 1), new(max_rows, torch.int64)
-        self.batch = KV4Batch(self.q_starts, self.ctx_lens, block_table, n_rows=max_rows, max_q_len=max_q_len, max_ctx_len=max_ctx_len)
+        self.batch = KV4Batch(self.q_starts, self.ctx_lens, block_table, n_rows=max_rows, max_q_len=max_q_len, max_ctx_len=max_ctx_len,
+                              held=self.held_out)
         pool = abi.lora_kv4_pool_t(_vector(free_pages, "free_pages", "i32", 1), _vector(n_free, "n_free", "i32", 1),
                                    _vector(held, "held", "i32", n_seqs), _vector(self.n_free_out, "n_free_out", "i32", 1),
                                    _vector(self.held_out, "held_out", "i32", n_seqs), self.batch.c.block_table,
