@@ -163,7 +163,7 @@ __device__ __forceinline__ Request request_of(const LogitsArgs& a, int s)
         r.end = __ldg(a.q_starts + s + 1);
     }
     r.ok = r.len >= 0 && r.len <= a.rules.ld_tokens && r.prompt >= 0 && r.prompt <= r.len && r.biases >= 0 && r.biases <= a.rules.ld_bias &&
-           r.first >= 0 && (!a.drafts || r.end <= a.n_rows);
+           r.first >= 0 && r.first <= r.end && (!a.drafts || r.end <= a.n_rows);   // (in this order their difference stays in 32 bits)
     r.counts = r.rule.repetition != 1.f || r.rule.frequency != 0.f || r.rule.presence != 0.f;
     r.plain = !r.ok || (!r.counts && r.biases == 0);
     return r;
