@@ -695,7 +695,8 @@ lora_status_t lora_kv4_attend_tree(lora_bf16_t* out, int ld_out, const lora_bf16
  * n_keep outside [0, min(n, ld_path)] (LORA_DEV_BAD_SEGMENT) or with a path
  * that does not rise inside its rows (LORA_DEV_BAD_POSITION).  Where a position
  * that moves lies or would come to lie in a page that a cache does not have
- * (LORA_DEV_BAD_PAGE), nothing moves in that cache.
+ * (LORA_DEV_BAD_PAGE), nothing moves in that cache, and lens[s] stays as it is,
+ * since the caches no longer hold the same rows behind base.
  * Two sequences that share a page which a row moves in race.
  * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL pointers,
  * n_caches < 0, the same pages twice, lens the same as ctx_lens), LORA_ERR_SHAPE (caches that

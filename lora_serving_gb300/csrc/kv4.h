@@ -160,6 +160,7 @@ struct KeepArgs {
     const int32_t* path;
     int ld_path;
     int32_t* lens;      // NULL in all launches but a call's first
+    int least_pages;    // pages of the smallest of the call's caches, whichever launch takes it
     int32_t* status;
 };
 cudaError_t launch_kv4_keep(const KeepArgs& a, int n_layers, cudaStream_t stream);

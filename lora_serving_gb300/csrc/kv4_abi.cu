@@ -263,8 +263,10 @@ lora_status_t lora_kv4_keep(const lora_kv4_cache_t* caches, int n_caches, const 
         LORA_TRY(check_cache(caches + i, c));
         if (i == 0) {
             a.cache = c;
+            a.least_pages = c.n_pages;
             LORA_TRY(check_batch(batch, c, a.batch));
         }
+        if (c.n_pages < a.least_pages) a.least_pages = c.n_pages;
         // the same pages twice would be moved twice: a bit for each of 256 classes of pointers, and a look at the others where it is set
         const unsigned bit = static_cast<unsigned>((reinterpret_cast<uintptr_t>(c.pages) >> 8) * 0x9E3779B97F4A7C15ull >> 56);
         if (seen[bit >> 6] >> (bit & 63) & 1u)

@@ -90,7 +90,8 @@ __global__ void __launch_bounds__(kThreads, 4) kv4_keep_kernel(const __grid_cons
         return;
     }
     last_page = __reduce_max_sync(0xFFFFFFFFu, last_page);
-    if (a.lens && layer0 == 0 && tid == 0) a.lens[s] = base + keep;
+    // (a sequence whose rows one of the caches cannot move has none of them from now on)
+    if (a.lens && layer0 == 0 && tid == 0 && last_page < static_cast<uint32_t>(a.least_pages)) a.lens[s] = base + keep;
     if (first == keep) return;
     if (tid < min(layers_each, n_layers - layer0) && last_page >= static_cast<uint32_t>(a.layers[layer0 + tid].n_pages)) flag(a.status, LORA_DEV_BAD_PAGE);
 
