@@ -10,7 +10,9 @@
 // waits for another: a page that was given back and is taken again in the same
 // call is read where it came from.  Where the counters' results go to
 // the place that other CTAs read them from, the CTAs are one cluster, whose one
-// barrier, begun before the sums, stands before these results alone.  A sequence
+// barrier, begun before the sums, stands before these results alone.  (What the
+// kernel writes, counters, stack and table, it reads by ordinary loads: the
+// read-only path is for what nobody writes while a kernel runs.)  A sequence
 // that asks for more than there is gets nothing, and with it none after it gets
 // any: the sums stay sums, no sequence waiting for another's answer.
 // Bound: latency, of a chain of loads, sums over the CTA, a search, and loads;
@@ -58,7 +60,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     int ctx[kOwn], held[kOwn];
     int faults = 0;
     uint32_t sum[3] = {0, 0, 0};
-    int n_free = __ldg(a.pool.n_free);
+    int n_free = *a.pool.n_free;
     if (n_free < 0 || n_free > a.pool.n_pages) {
         faults |= LORA_DEV_BAD_PAGE;
         n_free = 0;
@@ -66,12 +68,12 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     int q_of[kOwn], len_of[kOwn], held_of[kOwn];   // every load on its way before the first is looked at
     auto load = [&](const int32_t* from, int (&to)[kOwn]) {
         if (kOwn == 4 && a.wide_in && tid * 4 + 3 < n) {
-            const int4 x = __ldg(reinterpret_cast<const int4*>(from) + tid);
+            const int4 x = reinterpret_cast<const int4*>(from)[tid];
             to[0] = x.x; to[1 % kOwn] = x.y; to[2 % kOwn] = x.z; to[3 % kOwn] = x.w;
             return;
         }
 #pragma unroll
-        for (int i = 0; i < kOwn; ++i) to[i] = tid * kOwn + i < n ? __ldg(from + tid * kOwn + i) : 0;
+        for (int i = 0; i < kOwn; ++i) to[i] = tid * kOwn + i < n ? from[tid * kOwn + i] : 0;
     };
     load(a.q_lens, q_of);
     load(a.lens, len_of);
@@ -191,16 +193,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
     // The f-th page taken: from the stack's top, which is what has been given back, where it still lies.
     auto page_taken = [&](uint32_t f) -> int {
         const uint32_t from = there - 1 - f;
-        if (from < static_cast<uint32_t>(n_free)) return __ldg(stack + from);
+        if (from < static_cast<uint32_t>(n_free)) return stack[from];
         const int s = seq_at(back_at, from - n_free);
-        return __ldg(a.pool.block_table + static_cast<long long>(s) * a.pool.ld_table + (from - n_free - back_at[s]));
+        return a.pool.block_table[static_cast<long long>(s) * a.pool.ld_table + (from - n_free - back_at[s])];
     };
     const uint32_t n_back = there - n_free, n_taken = taken, runs = a.row_seq || a.positions || a.slots ? (a.max_rows + kRun - 1) / kRun : 0;
     for (uint32_t job = tid < workers ? rank * workers + tid : 0xFFFFFFFFu; job < runs + n_taken + n_back; job += ranks * workers) {
         if (job >= runs + n_taken) {   // a page given back: onto the stack
             const uint32_t f = job - runs - n_taken;
             const int s = seq_at(back_at, f);
-            stack[n_free + f] = __ldg(a.pool.block_table + static_cast<long long>(s) * a.pool.ld_table + (f - back_at[s]));
+            stack[n_free + f] = a.pool.block_table[static_cast<long long>(s) * a.pool.ld_table + (f - back_at[s])];
             continue;
         }
         if (job >= runs) {   // a page taken: into the table, behind those that the sequence holds
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1) kv4_plan_kernel(PlanArgs a, in
             page[k] = -1;
             if (seq[k] < 0) continue;
             const uint32_t at_page = (len[k] + t0 + k - static_cast<int>(row_at[seq[k]])) >> a.page_shift, h = held_s[seq[k]];
-            if (at_page < h) page[k] = __ldg(a.pool.block_table + static_cast<long long>(seq[k]) * a.pool.ld_table + at_page);
+            if (at_page < h) page[k] = a.pool.block_table[static_cast<long long>(seq[k]) * a.pool.ld_table + at_page];
             else page[k] = page_taken(need_at[seq[k]] + at_page - h);
         }
 #pragma unroll
