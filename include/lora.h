@@ -746,9 +746,10 @@ typedef struct {
  * Tokens outside [0, vocab), in tokens, drafts or bias_ids, count for nothing.
  * Of a token's entries in bias_ids the last one counts.
  * Device-detected faults, each of which leaves the row unwritten: row_seq
- * outside [-1, n_seqs), token_lens outside [0, ld_tokens], prompt_lens outside
- * [0, token_lens], n_bias outside [0, ld_bias], with drafts a row outside its
- * request's rows (LORA_DEV_BAD_SEGMENT); allowed_rows outside [-1, n_allowed)
+ * outside [-1, n_seqs) (below -1 without rules), token_lens outside
+ * [0, ld_tokens], prompt_lens outside [0, token_lens], n_bias outside
+ * [0, ld_bias], with drafts a row outside its request's rows
+ * (LORA_DEV_BAD_SEGMENT); allowed_rows outside [-1, n_allowed)
  * (LORA_DEV_SLOT_OUT_OF_RANGE).
  * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL pointers,
  * a negative count, an unknown type, drafts without rules, tree or q_starts,

@@ -148,6 +148,7 @@ struct Request {
 __device__ __forceinline__ Request request_of(const LogitsArgs& a, int s)
 {
     Request r{true, false, true, 0, 0, 0, 0, 0x7FFFFFFF, {1.f, 0.f, 0.f, nullptr}};
+    r.ok = s >= -1;
     if (!a.rules.tokens) return r;
     r.ok = s >= 0 && s < a.rules.n_seqs;
     if (!r.ok) return r;
