@@ -624,8 +624,8 @@ typedef struct {
  *      embedding (depth: depths[row], its depth in a drafted tree, or, with
  *      depths NULL, its number in the sequence), and its slot, page * page_size
  *      + place in the page (-1 where the table names no page); -1 in each for
- *      rows of sequences without a place and for rows past the last.  A depth outside [0, max_ctx_len) gives the
- *      position -1.
+ *      rows of sequences without a place and for rows past the last.  A depth
+ *      outside [0, max_ctx_len) gives the position -1.
  * q_starts, ctx_lens, block_table and, as held, held_out are those of a
  * lora_kv4_batch_t with n_rows = max_rows; the counts may change from call to
  * call, and replay to replay, within the bounds.
@@ -638,7 +638,9 @@ typedef struct {
  * max_q_len rows, with lens negative or ctx_lens above max_ctx_len, with held
  * outside [0, ld_table], or with rows past max_rows: it has no place, as in 3
  * (the row starts are cut to max_rows); one that has ended with such a held
- * gives nothing back.  LORA_DEV_BAD_PAGE: n_free outside [0, n_pages] counts
+ * gives nothing back.  One that has more than max_q_len rows in the batch is
+ * past the batch's own bound: append, attention and keep skip and flag it, and
+ * its rows are not written (they get no zeros).  LORA_DEV_BAD_PAGE: n_free outside [0, n_pages] counts
  * as 0, and pages given back past n_pages in all are dropped.
  * Errors (before anything is enqueued): LORA_ERR_INVALID_ARG (NULL pointers,
  * negative counts, no pages, ctx_lens the same as lens), LORA_ERR_SHAPE

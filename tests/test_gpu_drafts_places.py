@@ -65,3 +65,30 @@ def test_a_sequence_without_a_place_keeps_its_length(in_place):
     if in_place:
         abi.lora_kv4_plan(p, _i32([0, -1, 0, 1, 1, 0, 0, 0, 1]), lens, dev_status=st)
         assert p.ctx_lens.tolist() == [22, 0, 6, 31, 18, 0, 40, 0, 13]
+
+
+def test_more_rows_than_the_bound():
+    """A sequence past max_q_len has no place either, but its rows stay in the batch, whose bound they pass: append,
+    attention and keep skip it, flagged, and its rows are not written (no zeros)."""
+    q, cached = [9, 2, 3], [12, 20, 0]
+    p = store.KV4Plan.empty(3, 8, PAGE, max_rows=20, max_q_len=MAX_Q, max_ctx_len=MAX_CTX)
+    p.held.copy_(_i32([1, 2, 0]))
+    p.block_table[:, :2] = _i32([[0, -1], [1, 2], [-1, -1]])
+    p.n_free.fill_(5)
+    cache, lens, st = store.KV4Cache(8, PAGE, KV, D), _i32(cached), _i32([0])
+    abi.lora_kv4_plan(p, _i32(q), lens, dev_status=st)
+    assert abi.lora_read_device_status(st) == abi.LORA_DEV_BAD_SEGMENT
+    assert p.q_starts.tolist() == [0, 9, 11, 14] and p.ctx_lens.tolist() == [0, 22, 3]
+    assert p.row_seq.tolist() == [-1] * 9 + [1, 1, 2, 2, 2] + [-1] * 6
+    qkv = torch.randn(20, (H + 2 * KV) * D, device="cuda").bfloat16()
+    qr, o = (torch.full((20, H * D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    tree, ws = torch.full((20, 1), -1, dtype=torch.int32, device="cuda"), store.kv4_workspace(cache, H, p.batch)
+    for call in (lambda: abi.lora_kv4_append(qr, qkv, cache, p.batch, n_heads=H, q_off=0, k_off=H * D, v_off=(H + KV) * D, dev_status=st),
+                 lambda: abi.lora_kv4_attend_tree(o, qr, cache, p.batch, tree, ws, n_heads=H, scale=0.1, dev_status=st),
+                 lambda: abi.lora_kv4_keep(store.KV4Layers([cache]), p.batch, _i32([2, 1, 1]), _i32([[0, 1]] * 3), lens=lens, dev_status=st)):
+        st.zero_()
+        call()
+        assert abi.lora_read_device_status(st) == abi.LORA_DEV_BAD_SEGMENT
+    for t in (qr, o):
+        assert (t[:9] == 7).all() and (t[14:] == 7).all() and not (t[9:14] == 7).all(1).any()
+    assert lens.tolist() == [12, 21, 1]
