@@ -216,7 +216,7 @@ def _ld(t) -> int:
     return int(t.stride(0))
 
 
-_DTYPES = torch and {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "i64": torch.int64, "u8": torch.uint8,
+_DTYPES = torch and {"bf16": torch.bfloat16, "f32": torch.float32, "i32": torch.int32, "u8": torch.uint8,
                      "e4m3": torch.float8_e4m3fn}
 
 
