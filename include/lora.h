@@ -554,8 +554,9 @@ lora_status_t lora_kv4_read(lora_bf16_t* k, int ld_k, lora_bf16_t* v, int ld_v, 
  * largest vanishes), q is taken to fp16 after scaling
  * each row by a power of two (exact but for elements 2^-22 below the row's
  * largest), cached values to fp16.  A call repeats bit for bit; another batch
- * around the same rows may cut their sums at other places, and with them the
- * last bits.
+ * around the same rows, or other bounds, may cut their sums at other places, or
+ * go to the kernel for few rows, which takes K's values exactly, or to the one
+ * for many, and change the last bits.
  * Device-detected faults as above; LORA_DEV_TIMEOUT: a wait inside the call
  * ran out, and rows of the call are undefined.
  * Errors (before anything is enqueued): as lora_kv4_append, plus
@@ -662,7 +663,9 @@ lora_status_t lora_kv4_plan(int32_t* q_starts, int32_t* ctx_lens, int32_t* row_s
  * where depth is the number of its set bits below n less one (0 where it has
  * none).  Bits name ancestors and the row itself; any set is taken, the
  * window is not applied to it, and bits from n on are not looked at.  With
- * bits 0..i in row i (and a window of n at least) this is lora_kv4_attend.
+ * bits 0..i in row i (and a window of n at least) this is lora_kv4_attend, at
+ * a price: it goes through every pair of a sequence's rows, so that long
+ * prompts cost several times what they cost there.
  * tree  [dev] uint32 [n_rows][ld_tree], bit j % 32 of word j / 32;
  *       ld_tree >= ceil(max_q_len / 32)
  * All else, arguments, workspace, rounding, rows that see nothing or have no
@@ -684,16 +687,17 @@ lora_status_t lora_kv4_attend_tree(lora_bf16_t* out, int ld_out, const lora_bf16
  * for i < n_keep[s], in each of the caches (one per layer, all with the
  * batch's block table), bit for bit.  path[s] rises strictly within [0, n).
  * lens[s] = base + n_keep[s]: the sequence's cached positions from now on
- * (those behind hold what they held).
+ * (those behind hold what they held).  Without caches nothing happens.
  * caches  [host] n_caches structs of the same page size, heads and dimension
  * n_keep  [dev] int32 [n_seqs];  path [dev] int32 [n_seqs][ld_path]
  * lens    [dev] int32 [n_seqs] or NULL; not the batch's ctx_lens
  * A sequence without a place is left as it is, and so is its lens: one with
  * more rows than positions, or, where the batch names held, one without rows
  * and positions that holds pages (an ended one holds none, and its lens
- * becomes 0).  Without held a sequence that a plan refused and that has no
- * rows in the batch (it was idle, or max_rows cut them all) looks like an ended
- * one.  So is left, flagged, one with inconsistent tables or
+ * becomes 0; an idle one with pages and nothing cached is left, too, its lens
+ * being 0 already in the plan's array).  Without held a sequence that a plan
+ * refused and that has no rows in the batch (it was idle, or max_rows cut them
+ * all) looks like an ended one.  So is left, flagged, one with inconsistent tables or
  * n_keep outside [0, min(n, ld_path)] (LORA_DEV_BAD_SEGMENT) or with a path
  * that does not rise inside its rows (LORA_DEV_BAD_POSITION).  Where a position
  * that moves lies or would come to lie in a page that a cache does not have
@@ -734,7 +738,8 @@ typedef struct {
  *   x <- x + bias(v)
  *   x <- -infinity                                   if v is not allowed
  * in fp32, rounded once to out's type.
- * out        [dev] bf16 or fp32 [n_rows][ld_out]; may be logits itself where the types are the same
+ * out        [dev] bf16 or fp32 [n_rows][ld_out]; may be logits itself where the types are the same, and overlaps it
+ *            in no other way
  * logits     [dev] bf16 or fp32 [n_rows][ld]; both 16-byte aligned, ld and ld_out multiples of 8;
  *            columns from vocab on are neither read nor written (any vocab)
  * rules      [host] struct, or NULL: no penalties and biases

@@ -75,8 +75,11 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(AttendArgs a, kv4::Partials p0, kv4::Partials p1)
 {
     tc::grid_dep_wait();
-    // When the next launch may begin decides which SMs the next call's CTAs come to, and with that what they share on the way from
-    // memory: at once, here, 8 trees of 64 rows over 32768 positions take 415 us and 16 prompts 297; at the end 425 and 290.
+    // When the next launch may begin: at once, here, or at the end.  Measured (us, early / late).  Where the next launch is the same
+    // call again, it decides which SMs that call's CTAs come to, and prompts gain by the late one: 16 prompts 302 / 291, trees of
+    // 16 to 64 rows in a window 43.9 / 44.2.  Before a product of 4096 columns the early one gains a little: such trees 60.0 / 60.9,
+    // tokens of 64 requests 31.1 / 31.4, a window 79.2 / 79.8, prompts 608 / 604 to 609.  Before a norm they differ by less than
+    // runs do, but for small trees, 18.1 / 17.7.
     if (a.tree) tc::grid_dep_launch();
     const int n0 = p0.ctas * join_ctas(p0.rows, D);
     const bool second = static_cast<int>(blockIdx.x) >= n0;

@@ -13,7 +13,7 @@
 // Bound: latency, of the tables (path, pages) and then of the positions
 // themselves, 144 bytes in four places; beyond that the half words of V, which
 // DRAM fetches and writes by sectors.  Measured, start to start: 64 requests in
-// 32 layers (14 MB) 9.2 us, a quarter of a copy's rate; one request in 28 layers 2.6.
+// 32 layers (14 MB) 9.4 us, a quarter of a copy's rate; one request in 28 layers 2.5.
 #include <algorithm>
 
 #include "kv4.h"

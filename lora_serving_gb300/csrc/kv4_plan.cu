@@ -17,8 +17,8 @@
 // any: the sums stay sums, no sequence waiting for another's answer.
 // Bound: latency, of a chain of loads, sums over the CTA, a search, and loads;
 // with thousands of sequences the sums' instructions, which every CTA repeats.
-// Measured, start to start: 64 requests of a token 2.5 us, 256 with 16 prompts
-// among them (17 k rows) 3.5 (4.9 with the counters in place), 4096 trees 6.4 (8.4).
+// Measured, start to start: 64 requests of a token 2.6 us (3.0 with the counters
+// in place), 256 with 16 prompts among them (17 k rows) 3.6 (5.0), 4096 trees 6.3 (8.5).
 #include <algorithm>
 
 #include "kv4.h"
@@ -287,8 +287,8 @@ cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stre
     cudaError_t e = once_on_device(done, [] { return cudaFuncSetAttribute(kv4_plan_kernel<kOwn, kRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, 4 * (4 * kMaxSeqs + 1)); });
     if (e != cudaSuccess) return e;
     const long long jobs = (a.max_rows + kRun - 1ll) / kRun + a.n_seqs;
-    // Threads of a CTA that take jobs: 256 where the CTAs are enough for that (4096 trees, 32 k rows: 7.7 us, 9.4 in 64
-    // CTAs with two rounds; 262 k rows 11.5, with all threads 7.9).
+    // Threads of a CTA that take jobs: 256 where the CTAs are enough for that, all where they are not (4096 requests, 262 k rows:
+    // 13.0 us with 256, 7.2 with all; 31 k rows 5.9 and 5.9).
     const int workers = in_place || jobs > static_cast<long long>(device_sms()) * kFewThreads ? threads : kFewThreads;
     const int ranks = static_cast<int>(std::max(1ll, std::min((jobs + workers - 1) / workers, in_place ? kRanks + 0ll : device_sms() + 0ll)));
     PdlLaunch l(dim3(ranks), threads, smem, stream);
@@ -309,11 +309,11 @@ cudaError_t run(const PlanArgs& a, int threads, bool in_place, cudaStream_t stre
 cudaError_t launch_kv4_plan(const PlanArgs& a, cudaStream_t stream)
 {
     // Measured (us): a kernel that runs once is bound by the reading of its code, too: one sequence to a thread and one row to a
-    // job where that does (64 requests 2.8, in code for four of each 4.4; 17 k rows 3.9 and 6.2).  As many threads as that needs
-    // (300 requests 4.2, with 1024 threads 4.6), 256 at least, as long as the CTAs hold the rows (256 requests, 128 k rows: 6.8,
-    // with 1024 threads 5.0; in place, 15.5 k rows: 6.4 and 5.3, 4 k rows 4.2 both).  Runs of four rows only where a cluster's
-    // threads would go through more than two rounds (in place, 4096 requests: 31.6 k rows 9.6 and, one by one, 12.2; 16 k rows
-    // 9.9 and 8.8).
+    // job where that does (64 requests 2.5, in code for four of each 5.1; 256 of 68 rows 3.2 and 4.8).  As many threads as that
+    // needs (300 requests 3.3, with 1024 threads 3.8), 256 at least, as long as the CTAs hold the rows (256 requests, 128 k rows:
+    // 5.8, with 1024 threads 4.2; in place, 15 k rows: 8.9 and 4.8, 4 k rows 3.7 both).  Runs of four rows only where a cluster's
+    // threads would go through more than two rounds (in place, 4096 requests: 31 k rows 8.3 and, one by one, 9.7; 16 k rows
+    // 8.4 and 7.2).
     const bool in_place = a.pool.n_free_out == a.pool.n_free || a.pool.held_out == a.pool.held;
     const int fewest = std::min(std::max((a.n_seqs + 255) / 256 * 256, kFewThreads), kMaxThreads);
     const int threads = a.max_rows <= fewest * (in_place ? 2 * kRanks : device_sms()) ? fewest : kMaxThreads;

@@ -18,8 +18,8 @@
 // warp without rules) and the start of a CTA's first row: tables, tokens,
 // counts, 4 us, which few CTAs are there to hide.  Measured: 512 rows of 128256
 // tokens in trees of 32, bf16, masks and penalties 57 us (263 MB, 0.69 of a
-// copy's rate; with masks alone 44), 64 rows to fp32 14.1 (50 MB; 12.1), one row
-// of 32000 tokens 1.7, start to start.
+// copy's rate; with masks alone 44), 64 rows to fp32 14.4 (50 MB; 12.1), one row
+// of 32000 tokens 1.9, start to start.
 #include <algorithm>
 
 #include "kv4.h"
